@@ -1,7 +1,8 @@
 """libzero Python binding: the per-shard ZeRO step of mixed-precision AdamW on
 one GB300.
 
-A thin ctypes layer over the C ABI in include/zero.h: every function below
+A thin ctypes layer over the C ABI in include/zero.h, include/zero_units.h
+and include/zero_train.h: every function below
 has the C function's name and only marshals arguments (device pointers are
 plain Python ints, host arrays become C arrays); all computation happens in
 the sm_103a kernels of _lib/libzero.so. Loading fails loudly when the library
@@ -33,14 +34,24 @@ __all__ = [
     "zero_unit_plan_tensors", "zero_gather_units", "zero_shard_units",
     "ZeroStrategyCost", "zero_unit_plan_strategy_cost", "ZERO_FULL_SHARD", "ZERO_SHARD_GRAD_OP",
     "ZERO_NO_SHARD", "ZERO_HYBRID_SHARD", "ZERO_NO_RESHARD_AFTER_FORWARD",
+    "ZERO_FP32", "ZERO_MAX_LOGIT_ROW_BYTES", "ZERO_CKPT_BLOCK", "ZERO_CKPT_PAD",
+    "ZERO_ACT_GELU", "ZERO_ACT_SWIGLU", "ZeroPolicyParams",
+    "zero_embedding", "zero_embedding_workspace_bytes", "zero_embedding_grad",
+    "zero_ckpt_bytes", "zero_ckpt_save", "zero_ckpt_load", "zero_ckpt_act",
+    "zero_ckpt_act_grad", "zero_ckpt_wgrad", "zero_token_logp", "zero_policy_loss",
 ]
 
 ZERO_BF16 = 0
 ZERO_FP16 = 1
+ZERO_FP32 = 2
 ZERO_MAX_RANKS = 64
 ZERO_TILE_ELEMS = 4096
 ZERO_NORM_OWNER_BLOCKS = 16
 ZERO_UNIT_MAX_ALIGN = 4096
+ZERO_MAX_LOGIT_ROW_BYTES = 8 * 192 * 1024
+ZERO_CKPT_BLOCK = 32
+ZERO_CKPT_PAD = 128
+ZERO_ACT_GELU, ZERO_ACT_SWIGLU = range(2)
 (ZERO_FULL_SHARD, ZERO_SHARD_GRAD_OP, ZERO_NO_SHARD, ZERO_HYBRID_SHARD,
  ZERO_NO_RESHARD_AFTER_FORWARD) = range(5)
 
@@ -125,6 +136,11 @@ class ZeroStrategyCost(C.Structure):
                 ("shard_ranks", C.c_int32), ("gathers_per_unit", C.c_int32)]
 
 
+class ZeroPolicyParams(C.Structure):
+    """zero_train.h zero_policy_params: clip range and KL coefficient."""
+    _fields_ = [("clip_lo", C.c_double), ("clip_hi", C.c_double), ("kl_coef", C.c_double)]
+
+
 _lib = None
 _variant = "release"
 _VP = C.c_void_p
@@ -205,6 +221,23 @@ def lib():
                                                    _P(ZeroStrategyCost)]
         L.zero_gather_units.argtypes = [_VP, C.c_int32, C.c_int32, _P(_VP), _P(_VP), _VP]
         L.zero_shard_units.argtypes = [_VP, C.c_int32, C.c_int32, _P(_VP), _P(_VP), _VP]
+        i32, i64 = C.c_int32, C.c_int64
+        L.zero_embedding.argtypes = [_VP, i32, i64, _VP, i64, i64, C.c_float, i32, _VP, _VP]
+        L.zero_embedding_workspace_bytes.argtypes = [i64, i64, i64]
+        L.zero_embedding_workspace_bytes.restype = C.c_size_t
+        L.zero_embedding_grad.argtypes = [_VP, i32, i64, _VP, i64, i64, C.c_float, i32, i32, _VP,
+                                          _VP, _VP]
+        L.zero_ckpt_bytes.argtypes = [i64, i64]
+        L.zero_ckpt_bytes.restype = C.c_size_t
+        L.zero_ckpt_save.argtypes = [_VP, i64, i64, i64, i32, _VP, _VP]
+        L.zero_ckpt_load.argtypes = [_VP, i64, i64, i32, _VP, i64, _VP]
+        L.zero_ckpt_act.argtypes = [i32, _VP, _VP, i64, i64, i64, i32, _VP, i64, _VP, _VP, _VP]
+        L.zero_ckpt_act_grad.argtypes = [i32, _VP, _VP, _VP, i64, i64, i64, i32, _VP, _VP, _VP,
+                                         i64, _VP]
+        L.zero_ckpt_wgrad.argtypes = [_VP, i64, i64, _VP, i64, i64, i32, _VP, _VP, _VP]
+        L.zero_token_logp.argtypes = [_VP, i64, i64, i64, i32, _VP, i32, _VP, _VP]
+        L.zero_policy_loss.argtypes = [_VP, i64, i64, i64, i32, _VP, i32, _VP, _VP, _VP, _VP,
+                                       _P(ZeroPolicyParams), _VP, _VP, _VP, _VP, _VP, _VP]
         _lib = L
     return _lib
 
@@ -515,6 +548,74 @@ def zero_unit_plan_strategy_cost(plan, strategy, n_replicas=1):
     _check("zero_unit_plan_strategy_cost", lib().zero_unit_plan_strategy_cost(
         plan, strategy, n_replicas, C.byref(out)))
     return out
+
+
+# ------------------------------------------- forward and backward operators ----
+# Device pointers are ints (0 or None: NULL); argument layouts, types and
+# errors are in include/zero_train.h.
+
+def zero_embedding(tokens, token_bytes, n_tokens, table, vocab, dim, scale, dtype, out, stream=0):
+    _check("zero_embedding", lib().zero_embedding(
+        tokens or None, token_bytes, n_tokens, table or None, vocab, dim, scale, dtype,
+        out or None, stream or None))
+
+
+def zero_embedding_workspace_bytes(n_tokens, vocab, dim):
+    return int(lib().zero_embedding_workspace_bytes(n_tokens, vocab, dim))
+
+
+def zero_embedding_grad(tokens, token_bytes, n_tokens, dy, vocab, dim, scale, dtype, accumulate,
+                        grad, workspace, stream=0):
+    _check("zero_embedding_grad", lib().zero_embedding_grad(
+        tokens or None, token_bytes, n_tokens, dy or None, vocab, dim, scale, dtype,
+        int(accumulate), grad or None, workspace or None, stream or None))
+
+
+def zero_ckpt_bytes(rows, cols):
+    return int(lib().zero_ckpt_bytes(rows, cols))
+
+
+def zero_ckpt_save(x, rows, cols, ld, dtype, ckpt, stream=0):
+    _check("zero_ckpt_save", lib().zero_ckpt_save(x or None, rows, cols, ld, dtype, ckpt or None,
+                                                  stream or None))
+
+
+def zero_ckpt_load(ckpt, rows, cols, dtype, out, ld, stream=0):
+    _check("zero_ckpt_load", lib().zero_ckpt_load(ckpt or None, rows, cols, dtype, out or None,
+                                                  ld, stream or None))
+
+
+def zero_ckpt_act(act, x, u, rows, cols, ld, dtype, y, ld_y, ckpt_x, ckpt_u, stream=0):
+    _check("zero_ckpt_act", lib().zero_ckpt_act(
+        act, x or None, u or None, rows, cols, ld, dtype, y or None, ld_y, ckpt_x or None,
+        ckpt_u or None, stream or None))
+
+
+def zero_ckpt_act_grad(act, ckpt_x, ckpt_u, dy, rows, cols, ld_dy, dtype, dx, du, y, ld,
+                       stream=0):
+    _check("zero_ckpt_act_grad", lib().zero_ckpt_act_grad(
+        act, ckpt_x or None, ckpt_u or None, dy or None, rows, cols, ld_dy, dtype, dx or None,
+        du or None, y or None, ld, stream or None))
+
+
+def zero_ckpt_wgrad(ckpt, rows, cols, dy, n, ld, dtype, dw, d_scaler=0, stream=0):
+    _check("zero_ckpt_wgrad", lib().zero_ckpt_wgrad(
+        ckpt or None, rows, cols, dy or None, n, ld, dtype, dw or None, d_scaler or None,
+        stream or None))
+
+
+def zero_token_logp(logits, rows, vocab, ld, dtype, actions, action_bytes, logp, stream=0):
+    _check("zero_token_logp", lib().zero_token_logp(
+        logits or None, rows, vocab, ld, dtype, actions or None, action_bytes, logp or None,
+        stream or None))
+
+
+def zero_policy_loss(logits, rows, vocab, ld, dtype, actions, action_bytes, old_logp, ref_logp,
+                     advantage, weight, params, d_scaler, logp, loss, stats, dlogits, stream=0):
+    _check("zero_policy_loss", lib().zero_policy_loss(
+        logits or None, rows, vocab, ld, dtype, actions or None, action_bytes, old_logp or None,
+        ref_logp or None, advantage or None, weight or None, C.byref(params), d_scaler or None,
+        logp or None, loss or None, stats or None, dlogits or None, stream or None))
 
 
 # ------------------------------------------------------------ checked build --

@@ -42,6 +42,15 @@ static __device__ __noinline__ bool check_failed(int site, int64_t where) {
 }
 #define ZCHECK(cond, site, where) ((cond) ? true : check_failed((site), (where)))
 
+// The units behind zero_train.h define ZERO_CHECKED_LEAF and one collector
+// each; any other unit's collect_checks collects theirs too.
+extern "C" {
+int ze_collect_checks(unsigned long long* count, unsigned long long* first);
+int zc_collect_checks(unsigned long long* count, unsigned long long* first);
+int zp_collect_checks(unsigned long long* count, unsigned long long* first);
+int zw_collect_checks(unsigned long long* count, unsigned long long* first);
+}
+
 // this unit's counters: add them to *count, keep the first code if *first
 // is still 0, then clear them
 static inline int collect_checks(unsigned long long* count, unsigned long long* first) {
@@ -56,6 +65,11 @@ static inline int collect_checks(unsigned long long* count, unsigned long long* 
     return -1;
   *count += c;
   if (*first == 0) *first = f;
+#ifndef ZERO_CHECKED_LEAF
+  if (ze_collect_checks(count, first) || zc_collect_checks(count, first) ||
+      zp_collect_checks(count, first) || zw_collect_checks(count, first))
+    return -1;
+#endif
   return 0;
 }
 #else

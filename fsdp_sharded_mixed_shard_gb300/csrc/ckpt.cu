@@ -1,0 +1,385 @@
+/*
+ * ckpt.cu -- 8-bit activation checkpoints: writing, reading back, and the
+ * activation functions that make and use them (zero_train.h).
+ *
+ * One value in 32 shares a power-of-two step 2^k with its block: with
+ * 2^E <= max|x| < 2^(E+1), k = E - 6, so |x| / 2^k < 128 and q = rint(x / 2^k)
+ * fits 8 bits (127.5 and more is held at 127). Multiplying by a power of two
+ * is exact, so q * 2^k is exact in bf16 (8 significant bits) and fp16, and no
+ * reader of a checkpoint rounds it.
+ *
+ * All kernels here are bound by memory. A thread moves 8 neighbouring elements
+ * (16 bytes of the 16-bit side, 8 of the checkpoint), so four lanes share a
+ * block and its maximum takes two shuffles; a warp covers 256 columns of a
+ * row, a CTA eight rows at a time.
+ */
+#include "train.cuh"
+
+#include <algorithm>
+
+namespace zc {
+
+using namespace zt;
+
+constexpr int kRows = 8;        // rows per CTA step, one warp each
+constexpr int kThreads = 32 * kRows;
+constexpr int kCols = 32 * kVec;
+constexpr int kUnroll = 2;      // row steps per CTA
+
+// Eight elements of a row of 16-bit elements starting at column c; those at
+// or past `cols` are 0 (loads) or left alone (stores). kAlign: the bytes every
+// row start is a multiple of (16: one access, 4: two elements each, 2).
+template <int kAlign>
+__device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t cols) {
+  if constexpr (kAlign == 16) {
+    if (c + kVec <= cols) return __ldcs(reinterpret_cast<const uint4*>(row + c));
+  } else if constexpr (kAlign == 4) {
+    if (c + kVec <= cols) {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(row + c);
+      return make_uint4(p[0], p[1], p[2], p[3]);
+    }
+  }
+  uint32_t h[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) h[j] = c + j < cols ? row[c + j] : 0;
+  return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+}
+
+template <int kAlign>
+__device__ __forceinline__ void store8(uint16_t* row, int64_t c, int64_t cols, const uint4& v) {
+  if constexpr (kAlign == 16) {
+    if (c + kVec <= cols) {
+      __stcs(reinterpret_cast<uint4*>(row + c), v);
+      return;
+    }
+  } else if constexpr (kAlign == 4) {
+    if (c + kVec <= cols) {
+      uint32_t* p = reinterpret_cast<uint32_t*>(row + c);
+      p[0] = v.x, p[1] = v.y, p[2] = v.z, p[3] = v.w;
+      return;
+    }
+  }
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (c + j < cols) row[c + j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+}
+
+__device__ __forceinline__ float pow2(int k) {  // 2^k, -127 < k < 128
+  return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+}
+
+struct Ckpt {
+  int8_t* q;       // [rows][pitch]
+  uint8_t* scale;  // [rows][pitch / 32]
+};
+
+// Quantise the lane's eight values with its block's other three lanes and
+// store them; all lanes of the warp call it. `in` is false past the pitch.
+template <bool kBf16>
+__device__ __forceinline__ void save8(const Ckpt& k, int64_t row, int64_t c, int64_t pitch,
+                                      bool in, const float (&f)[8]) {
+  float top = 0.f;
+  bool finite = true;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float m = fabsf(f[j]);
+    finite = finite && m < __uint_as_float(0x7F800000u);  // false for NaN too
+    top = fmaxf(top, m);
+  }
+  uint32_t bits = finite ? __float_as_uint(top) : 0x7F800000u;
+  bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 1));
+  bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 2));
+  const int e = static_cast<int>(bits >> 23);  // biased exponent of the maximum; 255: not finite
+  const int low = kBf16 ? -126 : -24;
+  const int step = max(e - 127 - 6, low);
+  const float inv = e == 255 ? 0.f : pow2(-step);
+  uint32_t q[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float r = fminf(fmaxf(f[j] * inv, -127.f), 127.f);
+    q[j] = static_cast<uint32_t>(__float2int_rn(r)) & 0xFFu;
+  }
+  if (!in) return;
+  uint2 w;
+  w.x = q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24;
+  w.y = q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24;
+  if (e == 255) w = make_uint2(0, 0);
+  __stcs(reinterpret_cast<uint2*>(k.q + row * pitch + c), w);
+  if ((threadIdx.x & 3) == 0)
+    k.scale[row * (pitch / ZERO_CKPT_BLOCK) + c / ZERO_CKPT_BLOCK] =
+        static_cast<uint8_t>(e == 255 ? 255 : step + 127);
+}
+
+// The lane's eight checkpointed values.
+__device__ __forceinline__ void unpack8(const uint2& w, uint32_t scale, float (&f)[8]) {
+  const float s = scale == 255 ? __uint_as_float(0x7FC00000u)
+                               : __uint_as_float(scale << 23);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t word = j < 4 ? w.x : w.y;
+    f[j] = static_cast<float>(static_cast<int8_t>(word >> (8 * (j & 3)))) * s;
+  }
+}
+
+// p = 1 / (1 + exp(-z)) and q = 1 - p, from exp(-|z|): nothing overflows, and
+// both keep their relative accuracy down into the subnormal numbers.
+struct Gate {
+  float p, q;
+};
+
+__device__ __forceinline__ Gate sigmoid(float z) {
+  const float t = __expf(-fabsf(z));
+  const float big = __fdividef(1.f, 1.f + t), small = t * big;
+  return z >= 0.f ? Gate{big, small} : Gate{small, big};
+}
+
+// GELU's tanh form is x p(z) with z = 2 sqrt(2/pi) (x + 0.044715 x^3).
+constexpr float kGeluC = 1.5957691216057308f;  // 2 sqrt(2/pi)
+constexpr float kGeluA = 0.044715f;
+
+// held below overflow, so that p q z' is 0 and not 0 * inf far out
+__device__ __forceinline__ float square(float x) { return fminf(x * x, 1e30f); }
+
+__device__ __forceinline__ Gate gelu_gate(float x) {
+  return sigmoid(kGeluC * __fmaf_rn(kGeluA * square(x), x, x));
+}
+
+struct Args {
+  const uint16_t *x, *u, *dy;
+  uint16_t *y, *dx, *du;
+  Ckpt kx, ku;
+  int64_t rows, cols, pitch, ld, ld_y;  // ld: x, u (forward), dx, du, y (backward)
+  int64_t col_tiles;
+};
+
+enum Op { kSave, kLoad, kGelu, kSwiglu, kGeluGrad, kSwigluGrad };
+
+template <int kOp, bool kBf16, int kAlign>
+__global__ void __launch_bounds__(kThreads) ckpt_kernel(const Args a) {
+  pdl_begin();
+  const int lane = threadIdx.x & 31;
+  const int64_t tile = blockIdx.x;
+  const int64_t row_tile = tile / a.col_tiles;
+  const int64_t c = (tile - row_tile * a.col_tiles) * kCols + lane * kVec;
+  const int64_t row0 = row_tile * (kRows * kUnroll) + (threadIdx.x >> 5);
+  const bool in = c < a.pitch;
+  const int64_t blk = a.pitch / ZERO_CKPT_BLOCK;
+  if constexpr (kOp == kSave || kOp == kGelu || kOp == kSwiglu) {
+    uint4 vx[kUnroll], vu[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int64_t r = row0 + k * kRows;
+      vx[k] = vu[k] = make_uint4(0, 0, 0, 0);
+      if (r >= a.rows) continue;
+      vx[k] = load8<kAlign>(a.x + r * a.ld, c, a.cols);
+      if constexpr (kOp == kSwiglu) vu[k] = load8<kAlign>(a.u + r * a.ld, c, a.cols);
+    }
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int64_t r = row0 + k * kRows;
+      if (r >= a.rows) continue;  // the same for the whole warp
+      float x[8], u[8], y[8];
+      widen8<kBf16>(vx[k], x);
+      save8<kBf16>(a.kx, r, c, a.pitch, in, x);
+      if constexpr (kOp == kSwiglu) {
+        widen8<kBf16>(vu[k], u);
+        save8<kBf16>(a.ku, r, c, a.pitch, in, u);
+      }
+      if constexpr (kOp != kSave) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          y[j] = kOp == kSwiglu ? x[j] * sigmoid(x[j]).p * u[j] : x[j] * gelu_gate(x[j]).p;
+        store8<kAlign>(a.y + r * a.ld_y, c, a.cols, narrow8<kBf16>(y));
+      }
+    }
+  } else {
+    uint2 qx[kUnroll], qu[kUnroll];
+    uint32_t sx[kUnroll], su[kUnroll];
+    uint4 vd[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int64_t r = row0 + k * kRows;
+      qx[k] = qu[k] = make_uint2(0, 0);
+      sx[k] = su[k] = 0;
+      vd[k] = make_uint4(0, 0, 0, 0);
+      if (r >= a.rows || !in) continue;
+      qx[k] = __ldcs(reinterpret_cast<const uint2*>(a.kx.q + r * a.pitch + c));
+      sx[k] = a.kx.scale[r * blk + c / ZERO_CKPT_BLOCK];
+      if constexpr (kOp == kSwigluGrad) {
+        qu[k] = __ldcs(reinterpret_cast<const uint2*>(a.ku.q + r * a.pitch + c));
+        su[k] = a.ku.scale[r * blk + c / ZERO_CKPT_BLOCK];
+      }
+      if constexpr (kOp != kLoad) vd[k] = load8<kAlign>(a.dy + r * a.ld_y, c, a.cols);
+    }
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int64_t r = row0 + k * kRows;
+      if (r >= a.rows || c >= a.cols) continue;
+      float x[8], u[8], d[8], y[8], gx[8], gu[8];
+      unpack8(qx[k], sx[k], x);
+      if constexpr (kOp == kLoad) {
+        store8<kAlign>(a.y + r * a.ld, c, a.cols, narrow8<kBf16>(x));
+      } else {
+        if constexpr (kOp == kSwigluGrad) unpack8(qu[k], su[k], u);
+        widen8<kBf16>(vd[k], d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if constexpr (kOp == kSwigluGrad) {
+            // y = x p u, p = p(x): dy/dx = u p (1 + x q), dy/du = x p
+            const Gate g = sigmoid(x[j]);
+            const float xp = x[j] * g.p;
+            y[j] = xp * u[j];
+            gu[j] = d[j] * xp;
+            gx[j] = d[j] * u[j] * (g.p * __fmaf_rn(x[j], g.q, 1.f));
+          } else {
+            // y = x p(z), z' = c (1 + 3 a x^2): dy/dx = p + x p q z'
+            const Gate g = gelu_gate(x[j]);
+            y[j] = x[j] * g.p;
+            const float z1 = kGeluC * __fmaf_rn(3.f * kGeluA, square(x[j]), 1.f);
+            gx[j] = d[j] * __fmaf_rn(y[j] * g.q, z1, g.p);
+          }
+        }
+        store8<kAlign>(a.dx + r * a.ld, c, a.cols, narrow8<kBf16>(gx));
+        if constexpr (kOp == kSwigluGrad)
+          store8<kAlign>(a.du + r * a.ld, c, a.cols, narrow8<kBf16>(gu));
+        if (a.y) store8<kAlign>(a.y + r * a.ld, c, a.cols, narrow8<kBf16>(y));
+      }
+    }
+  }
+}
+
+constexpr int64_t kMaxGrid = 0x7fffffff;
+constexpr int64_t kMaxBytes = int64_t{1} << 62;
+
+int64_t pitch_of(int64_t cols) { return ceil_div(cols, ZERO_CKPT_PAD) * ZERO_CKPT_PAD; }
+
+bool sizes_ok(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 0 || cols > kMaxBytes / 4) return false;
+  const int64_t p = pitch_of(cols);
+  return p == 0 || rows <= kMaxBytes / 2 / p;
+}
+
+Ckpt ckpt_of(const void* p, int64_t rows, int64_t pitch) {
+  int8_t* q = static_cast<int8_t*>(const_cast<void*>(p));
+  return Ckpt{q, reinterpret_cast<uint8_t*>(q) + rows * pitch};
+}
+
+template <int kOp>
+int launch(Args& a, int32_t dtype, int align, void* stream) {
+  a.col_tiles = ceil_div(a.pitch, kCols);
+  const int64_t grid = a.col_tiles * ceil_div(a.rows, kRows * kUnroll);
+  if (grid > kMaxGrid) return ZERO_ERANGE;
+  void (*fn)(const Args) =
+      dtype == ZERO_BF16
+          ? (align == 16 ? ckpt_kernel<kOp, true, 16>
+                         : align == 4 ? ckpt_kernel<kOp, true, 4> : ckpt_kernel<kOp, true, 2>)
+          : (align == 16 ? ckpt_kernel<kOp, false, 16>
+                         : align == 4 ? ckpt_kernel<kOp, false, 4> : ckpt_kernel<kOp, false, 2>);
+  return status_of(launch_pdl(fn, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
+                              static_cast<cudaStream_t>(stream), a));
+}
+
+// what every row start of a [.., ld] array of 16-bit elements is a multiple of
+int row_align(const void* p, int64_t ld) {
+  if (aligned(p, 16) && ld % 8 == 0) return 16;
+  return aligned(p, 4) && ld % 2 == 0 ? 4 : 2;
+}
+
+}  // namespace zc
+
+#ifdef ZERO_CHECKED
+extern "C" int zc_collect_checks(unsigned long long* count, unsigned long long* first) {
+  return collect_checks(count, first);
+}
+#endif
+
+extern "C" {
+
+ZERO_API size_t zero_ckpt_bytes(int64_t rows, int64_t cols) {
+  if (!zc::sizes_ok(rows, cols)) return 0;
+  const int64_t p = zc::pitch_of(cols);
+  return static_cast<size_t>(rows * (p + p / ZERO_CKPT_BLOCK));
+}
+
+ZERO_API int zero_ckpt_save(const void* x, int64_t rows, int64_t cols, int64_t ld, int32_t dtype,
+                            void* ckpt, void* stream) {
+  using namespace zc;
+  if (!sizes_ok(rows, cols) || !is_dtype16(dtype) || ld < cols) return ZERO_EINVAL;
+  if (rows == 0 || cols == 0) return ZERO_OK;
+  if (!x || !ckpt) return ZERO_EINVAL;
+  if (!aligned(x, 2) || !aligned(ckpt, 16)) return ZERO_EALIGN;
+  Args a = {};
+  a.x = static_cast<const uint16_t*>(x);
+  a.rows = rows, a.cols = cols, a.pitch = pitch_of(cols), a.ld = ld;
+  a.kx = ckpt_of(ckpt, rows, a.pitch);
+  return launch<kSave>(a, dtype, row_align(x, ld), stream);
+}
+
+ZERO_API int zero_ckpt_load(const void* ckpt, int64_t rows, int64_t cols, int32_t dtype,
+                            void* out, int64_t ld, void* stream) {
+  using namespace zc;
+  if (!sizes_ok(rows, cols) || !is_dtype16(dtype) || ld < cols) return ZERO_EINVAL;
+  if (rows == 0 || cols == 0) return ZERO_OK;
+  if (!out || !ckpt) return ZERO_EINVAL;
+  if (!aligned(out, 2) || !aligned(ckpt, 16)) return ZERO_EALIGN;
+  Args a = {};
+  a.y = static_cast<uint16_t*>(out);
+  a.rows = rows, a.cols = cols, a.pitch = pitch_of(cols), a.ld = ld;
+  a.kx = ckpt_of(ckpt, rows, a.pitch);
+  return launch<kLoad>(a, dtype, row_align(out, ld), stream);
+}
+
+ZERO_API int zero_ckpt_act(int32_t act, const void* x, const void* u, int64_t rows, int64_t cols,
+                           int64_t ld, int32_t dtype, void* y, int64_t ld_y, void* ckpt_x,
+                           void* ckpt_u, void* stream) {
+  using namespace zc;
+  if (act != ZERO_ACT_GELU && act != ZERO_ACT_SWIGLU) return ZERO_EINVAL;
+  if (!sizes_ok(rows, cols) || !is_dtype16(dtype) || ld < cols || ld_y < cols) return ZERO_EINVAL;
+  const bool gated = act == ZERO_ACT_SWIGLU;
+  if (!gated && (u || ckpt_u)) return ZERO_EINVAL;
+  if (rows == 0 || cols == 0) return ZERO_OK;
+  if (!x || !y || !ckpt_x || (gated && (!u || !ckpt_u))) return ZERO_EINVAL;
+  if (!aligned(x, 2) || !aligned(u, 2) || !aligned(y, 2) || !aligned(ckpt_x, 16) ||
+      !aligned(ckpt_u, 16))
+    return ZERO_EALIGN;
+  Args a = {};
+  a.x = static_cast<const uint16_t*>(x);
+  a.u = static_cast<const uint16_t*>(u);
+  a.y = static_cast<uint16_t*>(y);
+  a.rows = rows, a.cols = cols, a.pitch = pitch_of(cols), a.ld = ld, a.ld_y = ld_y;
+  a.kx = ckpt_of(ckpt_x, rows, a.pitch);
+  if (gated) a.ku = ckpt_of(ckpt_u, rows, a.pitch);
+  const int align = std::min({row_align(x, ld), row_align(u, ld), row_align(y, ld_y)});
+  return gated ? launch<kSwiglu>(a, dtype, align, stream) : launch<kGelu>(a, dtype, align, stream);
+}
+
+ZERO_API int zero_ckpt_act_grad(int32_t act, const void* ckpt_x, const void* ckpt_u,
+                                const void* dy, int64_t rows, int64_t cols, int64_t ld_dy,
+                                int32_t dtype, void* dx, void* du, void* y, int64_t ld,
+                                void* stream) {
+  using namespace zc;
+  if (act != ZERO_ACT_GELU && act != ZERO_ACT_SWIGLU) return ZERO_EINVAL;
+  if (!sizes_ok(rows, cols) || !is_dtype16(dtype) || ld < cols || ld_dy < cols) return ZERO_EINVAL;
+  const bool gated = act == ZERO_ACT_SWIGLU;
+  if (!gated && (du || ckpt_u)) return ZERO_EINVAL;
+  if (rows == 0 || cols == 0) return ZERO_OK;
+  if (!ckpt_x || !dy || !dx || (gated && (!ckpt_u || !du))) return ZERO_EINVAL;
+  if ((dx == dy || du == dy) && ld != ld_dy) return ZERO_EINVAL;
+  if (!aligned(dy, 2) || !aligned(dx, 2) || !aligned(du, 2) || !aligned(y, 2) ||
+      !aligned(ckpt_x, 16) || !aligned(ckpt_u, 16))
+    return ZERO_EALIGN;
+  Args a = {};
+  a.dy = static_cast<const uint16_t*>(dy);
+  a.dx = static_cast<uint16_t*>(dx);
+  a.du = static_cast<uint16_t*>(du);
+  a.y = static_cast<uint16_t*>(y);
+  a.rows = rows, a.cols = cols, a.pitch = pitch_of(cols), a.ld = ld, a.ld_y = ld_dy;
+  a.kx = ckpt_of(ckpt_x, rows, a.pitch);
+  if (gated) a.ku = ckpt_of(ckpt_u, rows, a.pitch);
+  const int align = std::min({row_align(dy, ld_dy), row_align(dx, ld), row_align(du, ld), row_align(y, ld)});
+  return gated ? launch<kSwigluGrad>(a, dtype, align, stream)
+               : launch<kGeluGrad>(a, dtype, align, stream);
+}
+
+}  // extern "C"

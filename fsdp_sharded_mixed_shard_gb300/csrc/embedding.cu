@@ -1,0 +1,563 @@
+/*
+ * embedding.cu -- token lookup and the table's gradient (zero_train.h).
+ *
+ * Lookup: out[t, :] = round16(scale * table[id_t, :]). A warp moves a slice of
+ * 256 columns of four tokens at a time: four independent row loads in flight
+ * per warp. Bound by memory: 2 dim bytes read and written per token.
+ *
+ * Gradient: grad[v, :] = round16(scale * sum of dy[t, :] over id_t == v). The
+ * whole table is written, so the bound is 2 (T + V) dim bytes. Two parts:
+ *
+ * 1. The ids are sorted, equal ids in the order of their positions, by stable
+ *    counting passes over at most 9 bits each (17 bits of id: two passes).
+ *    hist_kernel counts the first pass's digits per chunk of the ids;
+ *    scatter_kernel ranks every id of its chunk (ids of a warp by
+ *    match.any, warps by a scan over their counts), writes (id, position) to
+ *    its place and counts the next pass's digits at the chunk that place
+ *    belongs to, so each further pass is one launch. Integer counts: the
+ *    order of their atomics does not matter.
+ * 2. rows_kernel merges the sorted ids with the table's rows into one list --
+ *    token, token, "row done", "row done", token, ... -- and cuts it into
+ *    runs of kRun items, so that a run costs the same whether it sums the
+ *    tokens of one frequent id or writes rows of zeros: item i of the sorted
+ *    ids is item i + id_i of the merged list, so a run finds its first token
+ *    by one search. A warp sums a run's 256-column slice in registers (eight
+ *    tokens' loads in flight) and stores each row as it is done. An id whose
+ *    tokens span runs leaves fp32 partial sums in the workspace, which
+ *    join_kernel adds in run order. The runs' bounds depend on the ids alone,
+ *    so the sums do not change from call to call.
+ */
+#include "train.cuh"
+
+#include <algorithm>
+
+namespace ze {
+
+using namespace zt;
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kSlice = 256;    // columns per warp: eight per lane
+constexpr int kLookup = 4;     // tokens per warp and step of the lookup
+constexpr int kRun = 64;       // items of the merged list per run
+constexpr int kBatch = 8;      // dy rows in flight per warp
+
+constexpr int kSortThreads = 512;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kDigits = 512;   // 9 bits per pass, one thread per digit
+constexpr int kTile = 1024;    // ids ranked at a time
+constexpr int kMaxChunks = 64; // chunks (CTAs) per pass
+constexpr int kMaxPasses = 3;
+static_assert(kDigits == kSortThreads, "one thread per digit");
+static_assert(kTile % kSortThreads == 0, "whole rounds");
+
+// eight columns of a row: neighbouring ones when rows are 16-byte aligned,
+// else every 32nd (the lanes of a warp then read neighbouring elements)
+template <bool kVecRows>
+__device__ __forceinline__ int64_t column(int64_t c0, int lane, int j) {
+  return kVecRows ? c0 + lane * kVec + j : c0 + lane + 32 * j;
+}
+
+template <bool kVecRows>
+__device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c0, int lane, int64_t dim) {
+  if constexpr (kVecRows) {
+    const int64_t c = c0 + lane * kVec;
+    return c < dim ? __ldcs(reinterpret_cast<const uint4*>(row + c)) : make_uint4(0, 0, 0, 0);
+  } else {
+    uint32_t h[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t c = column<false>(c0, lane, j);
+      h[j] = c < dim ? row[c] : 0;
+    }
+    return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+  }
+}
+
+template <bool kVecRows>
+__device__ __forceinline__ void store8(uint16_t* row, int64_t c0, int lane, int64_t dim,
+                                       const uint4& v) {
+  if constexpr (kVecRows) {
+    const int64_t c = c0 + lane * kVec;
+    if (c < dim) __stcs(reinterpret_cast<uint4*>(row + c), v);
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t c = column<false>(c0, lane, j);
+      if (c < dim) row[c] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+    }
+  }
+}
+
+// ------------------------------------------------------------------ lookup ----
+
+struct LookupArgs {
+  const void* tokens;
+  const uint16_t* table;
+  uint16_t* out;
+  int64_t n, vocab, dim, slices, units;
+  int32_t token_bytes;
+  float scale;
+};
+
+template <bool kBf16, bool kVecRows>
+__global__ void __launch_bounds__(kThreads) lookup_kernel(const LookupArgs a) {
+  pdl_begin();
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (unit >= a.units) return;
+  const int64_t group = unit / a.slices;
+  const int64_t c0 = (unit - group * a.slices) * kSlice;
+  const int64_t t0 = group * kLookup;
+  uint4 v[kLookup];
+#pragma unroll
+  for (int k = 0; k < kLookup; ++k) {
+    const int64_t t = t0 + k;
+    const int64_t id = t < a.n ? load_id(a.tokens, a.token_bytes, t, a.vocab) : -1;
+    v[k] = id >= 0 && ZCHECK(id < a.vocab, kSiteLoad, id)
+               ? load8<kVecRows>(a.table + id * a.dim, c0, lane, a.dim)
+               : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int k = 0; k < kLookup; ++k) {
+    const int64_t t = t0 + k;
+    if (t >= a.n) break;
+    float f[8];
+    widen8<kBf16>(v[k], f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] *= a.scale;
+    store8<kVecRows>(a.out + t * a.dim, c0, lane, a.dim, narrow8<kBf16>(f));
+  }
+}
+
+// -------------------------------------------------------------------- sort ----
+
+struct SortArgs {
+  const void* tokens;            // first pass reads the ids themselves
+  const uint32_t* key_in;        // later passes: ids and positions of the pass before
+  const uint32_t* pos_in;
+  uint32_t* key_out;
+  uint32_t* pos_out;
+  uint32_t* hist;                // this pass: [kDigits][kMaxChunks]
+  uint32_t* hist_next;           // next pass, or NULL
+  int64_t n, vocab, chunk;       // chunk: ids per CTA, a multiple of kTile
+  int32_t token_bytes, shift, bits, n_chunks, n_hists;
+};
+
+// padding ids sort after the last row
+__device__ __forceinline__ uint32_t first_key(const SortArgs& a, int64_t i) {
+  const int64_t id = load_id(a.tokens, a.token_bytes, i, a.vocab);
+  return static_cast<uint32_t>(id < 0 ? a.vocab : id);
+}
+
+// Digits of the first pass, counted per chunk; the other passes' counts are
+// cleared for the scatter kernels to add to.
+__global__ void __launch_bounds__(kSortThreads) hist_kernel(const SortArgs a) {
+  pdl_begin();
+  __shared__ uint32_t count[kDigits];
+  count[threadIdx.x] = 0;
+  __syncthreads();
+  const int64_t lo = blockIdx.x * a.chunk;
+  const int64_t hi = lo + a.chunk < a.n ? lo + a.chunk : a.n;
+  const uint32_t mask = (1u << a.bits) - 1;
+  for (int64_t i = lo + threadIdx.x; i < hi; i += kSortThreads)
+    atomicAdd(&count[first_key(a, i) & mask], 1u);
+  __syncthreads();
+  a.hist[threadIdx.x * kMaxChunks + blockIdx.x] = count[threadIdx.x];
+  const int total = (a.n_hists - 1) * kDigits * kMaxChunks;
+  for (int i = blockIdx.x * kSortThreads + threadIdx.x; i < total; i += gridDim.x * kSortThreads)
+    a.hist[kDigits * kMaxChunks + i] = 0;
+}
+
+__global__ void __launch_bounds__(kSortThreads) scatter_kernel(const SortArgs a) {
+  pdl_begin();
+  __shared__ uint32_t base[kDigits];               // next free place of each digit
+  __shared__ uint32_t of_warp[kSortWarps][kDigits];
+  __shared__ uint32_t warp_sum[kSortWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  {
+    // digit tid: all its ids, and those in the chunks before this one
+    uint32_t all = 0, before = 0;
+    for (int g = 0; g < a.n_chunks; ++g) {
+      const uint32_t c = a.hist[tid * kMaxChunks + g];
+      all += c;
+      before += g < static_cast<int>(blockIdx.x) ? c : 0;
+    }
+    uint32_t inc = all;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += y;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    uint32_t lower = 0;
+    for (int w = 0; w < warp; ++w) lower += warp_sum[w];
+    base[tid] = lower + inc - all + before;
+  }
+  const int64_t lo = blockIdx.x * a.chunk;
+  const int64_t hi = lo + a.chunk < a.n ? lo + a.chunk : a.n;
+  const uint32_t mask = (1u << a.bits) - 1;
+  constexpr int kRounds = kTile / kSortThreads;
+  for (int64_t t0 = lo; t0 < hi; t0 += kTile) {
+    for (int w = 0; w < kSortWarps; ++w) of_warp[w][tid] = 0;
+    __syncthreads();
+    uint32_t key[kRounds], pos[kRounds], rank[kRounds];
+    // warp w ranks ids [w, w + 1) * kTile / kSortWarps of the tile
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+      const int64_t i = t0 + (warp * kRounds + k) * 32 + lane;
+      const bool on = i < hi;
+      key[k] = !on ? 0xFFFFFFFFu : a.key_in ? a.key_in[i] : first_key(a, i);
+      pos[k] = !on ? 0 : a.pos_in ? a.pos_in[i] : static_cast<uint32_t>(i);
+      const uint32_t d = (key[k] >> a.shift) & mask;
+      const uint32_t same = __match_any_sync(0xffffffffu, on ? d : 0xFFFFFFFFu);
+      const uint32_t ahead = __popc(same & ((1u << lane) - 1));
+      const uint32_t seen = on ? of_warp[warp][d] : 0;
+      __syncwarp();
+      if (on && ahead == 0) of_warp[warp][d] = seen + __popc(same);
+      __syncwarp();
+      rank[k] = seen + ahead;
+    }
+    __syncthreads();
+    {
+      uint32_t run = base[tid];
+      for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t c = of_warp[w][tid];
+        of_warp[w][tid] = run;
+        run += c;
+      }
+      base[tid] = run;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+      const int64_t i = t0 + (warp * kRounds + k) * 32 + lane;
+      if (i >= hi) continue;
+      const uint32_t to = of_warp[warp][(key[k] >> a.shift) & mask] + rank[k];
+      if (!ZCHECK(to < a.n, kSiteStore, to)) continue;
+      a.key_out[to] = key[k];
+      a.pos_out[to] = pos[k];
+      if (a.hist_next) {
+        const uint32_t d = (key[k] >> (a.shift + a.bits)) & mask;
+        atomicAdd(&a.hist_next[d * kMaxChunks + to / a.chunk], 1u);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// -------------------------------------------------------------------- rows ----
+
+struct RowsArgs {
+  const uint32_t* key;   // sorted ids; padding ids are vocab
+  const uint32_t* pos;
+  const uint16_t* dy;
+  uint16_t* grad;
+  uint32_t* start;       // [n_runs + 1] first token of each run
+  float* out_part;       // [n_runs][width] sums of a run's last row, not done there
+  float* in_part;        // [n_runs][width] sums of a run's first row, begun before it
+  int64_t n, vocab, dim, slices, width, n_runs;
+  float scale;
+  int32_t accumulate;
+};
+
+// Number of tokens among the first `item` items of the merged list: the
+// tokens with i + key_i < item. All lanes search together, 32 probes a step.
+__device__ __forceinline__ int64_t tokens_before(const uint32_t* key, int64_t n, int64_t item,
+                                                 int lane) {
+  int64_t lo = 0, hi = n < item ? n : item;  // the answer is in [lo, hi]
+  while (lo < hi) {
+    const int64_t step = (hi - lo + 31) / 32;
+    const int64_t i = lo + (lane + 1) * step - 1;
+    const bool in = i < hi && i + key[i] < item;
+    const int count = __popc(__ballot_sync(0xffffffffu, in));
+    const int64_t new_lo = lo + count * step;
+    const int64_t new_hi = lo + (count + 1) * step - 1;
+    hi = new_hi < hi ? new_hi : hi;
+    lo = new_lo < hi ? new_lo : hi;
+  }
+  return lo;
+}
+
+template <bool kBf16, bool kVecRows>
+__device__ __forceinline__ void store_row(const RowsArgs& a, int64_t v, int64_t c0, int lane,
+                                          const float (&sum)[8], bool hit) {
+  if (a.accumulate && !hit) return;
+  uint16_t* row = a.grad + v * a.dim;
+  float f[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = sum[j] * a.scale;
+  if (a.accumulate) {
+    float old[8];
+    widen8<kBf16>(load8<kVecRows>(row, c0, lane, a.dim), old);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] += old[j];
+  }
+  store8<kVecRows>(row, c0, lane, a.dim, narrow8<kBf16>(f));
+}
+
+// fp32 partial sums sit lane by lane: lane l's eight columns at [l * 8, l * 8 + 8)
+__device__ __forceinline__ void store_part(float* part, int64_t c0, int lane,
+                                           const float (&s)[8]) {
+  float4* p = reinterpret_cast<float4*>(part + c0 + lane * kVec);
+  p[0] = make_float4(s[0], s[1], s[2], s[3]);
+  p[1] = make_float4(s[4], s[5], s[6], s[7]);
+}
+
+template <bool kBf16, bool kVecRows>
+__global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a) {
+  pdl_begin();
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t run = unit / a.slices;
+  if (run >= a.n_runs) return;
+  const int64_t c0 = (unit - run * a.slices) * kSlice;
+  const int64_t item0 = run * kRun;
+  const int64_t item1 = item0 + kRun < a.n + a.vocab ? item0 + kRun : a.n + a.vocab;
+  const int64_t i0 = tokens_before(a.key, a.n, item0, lane);
+  const int64_t i1 = tokens_before(a.key, a.n, item1, lane);
+  int64_t row = item0 - i0;             // rows done before this run
+  const int64_t row_end = item1 - i1;   // and before the next
+  if (c0 == 0 && lane == 0) a.start[run] = static_cast<uint32_t>(i0);
+  // the first row's earlier tokens are in an earlier run
+  bool begun = i0 > 0 && row < a.vocab && a.key[i0 - 1] == row;
+  bool hit = false;
+  float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  const auto done = [&]() {  // row `row` has all its tokens
+    if (begun) store_part(a.in_part + run * a.width, c0, lane, sum);
+    else store_row<kBf16, kVecRows>(a, row, c0, lane, sum, hit);
+    begun = hit = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] = 0.f;
+    ++row;
+  };
+  for (int64_t i = i0; i < i1; i += kBatch) {
+    uint4 v[kBatch];
+    uint32_t key[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const bool on = i + k < i1;
+      key[k] = on ? a.key[i + k] : 0xFFFFFFFFu;
+      v[k] = on && key[k] < a.vocab
+                 ? load8<kVecRows>(a.dy + static_cast<int64_t>(a.pos[i + k]) * a.dim, c0, lane,
+                                   a.dim)
+                 : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (i + k >= i1 || key[k] >= a.vocab) break;
+      while (row < key[k]) done();
+      float f[8];
+      widen8<kBf16>(v[k], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += f[j];
+      hit = true;
+    }
+  }
+  while (row < row_end) done();
+  if (hit || begun) store_part(a.out_part + run * a.width, c0, lane, sum);
+}
+
+// Rows whose tokens span runs: the partial sums of the runs before the one
+// that ends the row, in run order, then that run's own.
+template <bool kBf16, bool kVecRows>
+__global__ void __launch_bounds__(kThreads) join_kernel(const RowsArgs a) {
+  pdl_begin();
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t run = unit / a.slices;
+  if (run >= a.n_runs) return;
+  const int64_t c0 = (unit - run * a.slices) * kSlice;
+  const int64_t i0 = a.start[run];
+  const int64_t row = run * kRun - i0;
+  if (i0 == 0 || row >= a.vocab || a.key[i0 - 1] != row) return;
+  const int64_t item1 = (run + 1) * kRun;
+  const int64_t i1 = run + 1 < a.n_runs ? a.start[run + 1] : a.n;
+  if (run + 1 < a.n_runs && item1 - i1 <= row) return;  // the row goes on in the next run
+  // the row's first token, as an item of the merged list, names its first run
+  int64_t lo = 0, hi = i0;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (a.key[mid] < row) lo = mid + 1;
+    else hi = mid;
+  }
+  float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int64_t k = (lo + row) / kRun; k <= run; ++k) {
+    const float4* p = reinterpret_cast<const float4*>(
+        (k < run ? a.out_part : a.in_part) + k * a.width + c0 + lane * kVec);
+    const float4 x = p[0], y = p[1];
+    const float s[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] += s[j];
+  }
+  store_row<kBf16, kVecRows>(a, row, c0, lane, sum, true);
+}
+
+// -------------------------------------------------------------------- host ----
+
+struct Layout {
+  int64_t n_runs, width;
+  size_t hist, key[2], pos[2], start, out_part, in_part, bytes;
+};
+
+Layout layout_of(int64_t n, int64_t vocab, int64_t dim) {
+  Layout l = {};
+  l.n_runs = ceil_div(n + vocab, kRun);
+  l.width = ceil_div(dim, kSlice) * kSlice;
+  size_t at = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) & ~static_cast<size_t>(255);
+    return here;
+  };
+  l.hist = take(sizeof(uint32_t) * kMaxPasses * kDigits * kMaxChunks);
+  for (int k = 0; k < 2; ++k) {
+    l.key[k] = take(sizeof(uint32_t) * static_cast<size_t>(n));
+    l.pos[k] = take(sizeof(uint32_t) * static_cast<size_t>(n));
+  }
+  l.start = take(sizeof(uint32_t) * static_cast<size_t>(l.n_runs + 1));
+  l.out_part = take(sizeof(float) * static_cast<size_t>(l.n_runs * l.width));
+  l.in_part = take(sizeof(float) * static_cast<size_t>(l.n_runs * l.width));
+  l.bytes = at;
+  return l;
+}
+
+constexpr int64_t kMaxTokens = int64_t{1} << 28;
+constexpr int64_t kMaxVocab = int64_t{1} << 24;
+constexpr int64_t kMaxGrid = 0x7fffffff;
+
+template <bool kBf16, bool kVecRows>
+int launch_rows(const RowsArgs& a, cudaStream_t st) {
+  const unsigned grid = static_cast<unsigned>(ceil_div(a.n_runs * a.slices, kWarps));
+  cudaError_t e = launch_pdl(rows_kernel<kBf16, kVecRows>, dim3(grid), dim3(kThreads), 0, st, a);
+  if (e == cudaSuccess)
+    e = launch_pdl(join_kernel<kBf16, kVecRows>, dim3(grid), dim3(kThreads), 0, st, a);
+  return status_of(e);
+}
+
+}  // namespace ze
+
+#ifdef ZERO_CHECKED
+extern "C" int ze_collect_checks(unsigned long long* count, unsigned long long* first) {
+  return collect_checks(count, first);
+}
+#endif
+
+extern "C" {
+
+ZERO_API int zero_embedding(const void* tokens, int32_t token_bytes, int64_t n_tokens,
+                            const void* table, int64_t vocab, int64_t dim, float scale,
+                            int32_t dtype, void* out, void* stream) {
+  using namespace ze;
+  if (n_tokens < 0 || vocab < 0 || dim < 0 || !is_dtype16(dtype) ||
+      (token_bytes != 4 && token_bytes != 8))
+    return ZERO_EINVAL;
+  if (n_tokens > kMaxTokens || vocab > kMaxVocab || dim > kMaxTokens) return ZERO_ERANGE;
+  if (n_tokens == 0 || dim == 0) return ZERO_OK;
+  if (!tokens || !out || (!table && vocab)) return ZERO_EINVAL;
+  if (!aligned(tokens, token_bytes) || !aligned(table, 2) || !aligned(out, 2)) return ZERO_EALIGN;
+  LookupArgs a = {};
+  a.tokens = tokens;
+  a.table = static_cast<const uint16_t*>(table);
+  a.out = static_cast<uint16_t*>(out);
+  a.n = n_tokens;
+  a.vocab = vocab;
+  a.dim = dim;
+  a.slices = ceil_div(dim, kSlice);
+  a.units = ceil_div(n_tokens, kLookup) * a.slices;
+  a.token_bytes = token_bytes;
+  a.scale = scale;
+  const int64_t grid = ceil_div(a.units, kWarps);
+  if (grid > kMaxGrid) return ZERO_ERANGE;
+  const bool vec = dim % kVec == 0 && aligned(table, 16) && aligned(out, 16);
+  const auto fn = dtype == ZERO_BF16 ? (vec ? lookup_kernel<true, true> : lookup_kernel<true, false>)
+                                     : (vec ? lookup_kernel<false, true> : lookup_kernel<false, false>);
+  return status_of(launch_pdl(fn, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
+                              static_cast<cudaStream_t>(stream), a));
+}
+
+ZERO_API size_t zero_embedding_workspace_bytes(int64_t n_tokens, int64_t vocab, int64_t dim) {
+  using namespace ze;
+  if (n_tokens < 0 || vocab < 0 || dim < 0 || n_tokens > kMaxTokens || vocab > kMaxVocab ||
+      dim > kMaxTokens)
+    return 0;
+  return layout_of(n_tokens, vocab, dim).bytes;
+}
+
+ZERO_API int zero_embedding_grad(const void* tokens, int32_t token_bytes, int64_t n_tokens,
+                                 const void* dy, int64_t vocab, int64_t dim, float scale,
+                                 int32_t dtype, int32_t accumulate, void* grad,
+                                 void* workspace, void* stream) {
+  using namespace ze;
+  if (n_tokens < 0 || vocab < 0 || dim < 0 || !is_dtype16(dtype) ||
+      (token_bytes != 4 && token_bytes != 8) || (accumulate != 0 && accumulate != 1))
+    return ZERO_EINVAL;
+  if (n_tokens > kMaxTokens || vocab > kMaxVocab || dim > kMaxTokens) return ZERO_ERANGE;
+  if (vocab == 0 || dim == 0) return ZERO_OK;
+  if (!grad || !workspace || (n_tokens && (!tokens || !dy))) return ZERO_EINVAL;
+  if (!aligned(tokens, token_bytes) || !aligned(dy, 2) || !aligned(grad, 2) ||
+      !aligned(workspace, 16))
+    return ZERO_EALIGN;
+  const Layout l = layout_of(n_tokens, vocab, dim);
+  const int64_t slices = ceil_div(dim, kSlice);
+  if (ceil_div(l.n_runs * slices, kWarps) > kMaxGrid) return ZERO_ERANGE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint32_t* key[2] = {reinterpret_cast<uint32_t*>(ws + l.key[0]),
+                      reinterpret_cast<uint32_t*>(ws + l.key[1])};
+  uint32_t* pos[2] = {reinterpret_cast<uint32_t*>(ws + l.pos[0]),
+                      reinterpret_cast<uint32_t*>(ws + l.pos[1])};
+  int last = 0;
+  if (n_tokens > 0) {
+    int width = 1;  // bits of the ids, vocab itself (padding) among them
+    while ((vocab >> width) != 0) ++width;
+    const int passes = static_cast<int>(ceil_div(width, 9));
+    SortArgs s = {};
+    s.tokens = tokens;
+    s.token_bytes = token_bytes;
+    s.n = n_tokens;
+    s.vocab = vocab;
+    s.chunk = ceil_div(ceil_div(n_tokens, kMaxChunks), kTile) * kTile;
+    s.n_chunks = static_cast<int32_t>(ceil_div(n_tokens, s.chunk));
+    s.bits = static_cast<int32_t>(ceil_div(width, passes));
+    s.n_hists = passes;
+    uint32_t* hist = reinterpret_cast<uint32_t*>(ws + l.hist);
+    s.hist = hist;
+    cudaError_t e = launch_pdl(hist_kernel, dim3(s.n_chunks), dim3(kSortThreads), 0, st, s);
+    for (int p = 0; p < passes && e == cudaSuccess; ++p) {
+      s.key_in = p ? key[(p - 1) & 1] : nullptr;
+      s.pos_in = p ? pos[(p - 1) & 1] : nullptr;
+      last = p & 1;
+      s.key_out = key[last];
+      s.pos_out = pos[last];
+      s.hist = hist + static_cast<size_t>(p) * kDigits * kMaxChunks;
+      s.hist_next = p + 1 < passes ? s.hist + kDigits * kMaxChunks : nullptr;
+      s.shift = p * s.bits;
+      e = launch_pdl(scatter_kernel, dim3(s.n_chunks), dim3(kSortThreads), 0, st, s);
+    }
+    if (e != cudaSuccess) return ZERO_ECUDA;
+  }
+  RowsArgs a = {};
+  a.key = key[last];
+  a.pos = pos[last];
+  a.dy = static_cast<const uint16_t*>(dy);
+  a.grad = static_cast<uint16_t*>(grad);
+  a.start = reinterpret_cast<uint32_t*>(ws + l.start);
+  a.out_part = reinterpret_cast<float*>(ws + l.out_part);
+  a.in_part = reinterpret_cast<float*>(ws + l.in_part);
+  a.n = n_tokens;
+  a.vocab = vocab;
+  a.dim = dim;
+  a.slices = slices;
+  a.width = l.width;
+  a.n_runs = l.n_runs;
+  a.scale = scale;
+  a.accumulate = accumulate;
+  const bool vec = dim % kVec == 0 && aligned(dy, 16) && aligned(grad, 16);
+  if (dtype == ZERO_BF16) return vec ? launch_rows<true, true>(a, st) : launch_rows<true, false>(a, st);
+  return vec ? launch_rows<false, true>(a, st) : launch_rows<false, false>(a, st);
+}
+
+}  // extern "C"

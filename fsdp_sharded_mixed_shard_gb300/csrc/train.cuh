@@ -1,0 +1,91 @@
+// train.cuh -- what the kernels behind zero_train.h share: the element types,
+// 16-byte vectors of eight 16-bit elements, launch helpers and host checks.
+#ifndef ZERO_TRAIN_CUH
+#define ZERO_TRAIN_CUH
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+// this unit's violations are collected by the unit that owns the status call
+#define ZERO_CHECKED_LEAF
+#include "checked.cuh"
+#include "pdl.cuh"
+#include "zero_train.h"
+
+namespace zt {
+
+constexpr int kVec = 8;  // 16-bit elements per 16-byte vector
+
+// One 16-bit element (its bits) to fp32, exactly.
+template <bool kBf16>
+__device__ __forceinline__ float widen(uint32_t bits) {
+  if constexpr (kBf16) return __uint_as_float(bits << 16);
+  else return __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
+}
+
+// Both halves of a word to fp32, exactly.
+template <bool kBf16>
+__device__ __forceinline__ void widen2(uint32_t w, float& a, float& b) {
+  if constexpr (kBf16) {
+    a = __uint_as_float(w << 16);
+    b = __uint_as_float(w & 0xFFFF0000u);
+  } else {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    a = f.x;
+    b = f.y;
+  }
+}
+
+// fp32 to one 16-bit element, to nearest even.
+template <bool kBf16>
+__device__ __forceinline__ uint16_t narrow(float a) {
+  if constexpr (kBf16) return __bfloat16_as_ushort(__float2bfloat16_rn(a));
+  else return __half_as_ushort(__float2half_rn(a));
+}
+
+template <bool kBf16>
+__device__ __forceinline__ uint32_t narrow2(float a, float b) {
+  uint32_t w;
+  if constexpr (kBf16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+  return w;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void widen8(const uint4& v, float (&f)[8]) {
+  widen2<kBf16>(v.x, f[0], f[1]);
+  widen2<kBf16>(v.y, f[2], f[3]);
+  widen2<kBf16>(v.z, f[4], f[5]);
+  widen2<kBf16>(v.w, f[6], f[7]);
+}
+
+template <bool kBf16>
+__device__ __forceinline__ uint4 narrow8(const float (&f)[8]) {
+  return make_uint4(narrow2<kBf16>(f[0], f[1]), narrow2<kBf16>(f[2], f[3]),
+                    narrow2<kBf16>(f[4], f[5]), narrow2<kBf16>(f[6], f[7]));
+}
+
+// Token ids are int32 or int64; an id outside [0, limit) becomes -1.
+__device__ __forceinline__ int64_t load_id(const void* ids, int32_t bytes, int64_t i,
+                                           int64_t limit) {
+  const int64_t v = bytes == 4 ? static_cast<int64_t>(static_cast<const int32_t*>(ids)[i])
+                               : static_cast<const int64_t*>(ids)[i];
+  return v >= 0 && v < limit ? v : -1;
+}
+
+inline bool aligned(const void* p, size_t n) {
+  return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
+}
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+inline bool is_dtype16(int32_t d) { return d == ZERO_BF16 || d == ZERO_FP16; }
+
+inline int status_of(cudaError_t e) { return e == cudaSuccess ? ZERO_OK : ZERO_ECUDA; }
+
+}  // namespace zt
+
+#endif
