@@ -2,64 +2,523 @@
  * wgrad.cu -- weight gradient of a linear layer from its input's 8-bit
  * checkpoint (zero_train.h): dw[i, j] = sum over t of x^[t, i] dy[t, j].
  *
- * A CTA forms a 64 x 64 tile of dw, 16 tokens at a time through shared
- * memory, each thread 4 x 4 sums in fp32.
+ * A matrix product whose reduction runs over the tokens, the slow axis of
+ * both operands, on the 5th-generation tensor cores. A CTA forms a 128 x 256
+ * tile of dw in tensor memory (fp32), 64 tokens per step, through a ring of
+ * shared-memory stages:
+ *   copy warp     brings dy's 64 x 256 tile by TMA (128-byte swizzle, rows of
+ *                 64 columns: the tensor core's layout for an operand whose
+ *                 slow axis is the reduction);
+ *   8 value warps read the checkpoint's 64 x 128 tile into registers two steps
+ *                 ahead (a thread one block of 32 values and its scale), turn
+ *                 it into 16-bit values and store them in the same layout.
+ *                 q * 2^k is exact in the 16-bit type, so the operand is the
+ *                 checkpoint itself, without a rounding;
+ *   product warp  one thread issues four 128 x 256 x 16 products per stage.
+ * The value warps then read the sums from tensor memory, round them once and
+ * store them.
+ *
+ * Few tiles and many tokens: a cluster of 2, 4 or 8 CTAs shares a tile, each
+ * a part of the tokens; the sums meet in shared memory and every CTA adds its
+ * share of the rows over the cluster in rank order. The split depends on the
+ * sizes alone, so results do not change from call to call.
+ *
+ * Every wait is bounded (2 s); one that expires ends the CTA's work, its
+ * copies in flight are awaited (bounded too), the tile becomes NaN and the
+ * scaler's error word is raised.
  */
+#include <cuda.h>
+
 #include "train.cuh"
+
+#include <algorithm>
 
 namespace zw {
 
 using namespace zt;
 
-constexpr int kThreads = 256;
-constexpr int kTile = 64;
-constexpr int kStep = 16;
+constexpr int kValueWarps = 8;
+constexpr int kValueThreads = 32 * kValueWarps;
+constexpr int kCopyWarp = kValueWarps, kProductWarp = kValueWarps + 1;
+constexpr int kThreads = 32 * (kValueWarps + 2);
+constexpr int kM = 128, kN = 256, kK = 64;     // tile of dw, tokens per stage
+constexpr int kStages = 4;
+constexpr int kChunk = kK * 128;               // 64 tokens x 64 columns of 16 bits
+constexpr int kBytesA = kM / 64 * kChunk, kBytesB = kN / 64 * kChunk;
+constexpr int kStageBytes = kBytesA + kBytesB;
+constexpr int kJoinPitch = kN + 4;             // fp32 row of a tile in shared memory
+constexpr int kSmem = kStages * kStageBytes + 1024;
+constexpr int kMaxSplit = 8;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+static_assert(kM * kJoinPitch * 4 <= kStages * kStageBytes, "the tile fits the stages");
+static_assert(kM == ZERO_CKPT_PAD, "a checkpoint row is whole tiles");
 
 struct Args {
   const int8_t* q;
   const uint8_t* scale;
   const uint16_t* dy;
   uint16_t* dw;
+  zero_scaler* scaler;
   int64_t rows, cols, pitch, n, ld;
+  int32_t split, vec_out;
 };
 
-template <bool kBf16>
-__global__ void __launch_bounds__(kThreads) wgrad_kernel(const Args a) {
-  pdl_begin();
-  __shared__ float xs[kStep][kTile], ys[kStep][kTile];
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kTile;
-  const int64_t j0 = static_cast<int64_t>(blockIdx.y) * kTile;
-  const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
-  float sum[4][4] = {};
-  for (int64_t t0 = 0; t0 < a.rows; t0 += kStep) {
-    for (int k = threadIdx.x; k < kStep * kTile; k += kThreads) {
-      const int64_t t = t0 + k / kTile, i = i0 + k % kTile, j = j0 + k % kTile;
-      float x = 0.f, y = 0.f;
-      if (t < a.rows && i < a.cols) {
-        const uint32_t s = a.scale[t * (a.pitch / ZERO_CKPT_BLOCK) + i / ZERO_CKPT_BLOCK];
-        x = static_cast<float>(a.q[t * a.pitch + i]) *
-            (s == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(s << 23));
-      }
-      if (t < a.rows && j < a.n) y = widen<kBf16>(a.dy[t * a.ld + j]);
-      xs[k / kTile][k % kTile] = x;
-      ys[k / kTile][k % kTile] = y;
+// ------------------------------------------------------------- primitives ----
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+__device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count)
+               : "memory");
+}
+
+__device__ __forceinline__ void bar_arrive(uint64_t* bar) {
+  asm volatile("{\n .reg .b64 st;\n mbarrier.arrive.shared::cta.b64 st, [%0];\n}" ::"r"(
+                   smem_u32(bar))
+               : "memory");
+}
+
+__device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) {
+  asm volatile(
+      "{\n .reg .b64 st;\n mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n}" ::"r"(
+          smem_u32(bar)),
+      "r"(bytes)
+      : "memory");
+}
+
+__device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ uint64_t global_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+
+// true when the phase has completed; false once *failed is set or the limit
+// has passed (which sets it)
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* failed) {
+  if (bar_try(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  for (;;) {
+    if (bar_try(bar, parity)) return true;
+    if (*failed) return false;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      *failed = 1;
+      return false;
     }
-    __syncthreads();
-    for (int k = 0; k < kStep; ++k) {
-#pragma unroll
-      for (int p = 0; p < 4; ++p)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          sum[p][q] = __fmaf_rn(xs[k][ti * 4 + p], ys[k][tj * 4 + q], sum[p][q]);
-    }
-    __syncthreads();
   }
-  for (int p = 0; p < 4; ++p)
-    for (int q = 0; q < 4; ++q) {
-      const int64_t i = i0 + ti * 4 + p, j = j0 + tj * 4 + q;
-      if (i < a.cols && j < a.n && ZCHECK(i * a.n + j < a.cols * a.n, kSiteStore, i))
-        a.dw[i * a.n + j] = narrow<kBf16>(sum[p][q]);
+}
+
+__device__ __forceinline__ void copy_box(void* dst, const CUtensorMap* map, int32_t x, int32_t y,
+                                         uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Shared-memory operand whose reduction axis is the slow one, 128-byte
+// swizzle: rows of 64 elements (128 bytes), eight rows per 1024-byte atom
+// (the next eight reduction steps), the next 64 elements kChunk bytes on.
+__device__ __forceinline__ uint64_t operand(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) |
+         static_cast<uint64_t>(kChunk >> 4) << 16 | static_cast<uint64_t>(1024 >> 4) << 32 |
+         1ull << 46 | 2ull << 61;
+}
+
+// fp32 sums; both operands of the 16-bit type, slow axis reduced; 128 x 256
+template <bool kBf16>
+__host__ __device__ constexpr uint32_t product_desc() {
+  return 1u << 4 | (kBf16 ? 1u : 0u) << 7 | (kBf16 ? 1u : 0u) << 10 | 1u << 15 | 1u << 16 |
+         static_cast<uint32_t>(kN >> 3) << 17 | static_cast<uint32_t>(kM >> 4) << 24;
+}
+
+__device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t desc,
+                                        bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(desc), "r"(add ? 1u : 0u)
+      : "memory");
+}
+
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   smem_u32(bar))
+               : "memory");
+}
+
+// 32 lanes x 32 columns of tensor memory
+__device__ __forceinline__ void read_sums(uint32_t addr, float (&f)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+#pragma unroll
+  for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(r[j]);
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
+          : "memory");
+}
+
+// ------------------------------------------------------------------ values ----
+
+// One block's step 2^k in both halves of a word. 255 (not finite) becomes an
+// infinity or NaN that turns the block's zeros into NaN.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t step_pair(uint32_t s) {
+  uint32_t h;
+  if constexpr (kBf16) h = s << 7;
+  else h = s == 255 ? 0x7E00u : s >= 113 ? (s - 112) << 10 : 1u << (s - 103);
+  return h | h << 16;
+}
+
+// Two of a word's four int8 values (bytes 0 and 1, or 2 and 3) as a pair of
+// 16-bit floats times `step`: the byte's bits are put under the exponent of a
+// number whose last place is 1, and that number is taken off again.
+template <bool kBf16, int kHalf>
+__device__ __forceinline__ uint32_t value_pair(uint32_t w, uint32_t step) {
+  const uint32_t p = __byte_perm(w, 0, kHalf ? 0x4342 : 0x4140);
+  uint32_t r;
+  if constexpr (kBf16) {
+    // 128 + low seven bits, less 128 or (sign bit set) 256
+    const uint32_t lo = (p & 0x007F007Fu) | 0x43004300u, hi = (p & 0x00800080u) | 0x43004300u;
+    asm("{\n .reg .b32 d;\n sub.rn.bf16x2 d, %1, %2;\n mul.rn.bf16x2 %0, d, %3;\n}"
+        : "=r"(r)
+        : "r"(lo), "r"(hi), "r"(step));
+  } else {
+    // 1024 + (value + 128), less 1152
+    const uint32_t u = (p ^ 0x00800080u) | 0x64006400u;
+    asm("{\n .reg .b32 d;\n sub.rn.f16x2 d, %1, %2;\n mul.rn.f16x2 %0, d, %3;\n}"
+        : "=r"(r)
+        : "r"(u), "r"(0x64806480u), "r"(step));
+  }
+  return r;
+}
+
+struct Block {  // 32 checkpointed values of one token
+  uint4 lo, hi;
+  uint32_t scale;
+};
+
+__device__ __forceinline__ Block load_block(const Args& a, int64_t t, int64_t end, int64_t i) {
+  Block b;
+  b.lo = b.hi = make_uint4(0, 0, 0, 0);
+  b.scale = 127;
+  if (t < end && ZCHECK(t < a.rows && i + 32 <= a.pitch, kSiteLoad, t)) {
+    const uint4* p = reinterpret_cast<const uint4*>(a.q + t * a.pitch + i);
+    b.lo = p[0];
+    b.hi = p[1];
+    b.scale = a.scale[t * (a.pitch / ZERO_CKPT_BLOCK) + i / ZERO_CKPT_BLOCK];
+  }
+  return b;
+}
+
+// Store a block's 32 values for token row r, columns [32 blk, 32 blk + 32) of
+// the A tile. The 16-byte pieces of blocks 2 and 3 go in another order than
+// those of 0 and 1, so that the eight lanes of a store phase (two tokens,
+// four blocks) fall on eight different pieces of the 128-byte rows.
+template <bool kBf16>
+__device__ __forceinline__ void store_block(uint8_t* stage_a, const Block& b, int r, int blk) {
+  const uint32_t s = step_pair<kBf16>(b.scale);
+  const uint32_t w[8] = {b.lo.x, b.lo.y, b.lo.z, b.lo.w, b.hi.x, b.hi.y, b.hi.z, b.hi.w};
+  uint4 v[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    v[j] = make_uint4(value_pair<kBf16, 0>(w[2 * j], s), value_pair<kBf16, 1>(w[2 * j], s),
+                      value_pair<kBf16, 0>(w[2 * j + 1], s), value_pair<kBf16, 1>(w[2 * j + 1], s));
+  uint8_t* row = stage_a + (blk >> 1) * kChunk + r * 128;
+  const bool swap = blk & 2;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint4 x = swap ? v[j ^ 2] : v[j];
+    const int piece = (blk & 1) * 4 + (swap ? j ^ 2 : j);
+    *reinterpret_cast<uint4*>(row + ((piece ^ (r & 7)) << 4)) = x;
+  }
+}
+
+// dy's tile without TMA: rows that do not start on 16-byte boundaries
+__device__ __forceinline__ void load_dy(const Args& a, uint8_t* stage_b, int64_t t0, int64_t end,
+                                        int64_t j0, int tid) {
+  for (int p = tid; p < kK * (kN / 8); p += kValueThreads) {
+    const int r = p / (kN / 8), c = p % (kN / 8);  // token, piece of eight columns
+    const int64_t t = t0 + r, j = j0 + c * 8;
+    uint32_t h[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) h[k] = t < end && j + k < a.n ? a.dy[t * a.ld + j + k] : 0;
+    *reinterpret_cast<uint4*>(stage_b + (c >> 3) * kChunk + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+        make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+  }
+}
+
+// kCount sums of one row of dw, columns j, j + 1, ...
+template <bool kBf16, int kCount>
+__device__ __forceinline__ void store_sums(const Args& a, int64_t i, int64_t j,
+                                           const float (&f)[kCount]) {
+  if (i >= a.cols) return;
+  uint16_t* p = a.dw + i * a.n + j;
+#pragma unroll
+  for (int k = 0; k < kCount; k += 8) {
+    if (a.vec_out && j + k + 8 <= a.n) {
+      *reinterpret_cast<uint4*>(p + k) =
+          make_uint4(narrow2<kBf16>(f[k], f[k + 1]), narrow2<kBf16>(f[k + 2], f[k + 3]),
+                     narrow2<kBf16>(f[k + 4], f[k + 5]), narrow2<kBf16>(f[k + 6], f[k + 7]));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (j + k + e < a.n && ZCHECK(i * a.n + j + k + e < a.cols * a.n, kSiteStore, i))
+          p[k + e] = narrow<kBf16>(f[k + e]);
     }
+  }
+}
+
+// ------------------------------------------------------------------ kernel ----
+
+template <bool kBf16, bool kTma>
+__global__ void __launch_bounds__(kThreads, 1)
+    wgrad_kernel(const __grid_constant__ CUtensorMap map, const Args a) {
+  pdl_begin();
+  extern __shared__ uint8_t raw[];
+  uint8_t* stages = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  __shared__ uint64_t full_a[kStages], full_b[kStages], empty[kStages], done;
+  __shared__ uint32_t tmem_base;
+  __shared__ int failed;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = static_cast<int>(blockIdx.x) % a.split;
+  const int64_t tile = blockIdx.x / a.split;
+  const int64_t m_tiles = a.pitch / kM;
+  const int64_t i0 = tile % m_tiles * kM, j0 = tile / m_tiles * kN;
+  // this CTA's tokens: whole steps
+  const int64_t steps = (a.rows + kK - 1) / kK;
+  const int64_t s0 = steps * rank / a.split, s1 = steps * (rank + 1) / a.split;
+  const int n_it = static_cast<int>(s1 - s0);
+  const int64_t t_begin = s0 * kK;
+
+  if (warp == kProductWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&tmem_base)),
+                 "n"(kN)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      bar_init(&full_a[s], kValueWarps);
+      bar_init(&full_b[s], 1);
+      bar_init(&empty[s], 1);
+    }
+    bar_init(&done, 1);
+    failed = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = tmem_base;
+
+  if (warp == kCopyWarp) {
+    if (kTma && lane == 0) {
+      int it = 0;
+      for (; it < n_it; ++it) {
+        const int s = it % kStages;
+        if (it >= kStages && !bar_wait(&empty[s], (it / kStages - 1) & 1, &failed)) break;
+        uint8_t* b = stages + s * kStageBytes + kBytesA;
+        bar_expect(&full_b[s], kBytesB);
+#pragma unroll
+        for (int c = 0; c < kN / 64; ++c)
+          copy_box(b + c * kChunk, &map, static_cast<int32_t>(j0 + c * 64),
+                   static_cast<int32_t>(t_begin + static_cast<int64_t>(it) * kK), &full_b[s]);
+      }
+      if (it < n_it) {  // given up: the copies in flight still land in this CTA's memory
+        for (int k = it > kStages ? it - kStages : 0; k < it; ++k) {
+          const uint64_t t0 = global_ns();
+          while (!bar_try(&full_b[k % kStages], (k / kStages) & 1) &&
+                 global_ns() - t0 < kWaitLimitNs) {
+          }
+        }
+      }
+    }
+  } else if (warp == kProductWarp) {
+    if (lane == 0) {
+      bool ok = true;
+      for (int it = 0; it < n_it && ok; ++it) {
+        const int s = it % kStages;
+        const uint32_t parity = (it / kStages) & 1;
+        ok = bar_wait(&full_a[s], parity, &failed) &&
+             (!kTma || bar_wait(&full_b[s], parity, &failed));
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t at = smem_u32(stages + s * kStageBytes);
+#pragma unroll
+        for (int k = 0; k < kK / 16; ++k)
+          product(tmem, operand(at + k * 2048), operand(at + kBytesA + k * 2048),
+                  product_desc<kBf16>(), it > 0 || k > 0);
+        commit(&empty[s]);
+      }
+      commit(&done);
+    }
+  } else {
+    // value warps: thread -> token r of a step, block blk of the 128 columns
+    const int r = tid >> 2, blk = tid & 3;
+    const int64_t i = i0 + blk * 32;
+    const int64_t t_end = s1 * kK < a.rows ? s1 * kK : a.rows;
+    Block ahead[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) ahead[k] = load_block(a, t_begin + k * kK + r, t_end, i);
+    bool ok = true;
+    for (int it = 0; it < n_it && ok; it += 2) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (it + k >= n_it || !ok) break;
+        const int s = (it + k) % kStages;
+        ok = it + k < kStages || bar_wait(&empty[s], ((it + k) / kStages - 1) & 1, &failed);
+        if (!ok) break;
+        uint8_t* stage = stages + s * kStageBytes;
+        const int64_t t0 = t_begin + static_cast<int64_t>(it + k) * kK;
+        store_block<kBf16>(stage, ahead[k], r, blk);
+        ahead[k] = load_block(a, t0 + 2 * kK + r, t_end, i);
+        if constexpr (!kTma) load_dy(a, stage + kBytesA, t0, t_end, j0, tid);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) bar_arrive(&full_a[s]);
+      }
+    }
+    if (bar_wait(&done, 0, &failed)) asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  }
+  __syncthreads();
+
+  const bool bad = failed != 0;
+  const bool none = n_it == 0;  // no tokens here: zeros
+  if (bad && tid == 0 && a.scaler) atomicCAS(&a.scaler->error, 0, ZERO_DEVERR_TIMEOUT);
+  // value warp w: rows 32 (w mod 4) ..., columns 128 (w / 4) ...
+  const int row0 = (warp & 3) * 32, col0 = (warp >> 2) * (kN / 2);
+  const auto sums = [&](int c, float (&f)[32]) {
+    if (bad || none) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) f[j] = bad ? __uint_as_float(0x7FC00000u) : 0.f;
+    } else {
+      read_sums(tmem + (static_cast<uint32_t>(row0) << 16) + col0 + c, f);
+    }
+  };
+  if (a.split == 1) {
+    if (warp < kValueWarps) {
+#pragma unroll
+      for (int c = 0; c < kN / 2; c += 32) {
+        float f[32];
+        sums(c, f);
+        store_sums<kBf16>(a, i0 + row0 + lane, j0 + col0 + c, f);
+      }
+    }
+  } else {
+    float* tile_sums = reinterpret_cast<float*>(stages);
+    if (warp < kValueWarps) {
+#pragma unroll
+      for (int c = 0; c < kN / 2; c += 32) {
+        float f[32];
+        sums(c, f);
+        float4* p = reinterpret_cast<float4*>(tile_sums + (row0 + lane) * kJoinPitch + col0 + c);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          p[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+      }
+    }
+    cluster_sync();
+    // this CTA's share of the rows, eight columns per thread and turn
+    const int share = kM / a.split;
+    for (int p = tid; p < share * (kN / 8); p += kThreads) {
+      const int row = rank * share + p / (kN / 8), c = p % (kN / 8) * 8;
+      const uint32_t at = smem_u32(tile_sums + row * kJoinPitch + c);
+      float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      for (int k = 0; k < a.split; ++k) {
+        uint32_t remote;
+        float4 x, y;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(at), "r"(k));
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                     : "r"(remote)
+                     : "memory");
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
+                     : "r"(remote + 16)
+                     : "memory");
+        f[0] += x.x, f[1] += x.y, f[2] += x.z, f[3] += x.w;
+        f[4] += y.x, f[5] += y.y, f[6] += y.z, f[7] += y.w;
+      }
+      store_sums<kBf16>(a, i0 + row, j0 + c, f);
+    }
+    cluster_sync();  // no CTA ends while another reads its sums
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (warp == kProductWarp) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kN));
+  }
+}
+
+// -------------------------------------------------------------------- host ----
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+template <bool kBf16, bool kTma>
+int launch(const CUtensorMap& map, const Args& a, int64_t tiles, cudaStream_t st) {
+  const auto fn = wgrad_kernel<kBf16, kTma>;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+    return ZERO_ECUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.split));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = kProgrammaticLaunch ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return status_of(cudaLaunchKernelEx(&cfg, fn, map, a));
 }
 
 }  // namespace zw
@@ -89,12 +548,38 @@ ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const
   a.scale = static_cast<const uint8_t*>(ckpt) + rows * a.pitch;
   a.dy = static_cast<const uint16_t*>(dy);
   a.dw = static_cast<uint16_t*>(dw);
+  a.scaler = d_scaler;
   a.rows = rows, a.cols = cols, a.n = n, a.ld = ld;
-  const dim3 grid(static_cast<unsigned>(ceil_div(cols, kTile)),
-                  static_cast<unsigned>(ceil_div(n, kTile)));
-  if (grid.y > 65535) return ZERO_ERANGE;
-  return status_of(launch_pdl(dtype == ZERO_BF16 ? wgrad_kernel<true> : wgrad_kernel<false>, grid,
-                              dim3(kThreads), 0, static_cast<cudaStream_t>(stream), a));
+  a.vec_out = n % kVec == 0 && aligned(dw, 16);
+  const int64_t tiles = a.pitch / kM * ceil_div(n, kN);
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return ZERO_ECUDA;
+  // split the tokens while SMs would be idle and a part keeps four steps
+  a.split = 1;
+  while (a.split < kMaxSplit && tiles * a.split * 2 <= sms && rows >= a.split * 2 * 4 * kK)
+    a.split *= 2;
+  if (tiles * a.split > 0x7fffffff) return ZERO_ERANGE;
+  const bool bf16 = dtype == ZERO_BF16;
+  const bool tma = rows > 0 && ld % kVec == 0 && aligned(dy, 16);
+  CUtensorMap map = {};
+  if (tma) {
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return ZERO_ECUDA;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+    const cuuint32_t box[2] = {64, kK}, unit[2] = {1, 1};
+    if (encode(&map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+               const_cast<void*>(dy), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return ZERO_ECUDA;
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (bf16)
+    return tma ? launch<true, true>(map, a, tiles, st) : launch<true, false>(map, a, tiles, st);
+  return tma ? launch<false, true>(map, a, tiles, st) : launch<false, false>(map, a, tiles, st);
 }
 
 }  // extern "C"
