@@ -5,21 +5,30 @@
  * A row's softmax needs its maximum and sum before its gradient can be
  * written, so the row is read once into the shared memory of a cluster of 1
  * to 8 CTAs and the gradient is formed from there: rows * vocab elements read
- * and as many written, nothing in between. Each thread keeps a running
- * maximum m and sum s of exp(x - m) over its vectors (a new maximum rescales
- * s), the CTA joins its threads' pairs, and every CTA sends its pair to all
- * others of the cluster over distributed shared memory; all join them in rank
- * order, so all hold the same bits.
+ * and as many written, nothing in between. Each lane keeps a running maximum
+ * m and sum s of exp(x - m) over its vectors (a new maximum rescales s), the
+ * CTA joins its lanes' pairs, and every CTA sends its pair to all others of
+ * the cluster over distributed shared memory; all join them in rank order, so
+ * all hold the same bits.
+ *
+ * The row is cut into parts, kParts per warp and the same number of blocks
+ * (+-1) each. A part belongs to one warp from its bulk copy to its gradient:
+ * the warp waits for the copy, sums, later forms the gradient from the same
+ * bytes, and at once starts the copy of the next row's part into their place,
+ * so the next row arrives while this one's gradient leaves, and no barrier of
+ * the CTA stands between them.
  *
  * A row of an odd vocabulary starts anywhere. It is numbered in the 16-byte
- * blocks of its addresses: whole blocks move as blocks, the elements of the
- * first and last partial block one by one, and in shared memory the parts of
- * those blocks outside the row hold -inf, so the arithmetic sees whole blocks.
+ * blocks of its addresses; the first and last may hold elements of other
+ * rows, which are read as -inf and not written.
  */
 #include "train.cuh"
 
 #include <algorithm>
 #include <cmath>
+#include <map>
+#include <mutex>
+#include <tuple>
 
 namespace zp {
 
@@ -28,7 +37,10 @@ using namespace zt;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kParts = 4;      // parts of a row per warp
+constexpr int kBatch = 4;      // blocks per lane and step
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct Args {
   const uint8_t* logits;
@@ -42,46 +54,114 @@ struct Args {
   float lo, hi, beta;
 };
 
-// softmax statistics: largest value and sum of exp(x - m); (-inf, 0) for none
-struct Stat {
-  float m, s;
-};
-
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// exp(x - m) for m >= x; m finite
-__device__ __forceinline__ float exp_below(float x, float m) {
-  return exp2_fast((x - m) * kLog2e);
+// exp(x - m) is formed as 2^(x c - m c) with c = log2 e: one fused
+// multiply-add per element, and what m c loses in rounding is the same for
+// every element and cancels. From |m| = 2^100 on m c could overflow; there two
+// different 16-bit or fp32 numbers of m's size are more than 2^70 apart, so
+// any c gives 1 for x = m and 0 for the rest, and 1/2 stays finite.
+struct Base {
+  float c, mc;
+};
+
+__device__ __forceinline__ Base base_of(float m) {
+  const float at = m == -INFINITY ? 0.f : m;  // nothing but -inf so far
+  const float c = fabsf(at) < 0x1p100f ? kLog2e : 0.5f;
+  return Base{c, at * c};
+}
+
+// softmax statistics: largest value and sum of exp(x - m); (-inf, 0) for none
+struct Stat {
+  float m, s;
+};
+
+// a's sum over another, not smaller, maximum
+__device__ __forceinline__ float moved(const Stat& a, float m) {
+  // a side with nothing adds nothing; inf and NaN go on into the sum
+  return a.s == 0.f ? 0.f : a.s * exp2_fast(base_of(a.m).mc - base_of(m).mc);
 }
 
 __device__ __forceinline__ Stat join(const Stat& a, const Stat& b) {
   const float m = fmaxf(a.m, b.m);
-  // a side with nothing adds nothing; inf and NaN go on into the sum
-  const float sa = a.s == 0.f ? 0.f : a.s * exp_below(a.m, m);
-  const float sb = b.s == 0.f ? 0.f : b.s * exp_below(b.m, m);
-  return Stat{m, sa + sb};
+  return Stat{m, moved(a, m) + moved(b, m)};
 }
 
-// elements of a 16-byte block as fp32
+// Two fp32 values as one operand: sm_100's packed fp32 arithmetic does both
+// in one instruction, each rounded to nearest even.
+struct Pair {
+  uint64_t v;
+};
+
+__device__ __forceinline__ Pair pair(float x, float y) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(x), "f"(y));
+  return p;
+}
+
+__device__ __forceinline__ void unpair(const Pair& p, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p.v));
+}
+
+__device__ __forceinline__ Pair operator*(const Pair& a, const Pair& b) {
+  Pair p;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
+  return p;
+}
+
+__device__ __forceinline__ Pair fma2(const Pair& a, const Pair& b, const Pair& c) {
+  Pair p;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return p;
+}
+
+__device__ __forceinline__ Pair operator+(const Pair& a, const Pair& b) {
+  Pair p;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
+  return p;
+}
+
+// A 16-byte block of logits.
 template <int kType>
 struct Block {
+  static constexpr bool kBf16 = kType == ZERO_BF16;
   static constexpr int kElems = 8;
   static constexpr int kBytes = 2;
-  __device__ static __forceinline__ void get(const uint4& v, float (&f)[8]) {
-    widen8<kType == ZERO_BF16>(v, f);
+  static constexpr uint32_t kNone = kBf16 ? 0xFF80FF80u : 0xFC00FC00u;  // -inf, -inf
+  __device__ static __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (kBf16) asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
   }
-  __device__ static __forceinline__ uint4 put(const float (&f)[8]) {
-    return narrow8<kType == ZERO_BF16>(f);
+  // two running maxima; top() joins them
+  __device__ static __forceinline__ uint32_t max_of(const uint4& v, uint32_t so_far) {
+    return max2(so_far, max2(max2(v.x, v.y), max2(v.z, v.w)));
   }
+  __device__ static __forceinline__ float top(uint32_t w) {
+    float a, b;
+    widen2<kBf16>(w, a, b);
+    return fmaxf(a, b);
+  }
+  __device__ static __forceinline__ void get(const uint4& v, Pair (&f)[4]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float x, y;
+      widen2<kBf16>(w[j], x, y);
+      f[j] = pair(x, y);
+    }
+  }
+  __device__ static __forceinline__ uint4 put(const float (&f)[8]) { return narrow8<kBf16>(f); }
   __device__ static __forceinline__ float one(const uint8_t* p) {
-    return widen<kType == ZERO_BF16>(*reinterpret_cast<const uint16_t*>(p));
+    return widen<kBf16>(*reinterpret_cast<const uint16_t*>(p));
   }
   __device__ static __forceinline__ void set(uint8_t* p, float x) {
-    *reinterpret_cast<uint16_t*>(p) = narrow<kType == ZERO_BF16>(x);
+    *reinterpret_cast<uint16_t*>(p) = narrow<kBf16>(x);
   }
 };
 
@@ -89,9 +169,17 @@ template <>
 struct Block<ZERO_FP32> {
   static constexpr int kElems = 4;
   static constexpr int kBytes = 4;
-  __device__ static __forceinline__ void get(const uint4& v, float (&f)[4]) {
-    f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y);
-    f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+  static constexpr uint32_t kNone = 0xFF800000u;
+  __device__ static __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }
+  __device__ static __forceinline__ uint32_t max_of(const uint4& v, uint32_t so_far) {
+    return max2(so_far, max2(max2(v.x, v.y), max2(v.z, v.w)));
+  }
+  __device__ static __forceinline__ float top(uint32_t w) { return __uint_as_float(w); }
+  __device__ static __forceinline__ void get(const uint4& v, Pair (&f)[2]) {
+    f[0] = pair(__uint_as_float(v.x), __uint_as_float(v.y));
+    f[1] = pair(__uint_as_float(v.z), __uint_as_float(v.w));
   }
   __device__ static __forceinline__ uint4 put(const float (&f)[4]) {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
@@ -105,19 +193,56 @@ struct Block<ZERO_FP32> {
   }
 };
 
-template <int kElems>
-__device__ __forceinline__ void add_block(Stat& t, const float (&f)[kElems]) {
-  float top = f[0];
+template <int kType>
+__device__ __forceinline__ uint4 no_block() {
+  constexpr uint32_t w = Block<kType>::kNone;
+  return make_uint4(w, w, w, w);
+}
+
+// exp(x - m) of a block's elements
+template <int kType>
+__device__ __forceinline__ void exp_block(const uint4& v, const Pair& c, const Pair& minus_mc,
+                                          Pair (&e)[Block<kType>::kElems / 2]) {
+  Block<kType>::get(v, e);
 #pragma unroll
-  for (int j = 1; j < kElems; ++j) top = fmaxf(top, f[j]);
+  for (int j = 0; j < Block<kType>::kElems / 2; ++j) {
+    float x, y;
+    unpair(fma2(e[j], c, minus_mc), x, y);
+    e[j] = pair(exp2_fast(x), exp2_fast(y));
+  }
+}
+
+// kBatch blocks into a lane's statistics: one rescaling for all of them
+template <int kType>
+__device__ __forceinline__ void add_blocks(Stat& t, const uint4 (&v)[kBatch]) {
+  using B = Block<kType>;
+  uint32_t w = B::max_of(v[0], B::kNone);
+#pragma unroll
+  for (int k = 1; k < kBatch; ++k) w = B::max_of(v[k], w);
+  const float top = B::top(w);
   if (top > t.m) {
-    t.s = t.s == 0.f ? 0.f : t.s * exp_below(t.m, top);
+    t.s = moved(t, top);
     t.m = top;
   }
-  // nothing but -inf so far: no sum to form (a NaN beside it still counts)
-  const float m = t.m == -INFINITY ? 0.f : t.m;
+  const Base b = base_of(t.m);
+  const Pair c = pair(b.c, b.c), minus_mc = pair(-b.mc, -b.mc);
+  Pair sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
 #pragma unroll
-  for (int j = 0; j < kElems; ++j) t.s += exp_below(f[j], m);
+  for (int k = 0; k < kBatch; ++k) {
+    Pair e[B::kElems / 2];
+    exp_block<kType>(v[k], c, minus_mc, e);
+#pragma unroll
+    for (int j = 0; j < B::kElems / 2; ++j) sum[j & 1] = sum[j & 1] + e[j];
+  }
+  float x, y;
+  unpair(sum[0] + sum[1], x, y);
+  t.s += x + y;
+}
+
+// log(exp(x - m) / s)
+__device__ __forceinline__ float log_share(float x, const Stat& t) {
+  const Base b = base_of(t.m);
+  return __fmaf_rn(x, b.c, -b.mc) * (b.c == 0.5f ? 2.f : kLn2) - logf(t.s);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -147,139 +272,317 @@ __device__ __forceinline__ void send(Stat* local, uint32_t rank, const Stat& v) 
                : "memory");
 }
 
-template <int kType, bool kGrad>
-__global__ void __launch_bounds__(kThreads) policy_kernel(const Args a) {
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// Bulk copy of whole 16-byte blocks (possibly none) that completes one phase
+// of `bar`.
+__device__ __forceinline__ void copy_blocks(void* dst, const uint8_t* src, uint32_t bytes,
+                                            uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .b64 st;\n mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n}" ::"r"(
+          smem_u32(bar)),
+      "r"(bytes)
+      : "memory");
+  if (bytes)
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+            "r"(smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ uint64_t global_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
+  if (bar_try(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  for (;;) {
+    if (bar_try(bar, parity)) return true;
+    if (global_ns() - t0 > kWaitLimitNs) return false;
+  }
+}
+
+// A row as 16-byte blocks.
+struct Row {
+  const uint8_t* base;  // block 0; the row starts `head` bytes into it
+  int32_t head, n_blk;
+  int32_t end;          // head + the row's bytes
+  int32_t action;       // -1: left out
+  float weight;
+  __device__ __forceinline__ bool on() const { return action >= 0 && weight != 0.f; }
+};
+
+template <int kBytes, bool kGrad>
+__device__ __forceinline__ Row row_of(const Args& a, int64_t row) {
+  Row r;
+  const uint8_t* x = a.logits + row * a.ld * kBytes;
+  r.head = static_cast<int32_t>(reinterpret_cast<uintptr_t>(x) & 15);
+  r.base = x - r.head;
+  r.end = r.head + static_cast<int32_t>(a.vocab) * kBytes;
+  r.n_blk = (r.end + 15) >> 4;
+  r.action = static_cast<int32_t>(load_id(a.actions, a.action_bytes, row, a.vocab));
+  r.weight = kGrad ? a.weight[row] : 1.f;
+  return r;
+}
+
+// Block b of the row with -inf in place of what it holds of other rows (the
+// first and the last block may).
+template <int kType>
+__device__ __forceinline__ uint4 own_part(const Row& r, int32_t b, const uint4& v) {
+  using B = Block<kType>;
+  if (b != 0 && b != r.n_blk - 1) return v;
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const int lo = b == 0 ? r.head : 0;
+  const int hi = b == r.n_blk - 1 ? r.end - b * 16 : 16;
+#pragma unroll
+  for (int j = 0; j < B::kElems; ++j) {
+    const int at = j * B::kBytes;
+    if (at >= lo && at < hi) continue;
+    const uint32_t keep = B::kBytes == 4 ? 0u : (at & 2) ? 0x0000FFFFu : 0xFFFF0000u;
+    w[at >> 2] = (w[at >> 2] & keep) | (B::kNone & ~keep);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A lane's statistics joined over the CTA and then the cluster; all threads
+// of all CTAs call it and hold the same bits afterwards.
+__device__ __forceinline__ Stat join_all(Stat t, Stat* of_warp, Stat* of_cta, uint32_t rank,
+                                         uint32_t n_cta) {
+  const int tid = threadIdx.x, lane = tid & 31;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    const Stat o = {__shfl_xor_sync(0xffffffffu, t.m, d), __shfl_xor_sync(0xffffffffu, t.s, d)};
+    // the same operands in the same order on both lanes
+    t = (lane & d) ? join(o, t) : join(t, o);
+  }
+  if (lane == 0) of_warp[tid >> 5] = t;
+  __syncthreads();
+  if (tid < static_cast<int>(n_cta)) {
+    Stat c = of_warp[0];
+    for (int k = 1; k < kWarps; ++k) c = join(c, of_warp[k]);
+    if (n_cta == 1) of_cta[0] = c;
+    else send(&of_cta[rank], tid, c);
+  }
+  __syncwarp();
+  if (n_cta == 1) __syncthreads();
+  else cluster_sync();
+  t = of_cta[0];
+  for (uint32_t k = 1; k < n_cta; ++k) t = join(t, of_cta[k]);
+  return t;
+}
+
+// The row's logits as a single stream: statistics only.
+template <int kType>
+__global__ void __launch_bounds__(kThreads) logp_kernel(const Args a) {
+  pdl_begin();
+  using B = Block<kType>;
+  __shared__ Stat of_warp[kWarps];
+  __shared__ Stat of_cta[2][kMaxCluster];
+  const int tid = threadIdx.x;
+  const uint32_t rank = cluster_rank(), n_cta = cluster_size();
+  int parity = 0;
+  if (n_cta > 1) cluster_sync();  // every CTA of the cluster runs before any sends to it
+  for (int64_t row = blockIdx.x / n_cta; row < a.rows; row += gridDim.x / n_cta) {
+    const Row r = row_of<B::kBytes, false>(a, row);
+    float lp = 0.f;
+    if (r.on()) {
+      const float picked = B::one(r.base + r.head + r.action * B::kBytes);
+      const int32_t b0 = static_cast<int64_t>(r.n_blk) * rank / n_cta;
+      const int32_t b1 = static_cast<int64_t>(r.n_blk) * (rank + 1) / n_cta;
+      const uint4* blocks = reinterpret_cast<const uint4*>(r.base);
+      Stat t = {-INFINITY, 0.f};
+      for (int32_t b = b0 + tid; b < b1; b += kThreads * kBatch) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int32_t at = b + k * kThreads;
+          v[k] = at < b1 && ZCHECK(at < r.n_blk, kSiteLoad, at) ? __ldcs(blocks + at)
+                                                               : no_block<kType>();
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) v[k] = own_part<kType>(r, b + k * kThreads, v[k]);
+        add_blocks<kType>(t, v);
+      }
+      t = join_all(t, of_warp, of_cta[parity], rank, n_cta);
+      parity ^= 1;
+      lp = log_share(picked, t);
+    }
+    if (rank == 0 && tid == 0) a.logp[row] = lp;
+  }
+}
+
+template <int kType>
+__global__ void __launch_bounds__(kThreads, 3) policy_kernel(const Args a, const int32_t part_cap) {
   pdl_begin();
   using B = Block<kType>;
   extern __shared__ __align__(16) uint8_t stage[];
   __shared__ Stat of_warp[kWarps];
   __shared__ Stat of_cta[2][kMaxCluster];
+  __shared__ uint64_t landed[kWarps][kParts];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank(), n_cta = cluster_size();
-  const int64_t first = blockIdx.x / n_cta, step = gridDim.x / n_cta;
-  const float scale = kGrad && a.scaler ? a.scaler->scale : 1.f;
+  const int64_t step = gridDim.x / n_cta;
+  const float scale = a.scaler ? a.scaler->scale : 1.f;
+  const int64_t n_part = static_cast<int64_t>(n_cta) * kWarps * kParts;
+  const int64_t part0 = (static_cast<int64_t>(rank) * kWarps + warp) * kParts;
+  uint8_t* mine = stage + static_cast<int64_t>(warp) * kParts * part_cap * 16;
+  if (lane == 0) {
+    for (int p = 0; p < kParts; ++p)
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&landed[warp][p]))
+                   : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncwarp();
+  if (n_cta > 1) cluster_sync();  // every CTA of the cluster runs before any sends to it
+  else __syncthreads();
+  const auto block_of = [&](const Row& r, int p) {
+    return static_cast<int32_t>(r.n_blk * (part0 + p) / n_part);
+  };
+  const auto fetch = [&](const Row& r, int p) {  // one lane
+    const int32_t b0 = block_of(r, p), n = block_of(r, p + 1) - b0;
+    if (ZCHECK(n <= part_cap && b0 + n <= r.n_blk, kSiteStageBytes, n))
+      copy_blocks(mine + static_cast<int64_t>(p) * part_cap * 16,
+                  r.base + static_cast<int64_t>(b0) * 16, n * 16, &landed[warp][p]);
+  };
   int parity = 0;
-  cluster_sync();  // every CTA of the cluster runs before any sends to it
-  for (int64_t row = first; row < a.rows; row += step) {
-    const uint8_t* x = a.logits + row * a.ld * B::kBytes;
-    uint8_t* dx = kGrad && a.dlogits ? a.dlogits + row * a.ld * B::kBytes : nullptr;
-    // this CTA's blocks [b0, b1) of the row's n_blk; block 0 starts `head`
-    // bytes before the row
-    const int64_t bytes = a.vocab * B::kBytes;
-    const int64_t head = static_cast<int64_t>(reinterpret_cast<uintptr_t>(x) & 15);
-    const int64_t n_blk = (head + bytes + 15) / 16;
-    const int64_t b0 = n_blk * rank / n_cta, b1 = n_blk * (rank + 1) / n_cta;
-    const int64_t action = load_id(a.actions, a.action_bytes, row, a.vocab);
-    const float w = kGrad ? a.weight[row] : 1.f;
-    const bool on = action >= 0 && w != 0.f;
+  uint32_t phase = 0;
+  int64_t row = blockIdx.x / n_cta;
+  Row r = {};
+  if (row < a.rows) r = row_of<B::kBytes, true>(a, row);
+  bool fetched = false;  // this row's parts are on their way
+  while (row < a.rows) {
+    const int64_t next_row = row + step;
+    Row next = {};
+    next.action = -1;
+    if (next_row < a.rows) next = row_of<B::kBytes, true>(a, next_row);
     Stat t = {-INFINITY, 0.f};
-    float picked = 0.f;
+    float slope = 0.f, lp = 0.f, loss = 0.f;
+    const bool on = r.on();
     if (on) {
-      if (tid == 0) picked = B::one(x + action * B::kBytes);
-      for (int64_t b = b0 + tid; b < b1; b += kThreads) {
-        const int64_t at = b * 16 - head;  // byte of the row
-        uint4 v;
-        if (at >= 0 && at + 16 <= bytes) {
-          v = __ldcs(reinterpret_cast<const uint4*>(x + at));
-        } else {
+      if (!fetched && lane == 0) {
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) fetch(r, p);
+      }
+      const float picked = B::one(r.base + r.head + r.action * B::kBytes);
+      const float old = a.old_logp[row], adv = a.advantage[row];
+      const float ref = a.ref_logp && a.beta != 0.f ? a.ref_logp[row] : 0.f;
+#pragma unroll 1
+      for (int p = 0; p < kParts; ++p) {
+        const int32_t b0 = block_of(r, p), n = block_of(r, p + 1) - b0;
+        const uint4* part = reinterpret_cast<const uint4*>(mine + static_cast<int64_t>(p) * part_cap * 16);
+        if (!bar_wait(&landed[warp][p], phase)) t.s = __uint_as_float(0x7FC00000u);
+        const bool edge = b0 == 0 || b0 + n == r.n_blk;
+        for (int32_t k = lane; k < n; k += 32 * kBatch) {
+          uint4 v[kBatch];
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j)
+            v[j] = k + 32 * j < n ? part[k + 32 * j] : no_block<kType>();
+          if (edge) {
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) v[j] = own_part<kType>(r, b0 + k + 32 * j, v[j]);
+          }
+          add_blocks<kType>(t, v);
+        }
+      }
+      phase ^= 1;
+      t = join_all(t, of_warp, of_cta[parity], rank, n_cta);
+      parity ^= 1;
+      lp = log_share(picked, t);
+      const float ratio = expf(lp - old);
+      const float plain = ratio * adv, held = fminf(fmaxf(ratio, a.lo), a.hi) * adv;
+      const bool cut = held < plain;
+      loss = -(cut ? held : plain);
+      slope = cut ? 0.f : -plain;
+      if (a.ref_logp && a.beta != 0.f) {
+        const float d = ref - lp, e = expm1f(d);
+        loss = __fmaf_rn(a.beta, e - d, loss);
+        slope = __fmaf_rn(a.beta, -e, slope);
+      }
+      slope *= scale * r.weight;
+    }
+    if (rank == 0 && tid == 0) {
+      a.logp[row] = lp;
+      a.loss[row] = loss;
+    }
+    // the next row's parts follow this row's gradient out of the same place
+    const bool follow = on && next.on();
+    uint8_t* dx = a.dlogits ? a.dlogits + row * a.ld * B::kBytes - r.head : nullptr;
+    // whole blocks when dlogits lies on the 16-byte grid as the logits do
+    const bool same = (reinterpret_cast<uintptr_t>(dx) & 15) == 0;
+    const Base base = base_of(t.m);
+    const Pair c = pair(base.c, base.c), minus_mc = pair(-base.mc, -base.mc);
+    const float inv = -slope / t.s;
+    const Pair by = pair(inv, inv);
+    const int32_t action_at = r.head + r.action * B::kBytes;
+#pragma unroll 1
+    for (int p = 0; p < kParts; ++p) {
+      const int32_t b0 = block_of(r, p), n = dx ? block_of(r, p + 1) - b0 : 0;
+      const uint4* part = reinterpret_cast<const uint4*>(mine + static_cast<int64_t>(p) * part_cap * 16);
+      const bool plain = same && b0 != 0 && b0 + n != r.n_blk;
+      const int32_t special = (action_at >> 4) - b0;  // the block with the action, if in this part
+      uint4* to = reinterpret_cast<uint4*>(dx + static_cast<int64_t>(b0) * 16);
+      if (plain && !on) {
+        for (int32_t k = lane; k < n; k += 32) __stcs(to + k, make_uint4(0, 0, 0, 0));
+      } else if (plain && (special < 0 || special >= n)) {
+#pragma unroll 4
+        for (int32_t k = lane; k < n; k += 32) {
+          Pair e[B::kElems / 2];
+          exp_block<kType>(part[k], c, minus_mc, e);
           float f[B::kElems];
 #pragma unroll
-          for (int j = 0; j < B::kElems; ++j) {
-            const int64_t e = at + j * B::kBytes;
-            f[j] = e >= 0 && e < bytes ? B::one(x + e) : -INFINITY;
-          }
-          v = B::put(f);
+          for (int j = 0; j < B::kElems / 2; ++j) unpair(e[j] * by, f[2 * j], f[2 * j + 1]);
+          __stcs(to + k, B::put(f));
         }
-        if constexpr (kGrad) *reinterpret_cast<uint4*>(stage + (b - b0) * 16) = v;
-        float f[B::kElems];
-        B::get(v, f);
-        add_block(t, f);
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) {
-        const Stat o = {__shfl_xor_sync(0xffffffffu, t.m, d), __shfl_xor_sync(0xffffffffu, t.s, d)};
-        // the same operands in the same order on both lanes
-        t = (lane & d) ? join(o, t) : join(t, o);
-      }
-      if (lane == 0) of_warp[warp] = t;
-      __syncthreads();
-      if (tid < static_cast<int>(n_cta)) {
-        Stat c = of_warp[0];
-        for (int k = 1; k < kWarps; ++k) c = join(c, of_warp[k]);
-        send(&of_cta[parity][rank], tid, c);
-      }
-      __syncwarp();
-      cluster_sync();
-      t = of_cta[parity][0];
-      for (uint32_t k = 1; k < n_cta; ++k) t = join(t, of_cta[parity][k]);
-      parity ^= 1;
-    }
-    const float log_s = on ? logf(t.s) : 0.f;
-    float slope = 0.f;
-    __shared__ float shared_slope;
-    if (tid == 0) {
-      float lp = 0.f, loss = 0.f;
-      if (on) {
-        lp = (picked - t.m) - log_s;
-        if constexpr (kGrad) {
-          const float r = expf(lp - a.old_logp[row]), adv = a.advantage[row];
-          const float plain = r * adv, held = fminf(fmaxf(r, a.lo), a.hi) * adv;
-          const bool cut = held < plain;
-          loss = -(cut ? held : plain);
-          slope = cut ? 0.f : -plain;
-          if (a.ref_logp && a.beta != 0.f) {
-            const float d = a.ref_logp[row] - lp, e = expm1f(d);
-            loss = __fmaf_rn(a.beta, e - d, loss);
-            slope = __fmaf_rn(a.beta, -e, slope);
-          }
-          slope *= scale * w;
-        }
-      }
-      if (rank == 0) {
-        a.logp[row] = lp;
-        if constexpr (kGrad) a.loss[row] = loss;
-      }
-      if constexpr (kGrad) shared_slope = slope;
-    }
-    if constexpr (kGrad) {
-      if (!dx) {
-        __syncthreads();  // of_warp is free again
-        continue;
-      }
-      __syncthreads();
-      slope = shared_slope;
-      // dlogits = slope ([j == a] - p); the row's own blocks when it lies on
-      // the 16-byte grid as the logits do, else element by element
-      const bool same = (reinterpret_cast<uintptr_t>(dx) & 15) == static_cast<uintptr_t>(head);
-      const float m = t.m, inv = on ? -slope / t.s : 0.f;
-      for (int64_t b = b0 + tid; b < b1; b += kThreads) {
-        const int64_t at = b * 16 - head;
-        float f[B::kElems];
-        if (on) {
-          B::get(*reinterpret_cast<const uint4*>(stage + (b - b0) * 16), f);
-#pragma unroll
-          for (int j = 0; j < B::kElems; ++j) {
-            f[j] = exp_below(f[j], m) * inv;
-            if (at + j * B::kBytes == action * B::kBytes) f[j] += slope;
-          }
-        } else {
+      } else {
+#pragma unroll 1
+        for (int32_t k = lane; k < n; k += 32) {
+          const int32_t b = b0 + k;
+          float f[B::kElems];
 #pragma unroll
           for (int j = 0; j < B::kElems; ++j) f[j] = 0.f;
-        }
-        if (same && at >= 0 && at + 16 <= bytes) {
-          __stcs(reinterpret_cast<uint4*>(dx + at), B::put(f));
-        } else {
+          if (on) {
+            Pair e[B::kElems / 2];
+            exp_block<kType>(part[k], c, minus_mc, e);
 #pragma unroll
-          for (int j = 0; j < B::kElems; ++j) {
-            const int64_t e = at + j * B::kBytes;
-            if (e >= 0 && e < bytes) B::set(dx + e, f[j]);
+            for (int j = 0; j < B::kElems / 2; ++j) unpair(e[j] * by, f[2 * j], f[2 * j + 1]);
+#pragma unroll
+            for (int j = 0; j < B::kElems; ++j)
+              if (b * 16 + j * B::kBytes == action_at) f[j] += slope;
+          }
+          if (same && b * 16 >= r.head && b * 16 + 16 <= r.end) {
+            __stcs(to + k, B::put(f));
+          } else {
+#pragma unroll
+            for (int j = 0; j < B::kElems; ++j) {
+              const int32_t at = b * 16 + j * B::kBytes;
+              if (at >= r.head && at < r.end) B::set(dx + at, f[j]);
+            }
           }
         }
       }
-      __syncthreads();  // stage, of_warp and shared_slope are free again
-    } else {
-      __syncthreads();
+      __syncwarp();
+      if (follow && lane == 0) fetch(next, p);
     }
+    fetched = follow;
+    r = next;
+    row = next_row;
   }
 }
 
@@ -317,41 +620,75 @@ __global__ void __launch_bounds__(1024) stats_kernel(const Args a) {
   }
 }
 
-constexpr int kStageCap = 192 * 1024;  // a CTA's share of a row, at most
+constexpr int kStageCap = 196 * 1024;  // a CTA's share of a row, at most
 constexpr int kStageGoal = 72 * 1024;  // three CTAs per SM
+
+// bytes of shared memory per CTA for rows of at most `blocks` blocks
+int64_t stage_bytes(int64_t blocks, int n_cta, int32_t* part_cap) {
+  const int64_t cap = ceil_div(blocks, static_cast<int64_t>(n_cta) * kWarps * kParts);
+  *part_cap = static_cast<int32_t>(cap);
+  return cap * 16 * kWarps * kParts;
+}
+
+struct Launch {
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  Launch(int64_t clusters, int n_cta, size_t smem, cudaStream_t st) : cfg(), attr() {
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * n_cta));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = n_cta;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = kProgrammaticLaunch ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+  }
+};
+
+// Clusters of `fn` the device holds at once (0 on error). One more would
+// wait for a whole row of rows: the grid is exactly these.
+int resident_clusters(const void* fn, int n_cta, size_t smem) {
+  static std::mutex mu;
+  static std::map<std::tuple<const void*, int, int, size_t>, int> known;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  int& n = known[std::make_tuple(fn, dev, n_cta, smem)];
+  if (n == 0) {
+    Launch l(1, n_cta, smem, nullptr);
+    if ((smem && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageCap) !=
+                     cudaSuccess) ||
+        cudaOccupancyMaxActiveClusters(&n, fn, &l.cfg) != cudaSuccess)
+      n = 0;
+  }
+  return n;
+}
 
 template <int kType, bool kGrad>
 int launch(const Args& a, cudaStream_t st) {
   const int64_t blocks = (a.vocab * Block<kType>::kBytes + 15 + 15) / 16;
-  int n_cta = 1;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return ZERO_ECUDA;
-  while (n_cta < kMaxCluster && kGrad && ceil_div(blocks, n_cta) * 16 > kStageGoal) n_cta *= 2;
-  while (n_cta < kMaxCluster && a.rows * n_cta < 2 * sms && blocks / n_cta > 2 * kThreads) n_cta *= 2;
-  const size_t smem = kGrad ? static_cast<size_t>(ceil_div(blocks, n_cta) * 16) : 0;
+  int n_cta = 1;
+  int32_t cap = 0;
+  while (n_cta < kMaxCluster && kGrad && stage_bytes(blocks, n_cta, &cap) > kStageGoal) n_cta *= 2;
+  // few rows: more CTAs per row while each keeps two blocks per thread
+  while (n_cta < kMaxCluster && a.rows * n_cta < 2 * sms && blocks / n_cta > 2 * kThreads)
+    n_cta *= 2;
+  const int64_t smem = kGrad ? stage_bytes(blocks, n_cta, &cap) : 0;
   if (smem > kStageCap) return ZERO_ERANGE;
-  const void* fn = reinterpret_cast<const void*>(policy_kernel<kType, kGrad>);
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kStageCap) != cudaSuccess)
-    return ZERO_ECUDA;
-  const int per_sm = kGrad ? std::max<int>(1, std::min<int>(8, 220 * 1024 / static_cast<int>(smem + 1280))) : 8;
-  const int64_t clusters = std::min<int64_t>(a.rows, std::max<int64_t>(1, static_cast<int64_t>(sms) * per_sm / n_cta));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * n_cta));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = n_cta;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = kProgrammaticLaunch ? 1 : 0;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return status_of(cudaLaunchKernelEx(&cfg, policy_kernel<kType, kGrad>, a));
+  const void* fn = kGrad ? reinterpret_cast<const void*>(policy_kernel<kType>)
+                         : reinterpret_cast<const void*>(logp_kernel<kType>);
+  const int most = resident_clusters(fn, n_cta, static_cast<size_t>(smem));
+  if (most <= 0) return ZERO_ECUDA;
+  Launch l(std::min<int64_t>(a.rows, most), n_cta, static_cast<size_t>(smem), st);
+  return status_of(kGrad ? cudaLaunchKernelEx(&l.cfg, policy_kernel<kType>, a, cap)
+                         : cudaLaunchKernelEx(&l.cfg, logp_kernel<kType>, a));
 }
 
 template <bool kGrad>
@@ -369,7 +706,7 @@ int check(const void* logits, int64_t rows, int64_t vocab, int64_t ld, int32_t d
       (action_bytes != 4 && action_bytes != 8))
     return ZERO_EINVAL;
   const size_t size = dtype == ZERO_FP32 ? 4 : 2;
-  if (vocab > (int64_t{1} << 30) || rows > (int64_t{1} << 31) || ld > (int64_t{1} << 31))
+  if (vocab * static_cast<int64_t>(size) > (int64_t{1} << 30) || rows > (int64_t{1} << 31) || ld > (int64_t{1} << 31))
     return ZERO_ERANGE;
   if (rows == 0) return ZERO_OK;
   if (!logits || !actions || !logp) return ZERO_EINVAL;

@@ -148,10 +148,13 @@ ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const
  *
  * logits: [rows, vocab], row distance ld, of type dtype (ZERO_BF16, ZERO_FP16
  * or ZERO_FP32). -inf entries are tokens ruled out (probability 0); a row of
- * nothing but -inf, or one with a NaN or +inf, has logp NaN.
+ * nothing but -inf, or one with a NaN or +inf, has logp NaN. The calls may
+ * read the rest of the 16-byte blocks that hold the buffer's first and last
+ * elements (any cudaMalloc'd buffer covers them).
  * actions: the tokens taken, int32 or int64 (action_bytes 4 or 8).
  *   logp[t] = logits[t, a_t] - log(sum over j of exp(logits[t, j]))
- * An action outside [0, vocab) leaves its row out: logp 0.                    */
+ * An action outside [0, vocab) leaves its row out: logp 0. A row may have at
+ * most 2^30 bytes (ZERO_ERANGE).                                             */
 ZERO_API int zero_token_logp(const void* logits, int64_t rows, int64_t vocab, int64_t ld,
                              int32_t dtype, const void* actions, int32_t action_bytes,
                              float* logp, void* stream);
