@@ -86,9 +86,24 @@ __device__ __forceinline__ float moved(const Stat& a, float m) {
   return a.s == 0.f ? 0.f : a.s * exp2_fast(base_of(a.m).mc - base_of(m).mc);
 }
 
-__device__ __forceinline__ Stat join(const Stat& a, const Stat& b) {
-  const float m = fmaxf(a.m, b.m);
-  return Stat{m, moved(a, m) + moved(b, m)};
+// n pairs, in order
+__device__ __forceinline__ Stat join(const Stat* p, int n) {
+  float m = p[0].m;
+  for (int k = 1; k < n; ++k) m = fmaxf(m, p[k].m);
+  float s = moved(p[0], m);
+  for (int k = 1; k < n; ++k) s += moved(p[k], m);
+  return Stat{m, s};
+}
+
+// the pairs of a warp's lanes; all lanes hold the same bits afterwards
+__device__ __forceinline__ Stat join_lanes(Stat t) {
+  float m = t.m;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  float s = moved(t, m);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  return Stat{m, s};
 }
 
 // Two fp32 values as one operand: sm_100's packed fp32 arithmetic does both
@@ -263,15 +278,6 @@ __device__ __forceinline__ void cluster_sync() {
           : "memory");
 }
 
-// store one Stat into the same shared variable of CTA `rank` of the cluster
-__device__ __forceinline__ void send(Stat* local, uint32_t rank, const Stat& v) {
-  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(local));
-  uint32_t remote;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(at), "r"(rank));
-  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote), "f"(v.m), "f"(v.s)
-               : "memory");
-}
-
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
@@ -296,7 +302,7 @@ __device__ __forceinline__ void copy_blocks(void* dst, const uint8_t* src, uint3
 __device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
       " selp.u32 %0, 1, 0, p;\n}"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
@@ -311,7 +317,8 @@ __device__ __forceinline__ uint64_t global_ns() {
 }
 
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
-  if (bar_try(bar, parity)) return true;
+  for (int k = 0; k < 64; ++k)
+    if (bar_try(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   for (;;) {
     if (bar_try(bar, parity)) return true;
@@ -361,31 +368,59 @@ __device__ __forceinline__ uint4 own_part(const Row& r, int32_t b, const uint4& 
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// The pairs of a CTA's warps, of the cluster's CTAs, and the barrier that
+// counts the latter's arrival. Two of them in turn: for the row after next a
+// warp writes only after the next row's CTA barrier, and a CTA sends only once
+// every CTA has sent for the next row, so all have read this one.
+struct Exchange {
+  Stat of_warp[kWarps];
+  Stat of_cta[kMaxCluster];
+  uint64_t arrived;
+};
+
+__device__ __forceinline__ void bar_init(uint64_t* bar) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Store v into *to of CTA `rank`, counted by that CTA's barrier. (A cluster
+// barrier would also wait for this CTA's stores to dlogits, of no interest
+// here: 1 us and more per row.)
+__device__ __forceinline__ void send(Stat* to, uint64_t* bar, uint32_t rank, const Stat& v) {
+  uint32_t remote, remote_bar;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(to)), "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(remote_bar)
+               : "r"(smem_u32(bar)), "r"(rank));
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(
+          remote),
+      "r"(__float_as_uint(v.m)), "r"(__float_as_uint(v.s)), "r"(remote_bar)
+      : "memory");
+}
+
 // A lane's statistics joined over the CTA and then the cluster; all threads
-// of all CTAs call it and hold the same bits afterwards.
-__device__ __forceinline__ Stat join_all(Stat t, Stat* of_warp, Stat* of_cta, uint32_t rank,
-                                         uint32_t n_cta) {
+// of all CTAs call it for the same rows and hold the same bits afterwards.
+// `use` counts the calls.
+__device__ __forceinline__ Stat join_all(Stat t, Exchange (&x)[2], uint32_t rank, uint32_t n_cta,
+                                         uint32_t use) {
   const int tid = threadIdx.x, lane = tid & 31;
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    const Stat o = {__shfl_xor_sync(0xffffffffu, t.m, d), __shfl_xor_sync(0xffffffffu, t.s, d)};
-    // the same operands in the same order on both lanes
-    t = (lane & d) ? join(o, t) : join(t, o);
-  }
-  if (lane == 0) of_warp[tid >> 5] = t;
+  Exchange& e = x[use & 1];
+  t = join_lanes(t);
+  if (lane == 0) e.of_warp[tid >> 5] = t;
   __syncthreads();
+  if (n_cta == 1) return join(e.of_warp, kWarps);
   if (tid < static_cast<int>(n_cta)) {
-    Stat c = of_warp[0];
-    for (int k = 1; k < kWarps; ++k) c = join(c, of_warp[k]);
-    if (n_cta == 1) of_cta[0] = c;
-    else send(&of_cta[rank], tid, c);
+    t = join(e.of_warp, kWarps);
+    if (tid == 0)
+      asm volatile(
+          "{\n .reg .b64 st;\n mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n}" ::"r"(
+              smem_u32(&e.arrived)),
+          "r"(n_cta * static_cast<uint32_t>(sizeof(Stat)))
+          : "memory");
+    send(&e.of_cta[rank], &e.arrived, tid, t);
   }
-  __syncwarp();
-  if (n_cta == 1) __syncthreads();
-  else cluster_sync();
-  t = of_cta[0];
-  for (uint32_t k = 1; k < n_cta; ++k) t = join(t, of_cta[k]);
-  return t;
+  if (!bar_wait(&e.arrived, (use >> 1) & 1)) return Stat{t.m, __uint_as_float(0x7FC00000u)};
+  return join(e.of_cta, static_cast<int>(n_cta));
 }
 
 // The row's logits as a single stream: statistics only.
@@ -393,12 +428,17 @@ template <int kType>
 __global__ void __launch_bounds__(kThreads) logp_kernel(const Args a) {
   pdl_begin();
   using B = Block<kType>;
-  __shared__ Stat of_warp[kWarps];
-  __shared__ Stat of_cta[2][kMaxCluster];
+  __shared__ Exchange exchange[2];
   const int tid = threadIdx.x;
   const uint32_t rank = cluster_rank(), n_cta = cluster_size();
-  int parity = 0;
-  if (n_cta > 1) cluster_sync();  // every CTA of the cluster runs before any sends to it
+  uint32_t use = 0;
+  if (tid == 0) {
+    bar_init(&exchange[0].arrived);
+    bar_init(&exchange[1].arrived);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncwarp();
+  if (n_cta > 1) cluster_sync();  // every CTA of the cluster is ready before any sends to it
   for (int64_t row = blockIdx.x / n_cta; row < a.rows; row += gridDim.x / n_cta) {
     const Row r = row_of<B::kBytes, false>(a, row);
     float lp = 0.f;
@@ -420,8 +460,7 @@ __global__ void __launch_bounds__(kThreads) logp_kernel(const Args a) {
         for (int k = 0; k < kBatch; ++k) v[k] = own_part<kType>(r, b + k * kThreads, v[k]);
         add_blocks<kType>(t, v);
       }
-      t = join_all(t, of_warp, of_cta[parity], rank, n_cta);
-      parity ^= 1;
+      t = join_all(t, exchange, rank, n_cta, use++);
       lp = log_share(picked, t);
     }
     if (rank == 0 && tid == 0) a.logp[row] = lp;
@@ -433,27 +472,29 @@ __global__ void __launch_bounds__(kThreads, 3) policy_kernel(const Args a, const
   pdl_begin();
   using B = Block<kType>;
   extern __shared__ __align__(16) uint8_t stage[];
-  __shared__ Stat of_warp[kWarps];
-  __shared__ Stat of_cta[2][kMaxCluster];
+  __shared__ Exchange exchange[2];
   __shared__ uint64_t landed[kWarps][kParts];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank(), n_cta = cluster_size();
   const int64_t step = gridDim.x / n_cta;
   const float scale = a.scaler ? a.scaler->scale : 1.f;
-  const int64_t n_part = static_cast<int64_t>(n_cta) * kWarps * kParts;
-  const int64_t part0 = (static_cast<int64_t>(rank) * kWarps + warp) * kParts;
+  // the row is cut into n_cta kWarps kParts = 2^cut parts of equal size (+-1 block)
+  const int cut = __ffs(n_cta * kWarps * kParts) - 1;
+  const int32_t part0 = (rank * kWarps + warp) * kParts;
   uint8_t* mine = stage + static_cast<int64_t>(warp) * kParts * part_cap * 16;
   if (lane == 0) {
-    for (int p = 0; p < kParts; ++p)
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&landed[warp][p]))
-                   : "memory");
+    for (int p = 0; p < kParts; ++p) bar_init(&landed[warp][p]);
+    if (warp == 0) {
+      bar_init(&exchange[0].arrived);
+      bar_init(&exchange[1].arrived);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncwarp();
-  if (n_cta > 1) cluster_sync();  // every CTA of the cluster runs before any sends to it
+  if (n_cta > 1) cluster_sync();  // every CTA of the cluster is ready before any sends to it
   else __syncthreads();
   const auto block_of = [&](const Row& r, int p) {
-    return static_cast<int32_t>(r.n_blk * (part0 + p) / n_part);
+    return (r.n_blk * (part0 + p)) >> cut;
   };
   const auto fetch = [&](const Row& r, int p) {  // one lane
     const int32_t b0 = block_of(r, p), n = block_of(r, p + 1) - b0;
@@ -461,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 3) policy_kernel(const Args a, const
       copy_blocks(mine + static_cast<int64_t>(p) * part_cap * 16,
                   r.base + static_cast<int64_t>(b0) * 16, n * 16, &landed[warp][p]);
   };
-  int parity = 0;
+  uint32_t use = 0;
   uint32_t phase = 0;
   int64_t row = blockIdx.x / n_cta;
   Row r = {};
@@ -502,8 +543,7 @@ __global__ void __launch_bounds__(kThreads, 3) policy_kernel(const Args a, const
         }
       }
       phase ^= 1;
-      t = join_all(t, of_warp, of_cta[parity], rank, n_cta);
-      parity ^= 1;
+      t = join_all(t, exchange, rank, n_cta, use++);
       lp = log_share(picked, t);
       const float ratio = expf(lp - old);
       const float plain = ratio * adv, held = fminf(fmaxf(ratio, a.lo), a.hi) * adv;
