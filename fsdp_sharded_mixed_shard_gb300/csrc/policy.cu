@@ -86,15 +86,6 @@ __device__ __forceinline__ float moved(const Stat& a, float m) {
   return a.s == 0.f ? 0.f : a.s * exp2_fast(base_of(a.m).mc - base_of(m).mc);
 }
 
-// n pairs, in order
-__device__ __forceinline__ Stat join(const Stat* p, int n) {
-  float m = p[0].m;
-  for (int k = 1; k < n; ++k) m = fmaxf(m, p[k].m);
-  float s = moved(p[0], m);
-  for (int k = 1; k < n; ++k) s += moved(p[k], m);
-  return Stat{m, s};
-}
-
 // the pairs of a warp's lanes; all lanes hold the same bits afterwards
 __device__ __forceinline__ Stat join_lanes(Stat t) {
   float m = t.m;
@@ -369,9 +360,9 @@ __device__ __forceinline__ uint4 own_part(const Row& r, int32_t b, const uint4& 
 }
 
 // The pairs of a CTA's warps, of the cluster's CTAs, and the barrier that
-// counts the latter's arrival. Two of them in turn: for the row after next a
-// warp writes only after the next row's CTA barrier, and a CTA sends only once
-// every CTA has sent for the next row, so all have read this one.
+// counts the latter's arrival. Two of them in turn: a CTA sends for the row
+// after next only once every CTA has sent for the next row, hence read this
+// one.
 struct Exchange {
   Stat of_warp[kWarps];
   Stat of_cta[kMaxCluster];
@@ -398,29 +389,27 @@ __device__ __forceinline__ void send(Stat* to, uint64_t* bar, uint32_t rank, con
       : "memory");
 }
 
-// A lane's statistics joined over the CTA and then the cluster; all threads
-// of all CTAs call it for the same rows and hold the same bits afterwards.
-// `use` counts the calls.
-__device__ __forceinline__ Stat join_all(Stat t, Exchange (&x)[2], uint32_t rank, uint32_t n_cta,
+// The statistics of a row from its warps' pairs, by warp 0 of every CTA of
+// the cluster; its lanes hold the same bits afterwards. `use` counts the calls.
+__device__ __forceinline__ Stat join_all(Exchange (&x)[2], uint32_t rank, uint32_t n_cta,
                                          uint32_t use) {
-  const int tid = threadIdx.x, lane = tid & 31;
+  const uint32_t lane = threadIdx.x & 31;
   Exchange& e = x[use & 1];
-  t = join_lanes(t);
-  if (lane == 0) e.of_warp[tid >> 5] = t;
-  __syncthreads();
-  if (n_cta == 1) return join(e.of_warp, kWarps);
-  if (tid < static_cast<int>(n_cta)) {
-    t = join(e.of_warp, kWarps);
-    if (tid == 0)
+  const Stat none = {-INFINITY, 0.f};
+  const Stat t = join_lanes(lane < kWarps ? e.of_warp[lane] : none);
+  if (n_cta == 1) return t;
+  if (lane < n_cta) {
+    if (lane == 0)
       asm volatile(
           "{\n .reg .b64 st;\n mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n}" ::"r"(
               smem_u32(&e.arrived)),
           "r"(n_cta * static_cast<uint32_t>(sizeof(Stat)))
           : "memory");
-    send(&e.of_cta[rank], &e.arrived, tid, t);
+    send(&e.of_cta[rank], &e.arrived, lane, t);
   }
-  if (!bar_wait(&e.arrived, (use >> 1) & 1)) return Stat{t.m, __uint_as_float(0x7FC00000u)};
-  return join(e.of_cta, static_cast<int>(n_cta));
+  const bool ok = bar_wait(&e.arrived, (use >> 1) & 1);
+  return join_lanes(!ok ? Stat{0.f, __uint_as_float(0x7FC00000u)}
+                        : lane < n_cta ? e.of_cta[lane] : none);
 }
 
 // The row's logits as a single stream: statistics only.
@@ -460,12 +449,22 @@ __global__ void __launch_bounds__(kThreads) logp_kernel(const Args a) {
         for (int k = 0; k < kBatch; ++k) v[k] = own_part<kType>(r, b + k * kThreads, v[k]);
         add_blocks<kType>(t, v);
       }
-      t = join_all(t, exchange, rank, n_cta, use++);
-      lp = log_share(picked, t);
+      t = join_lanes(t);
+      if ((tid & 31) == 0) exchange[use & 1].of_warp[tid >> 5] = t;
+      __syncthreads();
+      if (tid < 32) lp = log_share(picked, join_all(exchange, rank, n_cta, use));
+      ++use;
     }
     if (rank == 0 && tid == 0) a.logp[row] = lp;
   }
 }
+
+// What warp 0 tells the others between a row's sums and its gradient.
+struct Turn {
+  Row next;
+  Base base;
+  float slope, inv;  // dloss/dlogp with its factors, and -slope / sum
+};
 
 template <int kType>
 __global__ void __launch_bounds__(kThreads, 3) policy_kernel(const Args a, const int32_t part_cap) {
@@ -474,10 +473,13 @@ __global__ void __launch_bounds__(kThreads, 3) policy_kernel(const Args a, const
   extern __shared__ __align__(16) uint8_t stage[];
   __shared__ Exchange exchange[2];
   __shared__ uint64_t landed[kWarps][kParts];
+  __shared__ Turn turn;
+  __shared__ float taken;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank(), n_cta = cluster_size();
   const int64_t step = gridDim.x / n_cta;
   const float scale = a.scaler ? a.scaler->scale : 1.f;
+  const bool kl = a.ref_logp && a.beta != 0.f;
   // the row is cut into n_cta kWarps kParts = 2^cut parts of equal size (+-1 block)
   const int cut = __ffs(n_cta * kWarps * kParts) - 1;
   const int32_t part0 = (rank * kWarps + warp) * kParts;
@@ -496,38 +498,44 @@ __global__ void __launch_bounds__(kThreads, 3) policy_kernel(const Args a, const
   const auto block_of = [&](const Row& r, int p) {
     return (r.n_blk * (part0 + p)) >> cut;
   };
+  const auto part_at = [&](int p) {
+    return reinterpret_cast<uint4*>(mine + static_cast<int64_t>(p) * part_cap * 16);
+  };
   const auto fetch = [&](const Row& r, int p) {  // one lane
     const int32_t b0 = block_of(r, p), n = block_of(r, p + 1) - b0;
     if (ZCHECK(n <= part_cap && b0 + n <= r.n_blk, kSiteStageBytes, n))
-      copy_blocks(mine + static_cast<int64_t>(p) * part_cap * 16,
-                  r.base + static_cast<int64_t>(b0) * 16, n * 16, &landed[warp][p]);
+      copy_blocks(part_at(p), r.base + static_cast<int64_t>(b0) * 16, n * 16, &landed[warp][p]);
   };
-  uint32_t use = 0;
-  uint32_t phase = 0;
+  uint32_t use = 0, phase = 0;
   int64_t row = blockIdx.x / n_cta;
-  Row r = {};
-  if (row < a.rows) r = row_of<B::kBytes, true>(a, row);
+  Row r = row_of<B::kBytes, true>(a, row);
   bool fetched = false;  // this row's parts are on their way
   while (row < a.rows) {
     const int64_t next_row = row + step;
+    const bool on = r.on();
+    // what warp 0 needs after the sums, asked for before them
+    float picked = 0.f, old = 0.f, adv = 0.f, ref = 0.f;
     Row next = {};
     next.action = -1;
-    if (next_row < a.rows) next = row_of<B::kBytes, true>(a, next_row);
-    Stat t = {-INFINITY, 0.f};
-    float slope = 0.f, lp = 0.f, loss = 0.f;
-    const bool on = r.on();
+    if (warp == 0) {
+      if (on) {
+        picked = B::one(r.base + r.head + r.action * B::kBytes);
+        old = a.old_logp[row];
+        adv = a.advantage[row];
+        if (kl) ref = a.ref_logp[row];
+      }
+      if (next_row < a.rows) next = row_of<B::kBytes, true>(a, next_row);
+    }
     if (on) {
       if (!fetched && lane == 0) {
 #pragma unroll
         for (int p = 0; p < kParts; ++p) fetch(r, p);
       }
-      const float picked = B::one(r.base + r.head + r.action * B::kBytes);
-      const float old = a.old_logp[row], adv = a.advantage[row];
-      const float ref = a.ref_logp && a.beta != 0.f ? a.ref_logp[row] : 0.f;
+      Stat t = {-INFINITY, 0.f};
 #pragma unroll 1
       for (int p = 0; p < kParts; ++p) {
         const int32_t b0 = block_of(r, p), n = block_of(r, p + 1) - b0;
-        const uint4* part = reinterpret_cast<const uint4*>(mine + static_cast<int64_t>(p) * part_cap * 16);
+        const uint4* part = part_at(p);
         if (!bar_wait(&landed[warp][p], phase)) t.s = __uint_as_float(0x7FC00000u);
         const bool edge = b0 == 0 || b0 + n == r.n_blk;
         for (int32_t k = lane; k < n; k += 32 * kBatch) {
@@ -543,38 +551,60 @@ __global__ void __launch_bounds__(kThreads, 3) policy_kernel(const Args a, const
         }
       }
       phase ^= 1;
-      t = join_all(t, exchange, rank, n_cta, use++);
-      lp = log_share(picked, t);
-      const float ratio = expf(lp - old);
-      const float plain = ratio * adv, held = fminf(fmaxf(ratio, a.lo), a.hi) * adv;
-      const bool cut = held < plain;
-      loss = -(cut ? held : plain);
-      slope = cut ? 0.f : -plain;
-      if (a.ref_logp && a.beta != 0.f) {
-        const float d = ref - lp, e = expm1f(d);
-        loss = __fmaf_rn(a.beta, e - d, loss);
-        slope = __fmaf_rn(a.beta, -e, slope);
+      t = join_lanes(t);
+      if (lane == 0) exchange[use & 1].of_warp[warp] = t;
+    }
+    // stored, so read: once this CTA has sent its sums, another may write the
+    // gradient over this logit (dlogits in the logits' place)
+    if (tid == 0) taken = picked;
+    __syncthreads();
+    if (warp == 0) {
+      Turn n = {};
+      n.next = next;
+      float lp = 0.f, loss = 0.f;
+      if (on) {
+        const Stat t = join_all(exchange, rank, n_cta, use);
+        lp = log_share(taken, t);
+        const float ratio = expf(lp - old);
+        const float plain = ratio * adv, held = fminf(fmaxf(ratio, a.lo), a.hi) * adv;
+        const bool cut = held < plain;
+        loss = -(cut ? held : plain);
+        float slope = cut ? 0.f : -plain;
+        if (kl) {
+          const float d = ref - lp, e = expm1f(d);
+          loss = __fmaf_rn(a.beta, e - d, loss);
+          slope = __fmaf_rn(a.beta, -e, slope);
+        }
+        slope *= scale * r.weight;
+        n.base = base_of(t.m);
+        n.slope = slope;
+        n.inv = -slope / t.s;
       }
-      slope *= scale * r.weight;
+      if (lane == 0) {
+        turn = n;
+        if (rank == 0) {
+          a.logp[row] = lp;
+          a.loss[row] = loss;
+        }
+      }
     }
-    if (rank == 0 && tid == 0) {
-      a.logp[row] = lp;
-      a.loss[row] = loss;
-    }
+    if (on) ++use;
+    __syncthreads();
+    next = turn.next;
     // the next row's parts follow this row's gradient out of the same place
     const bool follow = on && next.on();
     uint8_t* dx = a.dlogits ? a.dlogits + row * a.ld * B::kBytes - r.head : nullptr;
     // whole blocks when dlogits lies on the 16-byte grid as the logits do
     const bool same = (reinterpret_cast<uintptr_t>(dx) & 15) == 0;
-    const Base base = base_of(t.m);
+    const Base base = turn.base;
     const Pair c = pair(base.c, base.c), minus_mc = pair(-base.mc, -base.mc);
-    const float inv = -slope / t.s;
-    const Pair by = pair(inv, inv);
+    const Pair by = pair(turn.inv, turn.inv);
+    const float slope = turn.slope;
     const int32_t action_at = r.head + r.action * B::kBytes;
 #pragma unroll 1
     for (int p = 0; p < kParts; ++p) {
       const int32_t b0 = block_of(r, p), n = dx ? block_of(r, p + 1) - b0 : 0;
-      const uint4* part = reinterpret_cast<const uint4*>(mine + static_cast<int64_t>(p) * part_cap * 16);
+      const uint4* part = part_at(p);
       const bool plain = same && b0 != 0 && b0 + n != r.n_blk;
       const int32_t special = (action_at >> 4) - b0;  // the block with the action, if in this part
       uint4* to = reinterpret_cast<uint4*>(dx + static_cast<int64_t>(b0) * 16);
