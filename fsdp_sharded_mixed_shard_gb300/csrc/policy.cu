@@ -37,7 +37,7 @@ using namespace zt;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kParts = 4;      // parts of a row per warp
+constexpr int kParts = 2;      // parts of a row per warp
 constexpr int kBatch = 4;      // blocks per lane and step
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 3) policy_kernel(const Args a, const
   __shared__ float taken;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank(), n_cta = cluster_size();
-  const int64_t step = gridDim.x / n_cta;
+  const int64_t n_clusters = gridDim.x / n_cta;
   const float scale = a.scaler ? a.scaler->scale : 1.f;
   const bool kl = a.ref_logp && a.beta != 0.f;
   // the row is cut into n_cta kWarps kParts = 2^cut parts of equal size (+-1 block)
@@ -508,10 +508,11 @@ __global__ void __launch_bounds__(kThreads, 3) policy_kernel(const Args a, const
   };
   uint32_t use = 0, phase = 0;
   int64_t row = blockIdx.x / n_cta;
-  Row r = row_of<B::kBytes, true>(a, row);
+  Row r = {};
+  if (row < a.rows) r = row_of<B::kBytes, true>(a, row);
   bool fetched = false;  // this row's parts are on their way
   while (row < a.rows) {
-    const int64_t next_row = row + step;
+    const int64_t next_row = row + n_clusters;
     const bool on = r.on();
     // what warp 0 needs after the sums, asked for before them
     float picked = 0.f, old = 0.f, adv = 0.f, ref = 0.f;
@@ -538,14 +539,13 @@ __global__ void __launch_bounds__(kThreads, 3) policy_kernel(const Args a, const
         const uint4* part = part_at(p);
         if (!bar_wait(&landed[warp][p], phase)) t.s = __uint_as_float(0x7FC00000u);
         const bool edge = b0 == 0 || b0 + n == r.n_blk;
-        for (int32_t k = lane; k < n; k += 32 * kBatch) {
+        for (int32_t k0 = 0; k0 < n; k0 += 32 * kBatch) {
           uint4 v[kBatch];
 #pragma unroll
-          for (int j = 0; j < kBatch; ++j)
-            v[j] = k + 32 * j < n ? part[k + 32 * j] : no_block<kType>();
-          if (edge) {
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) v[j] = own_part<kType>(r, b0 + k + 32 * j, v[j]);
+          for (int j = 0; j < kBatch; ++j) {
+            const int32_t k = k0 + 32 * j + lane;
+            v[j] = k < n ? part[k] : no_block<kType>();
+            if (edge) v[j] = own_part<kType>(r, b0 + k, v[j]);
           }
           add_blocks<kType>(t, v);
         }
@@ -608,17 +608,27 @@ __global__ void __launch_bounds__(kThreads, 3) policy_kernel(const Args a, const
       const bool plain = same && b0 != 0 && b0 + n != r.n_blk;
       const int32_t special = (action_at >> 4) - b0;  // the block with the action, if in this part
       uint4* to = reinterpret_cast<uint4*>(dx + static_cast<int64_t>(b0) * 16);
+      // loops of the warp, not of the lane: lanes past the end sit a turn out
       if (plain && !on) {
         for (int32_t k = lane; k < n; k += 32) __stcs(to + k, make_uint4(0, 0, 0, 0));
       } else if (plain && (special < 0 || special >= n)) {
-#pragma unroll 4
-        for (int32_t k = lane; k < n; k += 32) {
-          Pair e[B::kElems / 2];
-          exp_block<kType>(part[k], c, minus_mc, e);
-          float f[B::kElems];
+        for (int32_t k0 = 0; k0 < n; k0 += 32 * kBatch) {
+          uint4 v[kBatch];
 #pragma unroll
-          for (int j = 0; j < B::kElems / 2; ++j) unpair(e[j] * by, f[2 * j], f[2 * j + 1]);
-          __stcs(to + k, B::put(f));
+          for (int j = 0; j < kBatch; ++j) {
+            const int32_t k = k0 + 32 * j + lane;
+            if (k < n) v[j] = part[k];
+          }
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            Pair e[B::kElems / 2];
+            exp_block<kType>(v[j], c, minus_mc, e);
+            float f[B::kElems];
+#pragma unroll
+            for (int i = 0; i < B::kElems / 2; ++i) unpair(e[i] * by, f[2 * i], f[2 * i + 1]);
+            const int32_t k = k0 + 32 * j + lane;
+            if (k < n) __stcs(to + k, B::put(f));
+          }
         }
       } else {
 #pragma unroll 1
