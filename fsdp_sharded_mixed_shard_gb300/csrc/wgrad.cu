@@ -3,29 +3,34 @@
  * checkpoint (zero_train.h): dw[i, j] = sum over t of x^[t, i] dy[t, j].
  *
  * A matrix product whose reduction runs over the tokens, the slow axis of
- * both operands, on the 5th-generation tensor cores. A CTA forms a 128 x 256
- * tile of dw in tensor memory (fp32), 64 tokens per step, through a ring of
- * shared-memory stages:
- *   copy warp     brings dy's 64 x 256 tile by TMA (128-byte swizzle, rows of
- *                 64 columns: the tensor core's layout for an operand whose
- *                 slow axis is the reduction);
- *   8 value warps read the checkpoint's 64 x 128 tile into registers two steps
- *                 ahead (a thread one block of 32 values and its scale), turn
- *                 it into 16-bit values and store them in the same layout.
- *                 q * 2^k is exact in the 16-bit type, so the operand is the
- *                 checkpoint itself, without a rounding;
- *   product warp  one thread issues four 128 x 256 x 16 products per stage.
- * The value warps then read the sums from tensor memory, round them once and
- * store them.
+ * both operands, on the 5th-generation tensor cores. A pair of CTAs (one
+ * tcgen05.mma over two SMs) forms a 256 x BN tile of dw, BN up to 256, in
+ * tensor memory (fp32), 64 tokens per step: each CTA holds 128 rows of the
+ * tile, 128 of the checkpoint's columns and half of dy's, so an SM takes in
+ * 24 KB per step of 512 tensor-core cycles (one CTA per tile would take in
+ * 40 KB, more than L2 delivers). Per CTA, through a ring of stages:
+ *   copy warp       brings its half of dy's 64 x BN tile by TMA (128-byte
+ *                   swizzle, rows of 64 columns: the tensor core's layout for
+ *                   an operand whose slow axis is the reduction);
+ *   16 value warps  in two groups, each every other step: read the
+ *                   checkpoint's 64 x 128 tile into registers ahead (a thread
+ *                   one block of 32 values and its scale), turn it into
+ *                   16-bit values and store them in the same layout. q * 2^k
+ *                   is exact in the 16-bit type, so the operand is the
+ *                   checkpoint itself, without a rounding;
+ *   product warp    (first CTA of the pair) one thread issues four
+ *                   256 x BN x 16 products per stage;
+ *   4 output warps  read a finished tile from one half of tensor memory, round
+ *                   once and store, while the next tile's sums form in the
+ *                   other half.
  *
- * Few tiles and many tokens: a cluster of 2, 4 or 8 CTAs shares a tile, each
- * a part of the tokens; the sums meet in shared memory and every CTA adds its
- * share of the rows over the cluster in rank order. The split depends on the
- * sizes alone, so results do not change from call to call.
+ * Few tiles and many tokens: a cluster of 2 or 4 pairs shares a tile, each
+ * pair a part of the tokens; the sums meet in shared memory and every CTA adds
+ * its share of the rows over the cluster in rank order. Split and tile width
+ * depend on the sizes alone, so results do not change from call to call.
  *
- * Every wait is bounded (2 s); one that expires ends the CTA's work, its
- * copies in flight are awaited (bounded too), the tile becomes NaN and the
- * scaler's error word is raised.
+ * Every wait is bounded (2 s); one that expires ends the work of its CTA, the
+ * tiles it had left become NaN and the scaler's error word is raised.
  */
 #include <cuda.h>
 
@@ -37,21 +42,22 @@ namespace zw {
 
 using namespace zt;
 
-constexpr int kValueWarps = 8;
-constexpr int kValueThreads = 32 * kValueWarps;
-constexpr int kCopyWarp = kValueWarps, kProductWarp = kValueWarps + 1;
-constexpr int kThreads = 32 * (kValueWarps + 2);
-constexpr int kM = 128, kN = 256, kK = 64;     // tile of dw, tokens per stage
-constexpr int kStages = 4;
+constexpr int kGroups = 2, kGroupWarps = 8;
+constexpr int kGroupThreads = 32 * kGroupWarps;
+constexpr int kCopyWarp = kGroups * kGroupWarps, kProductWarp = kCopyWarp + 1;
+constexpr int kOutWarp0 = kProductWarp + 1, kOutWarps = 4;
+constexpr int kThreads = 32 * (kOutWarp0 + kOutWarps);
+constexpr int kM = 128, kN = 256, kK = 64;     // rows per CTA, columns at most, tokens per stage
+constexpr int kStages = 6;
 constexpr int kChunk = kK * 128;               // 64 tokens x 64 columns of 16 bits
-constexpr int kBytesA = kM / 64 * kChunk, kBytesB = kN / 64 * kChunk;
+constexpr int kBytesA = kM / 64 * kChunk, kBytesB = kN / 2 / 64 * kChunk;
 constexpr int kStageBytes = kBytesA + kBytesB;
 constexpr int kJoinPitch = kN + 4;             // fp32 row of a tile in shared memory
 constexpr int kSmem = kStages * kStageBytes + 1024;
-constexpr int kMaxSplit = 8;
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr int kMaxSplit = 4;
+constexpr uint64_t kWaitLimitNs = 2000000000ull, kDrainNs = 1000000ull;
 static_assert(kM * kJoinPitch * 4 <= kStages * kStageBytes, "the tile fits the stages");
-static_assert(kM == ZERO_CKPT_PAD, "a checkpoint row is whole tiles");
+static_assert(kM == ZERO_CKPT_PAD, "a checkpoint row is whole CTA tiles");
 
 struct Args {
   const int8_t* q;
@@ -60,7 +66,7 @@ struct Args {
   uint16_t* dw;
   zero_scaler* scaler;
   int64_t rows, cols, pitch, n, ld;
-  int32_t split, vec_out;
+  int32_t split, vec_out, bn, m_tiles, tiles;
 };
 
 // ------------------------------------------------------------- primitives ----
@@ -74,18 +80,27 @@ __device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count) {
                : "memory");
 }
 
-__device__ __forceinline__ void bar_arrive(uint64_t* bar) {
-  asm volatile("{\n .reg .b64 st;\n mbarrier.arrive.shared::cta.b64 st, [%0];\n}" ::"r"(
-                   smem_u32(bar))
-               : "memory");
-}
-
 __device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) {
   asm volatile(
       "{\n .reg .b64 st;\n mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n}" ::"r"(
           smem_u32(bar)),
       "r"(bytes)
       : "memory");
+}
+
+// the same variable in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(p)), "r"(rank));
+  return remote;
+}
+
+// CTA-scope release: what it publishes is this CTA's own shared or tensor
+// memory, read by this SM's tensor core after the proxy fence that precedes it
+// (a cluster-scope release would wait for this thread's loads ahead as well).
+__device__ __forceinline__ void bar_arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
 }
 
 __device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity) {
@@ -120,12 +135,14 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatil
   }
 }
 
+// A box of dy into this CTA; its bytes are counted by the barrier at
+// `cluster_bar`, in this CTA or the other of the pair.
 __device__ __forceinline__ void copy_box(void* dst, const CUtensorMap* map, int32_t x, int32_t y,
-                                         uint64_t* bar) {
+                                         uint32_t cluster_bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+      ".cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(cluster_bar)
       : "memory");
 }
 
@@ -138,26 +155,29 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr) {
          1ull << 46 | 2ull << 61;
 }
 
-// fp32 sums; both operands of the 16-bit type, slow axis reduced; 128 x 256
+// fp32 sums; both operands of the 16-bit type, slow axis reduced; 256 x bn
 template <bool kBf16>
-__host__ __device__ constexpr uint32_t product_desc() {
+__device__ __forceinline__ uint32_t product_desc(int bn) {
   return 1u << 4 | (kBf16 ? 1u : 0u) << 7 | (kBf16 ? 1u : 0u) << 10 | 1u << 15 | 1u << 16 |
-         static_cast<uint32_t>(kN >> 3) << 17 | static_cast<uint32_t>(kM >> 4) << 24;
+         static_cast<uint32_t>(bn >> 3) << 17 | static_cast<uint32_t>(2 * kM >> 4) << 24;
 }
 
 __device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t desc,
                                         bool add) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
       "l"(a), "l"(b), "r"(desc), "r"(add ? 1u : 0u)
       : "memory");
 }
 
-__device__ __forceinline__ void commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_u32(bar))
-               : "memory");
+// arrive at `bar` of both CTAs of the pair once the products issued so far are done
+__device__ __forceinline__ void commit(uint64_t* bar, uint16_t pair_mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(smem_u32(bar)),
+      "h"(pair_mask)
+      : "memory");
 }
 
 // 32 lanes x 32 columns of tensor memory
@@ -180,6 +200,7 @@ __device__ __forceinline__ void read_sums(uint32_t addr, float (&f)[32]) {
 }
 
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile(
       "barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
           : "memory");
@@ -229,7 +250,7 @@ __device__ __forceinline__ Block load_block(const Args& a, int64_t t, int64_t en
   Block b;
   b.lo = b.hi = make_uint4(0, 0, 0, 0);
   b.scale = 127;
-  if (t < end && ZCHECK(t < a.rows && i + 32 <= a.pitch, kSiteLoad, t)) {
+  if (t < end && i < a.pitch && ZCHECK(t < a.rows && i + 32 <= a.pitch, kSiteLoad, t)) {
     const uint4* p = reinterpret_cast<const uint4*>(a.q + t * a.pitch + i);
     b.lo = p[0];
     b.hi = p[1];
@@ -261,11 +282,13 @@ __device__ __forceinline__ void store_block(uint8_t* stage_a, const Block& b, in
   }
 }
 
-// dy's tile without TMA: rows that do not start on 16-byte boundaries
+// This CTA's half of dy's tile without TMA: rows that do not start on 16-byte
+// boundaries.
 __device__ __forceinline__ void load_dy(const Args& a, uint8_t* stage_b, int64_t t0, int64_t end,
                                         int64_t j0, int tid) {
-  for (int p = tid; p < kK * (kN / 8); p += kValueThreads) {
-    const int r = p / (kN / 8), c = p % (kN / 8);  // token, piece of eight columns
+  const int pieces = a.bn / 16;  // pieces of eight columns per token
+  for (int p = tid; p < kK * pieces; p += kGroupThreads) {
+    const int r = p / pieces, c = p % pieces;
     const int64_t t = t0 + r, j = j0 + c * 8;
     uint32_t h[8];
 #pragma unroll
@@ -298,165 +321,224 @@ __device__ __forceinline__ void store_sums(const Args& a, int64_t i, int64_t j,
 
 // ------------------------------------------------------------------ kernel ----
 
+// A step of this pair's work: token block `step` of tile `tile`.
+struct Cursor {
+  int32_t tile, step;
+  __device__ __forceinline__ void advance(int by, int steps, int tile_stride) {
+    step += by;
+    while (step >= steps) {
+      step -= steps;
+      tile += tile_stride;
+    }
+  }
+};
+
+struct Ring {  // stage and the parity of its current use
+  int32_t stage = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void advance(int by) {
+    stage += by;
+    if (stage >= kStages) {
+      stage -= kStages;
+      parity ^= 1;
+    }
+  }
+};
+
 template <bool kBf16, bool kTma>
 __global__ void __launch_bounds__(kThreads, 1)
     wgrad_kernel(const __grid_constant__ CUtensorMap map, const Args a) {
   pdl_begin();
   extern __shared__ uint8_t raw[];
   uint8_t* stages = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  __shared__ uint64_t full_a[kStages], full_b[kStages], empty[kStages], done;
+  // full: in the pair's first CTA, counted by both; empty and done: in each
+  __shared__ uint64_t full_a[kStages], full_b[kStages], empty[kStages], done[2], free_sums[2];
   __shared__ uint32_t tmem_base;
   __shared__ int failed;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = static_cast<int>(blockIdx.x) % a.split;
-  const int64_t tile = blockIdx.x / a.split;
-  const int64_t m_tiles = a.pitch / kM;
-  const int64_t i0 = tile % m_tiles * kM, j0 = tile / m_tiles * kN;
-  // this CTA's tokens: whole steps
-  const int64_t steps = (a.rows + kK - 1) / kK;
-  const int64_t s0 = steps * rank / a.split, s1 = steps * (rank + 1) / a.split;
-  const int n_it = static_cast<int>(s1 - s0);
-  const int64_t t_begin = s0 * kK;
+  const int n_cta = 2 * a.split;
+  const int rank = static_cast<int>(blockIdx.x) % n_cta;
+  const int half = rank & 1, part = rank >> 1, leader = rank & ~1;
+  const int tile0 = static_cast<int>(blockIdx.x) / n_cta;
+  const int tile_stride = static_cast<int>(gridDim.x) / n_cta;
+  const int my_tiles = tile0 < a.tiles ? (a.tiles - tile0 + tile_stride - 1) / tile_stride : 0;
+  // this pair's tokens: whole steps
+  const int64_t all_steps = (a.rows + kK - 1) / kK;
+  const int64_t s0 = all_steps * part / a.split, s1 = all_steps * (part + 1) / a.split;
+  const int steps = static_cast<int>(s1 - s0);
+  const int64_t total = static_cast<int64_t>(steps) * my_tiles;
+  const int64_t t_begin = s0 * kK, t_end = s1 * kK < a.rows ? s1 * kK : a.rows;
+  const auto row_of = [&](int tile) {  // first row of dw of this CTA's part of the tile
+    return static_cast<int64_t>(tile % a.m_tiles) * (2 * kM) + half * kM;
+  };
+  const auto column_of = [&](int tile) { return static_cast<int64_t>(tile / a.m_tiles) * a.bn; };
 
   if (warp == kProductWarp) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&tmem_base)),
-                 "n"(kN)
+                 "n"(2 * kN)
                  : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      bar_init(&full_a[s], kValueWarps);
+      bar_init(&full_a[s], 2 * kGroupWarps);
       bar_init(&full_b[s], 1);
       bar_init(&empty[s], 1);
     }
-    bar_init(&done, 1);
+    for (int k = 0; k < 2; ++k) {
+      bar_init(&done[k], 1);
+      bar_init(&free_sums[k], 2 * kOutWarps);
+    }
     failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
+  cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_base;
 
-  if (warp == kCopyWarp) {
-    if (kTma && lane == 0) {
-      int it = 0;
-      for (; it < n_it; ++it) {
-        const int s = it % kStages;
-        if (it >= kStages && !bar_wait(&empty[s], (it / kStages - 1) & 1, &failed)) break;
-        uint8_t* b = stages + s * kStageBytes + kBytesA;
-        bar_expect(&full_b[s], kBytesB);
+  if (warp < kCopyWarp) {
+    // value warps: thread -> token r of a step, block blk of the CTA's 128 columns
+    const int group = warp / kGroupWarps, r = (tid % kGroupThreads) >> 2, blk = tid & 3;
+    Cursor ahead = {tile0, 0}, now = {tile0, 0};
+    Ring ring;
+    ring.advance(group);
+    if (steps > 0) {
+      ahead.advance(group, steps, tile_stride);
+      now = ahead;
+    }
+    const auto load = [&](int64_t it) {
+      const Block b = load_block(
+          a, it < total ? t_begin + static_cast<int64_t>(ahead.step) * kK + r : t_end, t_end,
+          row_of(ahead.tile) + blk * 32);
+      ahead.advance(kGroups, steps, tile_stride);
+      return b;
+    };
+    Block next[2];
+    if (total > 0) {
+      next[0] = load(group);
+      next[1] = load(group + kGroups);
+    }
+    bool ok = true;
+    for (int64_t it = group; it < total && ok; it += 2 * kGroups) {
 #pragma unroll
-        for (int c = 0; c < kN / 64; ++c)
-          copy_box(b + c * kChunk, &map, static_cast<int32_t>(j0 + c * 64),
-                   static_cast<int32_t>(t_begin + static_cast<int64_t>(it) * kK), &full_b[s]);
+      for (int k = 0; k < 2; ++k) {
+        const int64_t at = it + k * kGroups;
+        if (at >= total || !ok) break;
+        ok = at < kStages || bar_wait(&empty[ring.stage], ring.parity ^ 1, &failed);
+        if (!ok) break;
+        uint8_t* stage = stages + ring.stage * kStageBytes;
+        store_block<kBf16>(stage, next[k], r, blk);
+        next[k] = load(at + 2 * kGroups);
+        if constexpr (!kTma) {
+          load_dy(a, stage + kBytesA, t_begin + static_cast<int64_t>(now.step) * kK, t_end,
+                  column_of(now.tile) + half * (a.bn / 2), tid % kGroupThreads);
+          now.advance(kGroups, steps, tile_stride);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) bar_arrive_at(in_cta(&full_a[ring.stage], leader));
+        ring.advance(kGroups);
       }
-      if (it < n_it) {  // given up: the copies in flight still land in this CTA's memory
-        for (int k = it > kStages ? it - kStages : 0; k < it; ++k) {
-          const uint64_t t0 = global_ns();
-          while (!bar_try(&full_b[k % kStages], (k / kStages) & 1) &&
-                 global_ns() - t0 < kWaitLimitNs) {
-          }
+    }
+  } else if (warp == kCopyWarp) {
+    if (kTma && lane == 0) {
+      const int chunks = (a.bn / 2 + 63) / 64;
+      Cursor now = {tile0, 0};
+      Ring ring;
+      bool ok = true;
+      for (int64_t it = 0; it < total; ++it) {
+        ok = it < kStages || bar_wait(&empty[ring.stage], ring.parity ^ 1, &failed);
+        if (!ok) break;
+        if (half == 0) bar_expect(&full_b[ring.stage], 2 * chunks * kChunk);
+        uint8_t* b = stages + ring.stage * kStageBytes + kBytesA;
+        const uint32_t bar = in_cta(&full_b[ring.stage], leader);
+        const int64_t j0 = column_of(now.tile) + half * (a.bn / 2);
+        for (int c = 0; c < chunks; ++c)
+          copy_box(b + c * kChunk, &map, static_cast<int32_t>(j0 + c * 64),
+                   static_cast<int32_t>(t_begin + static_cast<int64_t>(now.step) * kK), bar);
+        now.advance(1, steps, tile_stride);
+        ring.advance(1);
+      }
+      if (!ok) {  // given up: let the copies in flight (microseconds) land first
+        const uint64_t t0 = global_ns();
+        while (global_ns() - t0 < kDrainNs) {
         }
       }
     }
   } else if (warp == kProductWarp) {
-    if (lane == 0) {
+    if (half == 0 && lane == 0) {
+      const uint16_t pair_mask = static_cast<uint16_t>(3u << leader);
+      const uint32_t desc = product_desc<kBf16>(a.bn);
+      Ring ring;
       bool ok = true;
-      for (int it = 0; it < n_it && ok; ++it) {
-        const int s = it % kStages;
-        const uint32_t parity = (it / kStages) & 1;
-        ok = bar_wait(&full_a[s], parity, &failed) &&
-             (!kTma || bar_wait(&full_b[s], parity, &failed));
-        if (!ok) break;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t at = smem_u32(stages + s * kStageBytes);
+      for (int k = 0; k < my_tiles && ok && steps > 0; ++k) {
+        const uint32_t sums = tmem + (k & 1) * kN;
+        ok = k < 2 || bar_wait(&free_sums[k & 1], ((k >> 1) - 1) & 1, &failed);
+        for (int step = 0; step < steps && ok; ++step) {
+          const int s = ring.stage;
+          ok = bar_wait(&full_a[s], ring.parity, &failed) &&
+               (!kTma || bar_wait(&full_b[s], ring.parity, &failed));
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint32_t at = smem_u32(stages + s * kStageBytes);
 #pragma unroll
-        for (int k = 0; k < kK / 16; ++k)
-          product(tmem, operand(at + k * 2048), operand(at + kBytesA + k * 2048),
-                  product_desc<kBf16>(), it > 0 || k > 0);
-        commit(&empty[s]);
+          for (int q = 0; q < kK / 16; ++q)
+            product(sums, operand(at + q * 2048), operand(at + kBytesA + q * 2048), desc,
+                    step > 0 || q > 0);
+          commit(&empty[s], pair_mask);
+          ring.advance(1);
+        }
+        commit(&done[k & 1], pair_mask);
       }
-      commit(&done);
     }
-  } else {
-    // value warps: thread -> token r of a step, block blk of the 128 columns
-    const int r = tid >> 2, blk = tid & 3;
-    const int64_t i = i0 + blk * 32;
-    const int64_t t_end = s1 * kK < a.rows ? s1 * kK : a.rows;
-    Block ahead[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) ahead[k] = load_block(a, t_begin + k * kK + r, t_end, i);
+  } else if (warp >= kOutWarp0) {
+    // this warp's quarter of tensor memory's lanes
+    const int row0 = (warp & 3) * 32;
     bool ok = true;
-    for (int it = 0; it < n_it && ok; it += 2) {
+    for (int k = 0; k < my_tiles; ++k) {
+      const int tile = tile0 + k * tile_stride;
+      if (steps > 0) ok = ok && bar_wait(&done[k & 1], (k >> 1) & 1, &failed);
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t sums = tmem + (static_cast<uint32_t>(row0) << 16) + (k & 1) * kN;
+      for (int c = 0; c < a.bn; c += 32) {
+        float f[32];
+        if (ok && steps > 0) {
+          read_sums(sums + c, f);
+        } else {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (it + k >= n_it || !ok) break;
-        const int s = (it + k) % kStages;
-        ok = it + k < kStages || bar_wait(&empty[s], ((it + k) / kStages - 1) & 1, &failed);
-        if (!ok) break;
-        uint8_t* stage = stages + s * kStageBytes;
-        const int64_t t0 = t_begin + static_cast<int64_t>(it + k) * kK;
-        store_block<kBf16>(stage, ahead[k], r, blk);
-        ahead[k] = load_block(a, t0 + 2 * kK + r, t_end, i);
-        if constexpr (!kTma) load_dy(a, stage + kBytesA, t0, t_end, j0, tid);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) bar_arrive(&full_a[s]);
+          for (int j = 0; j < 32; ++j) f[j] = ok ? 0.f : __uint_as_float(0x7FC00000u);
+        }
+        if (a.split == 1) {
+          store_sums<kBf16>(a, row_of(tile) + row0 + lane, column_of(tile) + c, f);
+        } else {
+          float4* p = reinterpret_cast<float4*>(
+              reinterpret_cast<float*>(stages) + (row0 + lane) * kJoinPitch + c);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            p[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+        }
       }
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) bar_arrive_at(in_cta(&free_sums[k & 1], leader));
     }
-    if (bar_wait(&done, 0, &failed)) asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   }
   __syncthreads();
-
-  const bool bad = failed != 0;
-  const bool none = n_it == 0;  // no tokens here: zeros
-  if (bad && tid == 0 && a.scaler) atomicCAS(&a.scaler->error, 0, ZERO_DEVERR_TIMEOUT);
-  // value warp w: rows 32 (w mod 4) ..., columns 128 (w / 4) ...
-  const int row0 = (warp & 3) * 32, col0 = (warp >> 2) * (kN / 2);
-  const auto sums = [&](int c, float (&f)[32]) {
-    if (bad || none) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) f[j] = bad ? __uint_as_float(0x7FC00000u) : 0.f;
-    } else {
-      read_sums(tmem + (static_cast<uint32_t>(row0) << 16) + col0 + c, f);
-    }
-  };
-  if (a.split == 1) {
-    if (warp < kValueWarps) {
-#pragma unroll
-      for (int c = 0; c < kN / 2; c += 32) {
-        float f[32];
-        sums(c, f);
-        store_sums<kBf16>(a, i0 + row0 + lane, j0 + col0 + c, f);
-      }
-    }
-  } else {
-    float* tile_sums = reinterpret_cast<float*>(stages);
-    if (warp < kValueWarps) {
-#pragma unroll
-      for (int c = 0; c < kN / 2; c += 32) {
-        float f[32];
-        sums(c, f);
-        float4* p = reinterpret_cast<float4*>(tile_sums + (row0 + lane) * kJoinPitch + col0 + c);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          p[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
-      }
-    }
-    cluster_sync();
-    // this CTA's share of the rows, eight columns per thread and turn
-    const int share = kM / a.split;
-    for (int p = tid; p < share * (kN / 8); p += kThreads) {
-      const int row = rank * share + p / (kN / 8), c = p % (kN / 8) * 8;
-      const uint32_t at = smem_u32(tile_sums + row * kJoinPitch + c);
+  cluster_sync();
+  if (failed && tid == 0 && a.scaler) atomicCAS(&a.scaler->error, 0, ZERO_DEVERR_TIMEOUT);
+  if (a.split > 1) {
+    // one tile per cluster: this CTA's share of its rows, eight columns per thread and turn
+    const float* tile_sums = reinterpret_cast<const float*>(stages);
+    const int share = kM / a.split, groups = a.bn / 8;
+    for (int p = tid; p < share * groups; p += kThreads) {
+      const int row = part * share + p / groups, c = p % groups * 8;
       float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
       for (int k = 0; k < a.split; ++k) {
-        uint32_t remote;
+        const uint32_t remote = in_cta(tile_sums + row * kJoinPitch + c, 2 * k + half);
         float4 x, y;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(at), "r"(k));
         asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                      : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
                      : "r"(remote)
@@ -468,15 +550,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         f[0] += x.x, f[1] += x.y, f[2] += x.z, f[3] += x.w;
         f[4] += y.x, f[5] += y.y, f[6] += y.z, f[7] += y.w;
       }
-      store_sums<kBf16>(a, i0 + row, j0 + c, f);
+      store_sums<kBf16>(a, row_of(tile0) + row, column_of(tile0) + c, f);
     }
     cluster_sync();  // no CTA ends while another reads its sums
   }
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  __syncthreads();
   if (warp == kProductWarp) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kN));
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(2 * kN));
   }
 }
 
@@ -501,12 +581,12 @@ EncodeTiled encode_tiled() {
 }
 
 template <bool kBf16, bool kTma>
-int launch(const CUtensorMap& map, const Args& a, int64_t tiles, cudaStream_t st) {
+int launch(const CUtensorMap& map, const Args& a, int clusters, cudaStream_t st) {
   const auto fn = wgrad_kernel<kBf16, kTma>;
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
     return ZERO_ECUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.split));
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * 2 * a.split));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
@@ -514,7 +594,7 @@ int launch(const CUtensorMap& map, const Args& a, int64_t tiles, cudaStream_t st
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = kProgrammaticLaunch ? 1 : 0;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = a.split;
+  attr[1].val.clusterDim.x = 2 * a.split;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
@@ -551,16 +631,29 @@ ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const
   a.scaler = d_scaler;
   a.rows = rows, a.cols = cols, a.n = n, a.ld = ld;
   a.vec_out = n % kVec == 0 && aligned(dw, 16);
-  const int64_t tiles = a.pitch / kM * ceil_div(n, kN);
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return ZERO_ECUDA;
-  // split the tokens while SMs would be idle and a part keeps four steps
+  const int64_t pairs = std::max(1, sms / 2), m_tiles = ceil_div(a.pitch, 2 * kM);
+  // the width whose tiles fill whole turns of the pairs best
+  int64_t best = 0;
+  for (int bn = kN; bn >= 128; bn -= 32) {
+    const int64_t cost = ceil_div(m_tiles * ceil_div(n, bn), pairs) * bn;
+    if (best == 0 || cost < best) {
+      best = cost;
+      a.bn = bn;
+    }
+  }
+  const int64_t tiles = m_tiles * ceil_div(n, a.bn);
+  if (tiles > 0x3fffffff) return ZERO_ERANGE;
+  a.m_tiles = static_cast<int32_t>(m_tiles);
+  a.tiles = static_cast<int32_t>(tiles);
+  // split the tokens while pairs would be idle and a part keeps four steps
   a.split = 1;
-  while (a.split < kMaxSplit && tiles * a.split * 2 <= sms && rows >= a.split * 2 * 4 * kK)
+  while (a.split < kMaxSplit && tiles * a.split * 2 <= pairs && rows >= a.split * 2 * 4 * kK)
     a.split *= 2;
-  if (tiles * a.split > 0x7fffffff) return ZERO_ERANGE;
+  const int clusters = static_cast<int>(std::min(tiles, a.split > 1 ? tiles : pairs));
   const bool bf16 = dtype == ZERO_BF16;
   const bool tma = rows > 0 && ld % kVec == 0 && aligned(dy, 16);
   CUtensorMap map = {};
@@ -578,8 +671,8 @@ ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (bf16)
-    return tma ? launch<true, true>(map, a, tiles, st) : launch<true, false>(map, a, tiles, st);
-  return tma ? launch<false, true>(map, a, tiles, st) : launch<false, false>(map, a, tiles, st);
+    return tma ? launch<true, true>(map, a, clusters, st) : launch<true, false>(map, a, clusters, st);
+  return tma ? launch<false, true>(map, a, clusters, st) : launch<false, false>(map, a, clusters, st);
 }
 
 }  // extern "C"
