@@ -215,7 +215,7 @@ __device__ __forceinline__ uint32_t step_pair(uint32_t s) {
   uint32_t h;
   if constexpr (kBf16) h = s << 7;
   else h = s == 255 ? 0x7E00u : s >= 113 ? (s - 112) << 10 : 1u << (s - 103);
-  return h | h << 16;
+  return h * 0x10001u;
 }
 
 // Two of a word's four int8 values (bytes 0 and 1, or 2 and 3) as a pair of
@@ -223,17 +223,17 @@ __device__ __forceinline__ uint32_t step_pair(uint32_t s) {
 // number whose last place is 1, and that number is taken off again.
 template <bool kBf16, int kHalf>
 __device__ __forceinline__ uint32_t value_pair(uint32_t w, uint32_t step) {
-  const uint32_t p = __byte_perm(w, 0, kHalf ? 0x4342 : 0x4140);
   uint32_t r;
   if constexpr (kBf16) {
     // 128 + low seven bits, less 128 or (sign bit set) 256
+    const uint32_t p = __byte_perm(w, 0, kHalf ? 0x4342 : 0x4140);
     const uint32_t lo = (p & 0x007F007Fu) | 0x43004300u, hi = (p & 0x00800080u) | 0x43004300u;
     asm("{\n .reg .b32 d;\n sub.rn.bf16x2 d, %1, %2;\n mul.rn.bf16x2 %0, d, %3;\n}"
         : "=r"(r)
         : "r"(lo), "r"(hi), "r"(step));
   } else {
-    // 1024 + (value + 128), less 1152
-    const uint32_t u = (p ^ 0x00800080u) | 0x64006400u;
+    // w holds value + 128: 1024 + (value + 128), less 1152
+    const uint32_t u = __byte_perm(w, 0x64646464u, kHalf ? 0x4342 : 0x4140);
     asm("{\n .reg .b32 d;\n sub.rn.f16x2 d, %1, %2;\n mul.rn.f16x2 %0, d, %3;\n}"
         : "=r"(r)
         : "r"(u), "r"(0x64806480u), "r"(step));
@@ -241,44 +241,55 @@ __device__ __forceinline__ uint32_t value_pair(uint32_t w, uint32_t step) {
   return r;
 }
 
-struct Block {  // 32 checkpointed values of one token
-  uint4 lo, hi;
-  uint32_t scale;
+// A thread's part of a step: 16 checkpointed values of each of two tokens,
+// four rows apart. Eight lanes read a row's 128 bytes together.
+struct Piece {
+  uint4 q[2];
+  uint32_t scale[2];
 };
 
-__device__ __forceinline__ Block load_block(const Args& a, int64_t t, int64_t end, int64_t i) {
-  Block b;
-  b.lo = b.hi = make_uint4(0, 0, 0, 0);
-  b.scale = 127;
-  if (t < end && i < a.pitch && ZCHECK(t < a.rows && i + 32 <= a.pitch, kSiteLoad, t)) {
-    const uint4* p = reinterpret_cast<const uint4*>(a.q + t * a.pitch + i);
-    b.lo = p[0];
-    b.hi = p[1];
-    b.scale = a.scale[t * (a.pitch / ZERO_CKPT_BLOCK) + i / ZERO_CKPT_BLOCK];
+// Where a thread's values of one tile are: q and scale of its first token of
+// the next step to load; left: tokens from there on (0 or less: none, or the
+// tile's columns lie past the checkpoint's).
+struct Source {
+  const int8_t* q;
+  const uint8_t* scale;
+  int32_t left;
+};
+
+__device__ __forceinline__ Piece load_piece(const Source& s, int64_t q_step, int64_t scale_step) {
+  Piece b;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    b.q[k] = make_uint4(0, 0, 0, 0);
+    b.scale[k] = 127;
+    if (s.left > 4 * k) {
+      b.q[k] = __ldg(reinterpret_cast<const uint4*>(s.q + k * q_step));
+      b.scale[k] = __ldg(s.scale + k * scale_step);
+    }
   }
   return b;
 }
 
-// Store a block's 32 values for token row r, columns [32 blk, 32 blk + 32) of
-// the A tile. The 16-byte pieces of blocks 2 and 3 go in another order than
-// those of 0 and 1, so that the eight lanes of a store phase (two tokens,
-// four blocks) fall on eight different pieces of the 128-byte rows.
+// Store token row r's 16 values of columns [16 p, 16 p + 16) of the A tile.
+// They are two 16-byte pieces; the upper four of eight lanes store theirs in
+// the other order, so that the eight lanes of a store phase fall on eight
+// different pieces of the 128-byte rows.
 template <bool kBf16>
-__device__ __forceinline__ void store_block(uint8_t* stage_a, const Block& b, int r, int blk) {
-  const uint32_t s = step_pair<kBf16>(b.scale);
-  const uint32_t w[8] = {b.lo.x, b.lo.y, b.lo.z, b.lo.w, b.hi.x, b.hi.y, b.hi.z, b.hi.w};
-  uint4 v[4];
+__device__ __forceinline__ void store_values(uint8_t* stage_a, const uint4& q, uint32_t scale,
+                                             int r, int p) {
+  const uint32_t s = step_pair<kBf16>(scale);
+  const bool swap = p >= 4;
+  uint32_t w[4] = {swap ? q.z : q.x, swap ? q.w : q.y, swap ? q.x : q.z, swap ? q.y : q.w};
+  uint8_t* row = stage_a + (p >> 2) * kChunk + r * 128;
+  const int at = (((p & 3) << 1 | (swap ? 1 : 0)) ^ (r & 7)) << 4;
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    v[j] = make_uint4(value_pair<kBf16, 0>(w[2 * j], s), value_pair<kBf16, 1>(w[2 * j], s),
-                      value_pair<kBf16, 0>(w[2 * j + 1], s), value_pair<kBf16, 1>(w[2 * j + 1], s));
-  uint8_t* row = stage_a + (blk >> 1) * kChunk + r * 128;
-  const bool swap = blk & 2;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint4 x = swap ? v[j ^ 2] : v[j];
-    const int piece = (blk & 1) * 4 + (swap ? j ^ 2 : j);
-    *reinterpret_cast<uint4*>(row + ((piece ^ (r & 7)) << 4)) = x;
+  for (int j = 0; j < 2; ++j) {
+    uint32_t x0 = w[2 * j], x1 = w[2 * j + 1];
+    if constexpr (!kBf16) x0 ^= 0x80808080u, x1 ^= 0x80808080u;
+    *reinterpret_cast<uint4*>(row + (at ^ (j << 4))) =
+        make_uint4(value_pair<kBf16, 0>(x0, s), value_pair<kBf16, 1>(x0, s),
+                   value_pair<kBf16, 0>(x1, s), value_pair<kBf16, 1>(x1, s));
   }
 }
 
@@ -400,26 +411,41 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_base;
 
   if (warp < kCopyWarp) {
-    // value warps: thread -> token r of a step, block blk of the CTA's 128 columns
-    const int group = warp / kGroupWarps, r = (tid % kGroupThreads) >> 2, blk = tid & 3;
+    // value warps: thread -> tokens r and r + 4 of a step, columns [16 p, 16 p + 16)
+    const int group = warp / kGroupWarps, r = (warp % kGroupWarps) * 8 + (lane >> 3), p = lane & 7;
+    const uint32_t arrive_at = in_cta(full_a, leader);
+    const int64_t blocks = a.pitch / ZERO_CKPT_BLOCK;
+    const int tokens = static_cast<int>(t_end - t_begin);
+    const auto source_of = [&](const Cursor& c) {
+      const int64_t i = row_of(c.tile) + p * 16;
+      const int32_t t = c.step * kK + r;
+      return Source{a.q + (t_begin + t) * a.pitch + i, a.scale + (t_begin + t) * blocks + (i >> 5),
+                    c.tile < a.tiles && i < a.pitch ? tokens - t : 0};
+    };
     Cursor ahead = {tile0, 0}, now = {tile0, 0};
     Ring ring;
     ring.advance(group);
-    if (steps > 0) {
-      ahead.advance(group, steps, tile_stride);
-      now = ahead;
-    }
-    const auto load = [&](int64_t it) {
-      const Block b = load_block(
-          a, it < total ? t_begin + static_cast<int64_t>(ahead.step) * kK + r : t_end, t_end,
-          row_of(ahead.tile) + blk * 32);
-      ahead.advance(kGroups, steps, tile_stride);
+    Piece next[2];
+    Source src = {};
+    const auto load = [&]() {
+      const Piece b = load_piece(src, 4 * a.pitch, 4 * blocks);
+      ahead.step += kGroups;
+      if (ahead.step < steps) {
+        src.q += kGroups * kK * a.pitch;
+        src.scale += kGroups * kK * blocks;
+        src.left -= src.left > 0 ? kGroups * kK : 0;
+      } else {
+        ahead.advance(0, steps, tile_stride);
+        src = source_of(ahead);
+      }
       return b;
     };
-    Block next[2];
     if (total > 0) {
-      next[0] = load(group);
-      next[1] = load(group + kGroups);
+      ahead.advance(group, steps, tile_stride);
+      now = ahead;
+      src = source_of(ahead);
+      next[0] = load();
+      next[1] = load();
     }
     bool ok = true;
     for (int64_t it = group; it < total && ok; it += 2 * kGroups) {
@@ -430,8 +456,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = at < kStages || bar_wait(&empty[ring.stage], ring.parity ^ 1, &failed);
         if (!ok) break;
         uint8_t* stage = stages + ring.stage * kStageBytes;
-        store_block<kBf16>(stage, next[k], r, blk);
-        next[k] = load(at + 2 * kGroups);
+        store_values<kBf16>(stage, next[k].q[0], next[k].scale[0], r, p);
+        store_values<kBf16>(stage, next[k].q[1], next[k].scale[1], r + 4, p);
+        next[k] = load();
         if constexpr (!kTma) {
           load_dy(a, stage + kBytesA, t_begin + static_cast<int64_t>(now.step) * kK, t_end,
                   column_of(now.tile) + half * (a.bn / 2), tid % kGroupThreads);
@@ -439,13 +466,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) bar_arrive_at(in_cta(&full_a[ring.stage], leader));
+        if (lane == 0) bar_arrive_at(arrive_at + ring.stage * 8);
         ring.advance(kGroups);
       }
     }
   } else if (warp == kCopyWarp) {
     if (kTma && lane == 0) {
       const int chunks = (a.bn / 2 + 63) / 64;
+      const uint32_t full_at = in_cta(full_b, leader);
       Cursor now = {tile0, 0};
       Ring ring;
       bool ok = true;
@@ -454,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         if (half == 0) bar_expect(&full_b[ring.stage], 2 * chunks * kChunk);
         uint8_t* b = stages + ring.stage * kStageBytes + kBytesA;
-        const uint32_t bar = in_cta(&full_b[ring.stage], leader);
+        const uint32_t bar = full_at + ring.stage * 8;
         const int64_t j0 = column_of(now.tile) + half * (a.bn / 2);
         for (int c = 0; c < chunks; ++c)
           copy_box(b + c * kChunk, &map, static_cast<int32_t>(j0 + c * 64),
