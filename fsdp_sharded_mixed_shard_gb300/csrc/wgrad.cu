@@ -48,15 +48,16 @@ constexpr int kCopyWarp = kGroups * kGroupWarps, kProductWarp = kCopyWarp + 1;
 constexpr int kOutWarp0 = kProductWarp + 1, kOutWarps = 4;
 constexpr int kThreads = 32 * (kOutWarp0 + kOutWarps);
 constexpr int kM = 128, kN = 256, kK = 64;     // rows per CTA, columns at most, tokens per stage
-constexpr int kStages = 6;
+constexpr int kAhead = 2;                       // a value thread's steps loaded ahead
 constexpr int kChunk = kK * 128;               // 64 tokens x 64 columns of 16 bits
 constexpr int kBytesA = kM / 64 * kChunk, kBytesB = kN / 2 / 64 * kChunk;
-constexpr int kStageBytes = kBytesA + kBytesB;
+constexpr int kRing = 192 * 1024;              // shared memory for stages
 constexpr int kJoinPitch = kN + 4;             // fp32 row of a tile in shared memory
-constexpr int kSmem = kStages * kStageBytes + 1024;
+constexpr int kSmem = kRing + 1024;
 constexpr int kMaxSplit = 4;
+constexpr int kValueCycles = 850, kOutCycles = 4000;
 constexpr uint64_t kWaitLimitNs = 2000000000ull, kDrainNs = 1000000ull;
-static_assert(kM * kJoinPitch * 4 <= kStages * kStageBytes, "the tile fits the stages");
+static_assert(kM * kJoinPitch * 4 <= kRing, "the tile fits the stages");
 static_assert(kM == ZERO_CKPT_PAD, "a checkpoint row is whole CTA tiles");
 
 struct Args {
@@ -103,10 +104,12 @@ __device__ __forceinline__ void bar_arrive_at(uint32_t cluster_addr) {
                : "memory");
 }
 
+// One try; the thread sleeps in it until the phase completes, at most about a
+// millisecond.
 __device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n"
       " selp.u32 %0, 1, 0, p;\n}"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
@@ -135,6 +138,11 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatil
   }
 }
 
+// all threads of a value group
+__device__ __forceinline__ void group_sync(int group) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroupThreads) : "memory");
+}
+
 // A box of dy into this CTA; its bytes are counted by the barrier at
 // `cluster_bar`, in this CTA or the other of the pair.
 __device__ __forceinline__ void copy_box(void* dst, const CUtensorMap* map, int32_t x, int32_t y,
@@ -148,11 +156,13 @@ __device__ __forceinline__ void copy_box(void* dst, const CUtensorMap* map, int3
 
 // Shared-memory operand whose reduction axis is the slow one, 128-byte
 // swizzle: rows of 64 elements (128 bytes), eight rows per 1024-byte atom
-// (the next eight reduction steps), the next 64 elements kChunk bytes on.
-__device__ __forceinline__ uint64_t operand(uint32_t addr) {
-  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) |
-         static_cast<uint64_t>(kChunk >> 4) << 16 | static_cast<uint64_t>(1024 >> 4) << 32 |
-         1ull << 46 | 2ull << 61;
+// (the next eight reduction steps), the next 64 elements kChunk bytes on. The
+// low word holds the address in 16-byte units and the chunk distance; stages
+// and reduction steps are added to it.
+constexpr uint32_t kOperandHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
+
+__device__ __forceinline__ uint32_t operand_low(uint32_t addr) {
+  return (addr & 0x3FFFF) >> 4 | static_cast<uint32_t>(kChunk >> 4) << 16;
 }
 
 // fp32 sums; both operands of the 16-bit type, slow axis reduced; 256 x bn
@@ -162,12 +172,13 @@ __device__ __forceinline__ uint32_t product_desc(int bn) {
          static_cast<uint32_t>(bn >> 3) << 17 | static_cast<uint32_t>(2 * kM >> 4) << 24;
 }
 
-__device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t desc,
-                                        bool add) {
+__device__ __forceinline__ void product(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t desc,
+                                        uint32_t add) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(desc), "r"(add ? 1u : 0u)
+      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n"
+      " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n}" ::"r"(d),
+      "r"(a_low), "r"(b_low), "r"(desc), "r"(add), "r"(kOperandHigh)
       : "memory");
 }
 
@@ -344,6 +355,7 @@ struct Cursor {
   }
 };
 
+template <int kStages>
 struct Ring {  // stage and the parity of its current use
   int32_t stage = 0;
   uint32_t parity = 0;
@@ -356,16 +368,19 @@ struct Ring {  // stage and the parity of its current use
   }
 };
 
-template <bool kBf16, bool kTma>
+// kWide: column groups of bn per tile (1 or 2), which share the checkpoint's
+// stage.
+template <bool kBf16, bool kTma, int kWide>
 __global__ void __launch_bounds__(kThreads, 1)
     wgrad_kernel(const __grid_constant__ CUtensorMap map, const Args a) {
   pdl_begin();
+  constexpr int kStageBytes = kBytesA + kWide * kBytesB, kStages = kRing / kStageBytes;
   extern __shared__ uint8_t raw[];
   uint8_t* stages = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   // full: in the pair's first CTA, counted by both; empty and done: in each
   __shared__ uint64_t full_a[kStages], full_b[kStages], empty[kStages], done[2], free_sums[2];
   __shared__ uint32_t tmem_base;
-  __shared__ int failed;
+  __shared__ int failed, group_ok[kGroups];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n_cta = 2 * a.split;
   const int rank = static_cast<int>(blockIdx.x) % n_cta;
@@ -382,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const auto row_of = [&](int tile) {  // first row of dw of this CTA's part of the tile
     return static_cast<int64_t>(tile % a.m_tiles) * (2 * kM) + half * kM;
   };
-  const auto column_of = [&](int tile) { return static_cast<int64_t>(tile / a.m_tiles) * a.bn; };
+  const auto column_of = [&](int tile) { return static_cast<int64_t>(tile / a.m_tiles) * (kWide * a.bn); };
 
   if (warp == kProductWarp) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -393,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      bar_init(&full_a[s], 2 * kGroupWarps);
+      bar_init(&full_a[s], 2);
       bar_init(&full_b[s], 1);
       bar_init(&empty[s], 1);
     }
@@ -423,9 +438,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     c.tile < a.tiles && i < a.pitch ? tokens - t : 0};
     };
     Cursor ahead = {tile0, 0}, now = {tile0, 0};
-    Ring ring;
+    Ring<kStages> ring;
     ring.advance(group);
-    Piece next[2];
+    Piece next[kAhead];
     Source src = {};
     const auto load = [&]() {
       const Piece b = load_piece(src, 4 * a.pitch, 4 * blocks);
@@ -444,51 +459,70 @@ __global__ void __launch_bounds__(kThreads, 1)
       ahead.advance(group, steps, tile_stride);
       now = ahead;
       src = source_of(ahead);
-      next[0] = load();
-      next[1] = load();
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) next[k] = load();
     }
     bool ok = true;
-    for (int64_t it = group; it < total && ok; it += 2 * kGroups) {
+    for (int64_t it = group; it < total && ok; it += kAhead * kGroups) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < kAhead; ++k) {
         const int64_t at = it + k * kGroups;
         if (at >= total || !ok) break;
-        ok = at < kStages || bar_wait(&empty[ring.stage], ring.parity ^ 1, &failed);
-        if (!ok) break;
+        // one warp of the group asks (many that poll slow what they wait for)
+        if (at >= kStages) {
+          if (warp % kGroupWarps == 0) {
+            const bool free = bar_wait(&empty[ring.stage], ring.parity ^ 1, &failed);
+            if (lane == 0) group_ok[group] = free;
+          }
+          group_sync(group);
+          ok = *static_cast<volatile int*>(&group_ok[group]) != 0;
+          if (!ok) break;
+        }
         uint8_t* stage = stages + ring.stage * kStageBytes;
         store_values<kBf16>(stage, next[k].q[0], next[k].scale[0], r, p);
         store_values<kBf16>(stage, next[k].q[1], next[k].scale[1], r + 4, p);
         next[k] = load();
         if constexpr (!kTma) {
-          load_dy(a, stage + kBytesA, t_begin + static_cast<int64_t>(now.step) * kK, t_end,
-                  column_of(now.tile) + half * (a.bn / 2), tid % kGroupThreads);
+          for (int w = 0; w < kWide; ++w)
+            load_dy(a, stage + kBytesA + w * kBytesB, t_begin + static_cast<int64_t>(now.step) * kK,
+                    t_end, column_of(now.tile) + w * a.bn + half * (a.bn / 2), tid % kGroupThreads);
           now.advance(kGroups, steps, tile_stride);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) bar_arrive_at(arrive_at + ring.stage * 8);
+        group_sync(group);
+        if (tid % kGroupThreads == 0) bar_arrive_at(arrive_at + ring.stage * 8);
         ring.advance(kGroups);
       }
     }
   } else if (warp == kCopyWarp) {
     if (kTma && lane == 0) {
+      // one thread's dependent instructions are slow beside 22 warps: what
+      // does not change from step to step is worked out before
       const int chunks = (a.bn / 2 + 63) / 64;
       const uint32_t full_at = in_cta(full_b, leader);
-      Cursor now = {tile0, 0};
-      Ring ring;
+      Ring<kStages> ring;
       bool ok = true;
-      for (int64_t it = 0; it < total; ++it) {
-        ok = it < kStages || bar_wait(&empty[ring.stage], ring.parity ^ 1, &failed);
-        if (!ok) break;
-        if (half == 0) bar_expect(&full_b[ring.stage], 2 * chunks * kChunk);
-        uint8_t* b = stages + ring.stage * kStageBytes + kBytesA;
-        const uint32_t bar = full_at + ring.stage * 8;
-        const int64_t j0 = column_of(now.tile) + half * (a.bn / 2);
-        for (int c = 0; c < chunks; ++c)
-          copy_box(b + c * kChunk, &map, static_cast<int32_t>(j0 + c * 64),
-                   static_cast<int32_t>(t_begin + static_cast<int64_t>(now.step) * kK), bar);
-        now.advance(1, steps, tile_stride);
-        ring.advance(1);
+      int left_fresh = kStages;
+      for (int k = 0; k < my_tiles && ok; ++k) {
+        const int32_t x = static_cast<int32_t>(column_of(tile0 + k * tile_stride) + half * (a.bn / 2));
+        int32_t y = static_cast<int32_t>(t_begin);
+        for (int step = 0; step < steps; ++step, y += kK) {
+          const int s = ring.stage;
+          if (left_fresh > 0) --left_fresh;
+          else if (!bar_wait(&empty[s], ring.parity ^ 1, &failed)) {
+            ok = false;
+            break;
+          }
+          if (half == 0) bar_expect(&full_b[s], 2 * kWide * chunks * kChunk);
+          uint8_t* b = stages + s * kStageBytes + kBytesA;
+#pragma unroll
+          for (int w = 0; w < kWide; ++w) {
+            copy_box(b + w * kBytesB, &map, x + w * a.bn, y, full_at + s * 8);
+            if (chunks > 1)
+              copy_box(b + w * kBytesB + kChunk, &map, x + w * a.bn + 64, y, full_at + s * 8);
+          }
+          ring.advance(1);
+        }
       }
       if (!ok) {  // given up: let the copies in flight (microseconds) land first
         const uint64_t t0 = global_ns();
@@ -500,26 +534,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (half == 0 && lane == 0) {
       const uint16_t pair_mask = static_cast<uint16_t>(3u << leader);
       const uint32_t desc = product_desc<kBf16>(a.bn);
-      Ring ring;
+      const uint32_t base = operand_low(smem_u32(stages));
+      Ring<kStages> ring;
       bool ok = true;
       for (int k = 0; k < my_tiles && ok && steps > 0; ++k) {
-        const uint32_t sums = tmem + (k & 1) * kN;
-        ok = k < 2 || bar_wait(&free_sums[k & 1], ((k >> 1) - 1) & 1, &failed);
+        // one group per tile: two tiles' sums in turn; two groups fill tensor memory
+        const int buf = kWide == 1 ? k & 1 : 0, use = kWide == 1 ? k >> 1 : k;
+        const uint32_t sums = tmem + buf * kN;
+        ok = use == 0 || bar_wait(&free_sums[buf], (use - 1) & 1, &failed);
         for (int step = 0; step < steps && ok; ++step) {
           const int s = ring.stage;
           ok = bar_wait(&full_a[s], ring.parity, &failed) &&
                (!kTma || bar_wait(&full_b[s], ring.parity, &failed));
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint32_t at = smem_u32(stages + s * kStageBytes);
+          const uint32_t at = base + s * (kStageBytes >> 4);
 #pragma unroll
           for (int q = 0; q < kK / 16; ++q)
-            product(sums, operand(at + q * 2048), operand(at + kBytesA + q * 2048), desc,
-                    step > 0 || q > 0);
+#pragma unroll
+            for (int w = 0; w < kWide; ++w)
+              product(sums + w * kN, at + q * (2048 >> 4),
+                      at + ((kBytesA + w * kBytesB) >> 4) + q * (2048 >> 4), desc,
+                      q > 0 ? 1u : step);
           commit(&empty[s], pair_mask);
           ring.advance(1);
         }
-        commit(&done[k & 1], pair_mask);
+        commit(&done[buf], pair_mask);
       }
     }
   } else if (warp >= kOutWarp0) {
@@ -528,30 +568,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int k = 0; k < my_tiles; ++k) {
       const int tile = tile0 + k * tile_stride;
-      if (steps > 0) ok = ok && bar_wait(&done[k & 1], (k >> 1) & 1, &failed);
+      const int buf = kWide == 1 ? k & 1 : 0, use = kWide == 1 ? k >> 1 : k;
+      if (steps > 0) ok = ok && bar_wait(&done[buf], use & 1, &failed);
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint32_t sums = tmem + (static_cast<uint32_t>(row0) << 16) + (k & 1) * kN;
-      for (int c = 0; c < a.bn; c += 32) {
+      const uint32_t sums = tmem + (static_cast<uint32_t>(row0) << 16) + buf * kN;
+      const int64_t i = row_of(tile) + row0 + lane, j = column_of(tile);
+#pragma unroll 1
+      for (int c = 0; c < kWide * a.bn; c += 32) {
         float f[32];
         if (ok && steps > 0) {
-          read_sums(sums + c, f);
+          read_sums(sums + (kWide == 2 && c >= a.bn ? kN - a.bn : 0) + c, f);
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) f[j] = ok ? 0.f : __uint_as_float(0x7FC00000u);
+          for (int e = 0; e < 32; ++e) f[e] = ok ? 0.f : __uint_as_float(0x7FC00000u);
         }
         if (a.split == 1) {
-          store_sums<kBf16>(a, row_of(tile) + row0 + lane, column_of(tile) + c, f);
+          store_sums<kBf16>(a, i, j + c, f);
         } else {
           float4* p = reinterpret_cast<float4*>(
               reinterpret_cast<float*>(stages) + (row0 + lane) * kJoinPitch + c);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            p[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+          for (int e = 0; e < 8; ++e)
+            p[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
         }
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
-      if (lane == 0) bar_arrive_at(in_cta(&free_sums[k & 1], leader));
+      if (lane == 0) bar_arrive_at(in_cta(&free_sums[buf], leader));
     }
   }
   __syncthreads();
@@ -608,9 +651,9 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-template <bool kBf16, bool kTma>
+template <bool kBf16, bool kTma, int kWide>
 int launch(const CUtensorMap& map, const Args& a, int clusters, cudaStream_t st) {
-  const auto fn = wgrad_kernel<kBf16, kTma>;
+  const auto fn = wgrad_kernel<kBf16, kTma, kWide>;
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
     return ZERO_ECUDA;
   cudaLaunchConfig_t cfg = {};
@@ -627,6 +670,12 @@ int launch(const CUtensorMap& map, const Args& a, int clusters, cudaStream_t st)
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return status_of(cudaLaunchKernelEx(&cfg, fn, map, a));
+}
+
+template <bool kBf16, bool kTma>
+int launch_wide(const CUtensorMap& map, const Args& a, int wide, int clusters, cudaStream_t st) {
+  return wide == 2 ? launch<kBf16, kTma, 2>(map, a, clusters, st)
+                   : launch<kBf16, kTma, 1>(map, a, clusters, st);
 }
 
 }  // namespace zw
@@ -664,22 +713,31 @@ ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return ZERO_ECUDA;
   const int64_t pairs = std::max(1, sms / 2), m_tiles = ceil_div(a.pitch, 2 * kM);
-  // the width whose tiles fill whole turns of the pairs best
+  // Tile width by the tensor-core cycles it takes, turns of all pairs times
+  // steps: a step takes 2 cycles per column, at least kValueCycles for the
+  // checkpoint's values; two column groups share those but leave the tensor
+  // cores idle while a tile is put out.
+  const int64_t steps = ceil_div(rows, kK);
+  int wide = 1;
   int64_t best = 0;
-  for (int bn = kN; bn >= 128; bn -= 32) {
-    const int64_t cost = ceil_div(m_tiles * ceil_div(n, bn), pairs) * bn;
-    if (best == 0 || cost < best) {
-      best = cost;
-      a.bn = bn;
+  for (int w = 1; w <= 2; ++w)
+    for (int bn = kN; bn >= 128; bn -= 32) {
+      const int64_t turns = ceil_div(m_tiles * ceil_div(n, w * bn), pairs);
+      const int64_t cost = turns * (steps * std::max<int64_t>(2 * w * bn, kValueCycles) +
+                                    (w == 2 ? kOutCycles : 0));
+      if (best == 0 || cost < best) {
+        best = cost;
+        a.bn = bn;
+        wide = w;
+      }
     }
-  }
-  const int64_t tiles = m_tiles * ceil_div(n, a.bn);
+  const int64_t tiles = m_tiles * ceil_div(n, wide * a.bn);
   if (tiles > 0x3fffffff) return ZERO_ERANGE;
   a.m_tiles = static_cast<int32_t>(m_tiles);
   a.tiles = static_cast<int32_t>(tiles);
   // split the tokens while pairs would be idle and a part keeps four steps
   a.split = 1;
-  while (a.split < kMaxSplit && tiles * a.split * 2 <= pairs && rows >= a.split * 2 * 4 * kK)
+  while (wide == 1 && a.split < kMaxSplit && tiles * a.split * 2 <= pairs && rows >= a.split * 2 * 4 * kK)
     a.split *= 2;
   const int clusters = static_cast<int>(std::min(tiles, a.split > 1 ? tiles : pairs));
   const bool bf16 = dtype == ZERO_BF16;
@@ -698,9 +756,10 @@ ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const
       return ZERO_ECUDA;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (bf16)
-    return tma ? launch<true, true>(map, a, clusters, st) : launch<true, false>(map, a, clusters, st);
-  return tma ? launch<false, true>(map, a, clusters, st) : launch<false, false>(map, a, clusters, st);
+  if (bf16) return tma ? launch_wide<true, true>(map, a, wide, clusters, st)
+                       : launch_wide<true, false>(map, a, wide, clusters, st);
+  return tma ? launch_wide<false, true>(map, a, wide, clusters, st)
+             : launch_wide<false, false>(map, a, wide, clusters, st);
 }
 
 }  // extern "C"
