@@ -74,41 +74,65 @@ struct Ckpt {
   uint8_t* scale;  // [rows][pitch / 32]
 };
 
-// Quantise the lane's eight values with its block's other three lanes and
+// Two 16-bit magnitudes at once: as integers they are ordered like the values,
+// infinity and NaN above all numbers.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// x held in [-limit, limit], pairs of 16-bit values
+template <bool kBf16>
+__device__ __forceinline__ uint32_t hold2(uint32_t x, uint32_t limit, uint32_t minus_limit) {
+  if constexpr (kBf16)
+    asm("{\n .reg .b32 t;\n min.bf16x2 t, %1, %2;\n max.bf16x2 %0, t, %3;\n}"
+        : "=r"(x)
+        : "r"(x), "r"(limit), "r"(minus_limit));
+  else
+    asm("{\n .reg .b32 t;\n min.f16x2 t, %1, %2;\n max.f16x2 %0, t, %3;\n}"
+        : "=r"(x)
+        : "r"(x), "r"(limit), "r"(minus_limit));
+  return x;
+}
+
+// Quantise the lane's eight values v with its block's other three lanes and
 // store them; all lanes of the warp call it. `in` is false past the pitch.
+// q = rint(x / 2^k) falls out of one fused multiply-add: added to 1.5 2^23, the
+// quotient is rounded to a whole number, ties to even, in the sum's last bits.
 template <bool kBf16>
 __device__ __forceinline__ void save8(const Ckpt& k, int64_t row, int64_t c, int64_t pitch,
-                                      bool in, const float (&f)[8]) {
-  float top = 0.f;
-  bool finite = true;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float m = fabsf(f[j]);
-    finite = finite && m < __uint_as_float(0x7F800000u);  // false for NaN too
-    top = fmaxf(top, m);
-  }
-  uint32_t bits = finite ? __float_as_uint(top) : 0x7F800000u;
-  bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 1));
-  bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 2));
-  const int e = static_cast<int>(bits >> 23);  // biased exponent of the maximum; 255: not finite
-  const int low = kBf16 ? -126 : -24;
-  const int step = max(e - 127 - 6, low);
-  const float inv = e == 255 ? 0.f : pow2(-step);
+                                      bool in, const uint4& v) {
+  constexpr uint32_t kAbs = 0x7FFF7FFFu;
+  uint32_t top = max_u16x2(max_u16x2(v.x & kAbs, v.y & kAbs), max_u16x2(v.z & kAbs, v.w & kAbs));
+  top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  top = max(top & 0xFFFFu, top >> 16);
+  const bool finite = top < (kBf16 ? 0x7F80u : 0x7C00u);
+  // biased exponent of the maximum (0 for zero and, in bf16, the subnormals)
+  const int e = static_cast<int>(__float_as_uint(widen<kBf16>(top)) >> 23);
+  const int step = max(e - 127 - 6, kBf16 ? -126 : -24);
+  const float inv = pow2(-step), most = 127.f * pow2(step);
+  const uint32_t limit = narrow2<kBf16>(most, most), minus = limit | 0x80008000u;
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t q[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float r = fminf(fmaxf(f[j] * inv, -127.f), 127.f);
-    q[j] = static_cast<uint32_t>(__float2int_rn(r)) & 0xFFu;
+  for (int j = 0; j < 4; ++j) {
+    float a, b;
+    widen2<kBf16>(hold2<kBf16>(w[j], limit, minus), a, b);
+    q[2 * j] = __float_as_uint(__fmaf_rn(a, inv, 12582912.f));
+    q[2 * j + 1] = __float_as_uint(__fmaf_rn(b, inv, 12582912.f));
   }
   if (!in) return;
-  uint2 w;
-  w.x = q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24;
-  w.y = q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24;
-  if (e == 255) w = make_uint2(0, 0);
-  __stcs(reinterpret_cast<uint2*>(k.q + row * pitch + c), w);
+  const auto low_bytes = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+  };
+  uint2 out = make_uint2(low_bytes(q[0], q[1], q[2], q[3]), low_bytes(q[4], q[5], q[6], q[7]));
+  if (!finite) out = make_uint2(0, 0);
+  __stcs(reinterpret_cast<uint2*>(k.q + row * pitch + c), out);
   if ((threadIdx.x & 3) == 0)
     k.scale[row * (pitch / ZERO_CKPT_BLOCK) + c / ZERO_CKPT_BLOCK] =
-        static_cast<uint8_t>(e == 255 ? 255 : step + 127);
+        static_cast<uint8_t>(finite ? step + 127 : 255);
 }
 
 // The lane's eight checkpointed values.
@@ -180,11 +204,11 @@ __global__ void __launch_bounds__(kThreads) ckpt_kernel(const Args a) {
       const int64_t r = row0 + k * kRows;
       if (r >= a.rows) continue;  // the same for the whole warp
       float x[8], u[8], y[8];
+      save8<kBf16>(a.kx, r, c, a.pitch, in, vx[k]);
       widen8<kBf16>(vx[k], x);
-      save8<kBf16>(a.kx, r, c, a.pitch, in, x);
       if constexpr (kOp == kSwiglu) {
+        save8<kBf16>(a.ku, r, c, a.pitch, in, vu[k]);
         widen8<kBf16>(vu[k], u);
-        save8<kBf16>(a.ku, r, c, a.pitch, in, u);
       }
       if constexpr (kOp != kSave) {
 #pragma unroll

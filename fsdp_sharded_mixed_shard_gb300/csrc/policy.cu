@@ -666,37 +666,56 @@ __global__ void __launch_bounds__(kThreads, 3) policy_kernel(const Args a, const
   }
 }
 
+// Sum with what each addition lost beside it (the file is built without
+// contraction and reassociation).
+struct Sum {
+  float hi = 0.f, lo = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    const float t = hi + x, b = t - hi;
+    lo += (hi - (t - b)) + (x - b);
+    hi = t;
+  }
+};
+
 // The four sums over the rows that are not left out, by one CTA: each thread
-// its rows in order, then a tree.
+// its rows in order, then a tree. fp64 would take most of this kernel's time
+// (15 us of 16 at 2048 rows); two fp32 words carry as much as a result holds.
 __global__ void __launch_bounds__(1024) stats_kernel(const Args a) {
   pdl_begin();
-  __shared__ double part[4][32];
+  __shared__ Sum part[4][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  double s[4] = {0, 0, 0, 0};
+  Sum s[4];
+#pragma unroll 2
   for (int64_t row = tid; row < a.rows; row += 1024) {
-    const float w = a.weight[row];
+    const float w = a.weight[row], lp = a.logp[row], old = a.old_logp[row];
+    const float adv = a.advantage[row], loss = a.loss[row];
+    const float ref = a.ref_logp ? a.ref_logp[row] : lp;
     if (w == 0.f || load_id(a.actions, a.action_bytes, row, a.vocab) < 0) continue;
-    const float lp = a.logp[row], r = expf(lp - a.old_logp[row]), adv = a.advantage[row];
-    s[0] += static_cast<double>(w) * a.loss[row];
-    if (a.ref_logp) {
-      const float d = a.ref_logp[row] - lp;
-      s[1] += static_cast<double>(w) * (expm1f(d) - d);
-    }
-    if (fminf(fmaxf(r, a.lo), a.hi) * adv < r * adv) s[2] += w;
-    s[3] += w;
+    const float r = expf(lp - old), d = ref - lp;
+    s[0].add(w * loss);
+    s[1].add(w * (expm1f(d) - d));
+    if (fminf(fmaxf(r, a.lo), a.hi) * adv < r * adv) s[2].add(w);
+    s[3].add(w);
   }
+  const auto tree = [](Sum& v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      const float hi = __shfl_down_sync(0xffffffffu, v.hi, d);
+      const float lo = __shfl_down_sync(0xffffffffu, v.lo, d);
+      v.add(hi);
+      v.lo += lo;
+    }
+  };
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], d);
+    tree(s[k]);
     if (lane == 0) part[k][warp] = s[k];
   }
   __syncthreads();
   if (warp < 4) {
-    double v = part[warp][lane];
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    if (lane == 0) a.stats[warp] = static_cast<float>(v);
+    Sum v = part[warp][lane];
+    tree(v);
+    if (lane == 0) a.stats[warp] = v.hi + v.lo;
   }
 }
 
