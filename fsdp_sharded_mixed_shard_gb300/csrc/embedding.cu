@@ -39,8 +39,9 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSlice = 256;    // columns per warp: eight per lane
 constexpr int kLookup = 4;     // tokens per warp and step of the lookup
-constexpr int kRun = 64;       // items of the merged list per run
+constexpr int kRun = 32;       // items of the merged list per run
 constexpr int kBatch = 8;      // dy rows in flight per warp
+static_assert(kRun % 32 == 0 && kRun <= 64 && 32 % kBatch == 0, "a run's tokens fit its lanes");
 
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
@@ -51,41 +52,34 @@ constexpr int kMaxPasses = 3;
 static_assert(kDigits == kSortThreads, "one thread per digit");
 static_assert(kTile % kSortThreads == 0, "whole rounds");
 
-// eight columns of a row: neighbouring ones when rows are 16-byte aligned,
-// else every 32nd (the lanes of a warp then read neighbouring elements)
+// A lane's eight neighbouring columns [c, c + 8) of a row; columns past dim
+// are 0 (loads) or left alone (stores). kVecRows: rows lie on the 16-byte grid
+// and dim is a multiple of 8.
 template <bool kVecRows>
-__device__ __forceinline__ int64_t column(int64_t c0, int lane, int j) {
-  return kVecRows ? c0 + lane * kVec + j : c0 + lane + 32 * j;
-}
-
-template <bool kVecRows>
-__device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c0, int lane, int64_t dim) {
-  if constexpr (kVecRows) {
-    const int64_t c = c0 + lane * kVec;
+__device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t dim) {
+  if constexpr (kVecRows)
     return c < dim ? __ldcs(reinterpret_cast<const uint4*>(row + c)) : make_uint4(0, 0, 0, 0);
-  } else {
-    uint32_t h[8];
+  if (c + kVec <= dim) return load8_any(row + c);
+  uint32_t h[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int64_t c = column<false>(c0, lane, j);
-      h[j] = c < dim ? row[c] : 0;
-    }
-    return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-  }
+  for (int j = 0; j < 8; ++j) h[j] = c + j < dim ? row[c + j] : 0;
+  return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
 }
 
 template <bool kVecRows>
-__device__ __forceinline__ void store8(uint16_t* row, int64_t c0, int lane, int64_t dim,
-                                       const uint4& v) {
+__device__ __forceinline__ void store8(uint16_t* row, int64_t c, int64_t dim, const uint4& v) {
   if constexpr (kVecRows) {
-    const int64_t c = c0 + lane * kVec;
     if (c < dim) __stcs(reinterpret_cast<uint4*>(row + c), v);
   } else {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    // word stores where the lane's first element lies on one
+    if ((reinterpret_cast<uintptr_t>(row + c) & 3) == 0 && c + kVec <= dim) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int64_t c = column<false>(c0, lane, j);
-      if (c < dim) row[c] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+      for (int j = 0; j < 4; ++j) reinterpret_cast<uint32_t*>(row + c)[j] = w[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + j < dim) row[c + j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
     }
   }
 }
@@ -116,7 +110,7 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const LookupArgs a) {
     const int64_t t = t0 + k;
     const int64_t id = t < a.n ? load_id(a.tokens, a.token_bytes, t, a.vocab) : -1;
     v[k] = id >= 0 && ZCHECK(id < a.vocab, kSiteLoad, id)
-               ? load8<kVecRows>(a.table + id * a.dim, c0, lane, a.dim)
+               ? load8<kVecRows>(a.table + id * a.dim, c0 + lane * kVec, a.dim)
                : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
@@ -127,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const LookupArgs a) {
     widen8<kBf16>(v[k], f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] *= a.scale;
-    store8<kVecRows>(a.out + t * a.dim, c0, lane, a.dim, narrow8<kBf16>(f));
+    store8<kVecRows>(a.out + t * a.dim, c0 + lane * kVec, a.dim, narrow8<kBf16>(f));
   }
 }
 
@@ -141,6 +135,7 @@ struct SortArgs {
   uint32_t* pos_out;
   uint32_t* hist;                // this pass: [kDigits][kMaxChunks]
   uint32_t* hist_next;           // next pass, or NULL
+  uint32_t* n_spans;             // cleared for rows_kernel
   int64_t n, vocab, chunk;       // chunk: ids per CTA, a multiple of kTile
   int32_t token_bytes, shift, bits, n_chunks, n_hists;
 };
@@ -157,6 +152,7 @@ __global__ void __launch_bounds__(kSortThreads) hist_kernel(const SortArgs a) {
   pdl_begin();
   __shared__ uint32_t count[kDigits];
   count[threadIdx.x] = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.n_spans = 0;
   __syncthreads();
   const int64_t lo = blockIdx.x * a.chunk;
   const int64_t hi = lo + a.chunk < a.n ? lo + a.chunk : a.n;
@@ -165,6 +161,9 @@ __global__ void __launch_bounds__(kSortThreads) hist_kernel(const SortArgs a) {
     atomicAdd(&count[first_key(a, i) & mask], 1u);
   __syncthreads();
   a.hist[threadIdx.x * kMaxChunks + blockIdx.x] = count[threadIdx.x];
+  // the scatter kernels read counts in fours
+  if (blockIdx.x == gridDim.x - 1)
+    for (int g = gridDim.x; g < kMaxChunks && (g & 3); ++g) a.hist[threadIdx.x * kMaxChunks + g] = 0;
   const int total = (a.n_hists - 1) * kDigits * kMaxChunks;
   for (int i = blockIdx.x * kSortThreads + threadIdx.x; i < total; i += gridDim.x * kSortThreads)
     a.hist[kDigits * kMaxChunks + i] = 0;
@@ -172,17 +171,36 @@ __global__ void __launch_bounds__(kSortThreads) hist_kernel(const SortArgs a) {
 
 __global__ void __launch_bounds__(kSortThreads) scatter_kernel(const SortArgs a) {
   pdl_begin();
+  constexpr int kRounds = kTile / kSortThreads;
   __shared__ uint32_t base[kDigits];               // next free place of each digit
   __shared__ uint32_t of_warp[kSortWarps][kDigits];
   __shared__ uint32_t warp_sum[kSortWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t lo = blockIdx.x * a.chunk;
+  const int64_t hi = lo + a.chunk < a.n ? lo + a.chunk : a.n;
+  const uint32_t mask = (1u << a.bits) - 1;
+  // warp w ranks ids [w, w + 1) * kTile / kSortWarps of a tile
+  uint32_t key[kRounds], pos[kRounds], rank[kRounds];
+  const auto load = [&](int64_t t0) {
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+      const int64_t i = t0 + (warp * kRounds + k) * 32 + lane;
+      key[k] = i >= hi ? 0xFFFFFFFFu : a.key_in ? a.key_in[i] : first_key(a, i);
+      pos[k] = i >= hi ? 0 : a.pos_in ? a.pos_in[i] : static_cast<uint32_t>(i);
+    }
+  };
+  load(lo);
   {
     // digit tid: all its ids, and those in the chunks before this one
+    const uint4* row = reinterpret_cast<const uint4*>(a.hist + tid * kMaxChunks);
+    const int me = blockIdx.x;
     uint32_t all = 0, before = 0;
-    for (int g = 0; g < a.n_chunks; ++g) {
-      const uint32_t c = a.hist[tid * kMaxChunks + g];
-      all += c;
-      before += g < static_cast<int>(blockIdx.x) ? c : 0;
+#pragma unroll 4
+    for (int g = 0; g < a.n_chunks; g += 4) {  // counts past n_chunks are 0
+      const uint4 c = row[g >> 2];
+      all += (c.x + c.y) + (c.z + c.w);
+      before += (g < me ? c.x : 0) + (g + 1 < me ? c.y : 0) + (g + 2 < me ? c.z : 0) +
+                (g + 3 < me ? c.w : 0);
     }
     uint32_t inc = all;
 #pragma unroll
@@ -191,26 +209,24 @@ __global__ void __launch_bounds__(kSortThreads) scatter_kernel(const SortArgs a)
       if (lane >= d) inc += y;
     }
     if (lane == 31) warp_sum[warp] = inc;
-    __syncthreads();
-    uint32_t lower = 0;
-    for (int w = 0; w < warp; ++w) lower += warp_sum[w];
-    base[tid] = lower + inc - all + before;
-  }
-  const int64_t lo = blockIdx.x * a.chunk;
-  const int64_t hi = lo + a.chunk < a.n ? lo + a.chunk : a.n;
-  const uint32_t mask = (1u << a.bits) - 1;
-  constexpr int kRounds = kTile / kSortThreads;
-  for (int64_t t0 = lo; t0 < hi; t0 += kTile) {
+#pragma unroll
     for (int w = 0; w < kSortWarps; ++w) of_warp[w][tid] = 0;
     __syncthreads();
-    uint32_t key[kRounds], pos[kRounds], rank[kRounds];
-    // warp w ranks ids [w, w + 1) * kTile / kSortWarps of the tile
+    uint32_t lower = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) lower += w < warp ? warp_sum[w] : 0;
+    base[tid] = lower + inc - all + before;
+  }
+  for (int64_t t0 = lo; t0 < hi; t0 += kTile) {
+    if (t0 > lo) {
+      load(t0);
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) of_warp[w][tid] = 0;
+      __syncthreads();
+    }
 #pragma unroll
     for (int k = 0; k < kRounds; ++k) {
-      const int64_t i = t0 + (warp * kRounds + k) * 32 + lane;
-      const bool on = i < hi;
-      key[k] = !on ? 0xFFFFFFFFu : a.key_in ? a.key_in[i] : first_key(a, i);
-      pos[k] = !on ? 0 : a.pos_in ? a.pos_in[i] : static_cast<uint32_t>(i);
+      const bool on = t0 + (warp * kRounds + k) * 32 + lane < hi;
       const uint32_t d = (key[k] >> a.shift) & mask;
       const uint32_t same = __match_any_sync(0xffffffffu, on ? d : 0xFFFFFFFFu);
       const uint32_t ahead = __popc(same & ((1u << lane) - 1));
@@ -222,11 +238,13 @@ __global__ void __launch_bounds__(kSortThreads) scatter_kernel(const SortArgs a)
     }
     __syncthreads();
     {
-      uint32_t run = base[tid];
+      uint32_t c[kSortWarps], run = base[tid];
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) c[w] = of_warp[w][tid];
+#pragma unroll
       for (int w = 0; w < kSortWarps; ++w) {
-        const uint32_t c = of_warp[w][tid];
         of_warp[w][tid] = run;
-        run += c;
+        run += c[w];
       }
       base[tid] = run;
     }
@@ -241,7 +259,7 @@ __global__ void __launch_bounds__(kSortThreads) scatter_kernel(const SortArgs a)
       a.pos_out[to] = pos[k];
       if (a.hist_next) {
         const uint32_t d = (key[k] >> (a.shift + a.bits)) & mask;
-        atomicAdd(&a.hist_next[d * kMaxChunks + to / a.chunk], 1u);
+        atomicAdd(&a.hist_next[d * kMaxChunks + to / static_cast<uint32_t>(a.chunk)], 1u);
       }
     }
     __syncthreads();
@@ -255,13 +273,28 @@ struct RowsArgs {
   const uint32_t* pos;
   const uint16_t* dy;
   uint16_t* grad;
-  uint32_t* start;       // [n_runs + 1] first token of each run
+  uint32_t* n_spans;     // rows whose tokens span runs: how many,
+  uint4* span;           // and row, first run, last run of each, in any order
   float* out_part;       // [n_runs][width] sums of a run's last row, not done there
   float* in_part;        // [n_runs][width] sums of a run's first row, begun before it
-  int64_t n, vocab, dim, slices, width, n_runs;
+  int64_t n, vocab, dim, width;
+  uint32_t slices, n_runs;
   float scale;
   int32_t accumulate;
 };
+
+// The slice of a run that a warp sums; run is n_runs or more for warps past
+// the last.
+struct Unit {
+  uint32_t run, slice;
+  int64_t c0;
+};
+
+__device__ __forceinline__ Unit unit_of(const RowsArgs& a, uint32_t unit) {
+  const uint32_t run = unit / a.slices;
+  const uint32_t slice = unit - run * a.slices;
+  return Unit{run, slice, static_cast<int64_t>(slice) * kSlice};
+}
 
 // Number of tokens among the first `item` items of the merged list: the
 // tokens with i + key_i < item. All lanes search together, 32 probes a step.
@@ -281,6 +314,20 @@ __device__ __forceinline__ int64_t tokens_before(const uint32_t* key, int64_t n,
   return lo;
 }
 
+// First of the sorted ids [0, n) that is `row` or more; all lanes search.
+__device__ __forceinline__ int64_t first_of(const uint32_t* key, int64_t n, int64_t row, int lane) {
+  int64_t lo = 0, hi = n;
+  while (lo < hi) {
+    const int64_t step = (hi - lo + 31) / 32;
+    const int64_t i = lo + (lane + 1) * step - 1;
+    const int count = __popc(__ballot_sync(0xffffffffu, i < hi && key[i] < row));
+    const int64_t new_hi = lo + (count + 1) * step - 1;
+    hi = new_hi < hi ? new_hi : hi;
+    lo = lo + count * step < hi ? lo + count * step : hi;
+  }
+  return lo;
+}
+
 template <bool kBf16, bool kVecRows>
 __device__ __forceinline__ void store_row(const RowsArgs& a, int64_t v, int64_t c0, int lane,
                                           const float (&sum)[8], bool hit) {
@@ -291,11 +338,11 @@ __device__ __forceinline__ void store_row(const RowsArgs& a, int64_t v, int64_t 
   for (int j = 0; j < 8; ++j) f[j] = sum[j] * a.scale;
   if (a.accumulate) {
     float old[8];
-    widen8<kBf16>(load8<kVecRows>(row, c0, lane, a.dim), old);
+    widen8<kBf16>(load8<kVecRows>(row, c0 + lane * kVec, a.dim), old);
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] += old[j];
   }
-  store8<kVecRows>(row, c0, lane, a.dim, narrow8<kBf16>(f));
+  store8<kVecRows>(row, c0 + lane * kVec, a.dim, narrow8<kBf16>(f));
 }
 
 // fp32 partial sums sit lane by lane: lane l's eight columns at [l * 8, l * 8 + 8)
@@ -306,49 +353,97 @@ __device__ __forceinline__ void store_part(float* part, int64_t c0, int lane,
   p[1] = make_float4(s[4], s[5], s[6], s[7]);
 }
 
+// Zeros for the n elements from p on, rows that follow one another and so one
+// piece of memory whatever their length: share `part` of `parts`, in 16-byte
+// blocks but for the ends.
+__device__ __forceinline__ void clear_share(uint16_t* p, int64_t n, uint32_t part, uint32_t parts,
+                                            int lane) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p), hi = lo + 2 * static_cast<uintptr_t>(n);
+  const uintptr_t in_lo = (lo + 15) & ~static_cast<uintptr_t>(15);
+  const uintptr_t in_hi = hi & ~static_cast<uintptr_t>(15);
+  if (part == 0) {  // at most seven elements before the first block and after the last
+    const uintptr_t head = in_lo < hi ? in_lo : hi;
+    if (lo + 2 * lane < head) p[lane] = 0;
+    if (in_hi >= in_lo && in_hi + 2 * lane < hi) reinterpret_cast<uint16_t*>(in_hi)[lane] = 0;
+  }
+  if (in_hi <= in_lo) return;
+  const uint32_t blocks = static_cast<uint32_t>((in_hi - in_lo) >> 4);
+  const uint32_t per = (blocks + parts - 1) / parts;
+  const uint32_t b0 = part * per, b1 = b0 + per < blocks ? b0 + per : blocks;
+  uint4* q = reinterpret_cast<uint4*>(in_lo);
+#pragma unroll 4
+  for (uint32_t b = b0 + lane; b < b1; b += 32) __stcs(q + b, make_uint4(0, 0, 0, 0));
+}
+
 template <bool kBf16, bool kVecRows>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a) {
   pdl_begin();
   const int lane = threadIdx.x & 31;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int64_t run = unit / a.slices;
-  if (run >= a.n_runs) return;
-  const int64_t c0 = (unit - run * a.slices) * kSlice;
-  const int64_t item0 = run * kRun;
+  const Unit u = unit_of(a, blockIdx.x * kWarps + (threadIdx.x >> 5));
+  if (u.run >= a.n_runs) return;
+  const int64_t run = u.run, c0 = u.c0, item0 = run * kRun;
   const int64_t item1 = item0 + kRun < a.n + a.vocab ? item0 + kRun : a.n + a.vocab;
   const int64_t i0 = tokens_before(a.key, a.n, item0, lane);
-  const int64_t i1 = tokens_before(a.key, a.n, item1, lane);
-  int64_t row = item0 - i0;             // rows done before this run
-  const int64_t row_end = item1 - i1;   // and before the next
-  if (c0 == 0 && lane == 0) a.start[run] = static_cast<uint32_t>(i0);
+  // the run's tokens are among the next kRun: their ids and positions, one or
+  // two per lane, and the id before them
+  constexpr int kPer = kRun / 32;
+  uint32_t key[kPer], pos[kPer];
+  int count = 0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int64_t i = i0 + k * 32 + lane;
+    key[k] = i < a.n ? a.key[i] : 0xFFFFFFFFu;
+    pos[k] = i < a.n ? a.pos[i] : 0;
+  }
+  const uint32_t before = i0 > 0 ? a.key[i0 - 1] : 0xFFFFFFFFu;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int64_t i = i0 + k * 32 + lane;
+    count += __popc(__ballot_sync(0xffffffffu, i < a.n && i + key[k] < item1));
+  }
+  int64_t row = item0 - i0;                      // rows done before this run
+  const int64_t row_end = item1 - (i0 + count);  // and before the next
   // the first row's earlier tokens are in an earlier run
-  bool begun = i0 > 0 && row < a.vocab && a.key[i0 - 1] == row;
+  bool begun = row < a.vocab && before == row;
+  if (begun && row < row_end && c0 == 0) {
+    // and its last in this one: join_kernel will add them up, from the run
+    // that has the row's first token as an item of the merged list
+    const int64_t first = (first_of(a.key, i0, row, lane) + row) / kRun;
+    if (lane == 0)
+      a.span[atomicAdd(a.n_spans, 1u)] =
+          make_uint4(static_cast<uint32_t>(row), static_cast<uint32_t>(first), u.run, 0);
+  }
   bool hit = false;
   float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  const auto done = [&]() {  // row `row` has all its tokens
+  // rows up to `end` have all their tokens: the first the sum, the rest none
+  const auto done_until = [&](int64_t end) {
+    if (row >= end) return;
     if (begun) store_part(a.in_part + run * a.width, c0, lane, sum);
     else store_row<kBf16, kVecRows>(a, row, c0, lane, sum, hit);
     begun = hit = false;
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] = 0.f;
     ++row;
+    if (!a.accumulate && row < end)
+      clear_share(a.grad + row * a.dim, (end - row) * a.dim, u.slice, a.slices, lane);
+    row = end;
   };
-  for (int64_t i = i0; i < i1; i += kBatch) {
+  for (int i = 0; i < count; i += kBatch) {
     uint4 v[kBatch];
-    uint32_t key[kBatch];
+    uint32_t id[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const bool on = i + k < i1;
-      key[k] = on ? a.key[i + k] : 0xFFFFFFFFu;
-      v[k] = on && key[k] < a.vocab
-                 ? load8<kVecRows>(a.dy + static_cast<int64_t>(a.pos[i + k]) * a.dim, c0, lane,
-                                   a.dim)
-                 : make_uint4(0, 0, 0, 0);
+      const int at = i + k;  // kBatch divides 32: one register of the lanes' per batch
+      const uint32_t p = __shfl_sync(0xffffffffu, at < 32 ? pos[0] : pos[kPer - 1], at & 31);
+      id[k] = __shfl_sync(0xffffffffu, at < 32 ? key[0] : key[kPer - 1], at & 31);
+      if (at >= count) id[k] = 0xFFFFFFFFu;
+      if (id[k] < a.vocab)
+        v[k] = load8<kVecRows>(a.dy + static_cast<int64_t>(p) * a.dim, c0 + lane * kVec, a.dim);
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      if (i + k >= i1 || key[k] >= a.vocab) break;
-      while (row < key[k]) done();
+      if (id[k] >= a.vocab) break;
+      done_until(id[k]);
       float f[8];
       widen8<kBf16>(v[k], f);
 #pragma unroll
@@ -356,7 +451,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a) {
       hit = true;
     }
   }
-  while (row < row_end) done();
+  done_until(row_end);
   if (hit || begun) store_part(a.out_part + run * a.width, c0, lane, sum);
 }
 
@@ -366,40 +461,31 @@ template <bool kBf16, bool kVecRows>
 __global__ void __launch_bounds__(kThreads) join_kernel(const RowsArgs a) {
   pdl_begin();
   const int lane = threadIdx.x & 31;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int64_t run = unit / a.slices;
-  if (run >= a.n_runs) return;
-  const int64_t c0 = (unit - run * a.slices) * kSlice;
-  const int64_t i0 = a.start[run];
-  const int64_t row = run * kRun - i0;
-  if (i0 == 0 || row >= a.vocab || a.key[i0 - 1] != row) return;
-  const int64_t item1 = (run + 1) * kRun;
-  const int64_t i1 = run + 1 < a.n_runs ? a.start[run + 1] : a.n;
-  if (run + 1 < a.n_runs && item1 - i1 <= row) return;  // the row goes on in the next run
-  // the row's first token, as an item of the merged list, names its first run
-  int64_t lo = 0, hi = i0;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (a.key[mid] < row) lo = mid + 1;
-    else hi = mid;
-  }
-  float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int64_t k = (lo + row) / kRun; k <= run; ++k) {
-    const float4* p = reinterpret_cast<const float4*>(
-        (k < run ? a.out_part : a.in_part) + k * a.width + c0 + lane * kVec);
-    const float4 x = p[0], y = p[1];
-    const float s[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  const uint32_t units = *a.n_spans * a.slices;
+  for (uint32_t at = blockIdx.x * kWarps + (threadIdx.x >> 5); at < units;
+       at += gridDim.x * kWarps) {
+    const Unit u = unit_of(a, at);
+    const uint4 span = a.span[u.run];
+    const float* part = a.out_part + u.c0 + lane * kVec;
+    float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 8
+    for (uint32_t k = span.y; k <= span.z; ++k) {
+      const float4* p = reinterpret_cast<const float4*>(
+          (k < span.z ? part : a.in_part + u.c0 + lane * kVec) + static_cast<int64_t>(k) * a.width);
+      const float4 x = p[0], y = p[1];
+      const float s[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum[j] += s[j];
+      for (int j = 0; j < 8; ++j) sum[j] += s[j];
+    }
+    store_row<kBf16, kVecRows>(a, span.x, u.c0, lane, sum, true);
   }
-  store_row<kBf16, kVecRows>(a, row, c0, lane, sum, true);
 }
 
 // -------------------------------------------------------------------- host ----
 
 struct Layout {
   int64_t n_runs, width;
-  size_t hist, key[2], pos[2], start, out_part, in_part, bytes;
+  size_t hist, n_spans, key[2], pos[2], span, out_part, in_part, bytes;
 };
 
 Layout layout_of(int64_t n, int64_t vocab, int64_t dim) {
@@ -413,11 +499,12 @@ Layout layout_of(int64_t n, int64_t vocab, int64_t dim) {
     return here;
   };
   l.hist = take(sizeof(uint32_t) * kMaxPasses * kDigits * kMaxChunks);
+  l.n_spans = take(sizeof(uint32_t));
   for (int k = 0; k < 2; ++k) {
     l.key[k] = take(sizeof(uint32_t) * static_cast<size_t>(n));
     l.pos[k] = take(sizeof(uint32_t) * static_cast<size_t>(n));
   }
-  l.start = take(sizeof(uint32_t) * static_cast<size_t>(l.n_runs + 1));
+  l.span = take(sizeof(uint4) * static_cast<size_t>(l.n_runs));
   l.out_part = take(sizeof(float) * static_cast<size_t>(l.n_runs * l.width));
   l.in_part = take(sizeof(float) * static_cast<size_t>(l.n_runs * l.width));
   l.bytes = at;
@@ -427,13 +514,17 @@ Layout layout_of(int64_t n, int64_t vocab, int64_t dim) {
 constexpr int64_t kMaxTokens = int64_t{1} << 28;
 constexpr int64_t kMaxVocab = int64_t{1} << 24;
 constexpr int64_t kMaxGrid = 0x7fffffff;
+constexpr unsigned kJoinGrid = 304;
 
 template <bool kBf16, bool kVecRows>
 int launch_rows(const RowsArgs& a, cudaStream_t st) {
-  const unsigned grid = static_cast<unsigned>(ceil_div(a.n_runs * a.slices, kWarps));
+  const unsigned grid =
+      static_cast<unsigned>(ceil_div(static_cast<int64_t>(a.n_runs) * a.slices, kWarps));
   cudaError_t e = launch_pdl(rows_kernel<kBf16, kVecRows>, dim3(grid), dim3(kThreads), 0, st, a);
-  if (e == cudaSuccess)
-    e = launch_pdl(join_kernel<kBf16, kVecRows>, dim3(grid), dim3(kThreads), 0, st, a);
+  // without tokens no row spans runs
+  if (e == cudaSuccess && a.n > 0)
+    e = launch_pdl(join_kernel<kBf16, kVecRows>, dim3(std::min(grid, kJoinGrid)), dim3(kThreads), 0,
+                   st, a);
   return status_of(e);
 }
 
@@ -502,7 +593,7 @@ ZERO_API int zero_embedding_grad(const void* tokens, int32_t token_bytes, int64_
     return ZERO_EALIGN;
   const Layout l = layout_of(n_tokens, vocab, dim);
   const int64_t slices = ceil_div(dim, kSlice);
-  if (ceil_div(l.n_runs * slices, kWarps) > kMaxGrid) return ZERO_ERANGE;
+  if (l.n_runs * slices > kMaxGrid) return ZERO_ERANGE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   uint32_t* key[2] = {reinterpret_cast<uint32_t*>(ws + l.key[0]),
@@ -523,6 +614,7 @@ ZERO_API int zero_embedding_grad(const void* tokens, int32_t token_bytes, int64_
     s.n_chunks = static_cast<int32_t>(ceil_div(n_tokens, s.chunk));
     s.bits = static_cast<int32_t>(ceil_div(width, passes));
     s.n_hists = passes;
+    s.n_spans = reinterpret_cast<uint32_t*>(ws + l.n_spans);
     uint32_t* hist = reinterpret_cast<uint32_t*>(ws + l.hist);
     s.hist = hist;
     cudaError_t e = launch_pdl(hist_kernel, dim3(s.n_chunks), dim3(kSortThreads), 0, st, s);
@@ -544,15 +636,16 @@ ZERO_API int zero_embedding_grad(const void* tokens, int32_t token_bytes, int64_
   a.pos = pos[last];
   a.dy = static_cast<const uint16_t*>(dy);
   a.grad = static_cast<uint16_t*>(grad);
-  a.start = reinterpret_cast<uint32_t*>(ws + l.start);
+  a.n_spans = reinterpret_cast<uint32_t*>(ws + l.n_spans);
+  a.span = reinterpret_cast<uint4*>(ws + l.span);
   a.out_part = reinterpret_cast<float*>(ws + l.out_part);
   a.in_part = reinterpret_cast<float*>(ws + l.in_part);
   a.n = n_tokens;
   a.vocab = vocab;
   a.dim = dim;
-  a.slices = slices;
+  a.slices = static_cast<uint32_t>(slices);
   a.width = l.width;
-  a.n_runs = l.n_runs;
+  a.n_runs = static_cast<uint32_t>(l.n_runs);
   a.scale = scale;
   a.accumulate = accumulate;
   const bool vec = dim % kVec == 0 && aligned(dy, 16) && aligned(grad, 16);

@@ -68,6 +68,27 @@ __device__ __forceinline__ uint4 narrow8(const float (&f)[8]) {
                     narrow2<kBf16>(f[4], f[5]), narrow2<kBf16>(f[6], f[7]));
 }
 
+// Eight 16-bit elements at any element address, from the one or two 16-byte
+// blocks that hold them; the caller knows that all eight lie in its buffer.
+// The words and the halfword the eight start at are picked in three steps.
+__device__ __forceinline__ uint4 load8_any(const uint16_t* p) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  const uint4* block = reinterpret_cast<const uint4*>(at & ~static_cast<uintptr_t>(15));
+  const uint4 x = __ldg(block);
+  const int d = static_cast<int>(at & 15);
+  if (d == 0) return x;
+  const uint4 y = __ldg(block + 1);
+  const uint32_t c[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  uint32_t t[6], w[5], o[4];
+#pragma unroll
+  for (int j = 0; j < 6; ++j) t[j] = d & 8 ? c[j + 2] : c[j];
+#pragma unroll
+  for (int j = 0; j < 5; ++j) w[j] = d & 4 ? t[j + 1] : t[j];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = d & 2 ? __funnelshift_r(w[j], w[j + 1], 16) : w[j];
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 // Token ids are int32 or int64; an id outside [0, limit) becomes -1.
 __device__ __forceinline__ int64_t load_id(const void* ids, int32_t bytes, int64_t i,
                                            int64_t limit) {
