@@ -24,45 +24,38 @@ using namespace zt;
 constexpr int kRows = 8;        // rows per CTA step, one warp each
 constexpr int kThreads = 32 * kRows;
 constexpr int kCols = 32 * kVec;
-constexpr int kUnroll = 2;      // row steps per CTA
 
 // Eight elements of a row of 16-bit elements starting at column c; those at
-// or past `cols` are 0 (loads) or left alone (stores). kAlign: the bytes every
-// row start is a multiple of (16: one access, 4: two elements each, 2).
-template <int kAlign>
+// or past `cols` are 0. kGrid: rows lie on the 16-byte grid.
+template <bool kGrid>
 __device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t cols) {
-  if constexpr (kAlign == 16) {
-    if (c + kVec <= cols) return __ldcs(reinterpret_cast<const uint4*>(row + c));
-  } else if constexpr (kAlign == 4) {
-    if (c + kVec <= cols) {
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(row + c);
-      return make_uint4(p[0], p[1], p[2], p[3]);
-    }
-  }
+  if (c + kVec <= cols)
+    return kGrid ? __ldcs(reinterpret_cast<const uint4*>(row + c)) : load8_any(row + c);
   uint32_t h[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) h[j] = c + j < cols ? row[c + j] : 0;
   return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
 }
 
-template <int kAlign>
-__device__ __forceinline__ void store8(uint16_t* row, int64_t c, int64_t cols, const uint4& v) {
-  if constexpr (kAlign == 16) {
+// A warp's 256 columns of a row from c0 on, those before `cols`; all lanes
+// call it.
+template <bool kGrid>
+__device__ __forceinline__ void store_row(uint8_t* stage, uint16_t* row, int64_t c0, int lane,
+                                          int64_t cols, const uint4& v) {
+  const int64_t c = c0 + lane * kVec;
+  if constexpr (kGrid) {
     if (c + kVec <= cols) {
       __stcs(reinterpret_cast<uint4*>(row + c), v);
       return;
     }
-  } else if constexpr (kAlign == 4) {
-    if (c + kVec <= cols) {
-      uint32_t* p = reinterpret_cast<uint32_t*>(row + c);
-      p[0] = v.x, p[1] = v.y, p[2] = v.z, p[3] = v.w;
-      return;
-    }
-  }
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (c + j < cols) row[c + j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+    for (int j = 0; j < 8; ++j)
+      if (c + j < cols) row[c + j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+  } else {
+    const int64_t left = cols - c0;
+    if (left > 0) store_any(stage, row + c0, left < kCols ? static_cast<int>(left) : kCols, lane, v);
+  }
 }
 
 __device__ __forceinline__ float pow2(int k) {  // 2^k, -127 < k < 128
@@ -179,13 +172,15 @@ struct Args {
 
 enum Op { kSave, kLoad, kGelu, kSwiglu, kGeluGrad, kSwigluGrad };
 
-template <int kOp, bool kBf16, int kAlign>
+template <int kOp, bool kBf16, bool kGrid, int kUnroll>
 __global__ void __launch_bounds__(kThreads) ckpt_kernel(const Args a) {
   pdl_begin();
+  __shared__ __align__(16) uint8_t stages[kGrid ? 1 : kRows][kGrid ? 16 : kStageWarp];
+  uint8_t* stage = stages[kGrid ? 0 : threadIdx.x >> 5];
   const int lane = threadIdx.x & 31;
   const int64_t tile = blockIdx.x;
   const int64_t row_tile = tile / a.col_tiles;
-  const int64_t c = (tile - row_tile * a.col_tiles) * kCols + lane * kVec;
+  const int64_t c0 = (tile - row_tile * a.col_tiles) * kCols, c = c0 + lane * kVec;
   const int64_t row0 = row_tile * (kRows * kUnroll) + (threadIdx.x >> 5);
   const bool in = c < a.pitch;
   const int64_t blk = a.pitch / ZERO_CKPT_BLOCK;
@@ -196,8 +191,8 @@ __global__ void __launch_bounds__(kThreads) ckpt_kernel(const Args a) {
       const int64_t r = row0 + k * kRows;
       vx[k] = vu[k] = make_uint4(0, 0, 0, 0);
       if (r >= a.rows) continue;
-      vx[k] = load8<kAlign>(a.x + r * a.ld, c, a.cols);
-      if constexpr (kOp == kSwiglu) vu[k] = load8<kAlign>(a.u + r * a.ld, c, a.cols);
+      vx[k] = load8<kGrid>(a.x + r * a.ld, c, a.cols);
+      if constexpr (kOp == kSwiglu) vu[k] = load8<kGrid>(a.u + r * a.ld, c, a.cols);
     }
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
@@ -214,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) ckpt_kernel(const Args a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           y[j] = kOp == kSwiglu ? x[j] * sigmoid(x[j]).p * u[j] : x[j] * gelu_gate(x[j]).p;
-        store8<kAlign>(a.y + r * a.ld_y, c, a.cols, narrow8<kBf16>(y));
+        store_row<kGrid>(stage, a.y + r * a.ld_y, c0, lane, a.cols, narrow8<kBf16>(y));
       }
     }
   } else {
@@ -234,16 +229,16 @@ __global__ void __launch_bounds__(kThreads) ckpt_kernel(const Args a) {
         qu[k] = __ldcs(reinterpret_cast<const uint2*>(a.ku.q + r * a.pitch + c));
         su[k] = a.ku.scale[r * blk + c / ZERO_CKPT_BLOCK];
       }
-      if constexpr (kOp != kLoad) vd[k] = load8<kAlign>(a.dy + r * a.ld_y, c, a.cols);
+      if constexpr (kOp != kLoad) vd[k] = load8<kGrid>(a.dy + r * a.ld_y, c, a.cols);
     }
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
       const int64_t r = row0 + k * kRows;
-      if (r >= a.rows || c >= a.cols) continue;
+      if (r >= a.rows) continue;  // the same for the whole warp
       float x[8], u[8], d[8], y[8], gx[8], gu[8];
       unpack8(qx[k], sx[k], x);
       if constexpr (kOp == kLoad) {
-        store8<kAlign>(a.y + r * a.ld, c, a.cols, narrow8<kBf16>(x));
+        store_row<kGrid>(stage, a.y + r * a.ld, c0, lane, a.cols, narrow8<kBf16>(x));
       } else {
         if constexpr (kOp == kSwigluGrad) unpack8(qu[k], su[k], u);
         widen8<kBf16>(vd[k], d);
@@ -264,16 +259,17 @@ __global__ void __launch_bounds__(kThreads) ckpt_kernel(const Args a) {
             gx[j] = d[j] * __fmaf_rn(y[j] * g.q, z1, g.p);
           }
         }
-        store8<kAlign>(a.dx + r * a.ld, c, a.cols, narrow8<kBf16>(gx));
+        store_row<kGrid>(stage, a.dx + r * a.ld, c0, lane, a.cols, narrow8<kBf16>(gx));
         if constexpr (kOp == kSwigluGrad)
-          store8<kAlign>(a.du + r * a.ld, c, a.cols, narrow8<kBf16>(gu));
-        if (a.y) store8<kAlign>(a.y + r * a.ld, c, a.cols, narrow8<kBf16>(y));
+          store_row<kGrid>(stage, a.du + r * a.ld, c0, lane, a.cols, narrow8<kBf16>(gu));
+        if (a.y) store_row<kGrid>(stage, a.y + r * a.ld, c0, lane, a.cols, narrow8<kBf16>(y));
       }
     }
   }
 }
 
 constexpr int64_t kMaxGrid = 0x7fffffff;
+constexpr int64_t kManyRows = 8 * 8 * 152 * 4;  // rows x column tiles: four turns of all SMs' CTAs
 constexpr int64_t kMaxBytes = int64_t{1} << 62;
 
 int64_t pitch_of(int64_t cols) { return ceil_div(cols, ZERO_CKPT_PAD) * ZERO_CKPT_PAD; }
@@ -289,26 +285,29 @@ Ckpt ckpt_of(const void* p, int64_t rows, int64_t pitch) {
   return Ckpt{q, reinterpret_cast<uint8_t*>(q) + rows * pitch};
 }
 
-template <int kOp>
-int launch(Args& a, int32_t dtype, int align, void* stream) {
-  a.col_tiles = ceil_div(a.pitch, kCols);
+template <int kOp, bool kGrid, int kUnroll>
+int launch_as(Args& a, int32_t dtype, cudaStream_t st) {
   const int64_t grid = a.col_tiles * ceil_div(a.rows, kRows * kUnroll);
   if (grid > kMaxGrid) return ZERO_ERANGE;
-  void (*fn)(const Args) =
-      dtype == ZERO_BF16
-          ? (align == 16 ? ckpt_kernel<kOp, true, 16>
-                         : align == 4 ? ckpt_kernel<kOp, true, 4> : ckpt_kernel<kOp, true, 2>)
-          : (align == 16 ? ckpt_kernel<kOp, false, 16>
-                         : align == 4 ? ckpt_kernel<kOp, false, 4> : ckpt_kernel<kOp, false, 2>);
-  return status_of(launch_pdl(fn, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
-                              static_cast<cudaStream_t>(stream), a));
+  return status_of(launch_pdl(dtype == ZERO_BF16 ? ckpt_kernel<kOp, true, kGrid, kUnroll>
+                                                 : ckpt_kernel<kOp, false, kGrid, kUnroll>,
+                              dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, st, a));
 }
 
-// what every row start of a [.., ld] array of 16-bit elements is a multiple of
-int row_align(const void* p, int64_t ld) {
-  if (aligned(p, 16) && ld % 8 == 0) return 16;
-  return aligned(p, 4) && ld % 2 == 0 ? 4 : 2;
+template <int kOp>
+int launch(Args& a, int32_t dtype, bool on_grid, void* stream) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  a.col_tiles = ceil_div(a.pitch, kCols);
+  if (!on_grid) return launch_as<kOp, false, 1>(a, dtype, st);
+  // two rows per warp once that leaves every SM its CTAs: 204 us against 213 at
+  // SwiGLU 8192 x 8192; one row 9.4 us against 11.1 at GELU 1024 x 2048
+  return a.col_tiles * a.rows >= kManyRows ? launch_as<kOp, true, 2>(a, dtype, st)
+                                           : launch_as<kOp, true, 1>(a, dtype, st);
 }
+
+// whether every row start of a [.., ld] array of 16-bit elements lies on the
+// 16-byte grid
+bool on_grid(const void* p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
 
 }  // namespace zc
 
@@ -337,7 +336,7 @@ ZERO_API int zero_ckpt_save(const void* x, int64_t rows, int64_t cols, int64_t l
   a.x = static_cast<const uint16_t*>(x);
   a.rows = rows, a.cols = cols, a.pitch = pitch_of(cols), a.ld = ld;
   a.kx = ckpt_of(ckpt, rows, a.pitch);
-  return launch<kSave>(a, dtype, row_align(x, ld), stream);
+  return launch<kSave>(a, dtype, on_grid(x, ld), stream);
 }
 
 ZERO_API int zero_ckpt_load(const void* ckpt, int64_t rows, int64_t cols, int32_t dtype,
@@ -351,7 +350,7 @@ ZERO_API int zero_ckpt_load(const void* ckpt, int64_t rows, int64_t cols, int32_
   a.y = static_cast<uint16_t*>(out);
   a.rows = rows, a.cols = cols, a.pitch = pitch_of(cols), a.ld = ld;
   a.kx = ckpt_of(ckpt, rows, a.pitch);
-  return launch<kLoad>(a, dtype, row_align(out, ld), stream);
+  return launch<kLoad>(a, dtype, on_grid(out, ld), stream);
 }
 
 ZERO_API int zero_ckpt_act(int32_t act, const void* x, const void* u, int64_t rows, int64_t cols,
@@ -374,7 +373,7 @@ ZERO_API int zero_ckpt_act(int32_t act, const void* x, const void* u, int64_t ro
   a.rows = rows, a.cols = cols, a.pitch = pitch_of(cols), a.ld = ld, a.ld_y = ld_y;
   a.kx = ckpt_of(ckpt_x, rows, a.pitch);
   if (gated) a.ku = ckpt_of(ckpt_u, rows, a.pitch);
-  const int align = std::min({row_align(x, ld), row_align(u, ld), row_align(y, ld_y)});
+  const bool align = on_grid(x, ld) && on_grid(u, ld) && on_grid(y, ld_y);
   return gated ? launch<kSwiglu>(a, dtype, align, stream) : launch<kGelu>(a, dtype, align, stream);
 }
 
@@ -401,7 +400,8 @@ ZERO_API int zero_ckpt_act_grad(int32_t act, const void* ckpt_x, const void* ckp
   a.rows = rows, a.cols = cols, a.pitch = pitch_of(cols), a.ld = ld, a.ld_y = ld_dy;
   a.kx = ckpt_of(ckpt_x, rows, a.pitch);
   if (gated) a.ku = ckpt_of(ckpt_u, rows, a.pitch);
-  const int align = std::min({row_align(dy, ld_dy), row_align(dx, ld), row_align(du, ld), row_align(y, ld)});
+  const bool align =
+      on_grid(dy, ld_dy) && on_grid(dx, ld) && on_grid(du, ld) && on_grid(y, ld);
   return gated ? launch<kSwigluGrad>(a, dtype, align, stream)
                : launch<kGeluGrad>(a, dtype, align, stream);
 }

@@ -66,23 +66,24 @@ __device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t d
   return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
 }
 
+// The warp's slice of a row from column c0 on; all lanes call it.
 template <bool kVecRows>
-__device__ __forceinline__ void store8(uint16_t* row, int64_t c, int64_t dim, const uint4& v) {
+__device__ __forceinline__ void store_slice(uint8_t* stage, uint16_t* row, int64_t c0, int lane,
+                                            int64_t dim, const uint4& v) {
   if constexpr (kVecRows) {
+    const int64_t c = c0 + lane * kVec;
     if (c < dim) __stcs(reinterpret_cast<uint4*>(row + c), v);
   } else {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    // word stores where the lane's first element lies on one
-    if ((reinterpret_cast<uintptr_t>(row + c) & 3) == 0 && c + kVec <= dim) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) reinterpret_cast<uint32_t*>(row + c)[j] = w[j];
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (c + j < dim) row[c + j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
-    }
+    const int64_t left = dim - c0;
+    store_any(stage, row + c0, left < kSlice ? static_cast<int>(left) : kSlice, lane, v);
   }
 }
+
+// stages of the CTA's warps for store_slice
+template <bool kVecRows>
+struct Stages {
+  __align__(16) uint8_t of_warp[kVecRows ? 1 : kWarps][kVecRows ? 16 : kStageWarp];
+};
 
 // ------------------------------------------------------------------ lookup ----
 
@@ -98,6 +99,8 @@ struct LookupArgs {
 template <bool kBf16, bool kVecRows>
 __global__ void __launch_bounds__(kThreads) lookup_kernel(const LookupArgs a) {
   pdl_begin();
+  __shared__ Stages<kVecRows> stages;
+  uint8_t* stage = stages.of_warp[kVecRows ? 0 : threadIdx.x >> 5];
   const int lane = threadIdx.x & 31;
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (unit >= a.units) return;
@@ -121,7 +124,7 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const LookupArgs a) {
     widen8<kBf16>(v[k], f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] *= a.scale;
-    store8<kVecRows>(a.out + t * a.dim, c0 + lane * kVec, a.dim, narrow8<kBf16>(f));
+    store_slice<kVecRows>(stage, a.out + t * a.dim, c0, lane, a.dim, narrow8<kBf16>(f));
   }
 }
 
@@ -329,8 +332,8 @@ __device__ __forceinline__ int64_t first_of(const uint32_t* key, int64_t n, int6
 }
 
 template <bool kBf16, bool kVecRows>
-__device__ __forceinline__ void store_row(const RowsArgs& a, int64_t v, int64_t c0, int lane,
-                                          const float (&sum)[8], bool hit) {
+__device__ __forceinline__ void store_row(const RowsArgs& a, uint8_t* stage, int64_t v,
+                                          int64_t c0, int lane, const float (&sum)[8], bool hit) {
   if (a.accumulate && !hit) return;
   uint16_t* row = a.grad + v * a.dim;
   float f[8];
@@ -342,7 +345,7 @@ __device__ __forceinline__ void store_row(const RowsArgs& a, int64_t v, int64_t 
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] += old[j];
   }
-  store8<kVecRows>(row, c0 + lane * kVec, a.dim, narrow8<kBf16>(f));
+  store_slice<kVecRows>(stage, row, c0, lane, a.dim, narrow8<kBf16>(f));
 }
 
 // fp32 partial sums sit lane by lane: lane l's eight columns at [l * 8, l * 8 + 8)
@@ -378,6 +381,8 @@ __device__ __forceinline__ void clear_share(uint16_t* p, int64_t n, uint32_t par
 template <bool kBf16, bool kVecRows>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a) {
   pdl_begin();
+  __shared__ Stages<kVecRows> stages;
+  uint8_t* stage = stages.of_warp[kVecRows ? 0 : threadIdx.x >> 5];
   const int lane = threadIdx.x & 31;
   const Unit u = unit_of(a, blockIdx.x * kWarps + (threadIdx.x >> 5));
   if (u.run >= a.n_runs) return;
@@ -419,7 +424,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a) {
   const auto done_until = [&](int64_t end) {
     if (row >= end) return;
     if (begun) store_part(a.in_part + run * a.width, c0, lane, sum);
-    else store_row<kBf16, kVecRows>(a, row, c0, lane, sum, hit);
+    else store_row<kBf16, kVecRows>(a, stage, row, c0, lane, sum, hit);
     begun = hit = false;
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] = 0.f;
@@ -460,6 +465,8 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a) {
 template <bool kBf16, bool kVecRows>
 __global__ void __launch_bounds__(kThreads) join_kernel(const RowsArgs a) {
   pdl_begin();
+  __shared__ Stages<kVecRows> stages;
+  uint8_t* stage = stages.of_warp[kVecRows ? 0 : threadIdx.x >> 5];
   const int lane = threadIdx.x & 31;
   const uint32_t units = *a.n_spans * a.slices;
   for (uint32_t at = blockIdx.x * kWarps + (threadIdx.x >> 5); at < units;
@@ -477,7 +484,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const RowsArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum[j] += s[j];
     }
-    store_row<kBf16, kVecRows>(a, span.x, u.c0, lane, sum, true);
+    store_row<kBf16, kVecRows>(a, stage, span.x, u.c0, lane, sum, true);
   }
 }
 

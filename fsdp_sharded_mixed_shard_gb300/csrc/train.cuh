@@ -68,16 +68,9 @@ __device__ __forceinline__ uint4 narrow8(const float (&f)[8]) {
                     narrow2<kBf16>(f[4], f[5]), narrow2<kBf16>(f[6], f[7]));
 }
 
-// Eight 16-bit elements at any element address, from the one or two 16-byte
-// blocks that hold them; the caller knows that all eight lie in its buffer.
-// The words and the halfword the eight start at are picked in three steps.
-__device__ __forceinline__ uint4 load8_any(const uint16_t* p) {
-  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-  const uint4* block = reinterpret_cast<const uint4*>(at & ~static_cast<uintptr_t>(15));
-  const uint4 x = __ldg(block);
-  const int d = static_cast<int>(at & 15);
-  if (d == 0) return x;
-  const uint4 y = __ldg(block + 1);
+// The 16 bytes that start d bytes (d even, 0 <= d < 16) into x and run on
+// into y, the block after it: words and halfword picked in three steps.
+__device__ __forceinline__ uint4 shifted(const uint4& x, const uint4& y, int d) {
   const uint32_t c[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
   uint32_t t[6], w[5], o[4];
 #pragma unroll
@@ -87,6 +80,49 @@ __device__ __forceinline__ uint4 load8_any(const uint16_t* p) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) o[j] = d & 2 ? __funnelshift_r(w[j], w[j + 1], 16) : w[j];
   return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Eight 16-bit elements at any element address, from the one or two 16-byte
+// blocks that hold them; the caller knows that all eight lie in its buffer.
+__device__ __forceinline__ uint4 load8_any(const uint16_t* p) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  const uint4* block = reinterpret_cast<const uint4*>(at & ~static_cast<uintptr_t>(15));
+  const uint4 x = *block;
+  const int d = static_cast<int>(at & 15);
+  return d ? shifted(x, block[1], d) : x;
+}
+
+// A warp's store of up to 256 neighbouring elements to any element address,
+// eight per lane (v), `count` of them in all: through shared memory, so that
+// whole 16-byte blocks of the destination leave as such and only the elements
+// before the first and after the last go one by one. All lanes call it; stage
+// is the warp's own kStageWarp bytes, 16-byte aligned.
+constexpr int kStageWarp = 16 + 512 + 16;
+
+__device__ __forceinline__ void store_any(uint8_t* stage, uint16_t* to, int count, int lane,
+                                          const uint4& v) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(to);
+  const int d = static_cast<int>(at & 15);
+  uint4* mine = reinterpret_cast<uint4*>(stage + 16);
+  __syncwarp();  // the stage's last use is read
+  mine[lane] = v;
+  __syncwarp();
+  // destination block k: bytes [16 k - d, 16 k - d + 16) of the run
+  uint8_t* blocks = reinterpret_cast<uint8_t*>(at - d);
+  const int bytes = 2 * count;
+  const auto block = [&](int k) {
+    if (16 * k - d < 0 || 16 * k - d + 16 > bytes) return;
+    const uint4 x = mine[k - (d ? 1 : 0)];
+    const uint4 y = mine[k];
+    __stcs(reinterpret_cast<uint4*>(blocks + 16 * k), d ? shifted(x, y, 16 - d) : x);
+  };
+  block(lane);  // block 32 is never whole unless d is 0, and then it is past the run
+  // at most seven elements before the first whole block and after the last
+  const uint16_t* elems = reinterpret_cast<const uint16_t*>(stage + 16);
+  const int head = d ? min((16 - d) >> 1, count) : 0;
+  const int tail = max(head, (((bytes + d) & ~15) - d) >> 1);
+  if (lane < head) to[lane] = elems[lane];
+  if (tail + lane < count) to[tail + lane] = elems[tail + lane];
 }
 
 // Token ids are int32 or int64; an id outside [0, limit) becomes -1.
