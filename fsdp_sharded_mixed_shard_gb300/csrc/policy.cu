@@ -54,12 +54,6 @@ struct Args {
   float lo, hi, beta;
 };
 
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // exp(x - m) is formed as 2^(x c - m c) with c = log2 e: one fused
 // multiply-add per element, and what m c loses in rounding is the same for
 // every element and cancels. From |m| = 2^100 on m c could overflow; there two
@@ -95,40 +89,6 @@ __device__ __forceinline__ Stat join_lanes(Stat t) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
   return Stat{m, s};
-}
-
-// Two fp32 values as one operand: sm_100's packed fp32 arithmetic does both
-// in one instruction, each rounded to nearest even.
-struct Pair {
-  uint64_t v;
-};
-
-__device__ __forceinline__ Pair pair(float x, float y) {
-  Pair p;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(x), "f"(y));
-  return p;
-}
-
-__device__ __forceinline__ void unpair(const Pair& p, float& x, float& y) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p.v));
-}
-
-__device__ __forceinline__ Pair operator*(const Pair& a, const Pair& b) {
-  Pair p;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
-  return p;
-}
-
-__device__ __forceinline__ Pair fma2(const Pair& a, const Pair& b, const Pair& c) {
-  Pair p;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return p;
-}
-
-__device__ __forceinline__ Pair operator+(const Pair& a, const Pair& b) {
-  Pair p;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
-  return p;
 }
 
 // A 16-byte block of logits.

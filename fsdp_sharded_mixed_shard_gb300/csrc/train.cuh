@@ -19,6 +19,46 @@ namespace zt {
 
 constexpr int kVec = 8;  // 16-bit elements per 16-byte vector
 
+// Two fp32 values as one operand: sm_100's packed fp32 arithmetic does both
+// in one instruction, each rounded to nearest even.
+struct Pair {
+  uint64_t v;
+};
+
+__device__ __forceinline__ Pair pair(float x, float y) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(x), "f"(y));
+  return p;
+}
+
+__device__ __forceinline__ void unpair(const Pair& p, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p.v));
+}
+
+__device__ __forceinline__ Pair operator*(const Pair& a, const Pair& b) {
+  Pair p;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
+  return p;
+}
+
+__device__ __forceinline__ Pair fma2(const Pair& a, const Pair& b, const Pair& c) {
+  Pair p;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return p;
+}
+
+__device__ __forceinline__ Pair operator+(const Pair& a, const Pair& b) {
+  Pair p;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
+  return p;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // One 16-bit element (its bits) to fp32, exactly.
 template <bool kBf16>
 __device__ __forceinline__ float widen(uint32_t bits) {

@@ -58,6 +58,7 @@ constexpr int kMaxSplit = 4;
 constexpr int kValueCycles = 850, kOutCycles = 4000;
 constexpr uint64_t kWaitLimitNs = 2000000000ull, kDrainNs = 1000000ull;
 static_assert(kM * kJoinPitch * 4 <= kRing, "the tile fits the stages");
+static_assert(kGroups == 2, "the second group brings dy when TMA cannot");
 static_assert(kM == ZERO_CKPT_PAD, "a checkpoint row is whole CTA tiles");
 
 struct Args {
@@ -282,62 +283,141 @@ __device__ __forceinline__ Piece load_piece(const Source& s, int64_t q_step, int
   return b;
 }
 
-// Store token row r's 16 values of columns [16 p, 16 p + 16) of the A tile.
-// They are two 16-byte pieces; the upper four of eight lanes store theirs in
-// the other order, so that the eight lanes of a store phase fall on eight
-// different pieces of the 128-byte rows.
+// Token row r's 16 values of columns [16 p, 16 p + 16) of the A tile: two
+// 16-byte pieces. The upper four of eight lanes take theirs in the other
+// order, so that the eight lanes of a store phase fall on eight different
+// pieces of the 128-byte rows.
+struct Values {
+  uint4 v[2];
+};
+
 template <bool kBf16>
-__device__ __forceinline__ void store_values(uint8_t* stage_a, const uint4& q, uint32_t scale,
-                                             int r, int p) {
+__device__ __forceinline__ Values values_of(const uint4& q, uint32_t scale, int p) {
   const uint32_t s = step_pair<kBf16>(scale);
   const bool swap = p >= 4;
-  uint32_t w[4] = {swap ? q.z : q.x, swap ? q.w : q.y, swap ? q.x : q.z, swap ? q.y : q.w};
-  uint8_t* row = stage_a + (p >> 2) * kChunk + r * 128;
-  const int at = (((p & 3) << 1 | (swap ? 1 : 0)) ^ (r & 7)) << 4;
+  const uint32_t w[4] = {swap ? q.z : q.x, swap ? q.w : q.y, swap ? q.x : q.z, swap ? q.y : q.w};
+  Values out;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     uint32_t x0 = w[2 * j], x1 = w[2 * j + 1];
     if constexpr (!kBf16) x0 ^= 0x80808080u, x1 ^= 0x80808080u;
-    *reinterpret_cast<uint4*>(row + (at ^ (j << 4))) =
-        make_uint4(value_pair<kBf16, 0>(x0, s), value_pair<kBf16, 1>(x0, s),
-                   value_pair<kBf16, 0>(x1, s), value_pair<kBf16, 1>(x1, s));
+    out.v[j] = make_uint4(value_pair<kBf16, 0>(x0, s), value_pair<kBf16, 1>(x0, s),
+                          value_pair<kBf16, 0>(x1, s), value_pair<kBf16, 1>(x1, s));
   }
+  return out;
 }
 
-// This CTA's half of dy's tile without TMA: rows that do not start on 16-byte
-// boundaries.
-__device__ __forceinline__ void load_dy(const Args& a, uint8_t* stage_b, int64_t t0, int64_t end,
-                                        int64_t j0, int tid) {
-  const int pieces = a.bn / 16;  // pieces of eight columns per token
-  for (int p = tid; p < kK * pieces; p += kGroupThreads) {
-    const int r = p / pieces, c = p % pieces;
-    const int64_t t = t0 + r, j = j0 + c * 8;
-    uint32_t h[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) h[k] = t < end && j + k < a.n ? a.dy[t * a.ld + j + k] : 0;
-    *reinterpret_cast<uint4*>(stage_b + (c >> 3) * kChunk + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-        make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-  }
+__device__ __forceinline__ void store_values(uint8_t* stage_a, const Values& x, int r, int p) {
+  uint8_t* row = stage_a + (p >> 2) * kChunk + r * 128;
+  const int at = (((p & 3) << 1 | (p >> 2)) ^ (r & 7)) << 4;
+  *reinterpret_cast<uint4*>(row + at) = x.v[0];
+  *reinterpret_cast<uint4*>(row + (at ^ 16)) = x.v[1];
 }
 
-// kCount sums of one row of dw, columns j, j + 1, ...
-template <bool kBf16, int kCount>
-__device__ __forceinline__ void store_sums(const Args& a, int64_t i, int64_t j,
-                                           const float (&f)[kCount]) {
-  if (i >= a.cols) return;
-  uint16_t* p = a.dw + i * a.n + j;
+// dy's half tile without TMA, for rows that do not start on 16-byte
+// boundaries: the 16-byte blocks that hold a token's 128 columns (17 where
+// they do not start on one) are copied as they lie, kRaw steps ahead, and
+// moved to their places in the stage from there. 16 threads per token, four
+// tokens (r, r + 16, ...) each.
+constexpr int kRaw = 5, kRawPitch = 17 * 16, kRawBytes = kK * kRawPitch;
+constexpr int kRounds = kK * 16 / kGroupThreads;
+
+__device__ __forceinline__ void copy_raw(uint8_t* raw, const Args& a, int64_t t0, int64_t end,
+                                         int64_t j0, int tid) {
+  const int c = tid & 15;
 #pragma unroll
-  for (int k = 0; k < kCount; k += 8) {
-    if (a.vec_out && j + k + 8 <= a.n) {
-      *reinterpret_cast<uint4*>(p + k) =
-          make_uint4(narrow2<kBf16>(f[k], f[k + 1]), narrow2<kBf16>(f[k + 2], f[k + 3]),
-                     narrow2<kBf16>(f[k + 4], f[k + 5]), narrow2<kBf16>(f[k + 6], f[k + 7]));
-    } else {
+  for (int k = 0; k < kRounds; ++k) {
+    const int r = (tid >> 4) + k * (kGroupThreads / 16);
+    const int64_t t = t0 + r;
+    const uintptr_t row = reinterpret_cast<uintptr_t>(a.dy + t * a.ld);
+    const uintptr_t stop = t < end ? row + 2 * a.n : 0;  // blocks from here on are zeros
+    const uintptr_t first = (row + 2 * j0) & ~static_cast<uintptr_t>(15);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (j + k + e < a.n && ZCHECK(i * a.n + j + k + e < a.cols * a.n, kSiteStore, i))
-          p[k + e] = narrow<kBf16>(f[k + e]);
+    for (int m = c; m < 17; m += 16) {
+      const uintptr_t from = first + 16 * m;
+      const bool in = from < stop && j0 < a.n;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                       smem_u32(raw + r * kRawPitch + m * 16)),
+                   "l"(in ? from : reinterpret_cast<uintptr_t>(a.dy) & ~static_cast<uintptr_t>(15)),
+                   "r"(in ? 16 : 0)
+                   : "memory");
     }
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+__device__ __forceinline__ void place_raw(const uint8_t* raw, const Args& a, uint8_t* stage_b,
+                                          int64_t t0, int64_t j0, int tid) {
+  const int c = tid & 15;
+  const int64_t left = a.n - (j0 + c * 8);
+  const int keep = left < 8 ? (left > 0 ? static_cast<int>(left) : 0) : 8;
+#pragma unroll
+  for (int k = 0; k < kRounds; ++k) {
+    const int r = (tid >> 4) + k * (kGroupThreads / 16);
+    const int d = static_cast<int>(reinterpret_cast<uintptr_t>(a.dy + (t0 + r) * a.ld + j0) & 15);
+    const uint4* block = reinterpret_cast<const uint4*>(raw + r * kRawPitch) + c;
+    const uint4 v = shifted(block[0], block[1], d);
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if (keep < 8) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = 2 * e + 1 < keep ? w[e] : 2 * e < keep ? w[e] & 0xFFFFu : 0;
+    }
+    *reinterpret_cast<uint4*>(stage_b + (c >> 3) * kChunk + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+        make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// An output warp's 32 rows x kOutCols sums in the 16-bit type. Rows of dw that
+// lie on the 16-byte grid take each lane's row as it is; others go through
+// shared memory, from which eight lanes store a row together, whole blocks as
+// such (a lane storing its own row element by element wrote every 32-byte
+// sector 16 times).
+constexpr int kOutCols = 64, kOutPitch = kOutCols * 2 + 16;
+
+template <bool kBf16>
+__device__ __forceinline__ void store_tile_part(const Args& a, uint8_t* stage, int64_t i0, int64_t j,
+                                                int lane, const float (&f)[32], int c) {
+  // columns [j + c, j + c + 32) of lane's row i0 + lane
+  const int64_t i = i0 + lane;
+  if (a.vec_out && i < a.cols) {
+    uint16_t* p = a.dw + i * a.n + j + c;
+#pragma unroll
+    for (int k = 0; k < 32; k += 8)  // n is a multiple of 8
+      if (j + c + k < a.n && ZCHECK(i * a.n + j + c + k + 8 <= a.cols * a.n, kSiteStore, i))
+        *reinterpret_cast<uint4*>(p + k) =
+            make_uint4(narrow2<kBf16>(f[k], f[k + 1]), narrow2<kBf16>(f[k + 2], f[k + 3]),
+                       narrow2<kBf16>(f[k + 4], f[k + 5]), narrow2<kBf16>(f[k + 6], f[k + 7]));
+  }
+  if (!a.vec_out) {
+    uint4* row = reinterpret_cast<uint4*>(stage + lane * kOutPitch + c * 2);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      row[k] = make_uint4(narrow2<kBf16>(f[8 * k], f[8 * k + 1]), narrow2<kBf16>(f[8 * k + 2], f[8 * k + 3]),
+                          narrow2<kBf16>(f[8 * k + 4], f[8 * k + 5]), narrow2<kBf16>(f[8 * k + 6], f[8 * k + 7]));
+  }
+}
+
+__device__ __forceinline__ void store_staged(const Args& a, const uint8_t* stage, int64_t i0,
+                                             int64_t j, int width, int lane) {
+  if (j >= a.n) return;
+  const int count = a.n - j < width ? static_cast<int>(a.n - j) : width;
+  const int k = lane & 7;
+#pragma unroll 2
+  for (int pass = 0; pass < 8; ++pass) {
+    const int row = pass * 4 + (lane >> 3);
+    if (i0 + row >= a.cols) continue;
+    uint16_t* to = a.dw + (i0 + row) * a.n + j;
+    const int d = static_cast<int>(reinterpret_cast<uintptr_t>(to) & 15), bytes = 2 * count;
+    const uint4* blocks = reinterpret_cast<const uint4*>(stage + row * kOutPitch);
+    const uint16_t* elems = reinterpret_cast<const uint16_t*>(blocks);
+    if (16 * k - d >= 0 && 16 * k - d + 16 <= bytes)
+      *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(to) + 16 * k - d) =
+          d ? shifted(blocks[k - 1], blocks[k], 16 - d) : blocks[k];
+    const int head = d ? min((16 - d) >> 1, count) : 0;
+    const int tail = max(head, (((bytes + d) & ~15) - d) >> 1);
+    if (k < head) to[k] = elems[k];
+    if (tail + k < count) to[tail + k] = elems[tail + k];
   }
 }
 
@@ -374,13 +454,16 @@ template <bool kBf16, bool kTma, int kWide>
 __global__ void __launch_bounds__(kThreads, 1)
     wgrad_kernel(const __grid_constant__ CUtensorMap map, const Args a) {
   pdl_begin();
-  constexpr int kStageBytes = kBytesA + kWide * kBytesB, kStages = kRing / kStageBytes;
+  constexpr int kStageBytes = kBytesA + kWide * kBytesB;
+  constexpr int kStages = kTma ? kRing / kStageBytes : (kRing - kRaw * kRawBytes) / kStageBytes;
+  static_assert(kTma || kWide == 1, "raw copies cover one column group");
   extern __shared__ uint8_t raw[];
   uint8_t* stages = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   // full: in the pair's first CTA, counted by both; empty and done: in each
   __shared__ uint64_t full_a[kStages], full_b[kStages], empty[kStages], done[2], free_sums[2];
   __shared__ uint32_t tmem_base;
   __shared__ int failed, group_ok[kGroups];
+  __shared__ __align__(16) uint8_t out_stage[kOutWarps][32 * kOutPitch];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n_cta = 2 * a.split;
   const int rank = static_cast<int>(blockIdx.x) % n_cta;
@@ -408,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      bar_init(&full_a[s], 2);
+      bar_init(&full_a[s], kTma ? 2 : 4);  // values, and without TMA dy, of both CTAs
       bar_init(&full_b[s], 1);
       bar_init(&empty[s], 1);
     }
@@ -437,61 +520,94 @@ __global__ void __launch_bounds__(kThreads, 1)
       return Source{a.q + (t_begin + t) * a.pitch + i, a.scale + (t_begin + t) * blocks + (i >> 5),
                     c.tile < a.tiles && i < a.pitch ? tokens - t : 0};
     };
-    Cursor ahead = {tile0, 0}, now = {tile0, 0};
+    // both groups in turn with TMA; without, the second brings dy for every step
+    constexpr int kTurn = kTma ? kGroups : 1;
+    const int turn0 = kTma ? group : 0;
+    Cursor ahead = {tile0, 0};
     Ring<kStages> ring;
-    ring.advance(group);
+    ring.advance(turn0);
     Piece next[kAhead];
     Source src = {};
     const auto load = [&]() {
       const Piece b = load_piece(src, 4 * a.pitch, 4 * blocks);
-      ahead.step += kGroups;
+      ahead.step += kTurn;
       if (ahead.step < steps) {
-        src.q += kGroups * kK * a.pitch;
-        src.scale += kGroups * kK * blocks;
-        src.left -= src.left > 0 ? kGroups * kK : 0;
+        src.q += kTurn * kK * a.pitch;
+        src.scale += kTurn * kK * blocks;
+        src.left -= src.left > 0 ? kTurn * kK : 0;
       } else {
         ahead.advance(0, steps, tile_stride);
         src = source_of(ahead);
       }
       return b;
     };
-    if (total > 0) {
-      ahead.advance(group, steps, tile_stride);
-      now = ahead;
-      src = source_of(ahead);
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) next[k] = load();
-    }
     bool ok = true;
-    for (int64_t it = group; it < total && ok; it += kAhead * kGroups) {
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int64_t at = it + k * kGroups;
-        if (at >= total || !ok) break;
-        // one warp of the group asks (many that poll slow what they wait for)
-        if (at >= kStages) {
-          if (warp % kGroupWarps == 0) {
-            const bool free = bar_wait(&empty[ring.stage], ring.parity ^ 1, &failed);
-            if (lane == 0) group_ok[group] = free;
-          }
-          group_sync(group);
-          ok = *static_cast<volatile int*>(&group_ok[group]) != 0;
-          if (!ok) break;
+    // the stage of the step at hand once it is free, or NULL: given up. One
+    // warp of the group asks (many that poll slow what they wait for).
+    const auto free_stage = [&](int64_t at) -> uint8_t* {
+      if (at >= kStages) {
+        if (warp % kGroupWarps == 0) {
+          const bool free = bar_wait(&empty[ring.stage], ring.parity ^ 1, &failed);
+          if (lane == 0) group_ok[group] = free;
         }
-        uint8_t* stage = stages + ring.stage * kStageBytes;
-        store_values<kBf16>(stage, next[k].q[0], next[k].scale[0], r, p);
-        store_values<kBf16>(stage, next[k].q[1], next[k].scale[1], r + 4, p);
-        next[k] = load();
-        if constexpr (!kTma) {
-          for (int w = 0; w < kWide; ++w)
-            load_dy(a, stage + kBytesA + w * kBytesB, t_begin + static_cast<int64_t>(now.step) * kK,
-                    t_end, column_of(now.tile) + w * a.bn + half * (a.bn / 2), tid % kGroupThreads);
-          now.advance(kGroups, steps, tile_stride);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         group_sync(group);
-        if (tid % kGroupThreads == 0) bar_arrive_at(arrive_at + ring.stage * 8);
-        ring.advance(kGroups);
+        ok = *static_cast<volatile int*>(&group_ok[group]) != 0;
+      }
+      return ok ? stages + ring.stage * kStageBytes : nullptr;
+    };
+    const auto stored = [&]() {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      group_sync(group);
+      if (tid % kGroupThreads == 0) bar_arrive_at(arrive_at + ring.stage * 8);
+      ring.advance(kTurn);
+    };
+    if (!kTma && group == 1) {
+      const int id = tid % kGroupThreads;
+      uint8_t* raw_ring = stages + kStages * kStageBytes;
+      const auto token = [&](const Cursor& c) { return t_begin + static_cast<int64_t>(c.step) * kK; };
+      const auto column = [&](const Cursor& c) { return column_of(c.tile) + half * (a.bn / 2); };
+      Cursor now = ahead;
+      const auto copy = [&](int64_t at, int slot) {  // a group of copies, empty past the end
+        copy_raw(raw_ring + slot * kRawBytes, a, token(ahead), at < total ? t_end : 0, column(ahead), id);
+        ahead.advance(1, steps, tile_stride);
+      };
+      int slot = 0;
+      for (int k = 0; k < kRaw && total > 0; ++k) copy(k, k);
+      for (int64_t at = 0; at < total; ++at) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 1) : "memory");
+        uint8_t* stage = free_stage(at);
+        if (!stage) break;
+        group_sync(group);  // every thread's copies of this step have landed
+        place_raw(raw_ring + slot * kRawBytes, a, stage + kBytesA, token(now), column(now), id);
+        now.advance(1, steps, tile_stride);
+        stored();
+        copy(at + kRaw, slot);
+        slot = slot + 1 == kRaw ? 0 : slot + 1;
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+      if (total > 0) {
+        ahead.advance(turn0, steps, tile_stride);
+        src = source_of(ahead);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) next[k] = load();
+      }
+      for (int64_t it = turn0; it < total && ok; it += kAhead * kTurn) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int64_t at = it + k * kTurn;
+          if (at >= total || !ok) break;
+          // worked out before the stage is free: only the stores stand between
+          // that and the products
+          const Values v0 = values_of<kBf16>(next[k].q[0], next[k].scale[0], p);
+          const Values v1 = values_of<kBf16>(next[k].q[1], next[k].scale[1], p);
+          uint8_t* stage = free_stage(at);
+          if (!stage) break;
+          store_values(stage, v0, r, p);
+          store_values(stage, v1, r + 4, p);
+          stored();
+          next[k] = load();  // not before: the proxy fence would wait for it
+        }
       }
     }
   } else if (warp == kCopyWarp) {
@@ -572,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (steps > 0) ok = ok && bar_wait(&done[buf], use & 1, &failed);
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t sums = tmem + (static_cast<uint32_t>(row0) << 16) + buf * kN;
-      const int64_t i = row_of(tile) + row0 + lane, j = column_of(tile);
+      const int64_t i0 = row_of(tile) + row0, j = column_of(tile);
 #pragma unroll 1
       for (int c = 0; c < kWide * a.bn; c += 32) {
         float f[32];
@@ -583,7 +699,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 32; ++e) f[e] = ok ? 0.f : __uint_as_float(0x7FC00000u);
         }
         if (a.split == 1) {
-          store_sums<kBf16>(a, i, j + c, f);
+          uint8_t* stage = out_stage[warp - kOutWarp0];
+          store_tile_part<kBf16>(a, stage, i0, j + (c & ~(kOutCols - 1)), lane, f, c & (kOutCols - 1));
+          if (!a.vec_out && ((c & 32) || c + 32 == kWide * a.bn)) {
+            __syncwarp();
+            store_staged(a, stage, i0, j + (c & ~(kOutCols - 1)), (c & 32) + 32, lane);
+            __syncwarp();
+          }
         } else {
           float4* p = reinterpret_cast<float4*>(
               reinterpret_cast<float*>(stages) + (row0 + lane) * kJoinPitch + c);
@@ -601,27 +723,46 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();
   if (failed && tid == 0 && a.scaler) atomicCAS(&a.scaler->error, 0, ZERO_DEVERR_TIMEOUT);
   if (a.split > 1) {
-    // one tile per cluster: this CTA's share of its rows, eight columns per thread and turn
+    // one tile per cluster: this CTA's share of its rows, a warp per row and
+    // eight columns per lane
     const float* tile_sums = reinterpret_cast<const float*>(stages);
-    const int share = kM / a.split, groups = a.bn / 8;
-    for (int p = tid; p < share * groups; p += kThreads) {
-      const int row = part * share + p / groups, c = p % groups * 8;
+    const int share = kM / a.split;
+    const int64_t j = column_of(tile0);
+    // the output warps' stages as one, a row's worth for each warp
+    uint8_t* stage = &out_stage[0][0] + warp * ((kStageWarp + 15) & ~15);
+    for (int m = warp; m < share; m += kThreads / 32) {
+      const int row = part * share + m;
+      const int64_t i = row_of(tile0) + row;
+      if (i >= a.cols) break;
       float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      for (int k = 0; k < a.split; ++k) {
-        const uint32_t remote = in_cta(tile_sums + row * kJoinPitch + c, 2 * k + half);
-        float4 x, y;
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-                     : "r"(remote)
-                     : "memory");
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
-                     : "r"(remote + 16)
-                     : "memory");
-        f[0] += x.x, f[1] += x.y, f[2] += x.z, f[3] += x.w;
-        f[4] += y.x, f[5] += y.y, f[6] += y.z, f[7] += y.w;
+      if (lane * 8 < a.bn) {
+        float4 x[kMaxSplit], y[kMaxSplit];
+#pragma unroll
+        for (int k = 0; k < kMaxSplit; ++k) {
+          if (k >= a.split) break;
+          const uint32_t remote = in_cta(tile_sums + row * kJoinPitch + lane * 8, 2 * k + half);
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(x[k].x), "=f"(x[k].y), "=f"(x[k].z), "=f"(x[k].w)
+                       : "r"(remote));
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(y[k].x), "=f"(y[k].y), "=f"(y[k].z), "=f"(y[k].w)
+                       : "r"(remote + 16));
+        }
+#pragma unroll
+        for (int k = 0; k < kMaxSplit; ++k) {
+          if (k >= a.split) break;
+          f[0] += x[k].x, f[1] += x[k].y, f[2] += x[k].z, f[3] += x[k].w;
+          f[4] += y[k].x, f[5] += y[k].y, f[6] += y[k].z, f[7] += y[k].w;
+        }
       }
-      store_sums<kBf16>(a, row_of(tile0) + row, column_of(tile0) + c, f);
+      const int64_t left = a.n - j;
+      const int count = left < a.bn ? static_cast<int>(left) : a.bn;
+      uint16_t* to = a.dw + i * a.n + j;
+      if (a.vec_out) {
+        if (lane * 8 < count) *reinterpret_cast<uint4*>(to + lane * 8) = narrow8<kBf16>(f);
+      } else {
+        store_any(stage, to, count, lane, narrow8<kBf16>(f));
+      }
     }
     cluster_sync();  // no CTA ends while another reads its sums
   }
@@ -672,12 +813,6 @@ int launch(const CUtensorMap& map, const Args& a, int clusters, cudaStream_t st)
   return status_of(cudaLaunchKernelEx(&cfg, fn, map, a));
 }
 
-template <bool kBf16, bool kTma>
-int launch_wide(const CUtensorMap& map, const Args& a, int wide, int clusters, cudaStream_t st) {
-  return wide == 2 ? launch<kBf16, kTma, 2>(map, a, clusters, st)
-                   : launch<kBf16, kTma, 1>(map, a, clusters, st);
-}
-
 }  // namespace zw
 
 #ifdef ZERO_CHECKED
@@ -713,6 +848,7 @@ ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return ZERO_ECUDA;
   const int64_t pairs = std::max(1, sms / 2), m_tiles = ceil_div(a.pitch, 2 * kM);
+  const bool tma = rows > 0 && ld % kVec == 0 && aligned(dy, 16);
   // Tile width by the tensor-core cycles it takes, turns of all pairs times
   // steps: a step takes 2 cycles per column, at least kValueCycles for the
   // checkpoint's values; two column groups share those but leave the tensor
@@ -720,7 +856,7 @@ ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const
   const int64_t steps = ceil_div(rows, kK);
   int wide = 1;
   int64_t best = 0;
-  for (int w = 1; w <= 2; ++w)
+  for (int w = 1; w <= (tma ? 2 : 1); ++w)
     for (int bn = kN; bn >= 128; bn -= 32) {
       const int64_t turns = ceil_div(m_tiles * ceil_div(n, w * bn), pairs);
       const int64_t cost = turns * (steps * std::max<int64_t>(2 * w * bn, kValueCycles) +
@@ -741,7 +877,6 @@ ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const
     a.split *= 2;
   const int clusters = static_cast<int>(std::min(tiles, a.split > 1 ? tiles : pairs));
   const bool bf16 = dtype == ZERO_BF16;
-  const bool tma = rows > 0 && ld % kVec == 0 && aligned(dy, 16);
   CUtensorMap map = {};
   if (tma) {
     const EncodeTiled encode = encode_tiled();
@@ -756,10 +891,12 @@ ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const
       return ZERO_ECUDA;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (bf16) return tma ? launch_wide<true, true>(map, a, wide, clusters, st)
-                       : launch_wide<true, false>(map, a, wide, clusters, st);
-  return tma ? launch_wide<false, true>(map, a, wide, clusters, st)
-             : launch_wide<false, false>(map, a, wide, clusters, st);
+  if (!tma) return bf16 ? launch<true, false, 1>(map, a, clusters, st)
+                        : launch<false, false, 1>(map, a, clusters, st);
+  if (wide == 2) return bf16 ? launch<true, true, 2>(map, a, clusters, st)
+                             : launch<false, true, 2>(map, a, clusters, st);
+  return bf16 ? launch<true, true, 1>(map, a, clusters, st)
+              : launch<false, true, 1>(map, a, clusters, st);
 }
 
 }  // extern "C"
