@@ -34,8 +34,7 @@ namespace zp {
 
 using namespace zt;
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxWarps = 8;   // per CTA; 1, 2, 4 or 8 by the row's length
 constexpr int kMaxCluster = 8;
 constexpr int kParts = 2;      // parts of a row per warp
 constexpr int kBatch = 4;      // blocks per lane and step
@@ -324,7 +323,7 @@ __device__ __forceinline__ uint4 own_part(const Row& r, int32_t b, const uint4& 
 // after next only once every CTA has sent for the next row, hence read this
 // one.
 struct Exchange {
-  Stat of_warp[kWarps];
+  Stat of_warp[kMaxWarps];
   Stat of_cta[kMaxCluster];
   uint64_t arrived;
 };
@@ -351,6 +350,7 @@ __device__ __forceinline__ void send(Stat* to, uint64_t* bar, uint32_t rank, con
 
 // The statistics of a row from its warps' pairs, by warp 0 of every CTA of
 // the cluster; its lanes hold the same bits afterwards. `use` counts the calls.
+template <int kWarps>
 __device__ __forceinline__ Stat join_all(Exchange (&x)[2], uint32_t rank, uint32_t n_cta,
                                          uint32_t use) {
   const uint32_t lane = threadIdx.x & 31;
@@ -373,9 +373,10 @@ __device__ __forceinline__ Stat join_all(Exchange (&x)[2], uint32_t rank, uint32
 }
 
 // The row's logits as a single stream: statistics only.
-template <int kType>
-__global__ void __launch_bounds__(kThreads) logp_kernel(const Args a) {
+template <int kType, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps) logp_kernel(const Args a) {
   pdl_begin();
+  constexpr int kThreads = 32 * kWarps;
   using B = Block<kType>;
   __shared__ Exchange exchange[2];
   const int tid = threadIdx.x;
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(kThreads) logp_kernel(const Args a) {
       t = join_lanes(t);
       if ((tid & 31) == 0) exchange[use & 1].of_warp[tid >> 5] = t;
       __syncthreads();
-      if (tid < 32) lp = log_share(picked, join_all(exchange, rank, n_cta, use));
+      if (tid < 32) lp = log_share(picked, join_all<kWarps>(exchange, rank, n_cta, use));
       ++use;
     }
     if (rank == 0 && tid == 0) a.logp[row] = lp;
@@ -426,8 +427,8 @@ struct Turn {
   float slope, inv;  // dloss/dlogp with its factors, and -slope / sum
 };
 
-template <int kType>
-__global__ void __launch_bounds__(kThreads, 3) policy_kernel(const Args a, const int32_t part_cap) {
+template <int kType, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, 24 / kWarps) policy_kernel(const Args a, const int32_t part_cap) {
   pdl_begin();
   using B = Block<kType>;
   extern __shared__ __align__(16) uint8_t stage[];
@@ -523,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 3) policy_kernel(const Args a, const
       n.next = next;
       float lp = 0.f, loss = 0.f;
       if (on) {
-        const Stat t = join_all(exchange, rank, n_cta, use);
+        const Stat t = join_all<kWarps>(exchange, rank, n_cta, use);
         lp = log_share(taken, t);
         const float ratio = expf(lp - old);
         const float plain = ratio * adv, held = fminf(fmaxf(ratio, a.lo), a.hi) * adv;
@@ -679,22 +680,23 @@ __global__ void __launch_bounds__(1024) stats_kernel(const Args a) {
   }
 }
 
+constexpr int kLaneBlocks = 16;
 constexpr int kStageCap = 196 * 1024;  // a CTA's share of a row, at most
 constexpr int kStageGoal = 72 * 1024;  // three CTAs per SM
 
 // bytes of shared memory per CTA for rows of at most `blocks` blocks
-int64_t stage_bytes(int64_t blocks, int n_cta, int32_t* part_cap) {
-  const int64_t cap = ceil_div(blocks, static_cast<int64_t>(n_cta) * kWarps * kParts);
+int64_t stage_bytes(int64_t blocks, int n_cta, int warps, int32_t* part_cap) {
+  const int64_t cap = ceil_div(blocks, static_cast<int64_t>(n_cta) * warps * kParts);
   *part_cap = static_cast<int32_t>(cap);
-  return cap * 16 * kWarps * kParts;
+  return cap * 16 * warps * kParts;
 }
 
 struct Launch {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  Launch(int64_t clusters, int n_cta, size_t smem, cudaStream_t st) : cfg(), attr() {
+  Launch(int64_t clusters, int n_cta, int warps, size_t smem, cudaStream_t st) : cfg(), attr() {
     cfg.gridDim = dim3(static_cast<unsigned>(clusters * n_cta));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(32 * warps);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -709,7 +711,7 @@ struct Launch {
 
 // Clusters of `fn` the device holds at once (0 on error). One more would
 // wait for a whole row of rows: the grid is exactly these.
-int resident_clusters(const void* fn, int n_cta, size_t smem) {
+int resident_clusters(const void* fn, int n_cta, int warps, size_t smem) {
   static std::mutex mu;
   static std::map<std::tuple<const void*, int, int, size_t>, int> known;
   int dev = 0;
@@ -717,13 +719,24 @@ int resident_clusters(const void* fn, int n_cta, size_t smem) {
   std::lock_guard<std::mutex> lock(mu);
   int& n = known[std::make_tuple(fn, dev, n_cta, smem)];
   if (n == 0) {
-    Launch l(1, n_cta, smem, nullptr);
+    Launch l(1, n_cta, warps, smem, nullptr);
     if ((smem && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageCap) !=
                      cudaSuccess) ||
         cudaOccupancyMaxActiveClusters(&n, fn, &l.cfg) != cudaSuccess)
       n = 0;
   }
   return n;
+}
+
+template <int kType, bool kGrad, int kWarps>
+int launch_warps(const Args& a, int n_cta, size_t smem, int32_t cap, cudaStream_t st) {
+  const void* fn = kGrad ? reinterpret_cast<const void*>(policy_kernel<kType, kWarps>)
+                         : reinterpret_cast<const void*>(logp_kernel<kType, kWarps>);
+  const int most = resident_clusters(fn, n_cta, kWarps, smem);
+  if (most <= 0) return ZERO_ECUDA;
+  Launch l(std::min<int64_t>(a.rows, most), n_cta, kWarps, smem, st);
+  return status_of(kGrad ? cudaLaunchKernelEx(&l.cfg, policy_kernel<kType, kWarps>, a, cap)
+                         : cudaLaunchKernelEx(&l.cfg, logp_kernel<kType, kWarps>, a));
 }
 
 template <int kType, bool kGrad>
@@ -733,21 +746,27 @@ int launch(const Args& a, cudaStream_t st) {
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return ZERO_ECUDA;
-  int n_cta = 1;
+  // Warps per CTA: up to kLaneBlocks blocks per lane, so that short rows run
+  // many to an SM (2000 rows of 1111: 8 warps 23.4 us, 1 warp SHORT us); more
+  // warps, then more CTAs, while few rows would leave SMs idle and each lane
+  // keeps two blocks.
+  int warps = 1, n_cta = 1;
   int32_t cap = 0;
-  while (n_cta < kMaxCluster && kGrad && stage_bytes(blocks, n_cta, &cap) > kStageGoal) n_cta *= 2;
-  // few rows: more CTAs per row while each keeps two blocks per thread
-  while (n_cta < kMaxCluster && a.rows * n_cta < 2 * sms && blocks / n_cta > 2 * kThreads)
+  while (warps < kMaxWarps && blocks > kLaneBlocks * 32 * warps) warps *= 2;
+  while (warps < kMaxWarps && a.rows * warps < 8 * sms && blocks > 2 * 2 * 32 * warps) warps *= 2;
+  while (n_cta < kMaxCluster && kGrad && stage_bytes(blocks, n_cta, warps, &cap) > kStageGoal)
     n_cta *= 2;
-  const int64_t smem = kGrad ? stage_bytes(blocks, n_cta, &cap) : 0;
+  while (n_cta < kMaxCluster && a.rows * n_cta < 2 * sms && blocks > 2 * 2 * 32 * warps * n_cta)
+    n_cta *= 2;
+  const int64_t smem = kGrad ? stage_bytes(blocks, n_cta, warps, &cap) : 0;
   if (smem > kStageCap) return ZERO_ERANGE;
-  const void* fn = kGrad ? reinterpret_cast<const void*>(policy_kernel<kType>)
-                         : reinterpret_cast<const void*>(logp_kernel<kType>);
-  const int most = resident_clusters(fn, n_cta, static_cast<size_t>(smem));
-  if (most <= 0) return ZERO_ECUDA;
-  Launch l(std::min<int64_t>(a.rows, most), n_cta, static_cast<size_t>(smem), st);
-  return status_of(kGrad ? cudaLaunchKernelEx(&l.cfg, policy_kernel<kType>, a, cap)
-                         : cudaLaunchKernelEx(&l.cfg, logp_kernel<kType>, a));
+  const size_t bytes = static_cast<size_t>(smem);
+  switch (warps) {
+    case 1: return launch_warps<kType, kGrad, 1>(a, n_cta, bytes, cap, st);
+    case 2: return launch_warps<kType, kGrad, 2>(a, n_cta, bytes, cap, st);
+    case 4: return launch_warps<kType, kGrad, 4>(a, n_cta, bytes, cap, st);
+    default: return launch_warps<kType, kGrad, 8>(a, n_cta, bytes, cap, st);
+  }
 }
 
 template <bool kGrad>

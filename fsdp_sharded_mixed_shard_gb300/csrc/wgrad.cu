@@ -318,53 +318,51 @@ __device__ __forceinline__ void store_values(uint8_t* stage_a, const Values& x, 
 // boundaries: the 16-byte blocks that hold a token's 128 columns (17 where
 // they do not start on one) are copied as they lie, kRaw steps ahead, and
 // moved to their places in the stage from there. 16 threads per token, four
-// tokens (r, r + 16, ...) each.
+// tokens (r, r + 16, ...) each. A step is 64 rows, 16 rows 32 ld bytes and a
+// tile's columns whole blocks, so the distance d of a thread's first byte from
+// its block is the same in every token, step and tile.
 constexpr int kRaw = 5, kRawPitch = 17 * 16, kRawBytes = kK * kRawPitch;
 constexpr int kRounds = kK * 16 / kGroupThreads;
 
-__device__ __forceinline__ void copy_raw(uint8_t* raw, const Args& a, int64_t t0, int64_t end,
-                                         int64_t j0, int tid) {
-  const int c = tid & 15;
+struct RawSource {
+  uintptr_t block;   // this thread's block of its first token of the next step to copy
+  int32_t left;      // tokens from there on
+  bool in, in_last;  // whether that block, and (16th thread's) the 17th, hold columns of dy
+};
+
+__device__ __forceinline__ void copy_raw(const RawSource& s, uint32_t raw, uintptr_t any,
+                                         int64_t row16, int c) {
 #pragma unroll
   for (int k = 0; k < kRounds; ++k) {
-    const int r = (tid >> 4) + k * (kGroupThreads / 16);
-    const int64_t t = t0 + r;
-    const uintptr_t row = reinterpret_cast<uintptr_t>(a.dy + t * a.ld);
-    const uintptr_t stop = t < end ? row + 2 * a.n : 0;  // blocks from here on are zeros
-    const uintptr_t first = (row + 2 * j0) & ~static_cast<uintptr_t>(15);
-#pragma unroll
-    for (int m = c; m < 17; m += 16) {
-      const uintptr_t from = first + 16 * m;
-      const bool in = from < stop && j0 < a.n;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                       smem_u32(raw + r * kRawPitch + m * 16)),
-                   "l"(in ? from : reinterpret_cast<uintptr_t>(a.dy) & ~static_cast<uintptr_t>(15)),
-                   "r"(in ? 16 : 0)
+    const uintptr_t from = s.block + k * row16;
+    const uint32_t to = raw + k * (16 * kRawPitch);
+    const bool on = s.left > 16 * k;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
+                 "l"(on && s.in ? from : any), "r"(on && s.in ? 16 : 0)
+                 : "memory");
+    if (c == 15)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + 16),
+                   "l"(on && s.in_last ? from + 16 : any), "r"(on && s.in_last ? 16 : 0)
                    : "memory");
-    }
   }
-  asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-__device__ __forceinline__ void place_raw(const uint8_t* raw, const Args& a, uint8_t* stage_b,
-                                          int64_t t0, int64_t j0, int tid) {
-  const int c = tid & 15;
-  const int64_t left = a.n - (j0 + c * 8);
-  const int keep = left < 8 ? (left > 0 ? static_cast<int>(left) : 0) : 8;
+// d: the thread's distance; keep: columns of its piece that dy has
+__device__ __forceinline__ void place_raw(const uint8_t* raw, uint8_t* stage_b, int r, int c, int d,
+                                          int keep) {
 #pragma unroll
   for (int k = 0; k < kRounds; ++k) {
-    const int r = (tid >> 4) + k * (kGroupThreads / 16);
-    const int d = static_cast<int>(reinterpret_cast<uintptr_t>(a.dy + (t0 + r) * a.ld + j0) & 15);
-    const uint4* block = reinterpret_cast<const uint4*>(raw + r * kRawPitch) + c;
-    const uint4 v = shifted(block[0], block[1], d);
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const uint4* block = reinterpret_cast<const uint4*>(raw + (r + 16 * k) * kRawPitch) + c;
+    uint4 v = shifted(block[0], block[1], d);
     if (keep < 8) {
+      uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         w[e] = 2 * e + 1 < keep ? w[e] : 2 * e < keep ? w[e] & 0xFFFFu : 0;
+      v = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    *reinterpret_cast<uint4*>(stage_b + (c >> 3) * kChunk + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-        make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(stage_b + (c >> 3) * kChunk + (r + 16 * k) * 128 +
+                              (((c & 7) ^ (r & 7)) << 4)) = v;
   }
 }
 
@@ -562,26 +560,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       ring.advance(kTurn);
     };
     if (!kTma && group == 1) {
-      const int id = tid % kGroupThreads;
+      const int row = (tid % kGroupThreads) >> 4, c = tid & 15;
       uint8_t* raw_ring = stages + kStages * kStageBytes;
-      const auto token = [&](const Cursor& c) { return t_begin + static_cast<int64_t>(c.step) * kK; };
-      const auto column = [&](const Cursor& c) { return column_of(c.tile) + half * (a.bn / 2); };
-      Cursor now = ahead;
-      const auto copy = [&](int64_t at, int slot) {  // a group of copies, empty past the end
-        copy_raw(raw_ring + slot * kRawBytes, a, token(ahead), at < total ? t_end : 0, column(ahead), id);
-        ahead.advance(1, steps, tile_stride);
+      const uint32_t raw_at = smem_u32(raw_ring) + row * kRawPitch + c * 16;
+      const uintptr_t base = reinterpret_cast<uintptr_t>(a.dy);
+      const uintptr_t any = base & ~static_cast<uintptr_t>(15);
+      const int64_t row16 = 32 * a.ld;
+      const int d = static_cast<int>((base + 2 * row * a.ld) & 15);
+      const auto column = [&](int tile) { return column_of(tile) + half * (a.bn / 2); };
+      const auto source_of = [&](const Cursor& at) {
+        const int64_t t = t_begin + static_cast<int64_t>(at.step) * kK + row;
+        const int64_t byte = 2 * column(at.tile) - d + 16 * c;  // of the row
+        return RawSource{base + 2 * t * a.ld + byte, static_cast<int32_t>(t_end - t),
+                         byte < 2 * a.n, byte + 16 < 2 * a.n};
       };
-      int slot = 0;
-      for (int k = 0; k < kRaw && total > 0; ++k) copy(k, k);
+      const auto keep_of = [&](int tile) {
+        const int64_t left = a.n - (column(tile) + 8 * c);
+        return left < 8 ? (left > 0 ? static_cast<int>(left) : 0) : 8;
+      };
+      Cursor now = ahead;
+      RawSource raw = source_of(ahead);
+      int keep = keep_of(now.tile), slot = 0;
+      const auto copy = [&](bool on, int to) {  // one group of copies, empty past the end
+        if (on) copy_raw(raw, raw_at + to * kRawBytes, any, row16, c);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (++ahead.step < steps) {
+          raw.block += 4 * row16;
+          raw.left -= kK;
+        } else {
+          ahead.advance(0, steps, tile_stride);
+          raw = source_of(ahead);
+        }
+      };
+      for (int k = 0; k < kRaw && total > 0; ++k) copy(k < total, k);
       for (int64_t at = 0; at < total; ++at) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 1) : "memory");
         uint8_t* stage = free_stage(at);
         if (!stage) break;
         group_sync(group);  // every thread's copies of this step have landed
-        place_raw(raw_ring + slot * kRawBytes, a, stage + kBytesA, token(now), column(now), id);
-        now.advance(1, steps, tile_stride);
+        place_raw(raw_ring + slot * kRawBytes, stage + kBytesA, row, c, d, keep);
+        if (++now.step == steps) {
+          now.advance(0, steps, tile_stride);
+          keep = keep_of(now.tile);
+        }
         stored();
-        copy(at + kRaw, slot);
+        copy(at + kRaw < total, slot);
         slot = slot + 1 == kRaw ? 0 : slot + 1;
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
