@@ -747,7 +747,7 @@ int launch(const Args& a, cudaStream_t st) {
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return ZERO_ECUDA;
   // Warps per CTA: up to kLaneBlocks blocks per lane, so that short rows run
-  // many to an SM (2000 rows of 1111: 8 warps 23.4 us, 1 warp SHORT us); more
+  // many to an SM (2000 rows of 1111: 8 warps 23.4 us, 1 warp 12.6 us); more
   // warps, then more CTAs, while few rows would leave SMs idle and each lane
   // keeps two blocks.
   int warps = 1, n_cta = 1;

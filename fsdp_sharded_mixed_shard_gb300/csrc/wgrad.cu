@@ -37,6 +37,7 @@
 #include "train.cuh"
 
 #include <algorithm>
+#include <mutex>
 
 namespace zw {
 
@@ -55,7 +56,9 @@ constexpr int kRing = 192 * 1024;              // shared memory for stages
 constexpr int kJoinPitch = kN + 4;             // fp32 row of a tile in shared memory
 constexpr int kSmem = kRing + 1024;
 constexpr int kMaxSplit = 4;
-constexpr int kValueCycles = 850, kOutCycles = 4000;
+// costs in cycles, from times at 768 x 2304 and 2048 x 8192 over 1 to 8192 tokens:
+// a step's values, a column put out, the join of a split
+constexpr int kValueCycles = 850, kOutCycles = 28, kJoinCycles = 3500;
 constexpr uint64_t kWaitLimitNs = 2000000000ull, kDrainNs = 1000000ull;
 static_assert(kM * kJoinPitch * 4 <= kRing, "the tile fits the stages");
 static_assert(kGroups == 2, "the second group brings dy when TMA cannot");
@@ -451,7 +454,6 @@ struct Ring {  // stage and the parity of its current use
 template <bool kBf16, bool kTma, int kWide>
 __global__ void __launch_bounds__(kThreads, 1)
     wgrad_kernel(const __grid_constant__ CUtensorMap map, const Args a) {
-  pdl_begin();
   constexpr int kStageBytes = kBytesA + kWide * kBytesB;
   constexpr int kStages = kTma ? kRing / kStageBytes : (kRing - kRaw * kRawBytes) / kStageBytes;
   static_assert(kTma || kWide == 1, "raw copies cover one column group");
@@ -505,6 +507,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_base;
+  // all up to here touches only this cluster's own memory and may run beside
+  // the kernel before this one
+  pdl_begin();
 
   if (warp < kCopyWarp) {
     // value warps: thread -> tokens r and r + 4 of a step, columns [16 p, 16 p + 16)
@@ -815,25 +820,53 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
+struct Launch {
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  Launch(int clusters, int split, cudaStream_t st) : cfg(), attr() {
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * 2 * split));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = kProgrammaticLaunch ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2 * split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+  }
+};
+
 template <bool kBf16, bool kTma, int kWide>
 int launch(const CUtensorMap& map, const Args& a, int clusters, cudaStream_t st) {
   const auto fn = wgrad_kernel<kBf16, kTma, kWide>;
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
     return ZERO_ECUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * 2 * a.split));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = kProgrammaticLaunch ? 1 : 0;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2 * a.split;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return status_of(cudaLaunchKernelEx(&cfg, fn, map, a));
+  Launch l(clusters, a.split, st);
+  return status_of(cudaLaunchKernelEx(&l.cfg, fn, map, a));
+}
+
+// Clusters of `split` pairs that the device holds at once (0 on error): SMs
+// come in groups that a cluster does not leave, so clusters of eight use fewer
+// of them than pairs do.
+int resident_clusters(int split) {
+  constexpr int kDevices = 64;
+  static std::mutex mu;
+  static int known[kDevices][kMaxSplit + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  int& n = known[dev][split];
+  if (n == 0) {
+    const auto fn = wgrad_kernel<true, true, 1>;
+    Launch l(1, split, nullptr);
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, fn, &l.cfg) != cudaSuccess)
+      n = 0;
+  }
+  return n;
 }
 
 }  // namespace zw
@@ -866,38 +899,38 @@ ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const
   a.scaler = d_scaler;
   a.rows = rows, a.cols = cols, a.n = n, a.ld = ld;
   a.vec_out = n % kVec == 0 && aligned(dw, 16);
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return ZERO_ECUDA;
-  const int64_t pairs = std::max(1, sms / 2), m_tiles = ceil_div(a.pitch, 2 * kM);
+  int fit[kMaxSplit + 1];
+  for (int split = 1; split <= kMaxSplit; split *= 2)
+    if ((fit[split] = resident_clusters(split)) <= 0) return ZERO_ECUDA;
+  const int64_t pairs = fit[1], m_tiles = ceil_div(a.pitch, 2 * kM);
   const bool tma = rows > 0 && ld % kVec == 0 && aligned(dy, 16);
-  // Tile width by the tensor-core cycles it takes, turns of all pairs times
-  // steps: a step takes 2 cycles per column, at least kValueCycles for the
-  // checkpoint's values; two column groups share those but leave the tensor
-  // cores idle while a tile is put out.
+  // Tile width, column groups and split of the tokens by the cycles they take:
+  // turns of all pairs times steps of 2 cycles per column, at least
+  // kValueCycles for the checkpoint's values; a tile put out alone at the end
+  // (two groups: every tile), and the join of a split. A split needs room for
+  // all its clusters at once and four steps in each part.
   const int64_t steps = ceil_div(rows, kK);
   int wide = 1;
   int64_t best = 0;
   for (int w = 1; w <= (tma ? 2 : 1); ++w)
-    for (int bn = kN; bn >= 128; bn -= 32) {
-      const int64_t turns = ceil_div(m_tiles * ceil_div(n, w * bn), pairs);
-      const int64_t cost = turns * (steps * std::max<int64_t>(2 * w * bn, kValueCycles) +
-                                    (w == 2 ? kOutCycles : 0));
-      if (best == 0 || cost < best) {
-        best = cost;
-        a.bn = bn;
-        wide = w;
+    for (int bn = kN; bn >= 128; bn -= 32)
+      for (int split = 1; split <= (w == 1 ? kMaxSplit : 1); split *= 2) {
+        const int64_t all = m_tiles * ceil_div(n, w * bn), turns = ceil_div(all, pairs);
+        if (split > 1 && (all > fit[split] || steps < 4 * split)) break;
+        const int64_t cost =
+            turns * ceil_div(steps, split) * std::max<int64_t>(2 * w * bn, kValueCycles) +
+            (w == 2 ? turns : 1) * kOutCycles * w * bn + (split > 1 ? kJoinCycles : 0);
+        if (best == 0 || cost < best) {
+          best = cost;
+          a.bn = bn;
+          a.split = split;
+          wide = w;
+        }
       }
-    }
   const int64_t tiles = m_tiles * ceil_div(n, wide * a.bn);
   if (tiles > 0x3fffffff) return ZERO_ERANGE;
   a.m_tiles = static_cast<int32_t>(m_tiles);
   a.tiles = static_cast<int32_t>(tiles);
-  // split the tokens while pairs would be idle and a part keeps four steps
-  a.split = 1;
-  while (wide == 1 && a.split < kMaxSplit && tiles * a.split * 2 <= pairs && rows >= a.split * 2 * 4 * kK)
-    a.split *= 2;
   const int clusters = static_cast<int>(std::min(tiles, a.split > 1 ? tiles : pairs));
   const bool bf16 = dtype == ZERO_BF16;
   CUtensorMap map = {};
