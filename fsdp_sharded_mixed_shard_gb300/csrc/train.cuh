@@ -108,9 +108,10 @@ __device__ __forceinline__ uint4 narrow8(const float (&f)[8]) {
                     narrow2<kBf16>(f[4], f[5]), narrow2<kBf16>(f[6], f[7]));
 }
 
-// The 16 bytes that start d bytes (d even, 0 <= d < 16) into x and run on
+// The 16 bytes that start d bytes (d even, 0 <= d <= 16) into x and run on
 // into y, the block after it: words and halfword picked in three steps.
 __device__ __forceinline__ uint4 shifted(const uint4& x, const uint4& y, int d) {
+  if (d == 16) return y;
   const uint32_t c[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
   uint32_t t[6], w[5], o[4];
 #pragma unroll
@@ -152,9 +153,9 @@ __device__ __forceinline__ void store_any(uint8_t* stage, uint16_t* to, int coun
   const int bytes = 2 * count;
   const auto block = [&](int k) {
     if (16 * k - d < 0 || 16 * k - d + 16 > bytes) return;
-    const uint4 x = mine[k - (d ? 1 : 0)];
+    const uint4 x = mine[k - 1];
     const uint4 y = mine[k];
-    __stcs(reinterpret_cast<uint4*>(blocks + 16 * k), d ? shifted(x, y, 16 - d) : x);
+    __stcs(reinterpret_cast<uint4*>(blocks + 16 * k), shifted(x, y, 16 - d));
   };
   block(lane);  // block 32 is never whole unless d is 0, and then it is past the run
   // at most seven elements before the first whole block and after the last

@@ -318,35 +318,36 @@ __device__ __forceinline__ void store_values(uint8_t* stage_a, const Values& x, 
 }
 
 // dy's half tile without TMA, for rows that do not start on 16-byte
-// boundaries: the 16-byte blocks that hold a token's 128 columns (17 where
-// they do not start on one) are copied as they lie, kRaw steps ahead, and
-// moved to their places in the stage from there. 16 threads per token, four
-// tokens (r, r + 16, ...) each. A step is 64 rows, 16 rows 32 ld bytes and a
-// tile's columns whole blocks, so the distance d of a thread's first byte from
-// its block is the same in every token, step and tile.
+// boundaries: the copy warp brings the 16-byte blocks that hold a token's 128
+// columns (17 where they do not start on one) as they lie, kRaw steps ahead,
+// and a value group moves them to their places in the stage. (The group's own
+// copies ahead would be waited for by its proxy fence, step by step.) Eight
+// rows are 16 ld bytes, a step 64 rows and a tile's columns whole blocks, so
+// the distance d of a row's first column from its block is the same in every
+// eighth token, in every step and tile.
 constexpr int kRaw = 5, kRawPitch = 17 * 16, kRawBytes = kK * kRawPitch;
 constexpr int kRounds = kK * 16 / kGroupThreads;
 
-struct RawSource {
-  uintptr_t block;   // this thread's block of its first token of the next step to copy
-  int32_t left;      // tokens from there on
-  bool in, in_last;  // whether that block, and (16th thread's) the 17th, hold columns of dy
-};
+__device__ __forceinline__ void copy_block(uint32_t to, uintptr_t from, bool on, uintptr_t any) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(on ? from : any),
+               "r"(on ? 16 : 0)
+               : "memory");
+}
 
-__device__ __forceinline__ void copy_raw(const RawSource& s, uint32_t raw, uintptr_t any,
-                                         int64_t row16, int c) {
+// Lane (class r of eight tokens, quarter g): blocks g, g + 4, g + 8, g + 12 of
+// tokens r, r + 8, ..., and the 17th for g = 0. from: block g of token r;
+// bytes: from there to the end of dy's row; left: tokens from token r on.
+__device__ __forceinline__ void copy_raw(uint32_t raw, uintptr_t from, int64_t bytes, int32_t left,
+                                         int64_t row8, int g, uintptr_t any) {
 #pragma unroll
-  for (int k = 0; k < kRounds; ++k) {
-    const uintptr_t from = s.block + k * row16;
-    const uint32_t to = raw + k * (16 * kRawPitch);
-    const bool on = s.left > 16 * k;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
-                 "l"(on && s.in ? from : any), "r"(on && s.in ? 16 : 0)
-                 : "memory");
-    if (c == 15)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + 16),
-                   "l"(on && s.in_last ? from + 16 : any), "r"(on && s.in_last ? 16 : 0)
-                   : "memory");
+  for (int i = 0; i < kK / 8; ++i) {
+    const bool on = left > 8 * i;
+    const uint32_t to = raw + i * (8 * kRawPitch);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      copy_block(to + 64 * k, from + 64 * k, on && bytes > 64 * k, any);
+    if (g == 0) copy_block(to + 256, from + 256, on && bytes > 256, any);
+    from += row8;
   }
 }
 
@@ -369,56 +370,48 @@ __device__ __forceinline__ void place_raw(const uint8_t* raw, uint8_t* stage_b, 
   }
 }
 
-// An output warp's 32 rows x kOutCols sums in the 16-bit type. Rows of dw that
-// lie on the 16-byte grid take each lane's row as it is; others go through
-// shared memory, from which eight lanes store a row together, whole blocks as
-// such (a lane storing its own row element by element wrote every 32-byte
-// sector 16 times).
-constexpr int kOutCols = 64, kOutPitch = kOutCols * 2 + 16;
-
+// An output warp's 32 columns of its lanes' rows, in the 16-bit type.
 template <bool kBf16>
-__device__ __forceinline__ void store_tile_part(const Args& a, uint8_t* stage, int64_t i0, int64_t j,
-                                                int lane, const float (&f)[32], int c) {
-  // columns [j + c, j + c + 32) of lane's row i0 + lane
-  const int64_t i = i0 + lane;
-  if (a.vec_out && i < a.cols) {
-    uint16_t* p = a.dw + i * a.n + j + c;
+__device__ __forceinline__ void narrow32(const float (&f)[32], uint4 (&v)[4]) {
 #pragma unroll
-    for (int k = 0; k < 32; k += 8)  // n is a multiple of 8
-      if (j + c + k < a.n && ZCHECK(i * a.n + j + c + k + 8 <= a.cols * a.n, kSiteStore, i))
-        *reinterpret_cast<uint4*>(p + k) =
-            make_uint4(narrow2<kBf16>(f[k], f[k + 1]), narrow2<kBf16>(f[k + 2], f[k + 3]),
-                       narrow2<kBf16>(f[k + 4], f[k + 5]), narrow2<kBf16>(f[k + 6], f[k + 7]));
-  }
-  if (!a.vec_out) {
-    uint4* row = reinterpret_cast<uint4*>(stage + lane * kOutPitch + c * 2);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      row[k] = make_uint4(narrow2<kBf16>(f[8 * k], f[8 * k + 1]), narrow2<kBf16>(f[8 * k + 2], f[8 * k + 3]),
-                          narrow2<kBf16>(f[8 * k + 4], f[8 * k + 5]), narrow2<kBf16>(f[8 * k + 6], f[8 * k + 7]));
-  }
+  for (int k = 0; k < 4; ++k)
+    v[k] = make_uint4(narrow2<kBf16>(f[8 * k], f[8 * k + 1]), narrow2<kBf16>(f[8 * k + 2], f[8 * k + 3]),
+                      narrow2<kBf16>(f[8 * k + 4], f[8 * k + 5]), narrow2<kBf16>(f[8 * k + 6], f[8 * k + 7]));
 }
 
-__device__ __forceinline__ void store_staged(const Args& a, const uint8_t* stage, int64_t i0,
-                                             int64_t j, int width, int lane) {
-  if (j >= a.n) return;
-  const int count = a.n - j < width ? static_cast<int>(a.n - j) : width;
-  const int k = lane & 7;
-#pragma unroll 2
+// Rows of dw off the 16-byte grid leave through shared memory, kOutCols columns
+// of 32 rows at a time and eight lanes per row, in the whole blocks of their
+// addresses (a lane storing its own row element by element wrote every 32-byte
+// sector 16 times). A block may begin in the columns before: each row's stage
+// starts with its last eight of those. Only the elements before a tile's first
+// block and after its last go one by one.
+constexpr int kOutCols = 64, kOutPitch = 16 + kOutCols * 2;
+
+// columns [c, c + width) of the tile's row that starts at `to`, which has
+// `count` columns
+__device__ __forceinline__ void store_staged(uint8_t* stage, uint16_t* to, int64_t n, int64_t rows,
+                                             int c, int width, int count, int lane) {
+  const int k = lane & 7, row0 = lane >> 3;
+  const int end = c + width < count ? c + width : count;  // columns there are so far
+#pragma unroll 4
   for (int pass = 0; pass < 8; ++pass) {
-    const int row = pass * 4 + (lane >> 3);
-    if (i0 + row >= a.cols) continue;
-    uint16_t* to = a.dw + (i0 + row) * a.n + j;
-    const int d = static_cast<int>(reinterpret_cast<uintptr_t>(to) & 15), bytes = 2 * count;
-    const uint4* blocks = reinterpret_cast<const uint4*>(stage + row * kOutPitch);
-    const uint16_t* elems = reinterpret_cast<const uint16_t*>(blocks);
-    if (16 * k - d >= 0 && 16 * k - d + 16 <= bytes)
-      *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(to) + 16 * k - d) =
-          d ? shifted(blocks[k - 1], blocks[k], 16 - d) : blocks[k];
-    const int head = d ? min((16 - d) >> 1, count) : 0;
-    const int tail = max(head, (((bytes + d) & ~15) - d) >> 1);
-    if (k < head) to[k] = elems[k];
-    if (tail + k < count) to[tail + k] = elems[tail + k];
+    const int row = pass * 4 + row0;
+    if (row >= rows) continue;
+    uint16_t* at = to + row * n;
+    const int d = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15);
+    const uint4* block = reinterpret_cast<const uint4*>(stage + row * kOutPitch + 16) + k;
+    const int begin = 2 * c + 16 * k - d;  // byte of the row the block starts at
+    if (begin >= 0 && begin + 16 <= 2 * end)
+      *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(at) + begin) =
+          shifted(block[-1], block[0], 16 - d);
+    if (c == 0 || end == count) {
+      const uint16_t* elems = reinterpret_cast<const uint16_t*>(stage + row * kOutPitch + 16);
+      const int head = d ? min((16 - d) >> 1, end) : 0;
+      if (c == 0 && k < head) at[k] = elems[k];
+      // elements of the block that no later columns complete
+      const int tail = max(c == 0 ? head : 0, (((2 * end + d) & ~15) - d) >> 1);
+      if (end == count && tail + k < end) at[tail + k] = elems[tail + k - c];
+    }
   }
 }
 
@@ -461,6 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* stages = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   // full: in the pair's first CTA, counted by both; empty and done: in each
   __shared__ uint64_t full_a[kStages], full_b[kStages], empty[kStages], done[2], free_sums[2];
+  __shared__ uint64_t raw_full[kRaw], raw_empty[kRaw];
   __shared__ uint32_t tmem_base;
   __shared__ int failed, group_ok[kGroups];
   __shared__ __align__(16) uint8_t out_stage[kOutWarps][32 * kOutPitch];
@@ -494,6 +488,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(&full_a[s], kTma ? 2 : 4);  // values, and without TMA dy, of both CTAs
       bar_init(&full_b[s], 1);
       bar_init(&empty[s], 1);
+    }
+    for (int k = 0; k < kRaw && !kTma; ++k) {
+      bar_init(&raw_full[k], 32);
+      bar_init(&raw_empty[k], 1);
     }
     for (int k = 0; k < 2; ++k) {
       bar_init(&done[k], 1);
@@ -566,53 +564,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (!kTma && group == 1) {
       const int row = (tid % kGroupThreads) >> 4, c = tid & 15;
-      uint8_t* raw_ring = stages + kStages * kStageBytes;
-      const uint32_t raw_at = smem_u32(raw_ring) + row * kRawPitch + c * 16;
-      const uintptr_t base = reinterpret_cast<uintptr_t>(a.dy);
-      const uintptr_t any = base & ~static_cast<uintptr_t>(15);
-      const int64_t row16 = 32 * a.ld;
-      const int d = static_cast<int>((base + 2 * row * a.ld) & 15);
-      const auto column = [&](int tile) { return column_of(tile) + half * (a.bn / 2); };
-      const auto source_of = [&](const Cursor& at) {
-        const int64_t t = t_begin + static_cast<int64_t>(at.step) * kK + row;
-        const int64_t byte = 2 * column(at.tile) - d + 16 * c;  // of the row
-        return RawSource{base + 2 * t * a.ld + byte, static_cast<int32_t>(t_end - t),
-                         byte < 2 * a.n, byte + 16 < 2 * a.n};
-      };
+      const uint8_t* raw_ring = stages + kStages * kStageBytes;
+      const int d = static_cast<int>((reinterpret_cast<uintptr_t>(a.dy) + 2 * row * a.ld) & 15);
       const auto keep_of = [&](int tile) {
-        const int64_t left = a.n - (column(tile) + 8 * c);
+        const int64_t left = a.n - (column_of(tile) + half * (a.bn / 2) + 8 * c);
         return left < 8 ? (left > 0 ? static_cast<int>(left) : 0) : 8;
       };
-      Cursor now = ahead;
-      RawSource raw = source_of(ahead);
+      Cursor now = {tile0, 0};
       int keep = keep_of(now.tile), slot = 0;
-      const auto copy = [&](bool on, int to) {  // one group of copies, empty past the end
-        if (on) copy_raw(raw, raw_at + to * kRawBytes, any, row16, c);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (++ahead.step < steps) {
-          raw.block += 4 * row16;
-          raw.left -= kK;
-        } else {
-          ahead.advance(0, steps, tile_stride);
-          raw = source_of(ahead);
-        }
-      };
-      for (int k = 0; k < kRaw && total > 0; ++k) copy(k < total, k);
+      uint32_t raw_parity = 0;
       for (int64_t at = 0; at < total; ++at) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 1) : "memory");
-        uint8_t* stage = free_stage(at);
-        if (!stage) break;
-        group_sync(group);  // every thread's copies of this step have landed
-        place_raw(raw_ring + slot * kRawBytes, stage + kBytesA, row, c, d, keep);
+        if (warp % kGroupWarps == 0) {
+          const bool landed = bar_wait(&raw_full[slot], raw_parity, &failed) &&
+                              (at < kStages || bar_wait(&empty[ring.stage], ring.parity ^ 1, &failed));
+          if (lane == 0) group_ok[group] = landed;
+        }
+        group_sync(group);
+        ok = *static_cast<volatile int*>(&group_ok[group]) != 0;
+        if (!ok) break;
+        place_raw(raw_ring + slot * kRawBytes, stages + ring.stage * kStageBytes + kBytesA, row, c, d,
+                  keep);
         if (++now.step == steps) {
           now.advance(0, steps, tile_stride);
           keep = keep_of(now.tile);
         }
         stored();
-        copy(at + kRaw < total, slot);
-        slot = slot + 1 == kRaw ? 0 : slot + 1;
+        if (tid % kGroupThreads == 0) bar_arrive_at(smem_u32(&raw_empty[slot]));
+        if (++slot == kRaw) {
+          slot = 0;
+          raw_parity ^= 1;
+        }
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
       if (total > 0) {
         ahead.advance(turn0, steps, tile_stride);
@@ -639,7 +621,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == kCopyWarp) {
-    if (kTma && lane == 0) {
+    if constexpr (!kTma) {
+      const int r = lane >> 2, g = lane & 3;
+      const uintptr_t base = reinterpret_cast<uintptr_t>(a.dy);
+      const uintptr_t any = base & ~static_cast<uintptr_t>(15);
+      const int64_t row8 = 16 * a.ld;
+      const int d = static_cast<int>((base + 2 * r * a.ld) & 15);
+      const uint32_t raw_at = smem_u32(stages + kStages * kStageBytes) + r * kRawPitch + g * 16;
+      Cursor now = {tile0, 0};
+      int slot = 0;
+      uint32_t parity = 0;
+      uintptr_t from = 0;
+      int64_t bytes = 0;
+      for (int64_t it = 0; it < total; ++it) {
+        if (now.step == 0) {
+          const int64_t column = 2 * (column_of(now.tile) + half * (a.bn / 2)) - d + 16 * g;
+          from = base + 2 * (t_begin + r) * a.ld + column;
+          bytes = 2 * a.n - column;
+        }
+        int ok = 1;
+        if (it >= kRaw && lane == 0) ok = bar_wait(&raw_empty[slot], parity ^ 1, &failed);
+        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+        const int64_t t = t_begin + static_cast<int64_t>(now.step) * kK + r;
+        copy_raw(raw_at + slot * kRawBytes, from, bytes, static_cast<int32_t>(t_end - t), row8, g, any);
+        // counts this lane's copies when they land
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                         smem_u32(&raw_full[slot]))
+                     : "memory");
+        from += 8 * row8;
+        now.advance(1, steps, tile_stride);
+        if (++slot == kRaw) {
+          slot = 0;
+          parity ^= 1;
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (lane == 0) {
       // one thread's dependent instructions are slow beside 22 warps: what
       // does not change from step to step is worked out before
       const int chunks = (a.bn / 2 + 63) / 64;
@@ -717,6 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t sums = tmem + (static_cast<uint32_t>(row0) << 16) + buf * kN;
       const int64_t i0 = row_of(tile) + row0, j = column_of(tile);
+      uint4 last = make_uint4(0, 0, 0, 0);  // the eight columns before, of this lane's row
 #pragma unroll 1
       for (int c = 0; c < kWide * a.bn; c += 32) {
         float f[32];
@@ -727,12 +745,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 32; ++e) f[e] = ok ? 0.f : __uint_as_float(0x7FC00000u);
         }
         if (a.split == 1) {
-          uint8_t* stage = out_stage[warp - kOutWarp0];
-          store_tile_part<kBf16>(a, stage, i0, j + (c & ~(kOutCols - 1)), lane, f, c & (kOutCols - 1));
-          if (!a.vec_out && ((c & 32) || c + 32 == kWide * a.bn)) {
-            __syncwarp();
-            store_staged(a, stage, i0, j + (c & ~(kOutCols - 1)), (c & 32) + 32, lane);
-            __syncwarp();
+          uint4 v[4];
+          narrow32<kBf16>(f, v);
+          uint16_t* to = a.dw + i0 * a.n + j;  // the tile's columns of this warp's first row
+          if (a.vec_out) {
+            uint4* row = reinterpret_cast<uint4*>(to + lane * a.n + c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)  // n is a multiple of 8
+              if (i0 + lane < a.cols && j + c + 8 * e < a.n &&
+                  ZCHECK((i0 + lane) * a.n + j + c + 8 * e + 8 <= a.cols * a.n, kSiteStore, i0))
+                row[e] = v[e];
+          } else if (j + (c & ~(kOutCols - 1)) < a.n) {
+            uint8_t* stage = out_stage[warp - kOutWarp0];
+            uint4* row = reinterpret_cast<uint4*>(stage + lane * kOutPitch);
+            const int part = c & (kOutCols - 1), count = static_cast<int>(min(a.n - j, static_cast<int64_t>(kWide * a.bn)));
+            if (part == 0) row[0] = last;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) row[1 + part / 8 + e] = v[e];
+            last = v[3];
+            if (part || c + 32 == kWide * a.bn) {
+              __syncwarp();
+              store_staged(stage, to, a.n, a.cols - i0, c - part, part + 32, count, lane);
+              __syncwarp();
+            }
           }
         } else {
           float4* p = reinterpret_cast<float4*>(
