@@ -269,6 +269,124 @@ __global__ void __launch_bounds__(kSortThreads) scatter_kernel(const SortArgs a)
   }
 }
 
+// The whole sort of up to kClusterMost ids by one cluster in one launch: each
+// CTA ranks its eighth of the ids, the CTAs read each other's counts from
+// shared memory, and the order between the passes goes through global memory.
+// The whole gradient against the separate launches: 64 ids 16.9 us, 20.1; 4000
+// ids 33.4, 35.1; 8192 ids the same; 16384 ids 118, 115 (more CTAs rank faster).
+constexpr int kCluster = 8, kClusterRounds = 2;
+constexpr int64_t kClusterMost = static_cast<int64_t>(kCluster) * kClusterRounds * kSortThreads;
+
+struct ClusterArgs {
+  const void* tokens;
+  uint32_t* key[2];
+  uint32_t* pos[2];
+  uint32_t* n_spans;
+  int64_t n, vocab;
+  int32_t token_bytes, bits, passes;
+};
+
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
+          : "memory");
+}
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads)
+    sort_kernel(const ClusterArgs a) {
+  pdl_begin();
+  __shared__ uint32_t count[kDigits];              // this CTA's ids of each digit
+  __shared__ uint32_t of_warp[kSortWarps][kDigits];
+  __shared__ uint32_t warp_sum[kSortWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, me = blockIdx.x;
+  // rounds of 32 ids per warp, the same for every CTA
+  const int rounds = static_cast<int>((a.n + kCluster * kSortThreads - 1) / (kCluster * kSortThreads));
+  const uint32_t n = static_cast<uint32_t>(a.n), mask = (1u << a.bits) - 1;
+  const uint32_t first = (me * kSortWarps + warp) * rounds * 32 + lane;
+  if (me == 0 && tid == 0) *a.n_spans = 0;
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int shift = pass * a.bits, from = (pass - 1) & 1;
+    uint32_t key[kClusterRounds], pos[kClusterRounds], rank[kClusterRounds];
+#pragma unroll
+    for (int k = 0; k < kClusterRounds; ++k) {
+      const uint32_t i = first + k * 32;
+      const bool on = k < rounds && i < n;
+      pos[k] = on ? pass ? a.pos[from][i] : i : 0;
+      key[k] = 0xFFFFFFFFu;
+      if (on && pass) key[k] = a.key[from][i];
+      if (on && !pass) {
+        const int64_t id = load_id(a.tokens, a.token_bytes, i, a.vocab);
+        key[k] = static_cast<uint32_t>(id < 0 ? a.vocab : id);  // padding sorts last
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) of_warp[w][tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kClusterRounds; ++k) {
+      if (k >= rounds) break;
+      const bool on = first + k * 32 < n;
+      const uint32_t d = (key[k] >> shift) & mask;
+      const uint32_t same = __match_any_sync(0xffffffffu, on ? d : 0xFFFFFFFFu);
+      const uint32_t ahead = __popc(same & ((1u << lane) - 1));
+      const uint32_t seen = on ? of_warp[warp][d] : 0;
+      __syncwarp();
+      if (on && ahead == 0) of_warp[warp][d] = seen + __popc(same);
+      __syncwarp();
+      rank[k] = seen + ahead;
+    }
+    __syncthreads();
+    uint32_t c[kSortWarps], run = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) c[w] = of_warp[w][tid];
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) {
+      const uint32_t x = c[w];
+      c[w] = run;
+      run += x;
+    }
+    count[tid] = run;
+    cluster_sync();
+    uint32_t all = 0, before = 0;
+#pragma unroll
+    for (int g = 0; g < kCluster; ++g) {
+      uint32_t remote, x;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                   : "=r"(remote)
+                   : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(&count[tid]))), "r"(g));
+      asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(remote) : "memory");
+      all += x;
+      before += g < me ? x : 0;
+    }
+    uint32_t inc = all;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += y;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    uint32_t base = inc - all + before;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) base += w < warp ? warp_sum[w] : 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) of_warp[w][tid] = base + c[w];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kClusterRounds; ++k) {
+      if (k >= rounds || first + k * 32 >= n) break;
+      const uint32_t to = of_warp[warp][(key[k] >> shift) & mask] + rank[k];
+      if (!ZCHECK(to < n, kSiteStore, to)) continue;
+      a.key[pass & 1][to] = key[k];
+      a.pos[pass & 1][to] = pos[k];
+    }
+    // the next pass reads what all CTAs wrote, and no CTA's counts go (by the
+    // next pass or its end) before all have read them
+    cluster_sync();
+  }
+}
+
 // -------------------------------------------------------------------- rows ----
 
 struct RowsArgs {
@@ -475,7 +593,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const RowsArgs a) {
     const uint4 span = a.span[u.run];
     const float* part = a.out_part + u.c0 + lane * kVec;
     float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 8
+#pragma unroll 16
     for (uint32_t k = span.y; k <= span.z; ++k) {
       const float4* p = reinterpret_cast<const float4*>(
           (k < span.z ? part : a.in_part + u.c0 + lane * kVec) + static_cast<int64_t>(k) * a.width);
@@ -612,29 +730,38 @@ ZERO_API int zero_embedding_grad(const void* tokens, int32_t token_bytes, int64_
     int width = 1;  // bits of the ids, vocab itself (padding) among them
     while ((vocab >> width) != 0) ++width;
     const int passes = static_cast<int>(ceil_div(width, 9));
-    SortArgs s = {};
-    s.tokens = tokens;
-    s.token_bytes = token_bytes;
-    s.n = n_tokens;
-    s.vocab = vocab;
-    s.chunk = ceil_div(ceil_div(n_tokens, kMaxChunks), kTile) * kTile;
-    s.n_chunks = static_cast<int32_t>(ceil_div(n_tokens, s.chunk));
-    s.bits = static_cast<int32_t>(ceil_div(width, passes));
-    s.n_hists = passes;
-    s.n_spans = reinterpret_cast<uint32_t*>(ws + l.n_spans);
-    uint32_t* hist = reinterpret_cast<uint32_t*>(ws + l.hist);
-    s.hist = hist;
-    cudaError_t e = launch_pdl(hist_kernel, dim3(s.n_chunks), dim3(kSortThreads), 0, st, s);
-    for (int p = 0; p < passes && e == cudaSuccess; ++p) {
-      s.key_in = p ? key[(p - 1) & 1] : nullptr;
-      s.pos_in = p ? pos[(p - 1) & 1] : nullptr;
-      last = p & 1;
-      s.key_out = key[last];
-      s.pos_out = pos[last];
-      s.hist = hist + static_cast<size_t>(p) * kDigits * kMaxChunks;
-      s.hist_next = p + 1 < passes ? s.hist + kDigits * kMaxChunks : nullptr;
-      s.shift = p * s.bits;
-      e = launch_pdl(scatter_kernel, dim3(s.n_chunks), dim3(kSortThreads), 0, st, s);
+    const int bits = static_cast<int>(ceil_div(width, passes));
+    uint32_t* n_spans = reinterpret_cast<uint32_t*>(ws + l.n_spans);
+    last = (passes - 1) & 1;
+    cudaError_t e = cudaSuccess;
+    if (n_tokens <= kClusterMost) {
+      ClusterArgs c = {tokens, {key[0], key[1]}, {pos[0], pos[1]}, n_spans, n_tokens, vocab,
+                       token_bytes, bits, passes};
+      e = launch_pdl(sort_kernel, dim3(kCluster), dim3(kSortThreads), 0, st, c);
+    } else {
+      SortArgs s = {};
+      s.tokens = tokens;
+      s.token_bytes = token_bytes;
+      s.n = n_tokens;
+      s.vocab = vocab;
+      s.chunk = ceil_div(ceil_div(n_tokens, kMaxChunks), kTile) * kTile;
+      s.n_chunks = static_cast<int32_t>(ceil_div(n_tokens, s.chunk));
+      s.bits = bits;
+      s.n_hists = passes;
+      s.n_spans = n_spans;
+      uint32_t* hist = reinterpret_cast<uint32_t*>(ws + l.hist);
+      s.hist = hist;
+      e = launch_pdl(hist_kernel, dim3(s.n_chunks), dim3(kSortThreads), 0, st, s);
+      for (int p = 0; p < passes && e == cudaSuccess; ++p) {
+        s.key_in = p ? key[(p - 1) & 1] : nullptr;
+        s.pos_in = p ? pos[(p - 1) & 1] : nullptr;
+        s.key_out = key[p & 1];
+        s.pos_out = pos[p & 1];
+        s.hist = hist + static_cast<size_t>(p) * kDigits * kMaxChunks;
+        s.hist_next = p + 1 < passes ? s.hist + kDigits * kMaxChunks : nullptr;
+        s.shift = p * s.bits;
+        e = launch_pdl(scatter_kernel, dim3(s.n_chunks), dim3(kSortThreads), 0, st, s);
+      }
     }
     if (e != cudaSuccess) return ZERO_ECUDA;
   }
