@@ -128,7 +128,7 @@ __device__ __forceinline__ void save8(const Ckpt& k, int64_t row, int64_t c, int
     q[2 * j] = __float_as_uint(a);
     q[2 * j + 1] = __float_as_uint(b);
   }
-  if (!in) return;
+  if (!in || !ZCHECK(c + kVec <= pitch, kSiteStore, c)) return;
   const auto low_bytes = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
   };
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) ckpt_kernel(const Args a) {
     uint2 qx = make_uint2(0, 0), qu = qx;
     uint32_t sx = 1, su = 1;
     uint4 vd = make_uint4(0, 0, 0, 0);
-    if (in) {
+    if (in && ZCHECK(r < a.rows && c + kVec <= a.pitch, kSiteLoad, c)) {
       qx = __ldcs(reinterpret_cast<const uint2*>(a.kx.q + r * a.pitch + c));
       sx = a.kx.scale[r * blk + c / ZERO_CKPT_BLOCK];
       if constexpr (kOp == kSwigluGrad) {

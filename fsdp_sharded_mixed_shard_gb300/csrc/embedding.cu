@@ -452,7 +452,7 @@ __device__ __forceinline__ int64_t first_of(const uint32_t* key, int64_t n, int6
 template <bool kBf16, bool kVecRows>
 __device__ __forceinline__ void store_row(const RowsArgs& a, uint8_t* stage, int64_t v,
                                           int64_t c0, int lane, const float (&sum)[8], bool hit) {
-  if (a.accumulate && !hit) return;
+  if ((a.accumulate && !hit) || !ZCHECK(v < a.vocab, kSiteStore, v)) return;
   uint16_t* row = a.grad + v * a.dim;
   float f[8];
 #pragma unroll
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] = 0.f;
     ++row;
-    if (!a.accumulate && row < end)
+    if (!a.accumulate && row < end && ZCHECK(end <= a.vocab, kSiteStore, end))
       clear_share(a.grad + row * a.dim, (end - row) * a.dim, u.slice, a.slices, lane);
     row = end;
   };
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a) {
       const uint32_t p = __shfl_sync(0xffffffffu, at < 32 ? pos[0] : pos[kPer - 1], at & 31);
       id[k] = __shfl_sync(0xffffffffu, at < 32 ? key[0] : key[kPer - 1], at & 31);
       if (at >= count) id[k] = 0xFFFFFFFFu;
-      if (id[k] < a.vocab)
+      if (id[k] < a.vocab && ZCHECK(p < a.n, kSiteLoad, p))
         v[k] = load8<kVecRows>(a.dy + static_cast<int64_t>(p) * a.dim, c0 + lane * kVec, a.dim);
     }
 #pragma unroll

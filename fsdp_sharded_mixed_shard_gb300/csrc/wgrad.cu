@@ -272,13 +272,14 @@ struct Source {
   int32_t left;
 };
 
-__device__ __forceinline__ Piece load_piece(const Source& s, int64_t q_step, int64_t scale_step) {
+__device__ __forceinline__ Piece load_piece(const Args& a, const Source& s, int64_t q_step,
+                                            int64_t scale_step) {
   Piece b;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     b.q[k] = make_uint4(0, 0, 0, 0);
     b.scale[k] = 127;
-    if (s.left > 4 * k) {
+    if (s.left > 4 * k && ZCHECK(s.q + k * q_step + 16 <= a.q + a.rows * a.pitch, kSiteLoad, s.left)) {
       b.q[k] = __ldg(reinterpret_cast<const uint4*>(s.q + k * q_step));
       b.scale[k] = __ldg(s.scale + k * scale_step);
     }
@@ -530,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Piece next[kAhead];
     Source src = {};
     const auto load = [&]() {
-      const Piece b = load_piece(src, 4 * a.pitch, 4 * blocks);
+      const Piece b = load_piece(a, src, 4 * a.pitch, 4 * blocks);
       ahead.step += kTurn;
       if (ahead.step < steps) {
         src.q += kTurn * kK * a.pitch;
