@@ -5,7 +5,8 @@
 // (its launch and CTA start-up overlap the previous kernel's tail). Every
 // kernel's first statement waits for the previous grid to complete and its
 // memory to be visible (griddepcontrol.wait, a no-op when there is no
-// programmatic dependency), so no kernel reads or writes anything early;
+// programmatic dependency), so no kernel reads or writes anything early (the
+// weight gradient sets up its own shared and tensor memory before that wait);
 // then it allows its own dependents to be scheduled. A dependent grid is
 // scheduled only after every CTA of this grid has executed the trigger or
 // exited, so a waiting dependent never holds resources the grid still needs.

@@ -712,20 +712,24 @@ struct Launch {
 // Clusters of `fn` the device holds at once (0 on error). One more would
 // wait for a whole row of rows: the grid is exactly these.
 int resident_clusters(const void* fn, int n_cta, int warps, size_t smem) {
-  static std::mutex mu;
-  static std::map<std::tuple<const void*, int, int, size_t>, int> known;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  std::lock_guard<std::mutex> lock(mu);
-  int& n = known[std::make_tuple(fn, dev, n_cta, smem)];
-  if (n == 0) {
-    Launch l(1, n_cta, warps, smem, nullptr);
-    if ((smem && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageCap) !=
-                     cudaSuccess) ||
-        cudaOccupancyMaxActiveClusters(&n, fn, &l.cfg) != cudaSuccess)
-      n = 0;
+  try {
+    static std::mutex mu;
+    static std::map<std::tuple<const void*, int, int, size_t>, int> known;
+    std::lock_guard<std::mutex> lock(mu);
+    int& n = known[std::make_tuple(fn, dev, n_cta, smem)];
+    if (n == 0) {
+      Launch l(1, n_cta, warps, smem, nullptr);
+      if ((smem && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        kStageCap) != cudaSuccess) ||
+          cudaOccupancyMaxActiveClusters(&n, fn, &l.cfg) != cudaSuccess)
+        n = 0;
+    }
+    return n;
+  } catch (...) {  // no exception leaves a C call
+    return 0;
   }
-  return n;
 }
 
 template <int kType, bool kGrad, int kWarps>

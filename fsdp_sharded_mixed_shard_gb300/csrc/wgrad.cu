@@ -37,7 +37,7 @@
 #include "train.cuh"
 
 #include <algorithm>
-#include <mutex>
+#include <atomic>
 
 namespace zw {
 
@@ -888,19 +888,18 @@ int launch(const CUtensorMap& map, const Args& a, int clusters, cudaStream_t st)
 // of them than pairs do.
 int resident_clusters(int split) {
   constexpr int kDevices = 64;
-  static std::mutex mu;
-  static int known[kDevices][kMaxSplit + 1];
+  static std::atomic<int> known[kDevices][kMaxSplit + 1];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
-  std::lock_guard<std::mutex> lock(mu);
-  int& n = known[dev][split];
+  int n = known[dev][split].load(std::memory_order_relaxed);
   if (n == 0) {
     const auto fn = wgrad_kernel<true, true, 1>;
     Launch l(1, split, nullptr);
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
             cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, fn, &l.cfg) != cudaSuccess)
-      n = 0;
+      return 0;
+    known[dev][split].store(n, std::memory_order_relaxed);
   }
   return n;
 }

@@ -564,3 +564,54 @@ def test_results_on_another_stream():
     assert (grad.double() - want).norm() <= 2 * U["bf16"] * want.norm()
     want = x.double().log_softmax(1).gather(1, tok.long()[:, None]).squeeze(1)
     assert (lp.double() - want).abs().max() < 1e-4
+
+
+def test_offsets_past_32_bits():
+    """Buffers of more than 2^32 bytes and 2^31 elements: the last rows are
+    where they should be."""
+    big = 2048 * 1_100_000                       # table elements, 4.5 GB
+    vocab, dim = 1_100_000, 2048
+    table = torch.zeros(big, dtype=torch.bfloat16, device="cuda").view(vocab, dim)
+    table[-1] = rand((1, dim), "bf16", 90)[0]
+    tok = torch.tensor([vocab - 1, 0, vocab - 1], dtype=torch.int32, device="cuda")
+    out = torch.empty(3, dim, dtype=torch.bfloat16, device="cuda")
+    Z.zero_embedding(tok.data_ptr(), 4, 3, table.data_ptr(), vocab, dim, 1.0, Z.ZERO_BF16,
+                     out.data_ptr(), stream())
+    assert torch.equal(out[0], table[-1]) and torch.equal(out[2], table[-1])
+    grad = table.fill_(7.0)
+    dy = rand((3, dim), "bf16", 91)
+    run_grad(tok, dy, vocab, dim, 1.0, "bf16", 0, grad)
+    want = (dy[0].double() + dy[2].double()).to(torch.bfloat16)
+    assert torch.equal(grad[-1], want) and torch.equal(grad[0], dy[1])
+    assert (grad[1:-1:4099] == 0).all() and (grad[-3:-1] == 0).all()
+    del table, grad
+    rows, cols = 70_000, 32_768                  # 2.3e9 activations
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[-1] = rand((1, cols), "bf16", 92)[0]
+    ck = torch.empty(Z.zero_ckpt_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+    Z.zero_ckpt_save(x.data_ptr(), rows, cols, cols, Z.ZERO_BF16, ck.data_ptr(), stream())
+    want = ckpt64(x[-1:])[2]
+    x.fill_(7.0)
+    Z.zero_ckpt_load(ck.data_ptr(), rows, cols, Z.ZERO_BF16, x.data_ptr(), cols, stream())
+    assert torch.equal(x[-1:].double(), want) and (x[:-1:997] == 0).all()
+    dy = torch.zeros(rows, 64, dtype=torch.bfloat16, device="cuda")
+    dy[-1, 3] = 2.0
+    dw = torch.empty(cols, 64, dtype=torch.bfloat16, device="cuda")
+    Z.zero_ckpt_wgrad(ck.data_ptr(), rows, cols, dy.data_ptr(), 64, 64, Z.ZERO_BF16, dw.data_ptr(),
+                      0, stream())
+    assert torch.equal(dw[:, 3].double(), 2.0 * want[0]) and (dw[:, 4:] == 0).all()
+    del x, ck, dy, dw
+    rows, v = 17_000, 128_256                    # 2.2e9 logits
+    x = torch.zeros(rows, v, dtype=torch.bfloat16, device="cuda")
+    x[-1] = rand((1, v), "bf16", 93)[0]
+    want = x[-1].double().log_softmax(0)
+    act = torch.full((rows,), v - 1, dtype=torch.int32, device="cuda")
+    w = torch.zeros(rows, device="cuda")
+    w[-1] = 1.0
+    one, hp = torch.ones(rows, device="cuda"), Z.ZeroPolicyParams(0.2, 0.2, 0.0)
+    lp, _, _ = run_policy(x, v, "bf16", act, one * want[-1].float(), None, one, w, hp, None, x)
+    assert abs(lp[-1].item() - want[-1].item()) < 1e-4 and (lp[:-1] == 0).all()
+    g = want.exp()
+    g[-1] -= 1.0
+    assert (x[-1].double() - g).norm() <= 2 * U["bf16"] * g.norm()
+    assert (x[:-1:997] == 0).all()
