@@ -3,29 +3,39 @@
  *
  * Lookup: out[t, :] = round16(scale * table[id_t, :]). A warp moves a slice of
  * 256 columns of four tokens at a time: four independent row loads in flight
- * per warp. Bound by memory: 2 dim bytes read and written per token.
+ * per warp. Bound by memory: 2 dim bytes read and written per token; 32768 x
+ * 2048 takes 30 us (9.0 TB/s of tokens, frequent rows coming from L2), 1024 x
+ * 768 4.0 us, the time of the call itself.
  *
  * Gradient: grad[v, :] = round16(scale * sum of dy[t, :] over id_t == v). The
  * whole table is written, so the bound is 2 (T + V) dim bytes. Two parts:
  *
  * 1. The ids are sorted, equal ids in the order of their positions, by stable
  *    counting passes over at most 9 bits each (17 bits of id: two passes).
- *    hist_kernel counts the first pass's digits per chunk of the ids;
- *    scatter_kernel ranks every id of its chunk (ids of a warp by
- *    match.any, warps by a scan over their counts), writes (id, position) to
- *    its place and counts the next pass's digits at the chunk that place
- *    belongs to, so each further pass is one launch. Integer counts: the
- *    order of their atomics does not matter.
+ *    Ids of a warp are ranked by match.any, warps by a scan over their counts.
+ *    Up to 8192 ids one cluster of eight CTAs does all passes in one launch
+ *    (sort_kernel). Beyond, hist_kernel counts the first pass's digits per
+ *    chunk of the ids and scatter_kernel places a chunk's ids and counts the
+ *    next pass's digits at the chunk each place belongs to, so each further
+ *    pass is one launch. Integer counts: the order of their atomics does not
+ *    matter.
  * 2. rows_kernel merges the sorted ids with the table's rows into one list --
  *    token, token, "row done", "row done", token, ... -- and cuts it into
  *    runs of kRun items, so that a run costs the same whether it sums the
- *    tokens of one frequent id or writes rows of zeros: item i of the sorted
- *    ids is item i + id_i of the merged list, so a run finds its first token
- *    by one search. A warp sums a run's 256-column slice in registers (eight
- *    tokens' loads in flight) and stores each row as it is done. An id whose
- *    tokens span runs leaves fp32 partial sums in the workspace, which
- *    join_kernel adds in run order. The runs' bounds depend on the ids alone,
- *    so the sums do not change from call to call.
+ *    tokens of one frequent id or clears rows: item i of the sorted ids is
+ *    item i + id_i of the merged list, so a run finds its first token by one
+ *    search of all lanes. A warp sums a run's 256-column slice in registers
+ *    (eight tokens' loads in flight) and stores each row as it is done; rows
+ *    without tokens follow one another in memory and are cleared in 16-byte
+ *    blocks whatever their length. An id whose tokens span runs leaves fp32
+ *    partial sums in the workspace, which join_kernel adds in run order. The
+ *    runs' bounds depend on the ids alone, so the sums do not change from call
+ *    to call.
+ *    Measured: 16384 x 2048 into 128256 rows 115 us (5.2 TB/s of 592 MB;
+ *    rows_kernel alone 96 us, 6.2 TB/s), 8192 x 768 into 50257 rows 36 us, of
+ *    which the sort and the join, bound by latency, take about 15. Runs of 64
+ *    items took 125 and 39 us; four tokens in flight 120 and 43 us; clearing
+ *    the table in a kernel beside the sort 145 and 36 us.
  */
 #include "train.cuh"
 

@@ -21,6 +21,13 @@
  * A row of an odd vocabulary starts anywhere. It is numbered in the 16-byte
  * blocks of its addresses; the first and last may hold elements of other
  * rows, which are read as -inf and not written.
+ *
+ * Bound by memory once the exponentials (two per element) are cheap: packed
+ * fp32 arithmetic, four blocks per lane and step, and the row's scalars by one
+ * warp. Measured: 4096 x 128256 bf16, a quarter of the rows left out, 297 us
+ * (91 % of copy bandwidth; ncu on 1024 rows: 400 MB moved for 394), 2048 x 50257
+ * 73 us (73 %: 6 or 7 rows per cluster), 16 x 50257 8.0 us. Log-probabilities
+ * alone stream the row through registers: 2048 x 128256 fp32 165 us (94 %).
  */
 #include "train.cuh"
 

@@ -4,30 +4,40 @@
  *
  * A matrix product whose reduction runs over the tokens, the slow axis of
  * both operands, on the 5th-generation tensor cores. A pair of CTAs (one
- * tcgen05.mma over two SMs) forms a 256 x BN tile of dw, BN up to 256, in
- * tensor memory (fp32), 64 tokens per step: each CTA holds 128 rows of the
- * tile, 128 of the checkpoint's columns and half of dy's, so an SM takes in
- * 24 KB per step of 512 tensor-core cycles (one CTA per tile would take in
- * 40 KB, more than L2 delivers). Per CTA, through a ring of stages:
- *   copy warp       brings its half of dy's 64 x BN tile by TMA (128-byte
- *                   swizzle, rows of 64 columns: the tensor core's layout for
- *                   an operand whose slow axis is the reduction);
+ * tcgen05.mma over two SMs) forms a tile of dw of 256 rows and one or two
+ * groups of up to 256 columns in tensor memory (fp32), 64 tokens per step:
+ * each CTA holds 128 rows of the tile, 128 of the checkpoint's columns and half
+ * of dy's. (One CTA per 128 x 256 tile took in 40 KB per step against 24, and
+ * the whole product 307 us against 255.) Per CTA, through a ring of stages:
+ *   copy warp       brings its half of dy's tile by TMA (128-byte swizzle, rows
+ *                   of 64 columns: the tensor core's layout for an operand
+ *                   whose slow axis is the reduction);
  *   16 value warps  in two groups, each every other step: read the
- *                   checkpoint's 64 x 128 tile into registers ahead (a thread
- *                   one block of 32 values and its scale), turn it into
- *                   16-bit values and store them in the same layout. q * 2^k
- *                   is exact in the 16-bit type, so the operand is the
- *                   checkpoint itself, without a rounding;
- *   product warp    (first CTA of the pair) one thread issues four
- *                   256 x BN x 16 products per stage;
- *   4 output warps  read a finished tile from one half of tensor memory, round
- *                   once and store, while the next tile's sums form in the
- *                   other half.
+ *                   checkpoint's 64 x 128 tile into registers two of its steps
+ *                   ahead (eight lanes a row), turn it into 16-bit values and
+ *                   store them in the same layout. q * 2^k is exact in the
+ *                   16-bit type, so the operand is the checkpoint itself,
+ *                   without a rounding;
+ *   product warp    (first CTA of the pair) one thread issues four products of
+ *                   16 tokens per column group and stage;
+ *   4 output warps  read a finished tile from tensor memory, round once and
+ *                   store. With one column group the next tile's sums form in
+ *                   the other half of tensor memory meanwhile; two groups fill
+ *                   it, and halve the value warps' work per product.
+ * A step's values take about 850 cycles, 256 columns' products 512, so two
+ * groups are what feeds the tensor cores: 8192 x 2048 x 8192 bf16 takes 157 us
+ * (1750 TFLOP/s, the rate cuBLAS sustains under the power cap, 1734) against
+ * 240 us with one group. 1024 x 768 x 2304 takes 13 us, of which 8 are set-up,
+ * the first copies' latency and the output.
  *
  * Few tiles and many tokens: a cluster of 2 or 4 pairs shares a tile, each
  * pair a part of the tokens; the sums meet in shared memory and every CTA adds
  * its share of the rows over the cluster in rank order. Split and tile width
- * depend on the sizes alone, so results do not change from call to call.
+ * depend on the sizes and the device alone, so results do not change from call
+ * to call.
+ *
+ * A dy whose rows do not start on 16-byte boundaries cannot come by TMA; its
+ * path is at copy_raw (8000 x 2000 x 5555: 430 us against 151 at 5552).
  *
  * Every wait is bounded (2 s); one that expires ends the work of its CTA, the
  * tiles it had left become NaN and the scaler's error word is raised.

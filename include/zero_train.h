@@ -23,8 +23,10 @@
  * tensor inside a flat buffer starts at any element: pointers to 16-bit and
  * 32-bit elements need their element's alignment only, checkpoint buffers and
  * workspaces 16 bytes (ZERO_EALIGN otherwise). Rows that start on 16-byte
- * boundaries are moved in 16-byte pieces, others in smaller ones, with the
- * same results. `ld` is the distance between the starts of two rows, in
+ * boundaries are moved as they are, others through 16-byte blocks that may
+ * hold neighbouring elements, with the same results: a call may read the rest
+ * of the block that holds a buffer's first or last element (any cudaMalloc'd
+ * buffer covers it), and writes its own elements only. `ld` is the distance between the starts of two rows, in
  * elements, at least the row length (ZERO_EINVAL). Calls with no rows (or no
  * elements) return ZERO_OK and write only what the call still defines (the
  * whole table's gradient, the four statistics). Input and output buffers must
@@ -148,9 +150,7 @@ ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const
  *
  * logits: [rows, vocab], row distance ld, of type dtype (ZERO_BF16, ZERO_FP16
  * or ZERO_FP32). -inf entries are tokens ruled out (probability 0); a row of
- * nothing but -inf, or one with a NaN or +inf, has logp NaN. The calls may
- * read the rest of the 16-byte blocks that hold the buffer's first and last
- * elements (any cudaMalloc'd buffer covers them).
+ * nothing but -inf, or one with a NaN or +inf, has logp NaN.
  * actions: the tokens taken, int32 or int64 (action_bytes 4 or 8).
  *   logp[t] = logits[t, a_t] - log(sum over j of exp(logits[t, j]))
  * An action outside [0, vocab) leaves its row out: logp 0. A row may have at
