@@ -23,7 +23,7 @@ LIBDIR = os.path.join(PKG, "_lib")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "--fmad=false", "-shared",
+NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "--fmad=false", "-shared", "--threads", "4",
                      "-Xcompiler", "-fPIC,-ffp-contract=off,-fvisibility=hidden"]
 
 ZERO_LIB = os.path.join(LIBDIR, "libzero.so")
