@@ -56,12 +56,9 @@ __device__ __forceinline__ void store_row(uint8_t* stage, uint16_t* row, int64_t
       if (c + j < cols) row[c + j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
   } else {
     const int64_t left = cols - c0;
-    if (left > 0) store_any(stage, row + c0, left < kCols ? static_cast<int>(left) : kCols, lane, v);
+    if (left > 0)
+      store_any(stage, row + c0, left < kCols ? static_cast<int>(left) : kCols, lane, v);
   }
-}
-
-__device__ __forceinline__ float pow2(int k) {  // 2^k, -127 < k < 128
-  return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
 }
 
 struct Ckpt {

@@ -176,7 +176,8 @@ __global__ void __launch_bounds__(kSortThreads) hist_kernel(const SortArgs a) {
   a.hist[threadIdx.x * kMaxChunks + blockIdx.x] = count[threadIdx.x];
   // the scatter kernels read counts in fours
   if (blockIdx.x == gridDim.x - 1)
-    for (int g = gridDim.x; g < kMaxChunks && (g & 3); ++g) a.hist[threadIdx.x * kMaxChunks + g] = 0;
+    for (int g = gridDim.x; g < kMaxChunks && (g & 3); ++g)
+      a.hist[threadIdx.x * kMaxChunks + g] = 0;
   const int total = (a.n_hists - 1) * kDigits * kMaxChunks;
   for (int i = blockIdx.x * kSortThreads + threadIdx.x; i < total; i += gridDim.x * kSortThreads)
     a.hist[kDigits * kMaxChunks + i] = 0;
@@ -311,7 +312,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads)
   __shared__ uint32_t warp_sum[kSortWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, me = blockIdx.x;
   // rounds of 32 ids per warp, the same for every CTA
-  const int rounds = static_cast<int>((a.n + kCluster * kSortThreads - 1) / (kCluster * kSortThreads));
+  constexpr int kRoundIds = kCluster * kSortThreads;
+  const int rounds = static_cast<int>((a.n + kRoundIds - 1) / kRoundIds);
   const uint32_t n = static_cast<uint32_t>(a.n), mask = (1u << a.bits) - 1;
   const uint32_t first = (me * kSortWarps + warp) * rounds * 32 + lane;
   if (me == 0 && tid == 0) *a.n_spans = 0;
@@ -698,8 +700,9 @@ ZERO_API int zero_embedding(const void* tokens, int32_t token_bytes, int64_t n_t
   const int64_t grid = ceil_div(a.units, kWarps);
   if (grid > kMaxGrid) return ZERO_ERANGE;
   const bool vec = dim % kVec == 0 && aligned(table, 16) && aligned(out, 16);
-  const auto fn = dtype == ZERO_BF16 ? (vec ? lookup_kernel<true, true> : lookup_kernel<true, false>)
-                                     : (vec ? lookup_kernel<false, true> : lookup_kernel<false, false>);
+  const auto fn = dtype == ZERO_BF16
+                      ? (vec ? lookup_kernel<true, true> : lookup_kernel<true, false>)
+                      : (vec ? lookup_kernel<false, true> : lookup_kernel<false, false>);
   return status_of(launch_pdl(fn, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
                               static_cast<cudaStream_t>(stream), a));
 }
@@ -793,7 +796,8 @@ ZERO_API int zero_embedding_grad(const void* tokens, int32_t token_bytes, int64_
   a.scale = scale;
   a.accumulate = accumulate;
   const bool vec = dim % kVec == 0 && aligned(dy, 16) && aligned(grad, 16);
-  if (dtype == ZERO_BF16) return vec ? launch_rows<true, true>(a, st) : launch_rows<true, false>(a, st);
+  if (dtype == ZERO_BF16)
+    return vec ? launch_rows<true, true>(a, st) : launch_rows<true, false>(a, st);
   return vec ? launch_rows<false, true>(a, st) : launch_rows<false, false>(a, st);
 }
 

@@ -344,7 +344,9 @@ __device__ __forceinline__ void bar_init(uint64_t* bar) {
 // here: 1 us and more per row.)
 __device__ __forceinline__ void send(Stat* to, uint64_t* bar, uint32_t rank, const Stat& v) {
   uint32_t remote, remote_bar;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(to)), "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(remote)
+               : "r"(smem_u32(to)), "r"(rank));
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
                : "=r"(remote_bar)
                : "r"(smem_u32(bar)), "r"(rank));
@@ -435,7 +437,8 @@ struct Turn {
 };
 
 template <int kType, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, 24 / kWarps) policy_kernel(const Args a, const int32_t part_cap) {
+__global__ void __launch_bounds__(32 * kWarps, 24 / kWarps)
+    policy_kernel(const Args a, const int32_t part_cap) {
   pdl_begin();
   using B = Block<kType>;
   extern __shared__ __align__(16) uint8_t stage[];
@@ -795,7 +798,9 @@ int check(const void* logits, int64_t rows, int64_t vocab, int64_t ld, int32_t d
       (action_bytes != 4 && action_bytes != 8))
     return ZERO_EINVAL;
   const size_t size = dtype == ZERO_FP32 ? 4 : 2;
-  if (vocab * static_cast<int64_t>(size) > (int64_t{1} << 30) || rows > (int64_t{1} << 31) || ld > (int64_t{1} << 31))
+  constexpr int64_t kMost = int64_t{1} << 31;
+  if (vocab > kMost || vocab * static_cast<int64_t>(size) > (int64_t{1} << 30) || rows > kMost ||
+      ld > kMost)
     return ZERO_ERANGE;
   if (rows == 0) return ZERO_OK;
   if (!logits || !actions || !logp) return ZERO_EINVAL;

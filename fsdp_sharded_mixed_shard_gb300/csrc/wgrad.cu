@@ -289,7 +289,8 @@ __device__ __forceinline__ Piece load_piece(const Args& a, const Source& s, int6
   for (int k = 0; k < 2; ++k) {
     b.q[k] = make_uint4(0, 0, 0, 0);
     b.scale[k] = 127;
-    if (s.left > 4 * k && ZCHECK(s.q + k * q_step + 16 <= a.q + a.rows * a.pitch, kSiteLoad, s.left)) {
+    if (s.left > 4 * k &&
+        ZCHECK(s.q + k * q_step + 16 <= a.q + a.rows * a.pitch, kSiteLoad, s.left)) {
       b.q[k] = __ldg(reinterpret_cast<const uint4*>(s.q + k * q_step));
       b.scale[k] = __ldg(s.scale + k * scale_step);
     }
@@ -386,8 +387,9 @@ template <bool kBf16>
 __device__ __forceinline__ void narrow32(const float (&f)[32], uint4 (&v)[4]) {
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    v[k] = make_uint4(narrow2<kBf16>(f[8 * k], f[8 * k + 1]), narrow2<kBf16>(f[8 * k + 2], f[8 * k + 3]),
-                      narrow2<kBf16>(f[8 * k + 4], f[8 * k + 5]), narrow2<kBf16>(f[8 * k + 6], f[8 * k + 7]));
+    v[k] = make_uint4(
+        narrow2<kBf16>(f[8 * k], f[8 * k + 1]), narrow2<kBf16>(f[8 * k + 2], f[8 * k + 3]),
+        narrow2<kBf16>(f[8 * k + 4], f[8 * k + 5]), narrow2<kBf16>(f[8 * k + 6], f[8 * k + 7]));
 }
 
 // Rows of dw off the 16-byte grid leave through shared memory, kOutCols columns
@@ -485,7 +487,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const auto row_of = [&](int tile) {  // first row of dw of this CTA's part of the tile
     return static_cast<int64_t>(tile % a.m_tiles) * (2 * kM) + half * kM;
   };
-  const auto column_of = [&](int tile) { return static_cast<int64_t>(tile / a.m_tiles) * (kWide * a.bn); };
+  const auto column_of = [&](int tile) {
+    return static_cast<int64_t>(tile / a.m_tiles) * (kWide * a.bn);
+  };
 
   if (warp == kProductWarp) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -586,15 +590,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t raw_parity = 0;
       for (int64_t at = 0; at < total; ++at) {
         if (warp % kGroupWarps == 0) {
-          const bool landed = bar_wait(&raw_full[slot], raw_parity, &failed) &&
-                              (at < kStages || bar_wait(&empty[ring.stage], ring.parity ^ 1, &failed));
+          const bool landed =
+              bar_wait(&raw_full[slot], raw_parity, &failed) &&
+              (at < kStages || bar_wait(&empty[ring.stage], ring.parity ^ 1, &failed));
           if (lane == 0) group_ok[group] = landed;
         }
         group_sync(group);
         ok = *static_cast<volatile int*>(&group_ok[group]) != 0;
         if (!ok) break;
-        place_raw(raw_ring + slot * kRawBytes, stages + ring.stage * kStageBytes + kBytesA, row, c, d,
-                  keep);
+        place_raw(raw_ring + slot * kRawBytes, stages + ring.stage * kStageBytes + kBytesA, row, c,
+                  d, keep);
         if (++now.step == steps) {
           now.advance(0, steps, tile_stride);
           keep = keep_of(now.tile);
@@ -654,7 +659,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (it >= kRaw && lane == 0) ok = bar_wait(&raw_empty[slot], parity ^ 1, &failed);
         if (!__shfl_sync(0xffffffffu, ok, 0)) break;
         const int64_t t = t_begin + static_cast<int64_t>(now.step) * kK + r;
-        copy_raw(raw_at + slot * kRawBytes, from, bytes, static_cast<int32_t>(t_end - t), row8, g, any);
+        copy_raw(raw_at + slot * kRawBytes, from, bytes, static_cast<int32_t>(t_end - t), row8, g,
+                 any);
         // counts this lane's copies when they land
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
                          smem_u32(&raw_full[slot]))
@@ -676,7 +682,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int left_fresh = kStages;
       for (int k = 0; k < my_tiles && ok; ++k) {
-        const int32_t x = static_cast<int32_t>(column_of(tile0 + k * tile_stride) + half * (a.bn / 2));
+        const int32_t x =
+            static_cast<int32_t>(column_of(tile0 + k * tile_stride) + half * (a.bn / 2));
         int32_t y = static_cast<int32_t>(t_begin);
         for (int step = 0; step < steps; ++step, y += kK) {
           const int s = ring.stage;
@@ -769,14 +776,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else if (j + (c & ~(kOutCols - 1)) < a.n) {
             uint8_t* stage = out_stage[warp - kOutWarp0];
             uint4* row = reinterpret_cast<uint4*>(stage + lane * kOutPitch);
-            const int part = c & (kOutCols - 1), count = static_cast<int>(min(a.n - j, static_cast<int64_t>(kWide * a.bn)));
-            if (part == 0) row[0] = last;
+            const int within = c & (kOutCols - 1);
+            const int count =
+                static_cast<int>(min(a.n - j, static_cast<int64_t>(kWide * a.bn)));
+            if (within == 0) row[0] = last;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) row[1 + part / 8 + e] = v[e];
+            for (int e = 0; e < 4; ++e) row[1 + within / 8 + e] = v[e];
             last = v[3];
-            if (part || c + 32 == kWide * a.bn) {
+            if (within || c + 32 == kWide * a.bn) {
               __syncwarp();
-              store_staged(stage, to, a.n, a.cols - i0, c - part, part + 32, count, lane);
+              store_staged(stage, to, a.n, a.cols - i0, c - within, within + 32, count, lane);
               __syncwarp();
             }
           }

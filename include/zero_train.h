@@ -26,12 +26,13 @@
  * boundaries are moved as they are, others through 16-byte blocks that may
  * hold neighbouring elements, with the same results: a call may read the rest
  * of the block that holds a buffer's first or last element (any cudaMalloc'd
- * buffer covers it), and writes its own elements only. `ld` is the distance between the starts of two rows, in
- * elements, at least the row length (ZERO_EINVAL). Calls with no rows (or no
- * elements) return ZERO_OK and write only what the call still defines (the
- * whole table's gradient, the four statistics). Input and output buffers must
- * not overlap unless stated. Sums, softmax statistics and activation functions
- * are computed in fp32 and each result is rounded once to its type, to nearest
+ * buffer covers it), and writes its own elements only.
+ * `ld` is the distance between the starts of two rows, in elements, at least
+ * the row length (ZERO_EINVAL). Calls with no rows (or no elements) return
+ * ZERO_OK and write only what the call still defines (the whole table's
+ * gradient, the four statistics). Input and output buffers must not overlap
+ * unless stated. Sums, softmax statistics and activation functions are
+ * computed in fp32 and each result is rounded once to its type, to nearest
  * even. Results do not depend on the run: no floating-point atomics, sums in a
  * fixed order.
  */
@@ -127,8 +128,8 @@ ZERO_API int zero_ckpt_act(int32_t act, const void* x, const void* u, int64_t ro
 /* The activation's gradient from the checkpoints, with dy [rows, cols] (row
  * distance ld_dy): dx = dy * df/dx, du = dy * df/du (NULL for ZERO_ACT_GELU)
  * at the checkpointed values. y, when not NULL, receives f of the checkpointed
- * values again (the next linear layer's weight gradient needs it). dx, du and y have row distance ld; dx or
- * du may be dy itself (with ld equal to ld_dy). */
+ * values again (the next linear layer's weight gradient needs it). dx, du and
+ * y have row distance ld; dx or du may be dy itself (with ld equal to ld_dy). */
 ZERO_API int zero_ckpt_act_grad(int32_t act, const void* ckpt_x, const void* ckpt_u,
                                 const void* dy, int64_t rows, int64_t cols, int64_t ld_dy,
                                 int32_t dtype, void* dx, void* du, void* y, int64_t ld,
