@@ -123,6 +123,8 @@ def test_loss():
         refused(EALIGN, f, *changed(ok, **bad))
     refused(EALIGN, f, *changed(ok, i4=Z.ZERO_FP32, i0=P + 2))
     refused(ERANGE, f, *changed(ok, i2=(1 << 30) + 1, i3=1 << 31))
+    # a row whose bytes pass 64 bits
+    refused(ERANGE, f, *changed(ok, i2=1 << 62, i3=1 << 62, i4=Z.ZERO_FP32))
     f(*changed(ok, i1=0, i0=0, i5=0, i7=0))
     hp = Z.ZeroPolicyParams(0.2, 0.2, 0.1)
     ok = [P, 4, 100, 104, BF, P, 4, P, P, P, P, hp, 0, P, P, P, P]
