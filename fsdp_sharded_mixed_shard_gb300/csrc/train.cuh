@@ -108,10 +108,9 @@ __device__ __forceinline__ uint4 narrow8(const float (&f)[8]) {
                     narrow2<kBf16>(f[4], f[5]), narrow2<kBf16>(f[6], f[7]));
 }
 
-// The 16 bytes that start d bytes (d even, 0 <= d <= 16) into x and run on
-// into y, the block after it: words and halfword picked in three steps.
+// The 16 bytes that start d bytes (d even, 0 <= d < 16) into x and run on into
+// y, the block after it: words and halfword picked in three steps.
 __device__ __forceinline__ uint4 shifted(const uint4& x, const uint4& y, int d) {
-  if (d == 16) return y;
   const uint32_t c[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
   uint32_t t[6], w[5], o[4];
 #pragma unroll
@@ -119,8 +118,13 @@ __device__ __forceinline__ uint4 shifted(const uint4& x, const uint4& y, int d) 
 #pragma unroll
   for (int j = 0; j < 5; ++j) w[j] = d & 4 ? t[j + 1] : t[j];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) o[j] = d & 2 ? __funnelshift_r(w[j], w[j + 1], 16) : w[j];
+  for (int j = 0; j < 4; ++j) o[j] = __funnelshift_r(w[j], w[j + 1], (d & 2) * 8);
   return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// The 16 bytes that end d bytes (d even, 0 <= d < 16) before the end of y.
+__device__ __forceinline__ uint4 shifted_back(const uint4& x, const uint4& y, int d) {
+  return d ? shifted(x, y, 16 - d) : y;
 }
 
 // Eight 16-bit elements at any element address, from the one or two 16-byte
@@ -155,7 +159,7 @@ __device__ __forceinline__ void store_any(uint8_t* stage, uint16_t* to, int coun
     if (16 * k - d < 0 || 16 * k - d + 16 > bytes) return;
     const uint4 x = mine[k - 1];
     const uint4 y = mine[k];
-    __stcs(reinterpret_cast<uint4*>(blocks + 16 * k), shifted(x, y, 16 - d));
+    __stcs(reinterpret_cast<uint4*>(blocks + 16 * k), shifted_back(x, y, d));
   };
   block(lane);  // block 32 is never whole unless d is 0, and then it is past the run
   // at most seven elements before the first whole block and after the last

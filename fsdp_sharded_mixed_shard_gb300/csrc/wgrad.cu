@@ -36,8 +36,10 @@
  * depend on the sizes and the device alone, so results do not change from call
  * to call.
  *
- * A dy whose rows do not start on 16-byte boundaries cannot come by TMA; its
- * path is at copy_raw (8000 x 2000 x 5555: 430 us against 151 at 5552).
+ * A dy whose rows do not start on 16-byte boundaries comes as the 16-byte
+ * blocks that hold it, and three groups of warps move it to its places beside
+ * the values (at place_raw; 8000 x 2000 x 5555: 309 us against 151 at 5552.
+ * One group for dy and two for the values took 416).
  *
  * Every wait is bounded (2 s); one that expires ends the work of its CTA, the
  * tiles it had left become NaN and the scaler's error word is raised.
@@ -53,16 +55,23 @@ namespace zw {
 
 using namespace zt;
 
-constexpr int kGroups = 2, kGroupWarps = 8;
+constexpr int kGroupWarps = 8;
 constexpr int kGroupThreads = 32 * kGroupWarps;
-constexpr int kCopyWarp = kGroups * kGroupWarps, kProductWarp = kCopyWarp + 1;
-constexpr int kOutWarp0 = kProductWarp + 1, kOutWarps = 4;
-constexpr int kThreads = 32 * (kOutWarp0 + kOutWarps);
+constexpr int kOutWarps = 4;
+// warps by role: groups that fill stages, copies, products, output. Groups that
+// also place dy take longer over a step, so there is one more.
+template <bool kTma>
+struct Roles {
+  static constexpr int kGroups = kTma ? 2 : 3;
+  static constexpr int kCopyWarp = kGroups * kGroupWarps, kProductWarp = kCopyWarp + 1;
+  static constexpr int kOutWarp0 = kProductWarp + 1, kWarps = kOutWarp0 + kOutWarps;
+  static constexpr int kThreads = 32 * kWarps;
+};
 constexpr int kM = 128, kN = 256, kK = 64;     // rows per CTA, columns at most, tokens per stage
 constexpr int kAhead = 2;                       // a value thread's steps loaded ahead
 constexpr int kChunk = kK * 128;               // 64 tokens x 64 columns of 16 bits
 constexpr int kBytesA = kM / 64 * kChunk, kBytesB = kN / 2 / 64 * kChunk;
-constexpr int kRing = 192 * 1024;              // shared memory for stages
+constexpr int kRing = 196 * 1024;              // shared memory for stages
 constexpr int kJoinPitch = kN + 4;             // fp32 row of a tile in shared memory
 constexpr int kSmem = kRing + 1024;
 constexpr int kMaxSplit = 4;
@@ -71,7 +80,6 @@ constexpr int kMaxSplit = 4;
 constexpr int kValueCycles = 850, kOutCycles = 28, kJoinCycles = 3500;
 constexpr uint64_t kWaitLimitNs = 2000000000ull, kDrainNs = 1000000ull;
 static_assert(kM * kJoinPitch * 4 <= kRing, "the tile fits the stages");
-static_assert(kGroups == 2, "the second group brings dy when TMA cannot");
 static_assert(kM == ZERO_CKPT_PAD, "a checkpoint row is whole CTA tiles");
 
 struct Args {
@@ -149,6 +157,13 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatil
       *failed = 1;
       return false;
     }
+  }
+}
+
+// given up: lets the copies in flight (microseconds) land
+__device__ __forceinline__ void drain() {
+  const uint64_t t0 = global_ns();
+  while (global_ns() - t0 < kDrainNs) {
   }
 }
 
@@ -329,56 +344,47 @@ __device__ __forceinline__ void store_values(uint8_t* stage_a, const Values& x, 
   *reinterpret_cast<uint4*>(row + (at ^ 16)) = x.v[1];
 }
 
-// dy's half tile without TMA, for rows that do not start on 16-byte
-// boundaries: the copy warp brings the 16-byte blocks that hold a token's 128
-// columns (17 where they do not start on one) as they lie, kRaw steps ahead,
-// and a value group moves them to their places in the stage. (The group's own
-// copies ahead would be waited for by its proxy fence, step by step.) Eight
-// rows are 16 ld bytes, a step 64 rows and a tile's columns whole blocks, so
-// the distance d of a row's first column from its block is the same in every
-// eighth token, in every step and tile.
-constexpr int kRaw = 5, kRawPitch = 17 * 16, kRawBytes = kK * kRawPitch;
-constexpr int kRounds = kK * 16 / kGroupThreads;
+// dy's half tile when its rows do not start on 16-byte boundaries, where no one
+// TMA map covers it: eight rows are 16 ld bytes, so each class of every eighth
+// token has a map of its own, from the boundary at or before its first element.
+// The copy warp brings a step's 64 tokens class by class, eight boxes of the
+// blocks that hold 128 columns (17 where they do not start on one), kRaw steps
+// ahead, and the groups move them to their places in the stage. A step is 64
+// rows and a tile's columns are whole blocks, so the distance d of a row's first
+// column from its block is its class's in every step and tile.
+constexpr int kClasses = 8, kRawColumns = 128 + 8;
+constexpr int kRaw = 4, kRawPitch = kRawColumns * 2, kRawBytes = kK * kRawPitch;
+static_assert(kK * 4 == kGroupThreads, "a thread places a quarter of a row");
 
-__device__ __forceinline__ void copy_block(uint32_t to, uintptr_t from, bool on, uintptr_t any) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(on ? from : any),
-               "r"(on ? 16 : 0)
-               : "memory");
-}
+template <bool kAligned>
+struct Maps {
+  CUtensorMap of[kAligned ? 1 : kClasses];
+};
 
-// Lane (class r of eight tokens, quarter g): blocks g, g + 4, g + 8, g + 12 of
-// tokens r, r + 8, ..., and the 17th for g = 0. from: block g of token r;
-// bytes: from there to the end of dy's row; left: tokens from token r on.
-__device__ __forceinline__ void copy_raw(uint32_t raw, uintptr_t from, int64_t bytes, int32_t left,
-                                         int64_t row8, int g, uintptr_t any) {
+// Token 8 i + r of a step, class r, pieces [4 part, 4 part + 4) of eight columns;
+// d: the class's distance; left: columns that dy has from the first piece on.
+// Eight lanes with the same part, eight r and eight i meet no bank twice, in the
+// raw rows (one piece further on with i) or the stage's (swizzled by r).
+__device__ __forceinline__ void place_raw(const uint8_t* raw, uint8_t* stage_b, int i, int r,
+                                          int part, int d, int64_t left) {
+  const uint4* from =
+      reinterpret_cast<const uint4*>(raw + (r * (kK / kClasses) + i) * kRawPitch) + 4 * part;
+  uint8_t* row = stage_b + (part >> 1) * kChunk + (8 * i + r) * 128;
+  uint4 next = from[0];
 #pragma unroll
-  for (int i = 0; i < kK / 8; ++i) {
-    const bool on = left > 8 * i;
-    const uint32_t to = raw + i * (8 * kRawPitch);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      copy_block(to + 64 * k, from + 64 * k, on && bytes > 64 * k, any);
-    if (g == 0) copy_block(to + 256, from + 256, on && bytes > 256, any);
-    from += row8;
-  }
-}
-
-// d: the thread's distance; keep: columns of its piece that dy has
-__device__ __forceinline__ void place_raw(const uint8_t* raw, uint8_t* stage_b, int r, int c, int d,
-                                          int keep) {
-#pragma unroll
-  for (int k = 0; k < kRounds; ++k) {
-    const uint4* block = reinterpret_cast<const uint4*>(raw + (r + 16 * k) * kRawPitch) + c;
-    uint4 v = shifted(block[0], block[1], d);
+  for (int e = 0; e < 4; ++e) {
+    const uint4 block = next;
+    next = from[e + 1];
+    uint4 v = shifted(block, next, d);
+    const int64_t keep = left - 8 * e;
     if (keep < 8) {
       uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[e] = 2 * e + 1 < keep ? w[e] : 2 * e < keep ? w[e] & 0xFFFFu : 0;
+      for (int k = 0; k < 4; ++k)
+        w[k] = 2 * k + 1 < keep ? w[k] : 2 * k < keep ? w[k] & 0xFFFFu : 0;
       v = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    *reinterpret_cast<uint4*>(stage_b + (c >> 3) * kChunk + (r + 16 * k) * 128 +
-                              (((c & 7) ^ (r & 7)) << 4)) = v;
+    *reinterpret_cast<uint4*>(row + ((((part & 1) * 4 + e) ^ r) << 4)) = v;
   }
 }
 
@@ -416,7 +422,7 @@ __device__ __forceinline__ void store_staged(uint8_t* stage, uint16_t* to, int64
     const int begin = 2 * c + 16 * k - d;  // byte of the row the block starts at
     if (begin >= 0 && begin + 16 <= 2 * end)
       *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(at) + begin) =
-          shifted(block[-1], block[0], 16 - d);
+          shifted_back(block[-1], block[0], d);
     if (c == 0 || end == count) {
       const uint16_t* elems = reinterpret_cast<const uint16_t*>(stage + row * kOutPitch + 16);
       const int head = d ? min((16 - d) >> 1, end) : 0;
@@ -458,11 +464,14 @@ struct Ring {  // stage and the parity of its current use
 // kWide: column groups of bn per tile (1 or 2), which share the checkpoint's
 // stage.
 template <bool kBf16, bool kTma, int kWide>
-__global__ void __launch_bounds__(kThreads, 1)
-    wgrad_kernel(const __grid_constant__ CUtensorMap map, const Args a) {
+__global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
+    wgrad_kernel(const __grid_constant__ Maps<kTma> maps, const Args a) {
   constexpr int kStageBytes = kBytesA + kWide * kBytesB;
   constexpr int kStages = kTma ? kRing / kStageBytes : (kRing - kRaw * kRawBytes) / kStageBytes;
   static_assert(kTma || kWide == 1, "raw copies cover one column group");
+  using R = Roles<kTma>;
+  constexpr int kCopyWarp = R::kCopyWarp, kProductWarp = R::kProductWarp;
+  constexpr int kOutWarp0 = R::kOutWarp0, kGroups = R::kGroups;
   extern __shared__ uint8_t raw[];
   uint8_t* stages = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   // full: in the pair's first CTA, counted by both; empty and done: in each
@@ -500,12 +509,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      bar_init(&full_a[s], kTma ? 2 : 4);  // values, and without TMA dy, of both CTAs
+      bar_init(&full_a[s], 2);
       bar_init(&full_b[s], 1);
       bar_init(&empty[s], 1);
     }
     for (int k = 0; k < kRaw && !kTma; ++k) {
-      bar_init(&raw_full[k], 32);
+      bar_init(&raw_full[k], 1);
       bar_init(&raw_empty[k], 1);
     }
     for (int k = 0; k < 2; ++k) {
@@ -536,21 +545,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       return Source{a.q + (t_begin + t) * a.pitch + i, a.scale + (t_begin + t) * blocks + (i >> 5),
                     c.tile < a.tiles && i < a.pitch ? tokens - t : 0};
     };
-    // both groups in turn with TMA; without, the second brings dy for every step
-    constexpr int kTurn = kTma ? kGroups : 1;
-    const int turn0 = kTma ? group : 0;
     Cursor ahead = {tile0, 0};
     Ring<kStages> ring;
-    ring.advance(turn0);
+    ring.advance(group);
     Piece next[kAhead];
     Source src = {};
     const auto load = [&]() {
       const Piece b = load_piece(a, src, 4 * a.pitch, 4 * blocks);
-      ahead.step += kTurn;
+      ahead.step += kGroups;
       if (ahead.step < steps) {
-        src.q += kTurn * kK * a.pitch;
-        src.scale += kTurn * kK * blocks;
-        src.left -= src.left > 0 ? kTurn * kK : 0;
+        src.q += kGroups * kK * a.pitch;
+        src.scale += kGroups * kK * blocks;
+        src.left -= src.left > 0 ? kGroups * kK : 0;
       } else {
         ahead.advance(0, steps, tile_stride);
         src = source_of(ahead);
@@ -558,12 +564,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       return b;
     };
     bool ok = true;
-    // the stage of the step at hand once it is free, or NULL: given up. One
-    // warp of the group asks (many that poll slow what they wait for).
+    // without TMA: the step at hand, the slot of its raw dy, and which part of
+    // that is this thread's
+    Cursor now = {tile0, 0};
+    Ring<kRaw> slot;
+    slot.advance(group);
+    const int place_r = lane & 7, place_i = (lane + warp) & 7;
+    const int distance =
+        static_cast<int>((reinterpret_cast<uintptr_t>(a.dy) + 2 * place_r * a.ld) & 15);
+    // the stage of the step at hand once it is free (and its raw dy is there),
+    // or NULL: given up. One warp of the group asks (many that poll slow what
+    // they wait for).
     const auto free_stage = [&](int64_t at) -> uint8_t* {
-      if (at >= kStages) {
+      if (!kTma || at >= kStages) {
         if (warp % kGroupWarps == 0) {
-          const bool free = bar_wait(&empty[ring.stage], ring.parity ^ 1, &failed);
+          const bool free =
+              (at < kStages || bar_wait(&empty[ring.stage], ring.parity ^ 1, &failed)) &&
+              (kTma || bar_wait(&raw_full[slot.stage], slot.parity, &failed));
           if (lane == 0) group_ok[group] = free;
         }
         group_sync(group);
@@ -575,104 +592,69 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       group_sync(group);
       if (tid % kGroupThreads == 0) bar_arrive_at(arrive_at + ring.stage * 8);
-      ring.advance(kTurn);
+      ring.advance(kGroups);
     };
-    if (!kTma && group == 1) {
-      const int row = (tid % kGroupThreads) >> 4, c = tid & 15;
-      const uint8_t* raw_ring = stages + kStages * kStageBytes;
-      const int d = static_cast<int>((reinterpret_cast<uintptr_t>(a.dy) + 2 * row * a.ld) & 15);
-      const auto keep_of = [&](int tile) {
-        const int64_t left = a.n - (column_of(tile) + half * (a.bn / 2) + 8 * c);
-        return left < 8 ? (left > 0 ? static_cast<int>(left) : 0) : 8;
-      };
-      Cursor now = {tile0, 0};
-      int keep = keep_of(now.tile), slot = 0;
-      uint32_t raw_parity = 0;
-      for (int64_t at = 0; at < total; ++at) {
-        if (warp % kGroupWarps == 0) {
-          const bool landed =
-              bar_wait(&raw_full[slot], raw_parity, &failed) &&
-              (at < kStages || bar_wait(&empty[ring.stage], ring.parity ^ 1, &failed));
-          if (lane == 0) group_ok[group] = landed;
-        }
-        group_sync(group);
-        ok = *static_cast<volatile int*>(&group_ok[group]) != 0;
-        if (!ok) break;
-        place_raw(raw_ring + slot * kRawBytes, stages + ring.stage * kStageBytes + kBytesA, row, c,
-                  d, keep);
-        if (++now.step == steps) {
-          now.advance(0, steps, tile_stride);
-          keep = keep_of(now.tile);
+    if (total > 0) {
+      ahead.advance(group, steps, tile_stride);
+      now = ahead;
+      src = source_of(ahead);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) next[k] = load();
+    }
+    for (int64_t it = group; it < total && ok; it += kAhead * kGroups) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int64_t at = it + k * kGroups;
+        if (at >= total || !ok) break;
+        // worked out before the stage is free: only the stores stand between
+        // that and the products
+        const Values v0 = values_of<kBf16>(next[k].q[0], next[k].scale[0], p);
+        const Values v1 = values_of<kBf16>(next[k].q[1], next[k].scale[1], p);
+        uint8_t* stage = free_stage(at);
+        if (!stage) break;
+        store_values(stage, v0, r, p);
+        store_values(stage, v1, r + 4, p);
+        if constexpr (!kTma) {
+          const int64_t left = a.n - (column_of(now.tile) + half * (a.bn / 2) + 32 * (lane >> 3));
+          place_raw(stages + kStages * kStageBytes + slot.stage * kRawBytes, stage + kBytesA,
+                    place_i, place_r, lane >> 3, distance, left);
         }
         stored();
-        if (tid % kGroupThreads == 0) bar_arrive_at(smem_u32(&raw_empty[slot]));
-        if (++slot == kRaw) {
-          slot = 0;
-          raw_parity ^= 1;
+        if constexpr (!kTma) {
+          if (tid % kGroupThreads == 0) bar_arrive_at(smem_u32(&raw_empty[slot.stage]));
+          slot.advance(kGroups);
+          now.advance(kGroups, steps, tile_stride);
         }
-      }
-    } else {
-      if (total > 0) {
-        ahead.advance(turn0, steps, tile_stride);
-        src = source_of(ahead);
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) next[k] = load();
-      }
-      for (int64_t it = turn0; it < total && ok; it += kAhead * kTurn) {
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          const int64_t at = it + k * kTurn;
-          if (at >= total || !ok) break;
-          // worked out before the stage is free: only the stores stand between
-          // that and the products
-          const Values v0 = values_of<kBf16>(next[k].q[0], next[k].scale[0], p);
-          const Values v1 = values_of<kBf16>(next[k].q[1], next[k].scale[1], p);
-          uint8_t* stage = free_stage(at);
-          if (!stage) break;
-          store_values(stage, v0, r, p);
-          store_values(stage, v1, r + 4, p);
-          stored();
-          next[k] = load();  // not before: the proxy fence would wait for it
-        }
+        next[k] = load();  // not before: the proxy fence would wait for it
       }
     }
   } else if (warp == kCopyWarp) {
     if constexpr (!kTma) {
-      const int r = lane >> 2, g = lane & 3;
-      const uintptr_t base = reinterpret_cast<uintptr_t>(a.dy);
-      const uintptr_t any = base & ~static_cast<uintptr_t>(15);
-      const int64_t row8 = 16 * a.ld;
-      const int d = static_cast<int>((base + 2 * r * a.ld) & 15);
-      const uint32_t raw_at = smem_u32(stages + kStages * kStageBytes) + r * kRawPitch + g * 16;
-      Cursor now = {tile0, 0};
-      int slot = 0;
-      uint32_t parity = 0;
-      uintptr_t from = 0;
-      int64_t bytes = 0;
-      for (int64_t it = 0; it < total; ++it) {
-        if (now.step == 0) {
-          const int64_t column = 2 * (column_of(now.tile) + half * (a.bn / 2)) - d + 16 * g;
-          from = base + 2 * (t_begin + r) * a.ld + column;
-          bytes = 2 * a.n - column;
+      if (lane == 0) {
+        uint8_t* raw_ring = stages + kStages * kStageBytes;
+        const uint32_t full_at = in_cta(raw_full, rank);
+        Cursor now = {tile0, 0};
+        int slot = 0;
+        uint32_t parity = 0;
+        bool ok = true;
+        for (int64_t it = 0; it < total; ++it) {
+          ok = it < kRaw || bar_wait(&raw_empty[slot], parity ^ 1, &failed);
+          if (!ok) break;
+          bar_expect(&raw_full[slot], kRawBytes);
+          const int32_t x = static_cast<int32_t>(column_of(now.tile) + half * (a.bn / 2));
+          const int32_t y = static_cast<int32_t>(s0 + now.step) * (kK / kClasses);
+#pragma unroll
+          for (int c = 0; c < kClasses; ++c)  // a class without tokens: past the end of another's
+            copy_box(raw_ring + slot * kRawBytes + c * (kRawBytes / kClasses), &maps.of[c], x,
+                     y + (c < a.rows ? 0 : 1), full_at + slot * 8);
+          now.advance(1, steps, tile_stride);
+          if (++slot == kRaw) {
+            slot = 0;
+            parity ^= 1;
+          }
         }
-        int ok = 1;
-        if (it >= kRaw && lane == 0) ok = bar_wait(&raw_empty[slot], parity ^ 1, &failed);
-        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-        const int64_t t = t_begin + static_cast<int64_t>(now.step) * kK + r;
-        copy_raw(raw_at + slot * kRawBytes, from, bytes, static_cast<int32_t>(t_end - t), row8, g,
-                 any);
-        // counts this lane's copies when they land
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
-                         smem_u32(&raw_full[slot]))
-                     : "memory");
-        from += 8 * row8;
-        now.advance(1, steps, tile_stride);
-        if (++slot == kRaw) {
-          slot = 0;
-          parity ^= 1;
-        }
+        if (!ok) drain();
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (lane == 0) {
       // one thread's dependent instructions are slow beside 22 warps: what
       // does not change from step to step is worked out before
@@ -696,18 +678,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* b = stages + s * kStageBytes + kBytesA;
 #pragma unroll
           for (int w = 0; w < kWide; ++w) {
-            copy_box(b + w * kBytesB, &map, x + w * a.bn, y, full_at + s * 8);
+            copy_box(b + w * kBytesB, &maps.of[0], x + w * a.bn, y, full_at + s * 8);
             if (chunks > 1)
-              copy_box(b + w * kBytesB + kChunk, &map, x + w * a.bn + 64, y, full_at + s * 8);
+              copy_box(b + w * kBytesB + kChunk, &maps.of[0], x + w * a.bn + 64, y,
+                       full_at + s * 8);
           }
           ring.advance(1);
         }
       }
-      if (!ok) {  // given up: let the copies in flight (microseconds) land first
-        const uint64_t t0 = global_ns();
-        while (global_ns() - t0 < kDrainNs) {
-        }
-      }
+      if (!ok) drain();
     }
   } else if (warp == kProductWarp) {
     if (half == 0 && lane == 0) {
@@ -813,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t j = column_of(tile0);
     // the output warps' stages as one, a row's worth for each warp
     uint8_t* stage = &out_stage[0][0] + warp * ((kStageWarp + 15) & ~15);
-    for (int m = warp; m < share; m += kThreads / 32) {
+    for (int m = warp; m < share; m += R::kWarps) {
       const int row = part * share + m;
       const int64_t i = row_of(tile0) + row;
       if (i >= a.cols) break;
@@ -875,12 +854,29 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
+// Map of `rows` rows of n elements, ld apart; boxes of 64 columns go to swizzled
+// stages, wider ones as they lie.
+bool encode_rows(CUtensorMap* map, uintptr_t base, int64_t n, int64_t rows, int64_t ld,
+                 uint32_t box_columns, uint32_t box_rows, bool bf16) {
+  const EncodeTiled encode = encode_tiled();
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[2] = {box_columns, box_rows}, unit[2] = {1, 1};
+  return encode &&
+         encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                reinterpret_cast<void*>(base), dims, strides, box, unit,
+                CU_TENSOR_MAP_INTERLEAVE_NONE,
+                box_columns == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct Launch {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  Launch(int clusters, int split, cudaStream_t st) : cfg(), attr() {
+  Launch(int clusters, int split, int threads, cudaStream_t st) : cfg(), attr() {
     cfg.gridDim = dim3(static_cast<unsigned>(clusters * 2 * split));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = st;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -894,12 +890,12 @@ struct Launch {
 };
 
 template <bool kBf16, bool kTma, int kWide>
-int launch(const CUtensorMap& map, const Args& a, int clusters, cudaStream_t st) {
+int launch(const Maps<kTma>& maps, const Args& a, int clusters, cudaStream_t st) {
   const auto fn = wgrad_kernel<kBf16, kTma, kWide>;
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
     return ZERO_ECUDA;
-  Launch l(clusters, a.split, st);
-  return status_of(cudaLaunchKernelEx(&l.cfg, fn, map, a));
+  Launch l(clusters, a.split, Roles<kTma>::kThreads, st);
+  return status_of(cudaLaunchKernelEx(&l.cfg, fn, maps, a));
 }
 
 // Clusters of `split` pairs that the device holds at once (0 on error): SMs
@@ -913,7 +909,7 @@ int resident_clusters(int split) {
   int n = known[dev][split].load(std::memory_order_relaxed);
   if (n == 0) {
     const auto fn = wgrad_kernel<true, true, 1>;
-    Launch l(1, split, nullptr);
+    Launch l(1, split, Roles<true>::kThreads, nullptr);
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
             cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, fn, &l.cfg) != cudaSuccess)
@@ -987,26 +983,27 @@ ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const
   a.tiles = static_cast<int32_t>(tiles);
   const int clusters = static_cast<int>(std::min(tiles, a.split > 1 ? tiles : pairs));
   const bool bf16 = dtype == ZERO_BF16;
-  CUtensorMap map = {};
-  if (tma) {
-    const EncodeTiled encode = encode_tiled();
-    if (!encode) return ZERO_ECUDA;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
-    const cuuint32_t box[2] = {64, kK}, unit[2] = {1, 1};
-    if (encode(&map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-               const_cast<void*>(dy), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return ZERO_ECUDA;
-  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (!tma) return bf16 ? launch<true, false, 1>(map, a, clusters, st)
-                        : launch<false, false, 1>(map, a, clusters, st);
-  if (wide == 2) return bf16 ? launch<true, true, 2>(map, a, clusters, st)
-                             : launch<false, true, 2>(map, a, clusters, st);
-  return bf16 ? launch<true, true, 1>(map, a, clusters, st)
-              : launch<false, true, 1>(map, a, clusters, st);
+  const uintptr_t at = reinterpret_cast<uintptr_t>(dy);
+  if (!tma) {
+    Maps<false> maps = {};
+    for (int64_t c = 0; c < kClasses && rows > 0; ++c) {
+      const int64_t first = c < rows ? c : 0;
+      const uintptr_t row = at + 2 * first * ld;
+      if (!encode_rows(&maps.of[c], row & ~static_cast<uintptr_t>(15),
+                       n + static_cast<int64_t>(row & 15) / 2, ceil_div(rows - first, kClasses),
+                       kClasses * ld, kRawColumns, kK / kClasses, bf16))
+        return ZERO_ECUDA;
+    }
+    return bf16 ? launch<true, false, 1>(maps, a, clusters, st)
+                : launch<false, false, 1>(maps, a, clusters, st);
+  }
+  Maps<true> maps = {};
+  if (!encode_rows(&maps.of[0], at, n, rows, ld, 64, kK, bf16)) return ZERO_ECUDA;
+  if (wide == 2) return bf16 ? launch<true, true, 2>(maps, a, clusters, st)
+                             : launch<false, true, 2>(maps, a, clusters, st);
+  return bf16 ? launch<true, true, 1>(maps, a, clusters, st)
+              : launch<false, true, 1>(maps, a, clusters, st);
 }
 
 }  // extern "C"
