@@ -38,7 +38,7 @@
  *
  * A dy whose rows do not start on 16-byte boundaries comes as the 16-byte
  * blocks that hold it, and three groups of warps move it to its places beside
- * the values (at place_raw; 8000 x 2000 x 5555: 309 us against 151 at 5552.
+ * the values (at place_raw; 8000 x 2000 x 5555: 251 us against 151 at 5552.
  * One group for dy and two for the values took 416).
  *
  * Every wait is bounded (2 s); one that expires ends the work of its CTA, the
@@ -354,37 +354,52 @@ __device__ __forceinline__ void store_values(uint8_t* stage_a, const Values& x, 
 // column from its block is its class's in every step and tile.
 constexpr int kClasses = 8, kRawColumns = 128 + 8;
 constexpr int kRaw = 4, kRawPitch = kRawColumns * 2, kRawBytes = kK * kRawPitch;
-static_assert(kK * 4 == kGroupThreads, "a thread places a quarter of a row");
+static_assert(kGroupWarps == kClasses && kK == 64, "a warp places eight rows of 16 pieces");
 
 template <bool kAligned>
 struct Maps {
   CUtensorMap of[kAligned ? 1 : kClasses];
 };
 
-// Token 8 i + r of a step, class r, pieces [4 part, 4 part + 4) of eight columns;
-// d: the class's distance; left: columns that dy has from the first piece on.
-// Eight lanes with the same part, eight r and eight i meet no bank twice, in the
-// raw rows (one piece further on with i) or the stage's (swizzled by r).
-__device__ __forceinline__ void place_raw(const uint8_t* raw, uint8_t* stage_b, int i, int r,
-                                          int part, int d, int64_t left) {
-  const uint4* from =
-      reinterpret_cast<const uint4*>(raw + (r * (kK / kClasses) + i) * kRawPitch) + 4 * part;
-  uint8_t* row = stage_b + (part >> 1) * kChunk + (8 * i + r) * 128;
-  uint4 next = from[0];
+// A warp places its class: pieces of eight columns, eight of a row by eight
+// lanes, which meet no bank twice, in the raw rows or the stage's. from, to: the
+// first of the lane's four pieces (rows 4 i apart, then 64 columns on). The
+// distance is the warp's own, so that a piece costs at most four shifts (picked
+// by selects from a distance per lane, 15: 309 us). Columns past dy's end are
+// whatever lies there: no column of dw that is stored depends on them.
+template <int kDistance>
+__device__ __forceinline__ void place_pieces(const uint8_t* from, uint8_t* to) {
+  constexpr int kWord = kDistance / 4;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const uint4 block = next;
-    next = from[e + 1];
-    uint4 v = shifted(block, next, d);
-    const int64_t keep = left - 8 * e;
-    if (keep < 8) {
-      uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  for (int k = 0; k < 4; ++k) {
+    const uint4* block =
+        reinterpret_cast<const uint4*>(from + (k & 1) * (4 * kRawPitch) + (k >> 1) * 128);
+    const uint4 x = block[0], y = kDistance ? block[1] : x;
+    const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    uint32_t v[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        w[k] = 2 * k + 1 < keep ? w[k] : 2 * k < keep ? w[k] & 0xFFFFu : 0;
-      v = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    *reinterpret_cast<uint4*>(row + ((((part & 1) * 4 + e) ^ r) << 4)) = v;
+    for (int j = 0; j < 4; ++j)
+      v[j] = kDistance & 2 ? __funnelshift_r(w[kWord + j], w[kWord + j + 1], 16) : w[kWord + j];
+    *reinterpret_cast<uint4*>(to + (k & 1) * (4 * 1024) + (k >> 1) * kChunk) =
+        make_uint4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+// r: the warp's class, d: its distance
+__device__ __forceinline__ void place_raw(const uint8_t* raw, uint8_t* stage_b, int r, int lane,
+                                          int d) {
+  const int i = lane >> 3, piece = lane & 7;
+  const uint8_t* from = raw + (r * (kK / kClasses) + i) * kRawPitch + piece * 16;
+  uint8_t* to = stage_b + (8 * i + r) * 128 + ((piece ^ r) << 4);
+  switch (d >> 1) {
+    case 0: return place_pieces<0>(from, to);
+    case 1: return place_pieces<2>(from, to);
+    case 2: return place_pieces<4>(from, to);
+    case 3: return place_pieces<6>(from, to);
+    case 4: return place_pieces<8>(from, to);
+    case 5: return place_pieces<10>(from, to);
+    case 6: return place_pieces<12>(from, to);
+    default: return place_pieces<14>(from, to);
   }
 }
 
@@ -412,7 +427,7 @@ __device__ __forceinline__ void store_staged(uint8_t* stage, uint16_t* to, int64
                                              int c, int width, int count, int lane) {
   const int k = lane & 7, row0 = lane >> 3;
   const int end = c + width < count ? c + width : count;  // columns there are so far
-#pragma unroll 4
+#pragma unroll 1
   for (int pass = 0; pass < 8; ++pass) {
     const int row = pass * 4 + row0;
     if (row >= rows) continue;
@@ -564,14 +579,12 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
       return b;
     };
     bool ok = true;
-    // without TMA: the step at hand, the slot of its raw dy, and which part of
-    // that is this thread's
-    Cursor now = {tile0, 0};
+    // off the grid: the slot of the step's raw dy, and the class this warp places
     Ring<kRaw> slot;
     slot.advance(group);
-    const int place_r = lane & 7, place_i = (lane + warp) & 7;
+    const int place_class = warp % kGroupWarps;
     const int distance =
-        static_cast<int>((reinterpret_cast<uintptr_t>(a.dy) + 2 * place_r * a.ld) & 15);
+        static_cast<int>((reinterpret_cast<uintptr_t>(a.dy) + 2 * place_class * a.ld) & 15);
     // the stage of the step at hand once it is free (and its raw dy is there),
     // or NULL: given up. One warp of the group asks (many that poll slow what
     // they wait for).
@@ -596,7 +609,6 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
     };
     if (total > 0) {
       ahead.advance(group, steps, tile_stride);
-      now = ahead;
       src = source_of(ahead);
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) next[k] = load();
@@ -614,16 +626,13 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
         if (!stage) break;
         store_values(stage, v0, r, p);
         store_values(stage, v1, r + 4, p);
-        if constexpr (!kTma) {
-          const int64_t left = a.n - (column_of(now.tile) + half * (a.bn / 2) + 32 * (lane >> 3));
+        if constexpr (!kTma)
           place_raw(stages + kStages * kStageBytes + slot.stage * kRawBytes, stage + kBytesA,
-                    place_i, place_r, lane >> 3, distance, left);
-        }
+                    place_class, lane, distance);
         stored();
         if constexpr (!kTma) {
           if (tid % kGroupThreads == 0) bar_arrive_at(smem_u32(&raw_empty[slot.stage]));
           slot.advance(kGroups);
-          now.advance(kGroups, steps, tile_stride);
         }
         next[k] = load();  // not before: the proxy fence would wait for it
       }
