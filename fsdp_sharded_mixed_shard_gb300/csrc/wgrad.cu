@@ -38,8 +38,8 @@
  *
  * A dy whose rows do not start on 16-byte boundaries comes as the 16-byte
  * blocks that hold it, and three groups of warps move it to its places beside
- * the values (at place_raw; 8000 x 2000 x 5555: 251 us against 151 at 5552.
- * One group for dy and two for the values took 416).
+ * the values (at Maps; 8000 x 2000 x 5555: 256 us against 152 at 5552. One
+ * group for dy and two for the values took 416).
  *
  * Every wait is bounded (2 s); one that expires ends the work of its CTA, the
  * tiles it had left become NaN and the scaler's error word is raised.
@@ -71,13 +71,16 @@ constexpr int kM = 128, kN = 256, kK = 64;     // rows per CTA, columns at most,
 constexpr int kAhead = 2;                       // a value thread's steps loaded ahead
 constexpr int kChunk = kK * 128;               // 64 tokens x 64 columns of 16 bits
 constexpr int kBytesA = kM / 64 * kChunk, kBytesB = kN / 2 / 64 * kChunk;
-constexpr int kRing = 196 * 1024;              // shared memory for stages
+constexpr int kRing = 198 * 1024;              // shared memory for stages
 constexpr int kJoinPitch = kN + 4;             // fp32 row of a tile in shared memory
 constexpr int kSmem = kRing + 1024;
 constexpr int kMaxSplit = 4;
 // costs in cycles, from times at 768 x 2304 and 2048 x 8192 over 1 to 8192 tokens:
 // a step's values, a column put out, the join of a split
 constexpr int kValueCycles = 850, kOutCycles = 28, kJoinCycles = 3500;
+// a step's values and one or two column groups of dy off the grid, from 8192 x
+// 2048 x 8191 (341 us with one group per tile, 313 with two)
+constexpr int kPlaceCycles[2] = {1250, 2200};
 constexpr uint64_t kWaitLimitNs = 2000000000ull, kDrainNs = 1000000ull;
 static_assert(kM * kJoinPitch * 4 <= kRing, "the tile fits the stages");
 static_assert(kM == ZERO_CKPT_PAD, "a checkpoint row is whole CTA tiles");
@@ -347,13 +350,18 @@ __device__ __forceinline__ void store_values(uint8_t* stage_a, const Values& x, 
 // dy's half tile when its rows do not start on 16-byte boundaries, where no one
 // TMA map covers it: eight rows are 16 ld bytes, so each class of every eighth
 // token has a map of its own, from the boundary at or before its first element.
-// The copy warp brings a step's 64 tokens class by class, eight boxes of the
-// blocks that hold 128 columns (17 where they do not start on one), kRaw steps
-// ahead, and the groups move them to their places in the stage. A step is 64
-// rows and a tile's columns are whole blocks, so the distance d of a row's first
-// column from its block is its class's in every step and tile.
+// The copy warp brings a step's 64 tokens class by class into the stage, eight
+// boxes of the blocks that hold 128 columns (17 where they do not start on one),
+// and a group moves them to their places there: every piece is in a register
+// before the first is put back. (Slots for the raw rows beside fewer stages spare
+// that wait; the same time, and no room for two column groups.) A step is 64 rows
+// and a tile's columns are whole blocks, so the distance d of a row's first
+// column from its block is its class's in every step and tile. Shared memory
+// bounds it: per step and group of 256 columns it moves 16 KB from the copies, 32
+// to the registers, 16 back and 16 to the products, beside 32 for the values.
 constexpr int kClasses = 8, kRawColumns = 128 + 8;
-constexpr int kRaw = 4, kRawPitch = kRawColumns * 2, kRawBytes = kK * kRawPitch;
+constexpr int kRawPitch = kRawColumns * 2, kRawBytes = kK * kRawPitch;
+static_assert(kRawBytes >= kBytesB && kRawBytes % 1024 == 0, "a stage of raw rows");
 static_assert(kGroupWarps == kClasses && kK == 64, "a warp places eight rows of 16 pieces");
 
 template <bool kAligned>
@@ -361,15 +369,21 @@ struct Maps {
   CUtensorMap of[kAligned ? 1 : kClasses];
 };
 
-// A warp places its class: pieces of eight columns, eight of a row by eight
-// lanes, which meet no bank twice, in the raw rows or the stage's. from, to: the
+// A warp moves its class: pieces of eight columns, eight of a row by eight
+// lanes, which meet no bank twice, in the raw rows or the placed ones. from: the
 // first of the lane's four pieces (rows 4 i apart, then 64 columns on). The
 // distance is the warp's own, so that a piece costs at most four shifts (picked
-// by selects from a distance per lane, 15: 309 us). Columns past dy's end are
-// whatever lies there: no column of dw that is stored depends on them.
+// by selects from a distance per lane, 15: 309 us against 251). Columns past
+// dy's end are whatever lies there: no column of dw that is stored depends on
+// them.
+struct Pieces {
+  uint4 v[4];
+};
+
 template <int kDistance>
-__device__ __forceinline__ void place_pieces(const uint8_t* from, uint8_t* to) {
+__device__ __forceinline__ Pieces take_pieces(const uint8_t* from) {
   constexpr int kWord = kDistance / 4;
+  Pieces p;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const uint4* block =
@@ -380,27 +394,31 @@ __device__ __forceinline__ void place_pieces(const uint8_t* from, uint8_t* to) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       v[j] = kDistance & 2 ? __funnelshift_r(w[kWord + j], w[kWord + j + 1], 16) : w[kWord + j];
-    *reinterpret_cast<uint4*>(to + (k & 1) * (4 * 1024) + (k >> 1) * kChunk) =
-        make_uint4(v[0], v[1], v[2], v[3]);
+    p.v[k] = make_uint4(v[0], v[1], v[2], v[3]);
   }
+  return p;
 }
 
 // r: the warp's class, d: its distance
-__device__ __forceinline__ void place_raw(const uint8_t* raw, uint8_t* stage_b, int r, int lane,
-                                          int d) {
-  const int i = lane >> 3, piece = lane & 7;
-  const uint8_t* from = raw + (r * (kK / kClasses) + i) * kRawPitch + piece * 16;
-  uint8_t* to = stage_b + (8 * i + r) * 128 + ((piece ^ r) << 4);
+__device__ __forceinline__ Pieces take_raw(const uint8_t* raw, int r, int lane, int d) {
+  const uint8_t* from = raw + (r * (kK / kClasses) + (lane >> 3)) * kRawPitch + (lane & 7) * 16;
   switch (d >> 1) {
-    case 0: return place_pieces<0>(from, to);
-    case 1: return place_pieces<2>(from, to);
-    case 2: return place_pieces<4>(from, to);
-    case 3: return place_pieces<6>(from, to);
-    case 4: return place_pieces<8>(from, to);
-    case 5: return place_pieces<10>(from, to);
-    case 6: return place_pieces<12>(from, to);
-    default: return place_pieces<14>(from, to);
+    case 0: return take_pieces<0>(from);
+    case 1: return take_pieces<2>(from);
+    case 2: return take_pieces<4>(from);
+    case 3: return take_pieces<6>(from);
+    case 4: return take_pieces<8>(from);
+    case 5: return take_pieces<10>(from);
+    case 6: return take_pieces<12>(from);
+    default: return take_pieces<14>(from);
   }
+}
+
+__device__ __forceinline__ void place(uint8_t* stage_b, const Pieces& p, int r, int lane) {
+  uint8_t* to = stage_b + (8 * (lane >> 3) + r) * 128 + (((lane & 7) ^ r) << 4);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    *reinterpret_cast<uint4*>(to + (k & 1) * (4 * 1024) + (k >> 1) * kChunk) = p.v[k];
 }
 
 // An output warp's 32 columns of its lanes' rows, in the 16-bit type.
@@ -481,17 +499,17 @@ struct Ring {  // stage and the parity of its current use
 template <bool kBf16, bool kTma, int kWide>
 __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
     wgrad_kernel(const __grid_constant__ Maps<kTma> maps, const Args a) {
-  constexpr int kStageBytes = kBytesA + kWide * kBytesB;
-  constexpr int kStages = kTma ? kRing / kStageBytes : (kRing - kRaw * kRawBytes) / kStageBytes;
-  static_assert(kTma || kWide == 1, "raw copies cover one column group");
+  constexpr int kStageB = kTma ? kBytesB : kRawBytes;  // a column group's dy
+  constexpr int kStageBytes = kBytesA + kWide * kStageB;
+  constexpr int kStages = kRing / kStageBytes;
   using R = Roles<kTma>;
   constexpr int kCopyWarp = R::kCopyWarp, kProductWarp = R::kProductWarp;
   constexpr int kOutWarp0 = R::kOutWarp0, kGroups = R::kGroups;
   extern __shared__ uint8_t raw[];
   uint8_t* stages = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  // full: in the pair's first CTA, counted by both; empty and done: in each
+  // full: in the pair's first CTA, counted by both (off the grid full_b in each,
+  // for its own groups); empty and done: in each
   __shared__ uint64_t full_a[kStages], full_b[kStages], empty[kStages], done[2], free_sums[2];
-  __shared__ uint64_t raw_full[kRaw], raw_empty[kRaw];
   __shared__ uint32_t tmem_base;
   __shared__ int failed, group_ok[kGroups];
   __shared__ __align__(16) uint8_t out_stage[kOutWarps][32 * kOutPitch];
@@ -527,10 +545,6 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
       bar_init(&full_a[s], 2);
       bar_init(&full_b[s], 1);
       bar_init(&empty[s], 1);
-    }
-    for (int k = 0; k < kRaw && !kTma; ++k) {
-      bar_init(&raw_full[k], 1);
-      bar_init(&raw_empty[k], 1);
     }
     for (int k = 0; k < 2; ++k) {
       bar_init(&done[k], 1);
@@ -579,21 +593,18 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
       return b;
     };
     bool ok = true;
-    // off the grid: the slot of the step's raw dy, and the class this warp places
-    Ring<kRaw> slot;
-    slot.advance(group);
+    // off the grid: the class this warp places
     const int place_class = warp % kGroupWarps;
     const int distance =
         static_cast<int>((reinterpret_cast<uintptr_t>(a.dy) + 2 * place_class * a.ld) & 15);
-    // the stage of the step at hand once it is free (and its raw dy is there),
+    // the stage of the step at hand once it is free (off the grid: has its dy),
     // or NULL: given up. One warp of the group asks (many that poll slow what
     // they wait for).
     const auto free_stage = [&](int64_t at) -> uint8_t* {
       if (!kTma || at >= kStages) {
         if (warp % kGroupWarps == 0) {
-          const bool free =
-              (at < kStages || bar_wait(&empty[ring.stage], ring.parity ^ 1, &failed)) &&
-              (kTma || bar_wait(&raw_full[slot.stage], slot.parity, &failed));
+          const bool free = kTma ? bar_wait(&empty[ring.stage], ring.parity ^ 1, &failed)
+                                 : bar_wait(&full_b[ring.stage], ring.parity, &failed);
           if (lane == 0) group_ok[group] = free;
         }
         group_sync(group);
@@ -626,49 +637,24 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
         if (!stage) break;
         store_values(stage, v0, r, p);
         store_values(stage, v1, r + 4, p);
-        if constexpr (!kTma)
-          place_raw(stages + kStages * kStageBytes + slot.stage * kRawBytes, stage + kBytesA,
-                    place_class, lane, distance);
-        stored();
         if constexpr (!kTma) {
-          if (tid % kGroupThreads == 0) bar_arrive_at(smem_u32(&raw_empty[slot.stage]));
-          slot.advance(kGroups);
+#pragma unroll 1
+          for (uint8_t* b = stage + kBytesA; b < stage + kStageBytes; b += kStageB) {
+            const Pieces pieces = take_raw(b, place_class, lane, distance);
+            group_sync(group);
+            place(b, pieces, place_class, lane);
+          }
         }
+        stored();
         next[k] = load();  // not before: the proxy fence would wait for it
       }
     }
   } else if (warp == kCopyWarp) {
-    if constexpr (!kTma) {
-      if (lane == 0) {
-        uint8_t* raw_ring = stages + kStages * kStageBytes;
-        const uint32_t full_at = in_cta(raw_full, rank);
-        Cursor now = {tile0, 0};
-        int slot = 0;
-        uint32_t parity = 0;
-        bool ok = true;
-        for (int64_t it = 0; it < total; ++it) {
-          ok = it < kRaw || bar_wait(&raw_empty[slot], parity ^ 1, &failed);
-          if (!ok) break;
-          bar_expect(&raw_full[slot], kRawBytes);
-          const int32_t x = static_cast<int32_t>(column_of(now.tile) + half * (a.bn / 2));
-          const int32_t y = static_cast<int32_t>(s0 + now.step) * (kK / kClasses);
-#pragma unroll
-          for (int c = 0; c < kClasses; ++c)  // a class without tokens: past the end of another's
-            copy_box(raw_ring + slot * kRawBytes + c * (kRawBytes / kClasses), &maps.of[c], x,
-                     y + (c < a.rows ? 0 : 1), full_at + slot * 8);
-          now.advance(1, steps, tile_stride);
-          if (++slot == kRaw) {
-            slot = 0;
-            parity ^= 1;
-          }
-        }
-        if (!ok) drain();
-      }
-    } else if (lane == 0) {
+    if (lane == 0) {
       // one thread's dependent instructions are slow beside 22 warps: what
       // does not change from step to step is worked out before
       const int chunks = (a.bn / 2 + 63) / 64;
-      const uint32_t full_at = in_cta(full_b, leader);
+      const uint32_t full_at = in_cta(full_b, kTma ? leader : rank);
       Ring<kStages> ring;
       bool ok = true;
       int left_fresh = kStages;
@@ -683,14 +669,24 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
             ok = false;
             break;
           }
-          if (half == 0) bar_expect(&full_b[s], 2 * kWide * chunks * kChunk);
           uint8_t* b = stages + s * kStageBytes + kBytesA;
+          if constexpr (kTma) {
+            if (half == 0) bar_expect(&full_b[s], 2 * kWide * chunks * kChunk);
 #pragma unroll
-          for (int w = 0; w < kWide; ++w) {
-            copy_box(b + w * kBytesB, &maps.of[0], x + w * a.bn, y, full_at + s * 8);
-            if (chunks > 1)
-              copy_box(b + w * kBytesB + kChunk, &maps.of[0], x + w * a.bn + 64, y,
-                       full_at + s * 8);
+            for (int w = 0; w < kWide; ++w) {
+              copy_box(b + w * kStageB, &maps.of[0], x + w * a.bn, y, full_at + s * 8);
+              if (chunks > 1)
+                copy_box(b + w * kStageB + kChunk, &maps.of[0], x + w * a.bn + 64, y,
+                         full_at + s * 8);
+            }
+          } else {
+            bar_expect(&full_b[s], kWide * kRawBytes);
+#pragma unroll
+            for (int c = 0; c < kClasses; ++c)
+#pragma unroll
+              for (int w = 0; w < kWide; ++w)  // no tokens: past the end of another class
+                copy_box(b + w * kStageB + c * (kRawBytes / kClasses), &maps.of[c], x + w * a.bn,
+                         y / kClasses + (c < a.rows ? 0 : 1), full_at + s * 8);
           }
           ring.advance(1);
         }
@@ -721,7 +717,7 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
 #pragma unroll
             for (int w = 0; w < kWide; ++w)
               product(sums + w * kN, at + q * (2048 >> 4),
-                      at + ((kBytesA + w * kBytesB) >> 4) + q * (2048 >> 4), desc,
+                      at + ((kBytesA + w * kStageB) >> 4) + q * (2048 >> 4), desc,
                       q > 0 ? 1u : step);
           commit(&empty[s], pair_mask);
           ring.advance(1);
@@ -964,20 +960,21 @@ ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const
   const int64_t pairs = fit[1], m_tiles = ceil_div(a.pitch, 2 * kM);
   const bool tma = rows > 0 && ld % kVec == 0 && aligned(dy, 16);
   // Tile width, column groups and split of the tokens by the cycles they take:
-  // turns of all pairs times steps of 2 cycles per column, at least
-  // kValueCycles for the checkpoint's values; a tile put out alone at the end
+  // turns of all pairs times steps of 2 cycles per column, at least what filling
+  // a stage takes; a tile put out alone at the end
   // (two groups: every tile), and the join of a split. A split needs room for
   // all its clusters at once and four steps in each part.
   const int64_t steps = ceil_div(rows, kK);
   int wide = 1;
   int64_t best = 0;
-  for (int w = 1; w <= (tma ? 2 : 1); ++w)
+  for (int w = 1; w <= 2; ++w)
     for (int bn = kN; bn >= 128; bn -= 32)
       for (int split = 1; split <= (w == 1 ? kMaxSplit : 1); split *= 2) {
         const int64_t all = m_tiles * ceil_div(n, w * bn), turns = ceil_div(all, pairs);
         if (split > 1 && (all > fit[split] || steps < 4 * split)) break;
+        const int64_t fill = tma ? kValueCycles : kPlaceCycles[w - 1];
         const int64_t cost =
-            turns * ceil_div(steps, split) * std::max<int64_t>(2 * w * bn, kValueCycles) +
+            turns * ceil_div(steps, split) * std::max<int64_t>(2 * w * bn, fill) +
             (w == 2 ? turns : 1) * kOutCycles * w * bn + (split > 1 ? kJoinCycles : 0);
         if (best == 0 || cost < best) {
           best = cost;
@@ -1004,6 +1001,8 @@ ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const
                        kClasses * ld, kRawColumns, kK / kClasses, bf16))
         return ZERO_ECUDA;
     }
+    if (wide == 2) return bf16 ? launch<true, false, 2>(maps, a, clusters, st)
+                               : launch<false, false, 2>(maps, a, clusters, st);
     return bf16 ? launch<true, false, 1>(maps, a, clusters, st)
                 : launch<false, false, 1>(maps, a, clusters, st);
   }

@@ -349,6 +349,28 @@ def test_weight_gradient(dtype, rows, cols, n, ld, shift):
     assert shift or torch.equal(again, dw)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows,cols,n,ld,shift", [
+    (2000, 2048, 4100, 4101, 3), (2000, 2048, 4096, 4104, 0),    # two column groups per tile
+    (5, 40, 33, 35, 1), (1, 64, 9, 9, 1), (7, 32, 130, 132, 6),  # fewer tokens than row distances
+    (73, 64, 140, 142, 2), (90, 64, 300, 304, 5),                # 4 of them, and 1
+])
+def test_weight_gradient_layouts(dtype, rows, cols, n, ld, shift):
+    test_weight_gradient(dtype, rows, cols, n, ld, shift)
+
+
+def test_weight_gradient_reads_its_own_rows():
+    """NaN in every element around dy's rows, which share their blocks, stays out."""
+    rows, cols, n, ld = 75, 64, 149, 151
+    x = rand((rows, cols), "bf16", 46)
+    whole, dy = offset_rows(rows, n, ld, "bf16", 3)
+    whole.fill_(float("nan"))
+    dy.copy_(rand((rows, n), "bf16", 47))
+    dw = torch.empty(cols, n, dtype=torch.bfloat16, device="cuda")
+    run_wgrad(x, dy, ld, "bf16", dw)
+    assert torch.isfinite(dw).all()
+
+
 def test_weight_gradient_exact_on_whole_numbers():
     """Whole numbers small enough that every partial sum is exact, so any tile,
     step or split that is dropped, doubled or misplaced shows."""
