@@ -32,7 +32,7 @@ constexpr int kCols = 32 * kVec;
 template <bool kGrid>
 __device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t cols) {
   if (c + kVec <= cols)
-    return kGrid ? __ldcs(reinterpret_cast<const uint4*>(row + c)) : load8_any(row + c);
+    return kGrid ? __ldcs(reinterpret_cast<const uint4*>(row + c)) : load8_any<true>(row + c);
   uint32_t h[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) h[j] = c + j < cols ? row[c + j] : 0;

@@ -69,7 +69,7 @@ template <bool kVecRows>
 __device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t dim) {
   if constexpr (kVecRows)
     return c < dim ? __ldcs(reinterpret_cast<const uint4*>(row + c)) : make_uint4(0, 0, 0, 0);
-  if (c + kVec <= dim) return load8_any(row + c);
+  if (c + kVec <= dim) return load8_any<false>(row + c);
   uint32_t h[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) h[j] = c + j < dim ? row[c + j] : 0;

@@ -108,8 +108,39 @@ __device__ __forceinline__ uint4 narrow8(const float (&f)[8]) {
                     narrow2<kBf16>(f[4], f[5]), narrow2<kBf16>(f[6], f[7]));
 }
 
-// The 16 bytes that start d bytes (d even, 0 <= d < 16) into x and run on into
-// y, the block after it: words and halfword picked in three steps.
+// The 16 bytes that start kDistance bytes (even, below 16) into x and run on
+// into y, the block after it.
+template <int kDistance>
+__device__ __forceinline__ uint4 shifted_by(const uint4& x, const uint4& y) {
+  constexpr int kWord = kDistance / 4;
+  const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    o[j] = kDistance & 2 ? __funnelshift_r(w[kWord + j], w[kWord + j + 1], 16) : w[kWord + j];
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// The same for a distance d in 0..16 that all lanes share (rows of a warp's
+// own): a branch and at most four shifts, where selects by d take 15 (SwiGLU
+// both ways, 8000 x 8001 bf16: 264 us against 276; the table gradient, which
+// loads many rows at once, 101 against 90 at 16384 x 1111).
+__device__ __forceinline__ uint4 shifted_alike(const uint4& x, const uint4& y, int d) {
+  switch (d >> 1) {
+    case 0: return x;
+    case 1: return shifted_by<2>(x, y);
+    case 2: return shifted_by<4>(x, y);
+    case 3: return shifted_by<6>(x, y);
+    case 4: return shifted_by<8>(x, y);
+    case 5: return shifted_by<10>(x, y);
+    case 6: return shifted_by<12>(x, y);
+    case 7: return shifted_by<14>(x, y);
+    default: return y;
+  }
+}
+
+// The same for d below 16 that may differ between lanes, or where a branch
+// would keep the loads behind it waiting: words and halfword picked in steps.
 __device__ __forceinline__ uint4 shifted(const uint4& x, const uint4& y, int d) {
   const uint32_t c[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
   uint32_t t[6], w[5], o[4];
@@ -122,19 +153,22 @@ __device__ __forceinline__ uint4 shifted(const uint4& x, const uint4& y, int d) 
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// The 16 bytes that end d bytes (d even, 0 <= d < 16) before the end of y.
+// The 16 bytes that end d bytes (even, below 16) before the end of y.
 __device__ __forceinline__ uint4 shifted_back(const uint4& x, const uint4& y, int d) {
   return d ? shifted(x, y, 16 - d) : y;
 }
 
 // Eight 16-bit elements at any element address, from the one or two 16-byte
 // blocks that hold them; the caller knows that all eight lie in its buffer.
+// kAlike: the warp's lanes load one row, nothing else is loaded meanwhile.
+template <bool kAlike>
 __device__ __forceinline__ uint4 load8_any(const uint16_t* p) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(p);
   const uint4* block = reinterpret_cast<const uint4*>(at & ~static_cast<uintptr_t>(15));
   const uint4 x = *block;
   const int d = static_cast<int>(at & 15);
-  return d ? shifted(x, block[1], d) : x;
+  if (d == 0) return x;
+  return kAlike ? shifted_alike(x, block[1], d) : shifted(x, block[1], d);
 }
 
 // A warp's store of up to 256 neighbouring elements to any element address,
@@ -159,7 +193,7 @@ __device__ __forceinline__ void store_any(uint8_t* stage, uint16_t* to, int coun
     if (16 * k - d < 0 || 16 * k - d + 16 > bytes) return;
     const uint4 x = mine[k - 1];
     const uint4 y = mine[k];
-    __stcs(reinterpret_cast<uint4*>(blocks + 16 * k), shifted_back(x, y, d));
+    __stcs(reinterpret_cast<uint4*>(blocks + 16 * k), shifted_alike(x, y, 16 - d));
   };
   block(lane);  // block 32 is never whole unless d is 0, and then it is past the run
   // at most seven elements before the first whole block and after the last

@@ -382,19 +382,13 @@ struct Pieces {
 
 template <int kDistance>
 __device__ __forceinline__ Pieces take_pieces(const uint8_t* from) {
-  constexpr int kWord = kDistance / 4;
   Pieces p;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const uint4* block =
         reinterpret_cast<const uint4*>(from + (k & 1) * (4 * kRawPitch) + (k >> 1) * 128);
-    const uint4 x = block[0], y = kDistance ? block[1] : x;
-    const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-    uint32_t v[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      v[j] = kDistance & 2 ? __funnelshift_r(w[kWord + j], w[kWord + j + 1], 16) : w[kWord + j];
-    p.v[k] = make_uint4(v[0], v[1], v[2], v[3]);
+    const uint4 x = block[0];
+    p.v[k] = kDistance ? shifted_by<kDistance>(x, block[1]) : x;
   }
   return p;
 }
