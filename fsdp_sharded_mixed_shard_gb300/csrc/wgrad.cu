@@ -30,7 +30,7 @@
  * 240 us with one group. 1024 x 768 x 2304 takes 13 us, of which 8 are set-up,
  * the first copies' latency and the output.
  *
- * Few tiles and many tokens: a cluster of 2 or 4 pairs shares a tile, each
+ * Few tiles and many tokens: a cluster of 2, 4 or 8 pairs shares a tile, each
  * pair a part of the tokens; the sums meet in shared memory and every CTA adds
  * its share of the rows over the cluster in rank order. Split and tile width
  * depend on the sizes and the device alone, so results do not change from call
@@ -74,10 +74,14 @@ constexpr int kBytesA = kM / 64 * kChunk, kBytesB = kN / 2 / 64 * kChunk;
 constexpr int kRing = 198 * 1024;              // shared memory for stages
 constexpr int kJoinPitch = kN + 4;             // fp32 row of a tile in shared memory
 constexpr int kSmem = kRing + 1024;
-constexpr int kMaxSplit = 4;
+constexpr int kMaxSplit = 8, kJoinAhead = 4;
 // costs in cycles, from times at 768 x 2304 and 2048 x 8192 over 1 to 8192 tokens:
 // a step's values, a column put out, the join of a split
 constexpr int kValueCycles = 850, kOutCycles = 28, kJoinCycles = 3500;
+// clusters of 16 CTAs, beside that: together and each. Only for the narrowest
+// tiles (8192 x 256 x 256: two clusters of 128 columns 21.9 us, one of 256
+// columns 29.3, smaller clusters 26.2; 8192 x 100 x 101: 24 against 32).
+constexpr int kBigClusterCycles = 4000, kPerBigCluster = 1000;
 // a step's values and one or two column groups of dy off the grid, from 8192 x
 // 2048 x 8191 (341 us with one group per tile, 313 with two)
 constexpr int kPlaceCycles[2] = {1250, 2200};
@@ -797,23 +801,26 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
       if (i >= a.cols) break;
       float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
       if (lane * 8 < a.bn) {
-        float4 x[kMaxSplit], y[kMaxSplit];
+        for (int k0 = 0; k0 < a.split; k0 += kJoinAhead) {
+          float4 x[kJoinAhead], y[kJoinAhead];
 #pragma unroll
-        for (int k = 0; k < kMaxSplit; ++k) {
-          if (k >= a.split) break;
-          const uint32_t remote = in_cta(tile_sums + row * kJoinPitch + lane * 8, 2 * k + half);
-          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                       : "=f"(x[k].x), "=f"(x[k].y), "=f"(x[k].z), "=f"(x[k].w)
-                       : "r"(remote));
-          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                       : "=f"(y[k].x), "=f"(y[k].y), "=f"(y[k].z), "=f"(y[k].w)
-                       : "r"(remote + 16));
-        }
+          for (int k = 0; k < kJoinAhead; ++k) {
+            if (k0 + k >= a.split) break;
+            const uint32_t remote =
+                in_cta(tile_sums + row * kJoinPitch + lane * 8, 2 * (k0 + k) + half);
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(x[k].x), "=f"(x[k].y), "=f"(x[k].z), "=f"(x[k].w)
+                         : "r"(remote));
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(y[k].x), "=f"(y[k].y), "=f"(y[k].z), "=f"(y[k].w)
+                         : "r"(remote + 16));
+          }
 #pragma unroll
-        for (int k = 0; k < kMaxSplit; ++k) {
-          if (k >= a.split) break;
-          f[0] += x[k].x, f[1] += x[k].y, f[2] += x[k].z, f[3] += x[k].w;
-          f[4] += y[k].x, f[5] += y[k].y, f[6] += y[k].z, f[7] += y[k].w;
+          for (int k = 0; k < kJoinAhead; ++k) {
+            if (k0 + k >= a.split) break;
+            f[0] += x[k].x, f[1] += x[k].y, f[2] += x[k].z, f[3] += x[k].w;
+            f[4] += y[k].x, f[5] += y[k].y, f[6] += y[k].z, f[7] += y[k].w;
+          }
         }
       }
       const int64_t left = a.n - j;
@@ -888,11 +895,19 @@ struct Launch {
   }
 };
 
+// the kernel's shared memory, and clusters of 16 CTAs
+template <class Kernel>
+bool prepare(Kernel fn) {
+  return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) ==
+             cudaSuccess &&
+         cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+             cudaSuccess;
+}
+
 template <bool kBf16, bool kTma, int kWide>
 int launch(const Maps<kTma>& maps, const Args& a, int clusters, cudaStream_t st) {
   const auto fn = wgrad_kernel<kBf16, kTma, kWide>;
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
-    return ZERO_ECUDA;
+  if (!prepare(fn)) return ZERO_ECUDA;
   Launch l(clusters, a.split, Roles<kTma>::kThreads, st);
   return status_of(cudaLaunchKernelEx(&l.cfg, fn, maps, a));
 }
@@ -909,9 +924,7 @@ int resident_clusters(int split) {
   if (n == 0) {
     const auto fn = wgrad_kernel<true, true, 1>;
     Launch l(1, split, Roles<true>::kThreads, nullptr);
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
-            cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, fn, &l.cfg) != cudaSuccess)
+    if (!prepare(fn) || cudaOccupancyMaxActiveClusters(&n, fn, &l.cfg) != cudaSuccess)
       return 0;
     known[dev][split].store(n, std::memory_order_relaxed);
   }
@@ -950,14 +963,15 @@ ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const
   a.vec_out = n % kVec == 0 && aligned(dw, 16);
   int fit[kMaxSplit + 1];
   for (int split = 1; split <= kMaxSplit; split *= 2)
-    if ((fit[split] = resident_clusters(split)) <= 0) return ZERO_ECUDA;
+    fit[split] = resident_clusters(split);
+  if (fit[1] <= 0) return ZERO_ECUDA;
   const int64_t pairs = fit[1], m_tiles = ceil_div(a.pitch, 2 * kM);
   const bool tma = rows > 0 && ld % kVec == 0 && aligned(dy, 16);
   // Tile width, column groups and split of the tokens by the cycles they take:
   // turns of all pairs times steps of 2 cycles per column, at least what filling
-  // a stage takes; a tile put out alone at the end
-  // (two groups: every tile), and the join of a split. A split needs room for
-  // all its clusters at once and four steps in each part.
+  // a stage takes; a tile put out alone at the end (two groups: every tile), and
+  // the join of a split. A split needs room for all its clusters at once and
+  // four steps in each part.
   const int64_t steps = ceil_div(rows, kK);
   int wide = 1;
   int64_t best = 0;
@@ -966,10 +980,12 @@ ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const
       for (int split = 1; split <= (w == 1 ? kMaxSplit : 1); split *= 2) {
         const int64_t all = m_tiles * ceil_div(n, w * bn), turns = ceil_div(all, pairs);
         if (split > 1 && (all > fit[split] || steps < 4 * split)) break;
+        if (split == kMaxSplit && bn > kM) break;
         const int64_t fill = tma ? kValueCycles : kPlaceCycles[w - 1];
         const int64_t cost =
             turns * ceil_div(steps, split) * std::max<int64_t>(2 * w * bn, fill) +
-            (w == 2 ? turns : 1) * kOutCycles * w * bn + (split > 1 ? kJoinCycles : 0);
+            (w == 2 ? turns : 1) * kOutCycles * w * bn + (split > 1 ? kJoinCycles : 0) +
+            (split == kMaxSplit ? kBigClusterCycles + kPerBigCluster * all : 0);
         if (best == 0 || cost < best) {
           best = cost;
           a.bn = bn;

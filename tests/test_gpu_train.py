@@ -354,6 +354,7 @@ def test_weight_gradient(dtype, rows, cols, n, ld, shift):
     (2000, 2048, 4100, 4101, 3), (2000, 2048, 4096, 4104, 0),    # two column groups per tile
     (5, 40, 33, 35, 1), (1, 64, 9, 9, 1), (7, 32, 130, 132, 6),  # fewer tokens than row distances
     (73, 64, 140, 142, 2), (90, 64, 300, 304, 5),                # 4 of them, and 1
+    (8192, 100, 101, 101, 0), (8190, 64, 96, 104, 0),            # tokens split eight ways
 ])
 def test_weight_gradient_layouts(dtype, rows, cols, n, ld, shift):
     test_weight_gradient(dtype, rows, cols, n, ld, shift)
