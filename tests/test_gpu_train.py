@@ -638,3 +638,20 @@ def test_offsets_past_32_bits():
     g[-1] -= 1.0
     assert (x[-1].double() - g).norm() <= 2 * U["bf16"] * g.norm()
     assert (x[:-1:997] == 0).all()
+
+
+@pytest.mark.parametrize("rows,cols,n", [(8192, 2048, 8192), (1024, 768, 2304), (3000, 200, 1111)])
+def test_weight_gradient_is_the_same_every_time(rows, cols, n):
+    """Alone, and with another gradient between two that nothing waits between."""
+    x, dy = [rand((rows, cols), "bf16", k) for k in (94, 95)], [rand((rows, n), "bf16", k, 0.1)
+                                                                  for k in (96, 97)]
+    dw = [torch.empty(cols, n, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    run_wgrad(x[0], dy[0], n, "bf16", dw[0])
+    torch.cuda.synchronize()
+    alone = dw[0].clone()
+    for _ in range(10):
+        dw[0].zero_()
+        torch.cuda.synchronize()
+        for k in (0, 1, 0):
+            run_wgrad(x[k], dy[k], n, "bf16", dw[k])
+        assert torch.equal(dw[0], alone)
