@@ -62,16 +62,20 @@ struct Args {
 
 // exp(x - m) is formed as 2^(x c - m c) with c = log2 e: one fused
 // multiply-add per element, and what m c loses in rounding is the same for
-// every element and cancels. From |m| = 2^100 on m c could overflow; there two
-// different 16-bit or fp32 numbers of m's size are more than 2^70 apart, so
-// any c gives 1 for x = m and 0 for the rest, and 1/2 stays finite.
+// every element and cancels. It is a factor of at most 2^64 (half an ulp of
+// m c) below |m| = kFar, and would pass fp32's range soon after. From there on
+// every other logit is at least 64 away from m, so that 2^(x - m) and
+// exp(x - m) alike are nothing beside the 1 of m itself: c = 1, whose products
+// are exact.
+constexpr float kFar = 0x1p30f;
+
 struct Base {
   float c, mc;
 };
 
 __device__ __forceinline__ Base base_of(float m) {
   const float at = m == -INFINITY ? 0.f : m;  // nothing but -inf so far
-  const float c = fabsf(at) < 0x1p100f ? kLog2e : 0.5f;
+  const float c = fabsf(at) < kFar ? kLog2e : 1.f;
   return Base{c, at * c};
 }
 
@@ -80,10 +84,12 @@ struct Stat {
   float m, s;
 };
 
-// a's sum over another, not smaller, maximum
+// a's sum over another, not smaller, maximum. Maxima on two sides of kFar are
+// so far apart that nothing of the smaller one's sum is left.
 __device__ __forceinline__ float moved(const Stat& a, float m) {
-  // a side with nothing adds nothing; inf and NaN go on into the sum
-  return a.s == 0.f ? 0.f : a.s * exp2_fast(base_of(a.m).mc - base_of(m).mc);
+  const Base from = base_of(a.m), to = base_of(m);
+  // a side with nothing adds nothing; NaN goes on into the sum
+  return a.s == 0.f ? 0.f : a.s * (from.c == to.c ? exp2_fast(from.mc - to.mc) : 0.f);
 }
 
 // the pairs of a warp's lanes; all lanes hold the same bits afterwards
@@ -214,7 +220,7 @@ __device__ __forceinline__ void add_blocks(Stat& t, const uint4 (&v)[kBatch]) {
 // log(exp(x - m) / s)
 __device__ __forceinline__ float log_share(float x, const Stat& t) {
   const Base b = base_of(t.m);
-  return __fmaf_rn(x, b.c, -b.mc) * (b.c == 0.5f ? 2.f : kLn2) - logf(t.s);
+  return __fmaf_rn(x, b.c, -b.mc) * (b.c == 1.f ? 1.f : kLn2) - logf(t.s);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
