@@ -217,10 +217,12 @@ __device__ __forceinline__ void add_blocks(Stat& t, const uint4 (&v)[kBatch]) {
   t.s += x + y;
 }
 
-// log(exp(x - m) / s)
+// log(exp(x - m) / s). The products x c and m c leave fp32 where x is a type's
+// lowest value (a masked token taken); the difference itself is the result there.
 __device__ __forceinline__ float log_share(float x, const Stat& t) {
   const Base b = base_of(t.m);
-  return __fmaf_rn(x, b.c, -b.mc) * (b.c == 1.f ? 1.f : kLn2) - logf(t.s);
+  const bool plain = b.c == 1.f || !(fabsf(x) < 0x1p126f);
+  return (plain ? x - t.m : __fmaf_rn(x, b.c, -b.mc) * kLn2) - logf(t.s);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {

@@ -1,5 +1,5 @@
 """Token log-probabilities and the policy loss on rows with odd values: large
-finite logits, masks among them."""
+finite logits, masks among them, and taken tokens of the type's lowest value."""
 import math
 
 import pytest
@@ -123,3 +123,29 @@ def test_masked_token_taken(dtype, rows, v, fill):
     act = x.float().argmin(1)
     want, bound, _ = logp64(x, act)
     within(token_logp(x, act), want, bound + want.abs() * 2.0 ** -22, "token logp")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32", "fp16"])
+@pytest.mark.parametrize("v", [40, 50257])
+def test_lowest_value_taken(dtype, v):
+    """The lowest finite value less a few units is that value in fp32, so the
+    ratio to a policy that says the same is 1 and its KL term 0."""
+    low = torch.finfo(DT[dtype]).min
+    x = rand((3, v), dtype, 14)
+    x[:, 5:] = low
+    x[2, 0] = -low / 2  # the sum of the two passes the type's range
+    act = torch.tensor([7, v - 1, 9], device="cuda", dtype=torch.int32)
+    want, _, p = logp64(x, act)
+    want = want.float()
+    lp = token_logp(x, act)
+    assert torch.isfinite(lp[:2]).all()
+    within(lp, want, want.abs().double() * 2.0 ** -22, "token logp")
+    adv = torch.tensor([1.0, -2.0, 0.5], device="cuda")
+    w = torch.ones(3, device="cuda")
+    dl = torch.empty_like(x)
+    got, loss, stats = T.run_policy(x[:2], v, dtype, act[:2], lp[:2], lp[:2], adv[:2], w[:2],
+                                    Z.ZeroPolicyParams(0.2, 0.2, 0.1), None, dl[:2])
+    assert torch.equal(got, lp[:2]) and torch.equal(loss, -adv[:2]) and stats[1] == 0
+    want_g = adv[:2, None].double() * p[:2]
+    want_g.scatter_add_(1, act[:2].long()[:, None], -adv[:2, None].double())
+    within(dl[:2], want_g, U[dtype] * want_g.abs() + 2.0 ** -18 * p[:2] + TINY[dtype], "dlogits")
