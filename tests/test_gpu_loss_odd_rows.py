@@ -1,5 +1,6 @@
 """Token log-probabilities and the policy loss on rows with odd values: large
-finite logits, masks among them, and taken tokens of the type's lowest value."""
+finite logits, masks among them, taken tokens of the type's lowest value and ruled-out
+tokens in the statistics."""
 import math
 
 import pytest
@@ -149,3 +150,17 @@ def test_lowest_value_taken(dtype, v):
     want_g = adv[:2, None].double() * p[:2]
     want_g.scatter_add_(1, act[:2].long()[:, None], -adv[:2, None].double())
     within(dl[:2], want_g, U[dtype] * want_g.abs() + 2.0 ** -18 * p[:2] + TINY[dtype], "dlogits")
+
+
+@pytest.mark.parametrize("rows", [5, 3000])
+def test_kl_statistic_without_a_reference(rows):
+    """No reference, no KL term: 0 also where the taken token is ruled out."""
+    v = 33
+    x = rand((rows, v), "bf16", 15)
+    x[3, 4] = float("-inf")
+    act = torch.full((rows,), 4, device="cuda", dtype=torch.int32)
+    one = torch.ones(rows, device="cuda")
+    lp, loss, stats = T.run_policy(x, v, "bf16", act, -one, None, one, one,
+                                   Z.ZeroPolicyParams(0.2, 0.2, 0.5), None, None)
+    assert lp[3] == float("-inf") and torch.isfinite(loss).all()
+    assert stats[1] == 0 and stats[3] == rows
