@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(32 * kWarps, 24 / kWarps)
 }
 
 // Sum with what each addition lost beside it (the file is built without
-// contraction and reassociation).
+// contraction and reassociation). Beside an infinite sum `lo` holds inf - inf.
 struct Sum {
   float hi = 0.f, lo = 0.f;
   __device__ __forceinline__ void add(float x) {
@@ -654,6 +654,7 @@ struct Sum {
     lo += (hi - (t - b)) + (x - b);
     hi = t;
   }
+  __device__ __forceinline__ float value() const { return fabsf(hi) < INFINITY ? hi + lo : hi; }
 };
 
 // The four sums over the rows that are not left out, by one CTA: each thread
@@ -694,7 +695,7 @@ __global__ void __launch_bounds__(1024) stats_kernel(const Args a) {
   if (warp < 4) {
     Sum v = part[warp][lane];
     tree(v);
-    if (lane == 0) a.stats[warp] = v.hi + v.lo;
+    if (lane == 0) a.stats[warp] = v.value();
   }
 }
 

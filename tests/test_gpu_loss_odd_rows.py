@@ -1,6 +1,6 @@
 """Token log-probabilities and the policy loss on rows with odd values: large
-finite logits, masks among them, taken tokens of the type's lowest value and ruled-out
-tokens in the statistics."""
+finite logits, masks among them, taken tokens of the type's lowest value, ruled-out tokens
+and infinite losses in the statistics."""
 import math
 
 import pytest
@@ -164,3 +164,24 @@ def test_kl_statistic_without_a_reference(rows):
                                    Z.ZeroPolicyParams(0.2, 0.2, 0.5), None, None)
     assert lp[3] == float("-inf") and torch.isfinite(loss).all()
     assert stats[1] == 0 and stats[3] == rows
+
+
+@pytest.mark.parametrize("rows,at", [(1, 0), (5, 3), (3000, 0), (3000, 1700), (3000, 2999)])
+def test_infinite_loss_in_the_statistics(rows, at):
+    """A ratio past fp32 with a negative advantage: that row's loss is +inf, and
+    so is the sum; the other sums do not change."""
+    v = 33
+    x = rand((rows, v), "bf16", 16)
+    act = torch.full((rows,), 4, device="cuda", dtype=torch.int32)
+    one = torch.ones(rows, device="cuda")
+    old = token_logp(x, act)
+    old[at] = -1000.0
+    lp, loss, stats = T.run_policy(x, v, "bf16", act, old, None, -one, one,
+                                   Z.ZeroPolicyParams(0.2, 0.2, 0.0), None, None)
+    assert loss[at] == math.inf and torch.isfinite(loss).sum() == rows - 1
+    assert stats[0] == math.inf and stats[1] == 0 and stats[2] == 0 and stats[3] == rows
+    # finite terms whose sum passes fp32, at ratios of 1: the call's own logp
+    big = torch.full((rows,), 3e38, device="cuda")
+    _, loss, stats = T.run_policy(x, v, "bf16", act, lp, None, -big, one,
+                                  Z.ZeroPolicyParams(0.2, 0.2, 0.0), None, None)
+    assert torch.equal(loss, big) and stats[0] == (math.inf if rows > 1 else 3e38)
