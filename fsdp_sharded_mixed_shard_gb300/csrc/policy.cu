@@ -669,14 +669,15 @@ __global__ void __launch_bounds__(1024) stats_kernel(const Args a) {
   for (int64_t row = tid; row < a.rows; row += 1024) {
     const float w = a.weight[row], lp = a.logp[row], old = a.old_logp[row];
     const float adv = a.advantage[row], loss = a.loss[row];
-    const float ref = a.ref_logp ? a.ref_logp[row] : 0.f;
+    const float ref = a.ref_logp ? a.ref_logp[row] : lp;
     if (w == 0.f || load_id(a.actions, a.action_bytes, row, a.vocab) < 0) continue;
-    const float r = expf(lp - old), d = a.ref_logp ? ref - lp : 0.f;  // no KL term
+    const float r = expf(lp - old), d = ref - lp;
     s[0].add(w * loss);
     s[1].add(w * (expm1f(d) - d));
     if (fminf(fmaxf(r, a.lo), a.hi) * adv < r * adv) s[2].add(w);
     s[3].add(w);
   }
+  if (!a.ref_logp) s[1] = Sum();  // no KL term, also where lp - lp is not 0
   const auto tree = [](Sum& v) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
