@@ -702,6 +702,10 @@ __global__ void __launch_bounds__(1024) stats_kernel(const Args a) {
 
 constexpr int kLaneBlocks = 16;
 constexpr int kStageCap = 196 * 1024;  // a CTA's share of a row, at most
+// the longest row off the 16-byte grid has a block more; whole blocks per part
+static_assert(((ZERO_MAX_LOGIT_ROW_BYTES / 16 + 1) / (kMaxCluster * kMaxWarps * kParts) + 1) *
+                      (16 * kMaxWarps * kParts) <= kStageCap,
+              "a cluster holds the longest row");
 constexpr int kStageGoal = 72 * 1024;  // three CTAs per SM
 
 // bytes of shared memory per CTA for rows of at most `blocks` blocks
@@ -858,8 +862,7 @@ ZERO_API int zero_policy_loss(const void* logits, int64_t rows, int64_t vocab, i
       !(params->kl_coef >= 0) || std::isinf(params->clip_hi) || std::isinf(params->kl_coef))
     return ZERO_EINVAL;
   const size_t size = dtype == ZERO_FP32 ? 4 : 2;
-  if (vocab * static_cast<int64_t>(size) > ZERO_MAX_LOGIT_ROW_BYTES - 16 * kMaxCluster)
-    return ZERO_ERANGE;
+  if (vocab * static_cast<int64_t>(size) > ZERO_MAX_LOGIT_ROW_BYTES) return ZERO_ERANGE;
   if (rows && (!old_logp || !advantage || !weight || !loss)) return ZERO_EINVAL;
   if (!aligned(old_logp, 4) || !aligned(ref_logp, 4) || !aligned(advantage, 4) ||
       !aligned(weight, 4) || !aligned(loss, 4) || !aligned(stats, 4) || !aligned(dlogits, size) ||

@@ -1,6 +1,6 @@
 """Token log-probabilities and the policy loss on rows with odd values: large
 finite logits, masks among them, taken tokens of the type's lowest value, ruled-out tokens
-and infinite losses in the statistics."""
+and infinite losses in the statistics, rows of the largest length."""
 import math
 
 import pytest
@@ -185,3 +185,10 @@ def test_infinite_loss_in_the_statistics(rows, at):
     _, loss, stats = T.run_policy(x, v, "bf16", act, lp, None, -big, one,
                                   Z.ZeroPolicyParams(0.2, 0.2, 0.0), None, None)
     assert torch.equal(loss, big) and stats[0] == (math.inf if rows > 1 else 3e38)
+
+
+@pytest.mark.parametrize("dtype,shift", [("bf16", 0), ("bf16", 1), ("bf16", 7), ("fp16", 3),
+                                         ("fp32", 0), ("fp32", 3)])
+def test_rows_of_the_largest_length(dtype, shift):
+    v = Z.ZERO_MAX_LOGIT_ROW_BYTES // (4 if dtype == "fp32" else 2)
+    T.test_policy_loss(2, v, v, shift, dtype)

@@ -142,3 +142,14 @@ def test_loss():
         refused(EINVAL, f, *changed(ok, i11=Z.ZeroPolicyParams(lo, hi, beta)))
     most = Z.ZERO_MAX_LOGIT_ROW_BYTES // 2
     refused(ERANGE, f, *changed(ok, i2=most + 1, i3=most + 1))
+
+
+def test_longest_loss_row():
+    """A row of exactly ZERO_MAX_LOGIT_ROW_BYTES passes the length check (the
+    refusal is a later one), one element more does not."""
+    hp = Z.ZeroPolicyParams(0.2, 0.2, 0.1)
+    for dt, size in ((BF, 2), (Z.ZERO_FP16, 2), (Z.ZERO_FP32, 4)):
+        v = Z.ZERO_MAX_LOGIT_ROW_BYTES // size
+        ok = [P, 4, v, v, dt, P, 4, P, P, P, P, hp, 0, P, P + 2, P, P]
+        refused(EALIGN, Z.zero_policy_loss, *ok)
+        refused(ERANGE, Z.zero_policy_loss, *changed(ok, i2=v + 1, i3=v + 1))
