@@ -304,6 +304,8 @@ struct Source {
   int32_t left;
 };
 
+// Ordinary loads: the kernel before may have written the checkpoint while this
+// one was already resident, which the read-only path does not allow for.
 __device__ __forceinline__ Piece load_piece(const Args& a, const Source& s, int64_t q_step,
                                             int64_t scale_step) {
   Piece b;
@@ -313,8 +315,8 @@ __device__ __forceinline__ Piece load_piece(const Args& a, const Source& s, int6
     b.scale[k] = 127;
     if (s.left > 4 * k &&
         ZCHECK(s.q + k * q_step + 16 <= a.q + a.rows * a.pitch, kSiteLoad, s.left)) {
-      b.q[k] = __ldg(reinterpret_cast<const uint4*>(s.q + k * q_step));
-      b.scale[k] = __ldg(s.scale + k * scale_step);
+      b.q[k] = *reinterpret_cast<const uint4*>(s.q + k * q_step);
+      b.scale[k] = s.scale[k * scale_step];
     }
   }
   return b;
