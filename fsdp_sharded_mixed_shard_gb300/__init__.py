@@ -39,6 +39,7 @@ __all__ = [
     "zero_embedding", "zero_embedding_workspace_bytes", "zero_embedding_grad",
     "zero_ckpt_bytes", "zero_ckpt_save", "zero_ckpt_load", "zero_ckpt_act",
     "zero_ckpt_act_grad", "zero_ckpt_wgrad", "zero_token_logp", "zero_policy_loss",
+    "ZERO_PLANT_NOTHING", "ZERO_PLANT_NO_COPY", "zero_selftest_plant",
 ]
 
 ZERO_BF16 = 0
@@ -52,6 +53,7 @@ ZERO_MAX_LOGIT_ROW_BYTES = 8 * 192 * 1024
 ZERO_CKPT_BLOCK = 32
 ZERO_CKPT_PAD = 128
 ZERO_ACT_GELU, ZERO_ACT_SWIGLU = range(2)
+ZERO_PLANT_NOTHING, ZERO_PLANT_NO_COPY = range(2)
 (ZERO_FULL_SHARD, ZERO_SHARD_GRAD_OP, ZERO_NO_SHARD, ZERO_HYBRID_SHARD,
  ZERO_NO_RESHARD_AFTER_FORWARD) = range(5)
 
@@ -238,6 +240,7 @@ def lib():
         L.zero_token_logp.argtypes = [_VP, i64, i64, i64, i32, _VP, i32, _VP, _VP]
         L.zero_policy_loss.argtypes = [_VP, i64, i64, i64, i32, _VP, i32, _VP, _VP, _VP, _VP,
                                        _P(ZeroPolicyParams), _VP, _VP, _VP, _VP, _VP, _VP]
+        L.zero_selftest_plant.argtypes = [i32, i64, i64]
         _lib = L
     return _lib
 
@@ -628,6 +631,10 @@ def zero_checked_status(stream=0):
     _check("zero_checked_status", lib().zero_checked_status(C.byref(n), C.byref(first),
                                                             _vp(stream)))
     return n.value, first.value
+
+
+def zero_selftest_plant(what, at=0, limit_ns=20_000_000):
+    _check("zero_selftest_plant", lib().zero_selftest_plant(what, at, limit_ns))
 
 
 def zero_selftest_check(stream=0):

@@ -299,6 +299,11 @@ bool on_grid(const void* p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; 
 }  // namespace zc
 
 #ifdef ZERO_CHECKED
+namespace zt {
+static Plant g_plant = {ZERO_PLANT_NOTHING, 0, kWaitLimitNs};
+Plant planted() { return g_plant; }
+}  // namespace zt
+
 extern "C" int zc_collect_checks(unsigned long long* count, unsigned long long* first) {
   return collect_checks(count, first);
 }
@@ -391,6 +396,19 @@ ZERO_API int zero_ckpt_act_grad(int32_t act, const void* ckpt_x, const void* ckp
       on_grid(dy, ld_dy) && on_grid(dx, ld) && on_grid(du, ld) && on_grid(y, ld);
   return gated ? launch<kSwigluGrad>(a, dtype, align, stream)
                : launch<kGeluGrad>(a, dtype, align, stream);
+}
+
+ZERO_API int zero_selftest_plant(int32_t what, int64_t at, int64_t limit_ns) {
+  if (what < ZERO_PLANT_NOTHING || what > ZERO_PLANT_NO_COPY || limit_ns < 1 ||
+      limit_ns > 1000000000)
+    return ZERO_EINVAL;
+#ifdef ZERO_CHECKED
+  zt::g_plant = {what, at, what ? static_cast<uint64_t>(limit_ns) : zt::kWaitLimitNs};
+  return ZERO_OK;
+#else
+  (void)at;
+  return ZERO_ESTATE;
+#endif
 }
 
 }  // extern "C"

@@ -204,6 +204,46 @@ __device__ __forceinline__ void store_any(uint8_t* stage, uint16_t* to, int coun
   if (tail + lane < count) to[tail + lane] = elems[tail + lane];
 }
 
+__device__ __forceinline__ uint64_t global_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+
+// given up: lets the copies and products in flight (microseconds) land
+__device__ __forceinline__ void drain() {
+  constexpr uint64_t kDrainNs = 1000000;
+  const uint64_t t0 = global_ns();
+  while (global_ns() - t0 < kDrainNs) {
+  }
+}
+
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+
+// A mistake to make on purpose (zero_selftest_plant), and how long a wait may
+// take; the release build has neither.
+struct Plant {
+#ifdef ZERO_CHECKED
+  int32_t what;
+  int64_t at;
+  uint64_t limit_ns;
+  __device__ __forceinline__ bool holds(int32_t kind, int64_t where) const {
+    return what == kind && at == where;
+  }
+  __device__ __forceinline__ uint64_t limit() const { return limit_ns; }
+#else
+  __device__ __forceinline__ bool holds(int32_t, int64_t) const { return false; }
+  __device__ __forceinline__ uint64_t limit() const { return kWaitLimitNs; }
+#endif
+};
+
+// the plant for a launch
+#ifdef ZERO_CHECKED
+Plant planted();
+#else
+inline Plant planted() { return Plant{}; }
+#endif
+
 // Token ids are int32 or int64; an id outside [0, limit) becomes -1.
 __device__ __forceinline__ int64_t load_id(const void* ids, int32_t bytes, int64_t i,
                                            int64_t limit) {

@@ -41,8 +41,10 @@
  * the values (at Maps; 8000 x 2000 x 5555: 256 us against 152 at 5552. One
  * group for dy and two for the values took 416).
  *
- * Every wait is bounded (2 s); one that expires ends the work of its CTA, the
- * tiles it had left become NaN and the scaler's error word is raised.
+ * Every wait is bounded (2 s). One that expires ends the work of its cluster:
+ * the sums of a tile are given out only when all its products were issued, the
+ * tiles left become NaN, copies and products in flight land before the CTAs
+ * end, and the scaler's error word is raised.
  */
 #include <cuda.h>
 
@@ -85,7 +87,6 @@ constexpr int kBigClusterCycles = 4000, kPerBigCluster = 1000;
 // a step's values and one or two column groups of dy off the grid, from 8192 x
 // 2048 x 8191 (341 us with one group per tile, 313 with two)
 constexpr int kPlaceCycles[2] = {1250, 2200};
-constexpr uint64_t kWaitLimitNs = 2000000000ull, kDrainNs = 1000000ull;
 static_assert(kM * kJoinPitch * 4 <= kRing, "the tile fits the stages");
 static_assert(kM == ZERO_CKPT_PAD, "a checkpoint row is whole CTA tiles");
 
@@ -97,6 +98,7 @@ struct Args {
   zero_scaler* scaler;
   int64_t rows, cols, pitch, n, ld;
   int32_t split, vec_out, bn, m_tiles, tiles;
+  Plant plant;
 };
 
 // ------------------------------------------------------------- primitives ----
@@ -146,31 +148,28 @@ __device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-__device__ __forceinline__ uint64_t global_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
+// Sets *failed in every CTA of the cluster (each stays until all have ended).
+__device__ __forceinline__ void give_up(int* failed) {
+  uint32_t n;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+  for (uint32_t r = 0; r < n; ++r)
+    asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], 1;" ::"r"(in_cta(failed, r))
+                 : "memory");
 }
 
 // true when the phase has completed; false once *failed is set or the limit
 // has passed (which sets it)
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* failed) {
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, int* failed,
+                                         uint64_t limit) {
   if (bar_try(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   for (;;) {
     if (bar_try(bar, parity)) return true;
-    if (*failed) return false;
-    if (global_ns() - t0 > kWaitLimitNs) {
-      *failed = 1;
+    if (*static_cast<volatile int*>(failed)) return false;
+    if (global_ns() - t0 > limit) {
+      give_up(failed);
       return false;
     }
-  }
-}
-
-// given up: lets the copies in flight (microseconds) land
-__device__ __forceinline__ void drain() {
-  const uint64_t t0 = global_ns();
-  while (global_ns() - t0 < kDrainNs) {
   }
 }
 
@@ -513,6 +512,7 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
   __shared__ int failed, group_ok[kGroups];
   __shared__ __align__(16) uint8_t out_stage[kOutWarps][32 * kOutPitch];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint64_t limit = a.plant.limit();
   const int n_cta = 2 * a.split;
   const int rank = static_cast<int>(blockIdx.x) % n_cta;
   const int half = rank & 1, part = rank >> 1, leader = rank & ~1;
@@ -602,8 +602,8 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
     const auto free_stage = [&](int64_t at) -> uint8_t* {
       if (!kTma || at >= kStages) {
         if (warp % kGroupWarps == 0) {
-          const bool free = kTma ? bar_wait(&empty[ring.stage], ring.parity ^ 1, &failed)
-                                 : bar_wait(&full_b[ring.stage], ring.parity, &failed);
+          const bool free = kTma ? bar_wait(&empty[ring.stage], ring.parity ^ 1, &failed, limit)
+                                 : bar_wait(&full_b[ring.stage], ring.parity, &failed, limit);
           if (lane == 0) group_ok[group] = free;
         }
         group_sync(group);
@@ -664,9 +664,14 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
         for (int step = 0; step < steps; ++step, y += kK) {
           const int s = ring.stage;
           if (left_fresh > 0) --left_fresh;
-          else if (!bar_wait(&empty[s], ring.parity ^ 1, &failed)) {
+          else if (!bar_wait(&empty[s], ring.parity ^ 1, &failed, limit)) {
             ok = false;
             break;
+          }
+          if (blockIdx.x == 0 &&
+              a.plant.holds(ZERO_PLANT_NO_COPY, static_cast<int64_t>(k) * steps + step)) {
+            ring.advance(1);
+            continue;
           }
           uint8_t* b = stages + s * kStageBytes + kBytesA;
           if constexpr (kTma) {
@@ -690,7 +695,6 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
           ring.advance(1);
         }
       }
-      if (!ok) drain();
     }
   } else if (warp == kProductWarp) {
     if (half == 0 && lane == 0) {
@@ -703,11 +707,11 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
         // one group per tile: two tiles' sums in turn; two groups fill tensor memory
         const int buf = kWide == 1 ? k & 1 : 0, use = kWide == 1 ? k >> 1 : k;
         const uint32_t sums = tmem + buf * kN;
-        ok = use == 0 || bar_wait(&free_sums[buf], (use - 1) & 1, &failed);
+        ok = use == 0 || bar_wait(&free_sums[buf], (use - 1) & 1, &failed, limit);
         for (int step = 0; step < steps && ok; ++step) {
           const int s = ring.stage;
-          ok = bar_wait(&full_a[s], ring.parity, &failed) &&
-               (!kTma || bar_wait(&full_b[s], ring.parity, &failed));
+          ok = bar_wait(&full_a[s], ring.parity, &failed, limit) &&
+               (!kTma || bar_wait(&full_b[s], ring.parity, &failed, limit));
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           const uint32_t at = base + s * (kStageBytes >> 4);
@@ -721,7 +725,7 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
           commit(&empty[s], pair_mask);
           ring.advance(1);
         }
-        commit(&done[buf], pair_mask);
+        if (ok) commit(&done[buf], pair_mask);  // whole sums only
       }
     }
   } else if (warp >= kOutWarp0) {
@@ -731,7 +735,9 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
     for (int k = 0; k < my_tiles; ++k) {
       const int tile = tile0 + k * tile_stride;
       const int buf = kWide == 1 ? k & 1 : 0, use = kWide == 1 ? k >> 1 : k;
-      if (steps > 0) ok = ok && bar_wait(&done[buf], use & 1, &failed);
+      // the warp's verdict: its lanes read tensor memory together
+      if (steps > 0 && ok)
+        ok = __all_sync(0xffffffffu, bar_wait(&done[buf], use & 1, &failed, limit));
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t sums = tmem + (static_cast<uint32_t>(row0) << 16) + buf * kN;
       const int64_t i0 = row_of(tile) + row0, j = column_of(tile);
@@ -782,12 +788,19 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
-      if (lane == 0) bar_arrive_at(in_cta(&free_sums[buf], leader));
+      // given up: the sums stay taken, others may still read theirs
+      if (ok && lane == 0) bar_arrive_at(in_cta(&free_sums[buf], leader));
     }
   }
   __syncthreads();
   cluster_sync();
-  if (failed && tid == 0 && a.scaler) atomicCAS(&a.scaler->error, 0, ZERO_DEVERR_TIMEOUT);
+  // no thread of the cluster starts a copy or a product any more, and all its
+  // CTAs know if one gave up
+  const bool gave_up = *static_cast<volatile int*>(&failed) != 0;
+  if (gave_up) {
+    drain();
+    if (tid == 0 && a.scaler) atomicCAS(&a.scaler->error, 0, ZERO_DEVERR_TIMEOUT);
+  }
   if (a.split > 1) {
     // one tile per cluster: this CTA's share of its rows, a warp per row and
     // eight columns per lane
@@ -823,6 +836,10 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
             f[4] += y[k].x, f[5] += y[k].y, f[6] += y[k].z, f[7] += y[k].w;
           }
         }
+      }
+      if (gave_up) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(0x7FC00000u);
       }
       const int64_t left = a.n - j;
       const int count = left < a.bn ? static_cast<int>(left) : a.bn;
@@ -960,6 +977,7 @@ ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const
   a.dy = static_cast<const uint16_t*>(dy);
   a.dw = static_cast<uint16_t*>(dw);
   a.scaler = d_scaler;
+  a.plant = planted();
   a.rows = rows, a.cols = cols, a.n = n, a.ld = ld;
   a.vec_out = n % kVec == 0 && aligned(dw, 16);
   int fit[kMaxSplit + 1];

@@ -191,6 +191,21 @@ ZERO_API int zero_policy_loss(const void* logits, int64_t rows, int64_t vocab, i
                               float* logp, float* loss, float* stats, void* dlogits,
                               void* stream);
 
+/* --------------------------------------------------------------- self-test --
+ *
+ * Checked build (libzero_checked.so) only; ZERO_ESTATE in the release build.
+ * Plants a mistake in the calls that follow in this process, until it is
+ * called with ZERO_PLANT_NOTHING; a wait then expires after limit_ns (1 to
+ * 10^9, ZERO_EINVAL otherwise) in place of 2 s. Nothing faults or hangs: the
+ * kernels give up as they do after any wait that expires.
+ *   ZERO_PLANT_NO_COPY  zero_ckpt_wgrad: the first CTA leaves out the copy of
+ *                       its step `at` */
+typedef enum zero_plant {
+  ZERO_PLANT_NOTHING = 0,
+  ZERO_PLANT_NO_COPY = 1
+} zero_plant;
+ZERO_API int zero_selftest_plant(int32_t what, int64_t at, int64_t limit_ns);
+
 #ifdef __cplusplus
 }
 #endif

@@ -153,3 +153,11 @@ def test_longest_loss_row():
         ok = [P, 4, v, v, dt, P, 4, P, P, P, P, hp, 0, P, P + 2, P, P]
         refused(EALIGN, Z.zero_policy_loss, *ok)
         refused(ERANGE, Z.zero_policy_loss, *changed(ok, i2=v + 1, i3=v + 1))
+
+
+def test_plant_is_refused():
+    """Bad arguments, and in the release build every plant."""
+    for args in ((-1,), (99,), (Z.ZERO_PLANT_NO_COPY, 0, 0), (Z.ZERO_PLANT_NO_COPY, 0, 10**10)):
+        refused(EINVAL, Z.zero_selftest_plant, *args)
+    for what in (Z.ZERO_PLANT_NOTHING, Z.ZERO_PLANT_NO_COPY):
+        refused(-6, Z.zero_selftest_plant, what)
