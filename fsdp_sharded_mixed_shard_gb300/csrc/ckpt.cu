@@ -399,7 +399,7 @@ ZERO_API int zero_ckpt_act_grad(int32_t act, const void* ckpt_x, const void* ckp
 }
 
 ZERO_API int zero_selftest_plant(int32_t what, int64_t at, int64_t limit_ns) {
-  if (what < ZERO_PLANT_NOTHING || what > ZERO_PLANT_NO_COPY || limit_ns < 1 ||
+  if (what < ZERO_PLANT_NOTHING || what > ZERO_PLANT_NO_SEND || limit_ns < 1 ||
       limit_ns > 1000000000)
     return ZERO_EINVAL;
 #ifdef ZERO_CHECKED

@@ -45,10 +45,9 @@ constexpr int kMaxWarps = 8;   // per CTA; 1, 2, 4 or 8 by the row's length
 constexpr int kMaxCluster = 8;
 constexpr int kParts = 2;      // parts of a row per warp
 constexpr int kBatch = 4;      // blocks per lane and step
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-struct Args {
+struct Args : Plant {
   const uint8_t* logits;
   uint8_t* dlogits;
   const void* actions;
@@ -243,6 +242,13 @@ __device__ __forceinline__ void cluster_sync() {
           : "memory");
 }
 
+// every thread of the cluster is here; nothing is said about memory
+__device__ __forceinline__ void cluster_meet() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n barrier.cluster.wait.aligned;" ::
+                   : "memory");
+}
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
@@ -275,19 +281,26 @@ __device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-__device__ __forceinline__ uint64_t global_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
+__device__ __forceinline__ bool is_set(const int* flag) {
+  return *static_cast<const volatile int*>(flag) != 0;
 }
 
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
+// true when the phase has completed; false once *lost is set or the limit has
+// passed, which sets it. A CTA that has lost a wait neither copies nor sends any
+// more, as its barriers may be a turn off, and its rows are NaN from then on; the
+// waits of the cluster's other CTAs for it expire in their turn.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, uint64_t limit,
+                                         int* lost) {
   for (int k = 0; k < 64; ++k)
     if (bar_try(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   for (;;) {
     if (bar_try(bar, parity)) return true;
-    if (global_ns() - t0 > kWaitLimitNs) return false;
+    if (is_set(lost)) return false;
+    if (global_ns() - t0 > limit) {
+      *static_cast<volatile int*>(lost) = 1;
+      return false;
+    }
   }
 }
 
@@ -369,12 +382,13 @@ __device__ __forceinline__ void send(Stat* to, uint64_t* bar, uint32_t rank, con
 // the cluster; its lanes hold the same bits afterwards. `use` counts the calls.
 template <int kWarps>
 __device__ __forceinline__ Stat join_all(Exchange (&x)[2], uint32_t rank, uint32_t n_cta,
-                                         uint32_t use) {
+                                         uint32_t use, const Args& a, int64_t row, int* lost) {
   const uint32_t lane = threadIdx.x & 31;
   Exchange& e = x[use & 1];
-  const Stat none = {-INFINITY, 0.f};
-  const Stat t = join_lanes(lane < kWarps ? e.of_warp[lane] : none);
-  if (n_cta == 1) return t;
+  const Stat none = {-INFINITY, 0.f}, nan = {0.f, __uint_as_float(0x7FC00000u)};
+  const bool gone = is_set(lost);  // by a warp before the CTA's barrier, or this one earlier
+  const Stat t = join_lanes(gone ? nan : lane < kWarps ? e.of_warp[lane] : none);
+  if (n_cta == 1 || gone) return t;
   if (lane < n_cta) {
     if (lane == 0)
       asm volatile(
@@ -382,11 +396,18 @@ __device__ __forceinline__ Stat join_all(Exchange (&x)[2], uint32_t rank, uint32
               smem_u32(&e.arrived)),
           "r"(n_cta * static_cast<uint32_t>(sizeof(Stat)))
           : "memory");
-    send(&e.of_cta[rank], &e.arrived, lane, t);
+    if (!(rank == 1 && a.holds(ZERO_PLANT_NO_SEND, row)))
+      send(&e.of_cta[rank], &e.arrived, lane, t);
   }
-  const bool ok = bar_wait(&e.arrived, (use >> 1) & 1);
-  return join_lanes(!ok ? Stat{0.f, __uint_as_float(0x7FC00000u)}
-                        : lane < n_cta ? e.of_cta[lane] : none);
+  const bool ok = bar_wait(&e.arrived, (use >> 1) & 1, a.limit(), lost);
+  return join_lanes(!ok ? nan : lane < n_cta ? e.of_cta[lane] : none);
+}
+
+// The end of a CTA: no other sends to it any more, and where a wait expired,
+// what is still on its way (microseconds) lands.
+__device__ __forceinline__ void leave(uint32_t n_cta, int* lost) {
+  if (n_cta > 1) cluster_meet();
+  if (is_set(lost)) drain();
 }
 
 // The row's logits as a single stream: statistics only.
@@ -398,14 +419,17 @@ __global__ void __launch_bounds__(32 * kWarps) logp_kernel(const Args a) {
   __shared__ Exchange exchange[2];
   const int tid = threadIdx.x;
   const uint32_t rank = cluster_rank(), n_cta = cluster_size();
+  __shared__ int lost;
   uint32_t use = 0;
   if (tid == 0) {
+    lost = 0;
     bar_init(&exchange[0].arrived);
     bar_init(&exchange[1].arrived);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncwarp();
   if (n_cta > 1) cluster_sync();  // every CTA of the cluster is ready before any sends to it
+  else __syncthreads();
   for (int64_t row = blockIdx.x / n_cta; row < a.rows; row += gridDim.x / n_cta) {
     const Row r = row_of<B::kBytes, false>(a, row);
     float lp = 0.f;
@@ -430,11 +454,14 @@ __global__ void __launch_bounds__(32 * kWarps) logp_kernel(const Args a) {
       t = join_lanes(t);
       if ((tid & 31) == 0) exchange[use & 1].of_warp[tid >> 5] = t;
       __syncthreads();
-      if (tid < 32) lp = log_share(picked, join_all<kWarps>(exchange, rank, n_cta, use));
+      if (tid < 32)
+        lp = log_share(picked,
+                       join_all<kWarps>(exchange, rank, n_cta, use, a, row, &lost));
       ++use;
     }
     if (rank == 0 && tid == 0) a.logp[row] = lp;
   }
+  leave(n_cta, &lost);
 }
 
 // What warp 0 tells the others between a row's sums and its gradient.
@@ -454,6 +481,7 @@ __global__ void __launch_bounds__(32 * kWarps, 24 / kWarps)
   __shared__ uint64_t landed[kWarps][kParts];
   __shared__ Turn turn;
   __shared__ float taken;
+  __shared__ int lost;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank(), n_cta = cluster_size();
   const int64_t n_clusters = gridDim.x / n_cta;
@@ -466,6 +494,7 @@ __global__ void __launch_bounds__(32 * kWarps, 24 / kWarps)
   if (lane == 0) {
     for (int p = 0; p < kParts; ++p) bar_init(&landed[warp][p]);
     if (warp == 0) {
+      lost = 0;
       bar_init(&exchange[0].arrived);
       bar_init(&exchange[1].arrived);
     }
@@ -480,7 +509,8 @@ __global__ void __launch_bounds__(32 * kWarps, 24 / kWarps)
   const auto part_at = [&](int p) {
     return reinterpret_cast<uint4*>(mine + static_cast<int64_t>(p) * part_cap * 16);
   };
-  const auto fetch = [&](const Row& r, int p) {  // one lane
+  const auto fetch = [&](const Row& r, int64_t row, int p) {  // one lane
+    if (part0 + p == 0 && a.holds(ZERO_PLANT_NO_COPY, row)) return;
     const int32_t b0 = block_of(r, p), n = block_of(r, p + 1) - b0;
     if (ZCHECK(n <= part_cap && b0 + n <= r.n_blk, kSiteStageBytes, n))
       copy_blocks(part_at(p), r.base + static_cast<int64_t>(b0) * 16, n * 16, &landed[warp][p]);
@@ -507,16 +537,16 @@ __global__ void __launch_bounds__(32 * kWarps, 24 / kWarps)
       if (next_row < a.rows) next = row_of<B::kBytes, true>(a, next_row);
     }
     if (on) {
-      if (!fetched && lane == 0) {
+      if (!fetched && lane == 0 && !is_set(&lost)) {
 #pragma unroll
-        for (int p = 0; p < kParts; ++p) fetch(r, p);
+        for (int p = 0; p < kParts; ++p) fetch(r, row, p);
       }
       Stat t = {-INFINITY, 0.f};
 #pragma unroll 1
       for (int p = 0; p < kParts; ++p) {
         const int32_t b0 = block_of(r, p), n = block_of(r, p + 1) - b0;
         const uint4* part = part_at(p);
-        if (!bar_wait(&landed[warp][p], phase)) t.s = __uint_as_float(0x7FC00000u);
+        bar_wait(&landed[warp][p], phase, a.limit(), &lost);
         const bool edge = b0 == 0 || b0 + n == r.n_blk;
         for (int32_t k0 = 0; k0 < n; k0 += 32 * kBatch) {
           uint4 v[kBatch];
@@ -542,7 +572,7 @@ __global__ void __launch_bounds__(32 * kWarps, 24 / kWarps)
       n.next = next;
       float lp = 0.f, loss = 0.f;
       if (on) {
-        const Stat t = join_all<kWarps>(exchange, rank, n_cta, use);
+        const Stat t = join_all<kWarps>(exchange, rank, n_cta, use, a, row, &lost);
         lp = log_share(taken, t);
         const float ratio = expf(lp - old);
         const float plain = ratio * adv, held = fminf(fmaxf(ratio, a.lo), a.hi) * adv;
@@ -571,7 +601,7 @@ __global__ void __launch_bounds__(32 * kWarps, 24 / kWarps)
     __syncthreads();
     next = turn.next;
     // the next row's parts follow this row's gradient out of the same place
-    const bool follow = on && next.on();
+    const bool follow = on && next.on() && !is_set(&lost);
     uint8_t* dx = a.dlogits ? a.dlogits + row * a.ld * B::kBytes - r.head : nullptr;
     // whole blocks when dlogits lies on the 16-byte grid as the logits do
     const bool same = (reinterpret_cast<uintptr_t>(dx) & 15) == 0;
@@ -637,12 +667,13 @@ __global__ void __launch_bounds__(32 * kWarps, 24 / kWarps)
         }
       }
       __syncwarp();
-      if (follow && lane == 0) fetch(next, p);
+      if (follow && lane == 0) fetch(next, next_row, p);
     }
     fetched = follow;
     r = next;
     row = next_row;
   }
+  leave(n_cta, &lost);
 }
 
 // Sum with what each addition lost beside it (the file is built without
@@ -839,7 +870,7 @@ ZERO_API int zero_token_logp(const void* logits, int64_t rows, int64_t vocab, in
   using namespace zp;
   const int rc = check(logits, rows, vocab, ld, dtype, actions, action_bytes, logp);
   if (rc != ZERO_OK || rows == 0) return rc;
-  Args a = {};
+  Args a = new_args<Args>();
   a.logits = static_cast<const uint8_t*>(logits);
   a.actions = actions;
   a.action_bytes = action_bytes;
@@ -868,7 +899,7 @@ ZERO_API int zero_policy_loss(const void* logits, int64_t rows, int64_t vocab, i
       !aligned(weight, 4) || !aligned(loss, 4) || !aligned(stats, 4) || !aligned(dlogits, size) ||
       !aligned(d_scaler, 16))
     return ZERO_EALIGN;
-  Args a = {};
+  Args a = new_args<Args>();
   a.logits = static_cast<const uint8_t*>(logits);
   a.dlogits = static_cast<uint8_t*>(dlogits);
   a.actions = actions;

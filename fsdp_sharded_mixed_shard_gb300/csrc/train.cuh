@@ -221,7 +221,9 @@ __device__ __forceinline__ void drain() {
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 // A mistake to make on purpose (zero_selftest_plant), and how long a wait may
-// take; the release build has neither.
+// take: a base of the kernels' arguments, with nothing in it in the release
+// build. (An empty member changed the policy kernel's code: 72.8 to 73.5 us at
+// 2048 x 50257.)
 struct Plant {
 #ifdef ZERO_CHECKED
   int32_t what;
@@ -237,11 +239,18 @@ struct Plant {
 #endif
 };
 
-// the plant for a launch
+// arguments of a launch with the plant that holds for it, all else 0
 #ifdef ZERO_CHECKED
 Plant planted();
+template <class Args>
+Args new_args() {
+  Args a = {};
+  static_cast<Plant&>(a) = planted();
+  return a;
+}
 #else
-inline Plant planted() { return Plant{}; }
+template <class Args>
+Args new_args() { return Args{}; }
 #endif
 
 // Token ids are int32 or int64; an id outside [0, limit) becomes -1.

@@ -90,7 +90,7 @@ constexpr int kPlaceCycles[2] = {1250, 2200};
 static_assert(kM * kJoinPitch * 4 <= kRing, "the tile fits the stages");
 static_assert(kM == ZERO_CKPT_PAD, "a checkpoint row is whole CTA tiles");
 
-struct Args {
+struct Args : Plant {
   const int8_t* q;
   const uint8_t* scale;
   const uint16_t* dy;
@@ -98,7 +98,6 @@ struct Args {
   zero_scaler* scaler;
   int64_t rows, cols, pitch, n, ld;
   int32_t split, vec_out, bn, m_tiles, tiles;
-  Plant plant;
 };
 
 // ------------------------------------------------------------- primitives ----
@@ -512,7 +511,7 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
   __shared__ int failed, group_ok[kGroups];
   __shared__ __align__(16) uint8_t out_stage[kOutWarps][32 * kOutPitch];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint64_t limit = a.plant.limit();
+  const uint64_t limit = a.limit();
   const int n_cta = 2 * a.split;
   const int rank = static_cast<int>(blockIdx.x) % n_cta;
   const int half = rank & 1, part = rank >> 1, leader = rank & ~1;
@@ -669,7 +668,7 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
             break;
           }
           if (blockIdx.x == 0 &&
-              a.plant.holds(ZERO_PLANT_NO_COPY, static_cast<int64_t>(k) * steps + step)) {
+              a.holds(ZERO_PLANT_NO_COPY, static_cast<int64_t>(k) * steps + step)) {
             ring.advance(1);
             continue;
           }
@@ -970,14 +969,13 @@ ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const
   if (!dw || (rows && (!ckpt || !dy))) return ZERO_EINVAL;
   if (!aligned(ckpt, 16) || !aligned(dy, 2) || !aligned(dw, 2) || !aligned(d_scaler, 16))
     return ZERO_EALIGN;
-  Args a = {};
+  Args a = new_args<Args>();
   a.q = static_cast<const int8_t*>(ckpt);
   a.pitch = ceil_div(cols, ZERO_CKPT_PAD) * ZERO_CKPT_PAD;
   a.scale = static_cast<const uint8_t*>(ckpt) + rows * a.pitch;
   a.dy = static_cast<const uint16_t*>(dy);
   a.dw = static_cast<uint16_t*>(dw);
   a.scaler = d_scaler;
-  a.plant = planted();
   a.rows = rows, a.cols = cols, a.n = n, a.ld = ld;
   a.vec_out = n % kVec == 0 && aligned(dw, 16);
   int fit[kMaxSplit + 1];

@@ -149,6 +149,8 @@ ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const
 
 /* -------------------------------------------------------------------- loss --
  *
+ * A pipeline wait that expires (2 s) makes the rows that its CTAs had left NaN.
+ *
  * logits: [rows, vocab], row distance ld, of type dtype (ZERO_BF16, ZERO_FP16
  * or ZERO_FP32). -inf entries are tokens ruled out (probability 0); a row of
  * nothing but -inf, or one with a NaN or +inf, has logp NaN.
@@ -199,10 +201,14 @@ ZERO_API int zero_policy_loss(const void* logits, int64_t rows, int64_t vocab, i
  * 10^9, ZERO_EINVAL otherwise) in place of 2 s. Nothing faults or hangs: the
  * kernels give up as they do after any wait that expires.
  *   ZERO_PLANT_NO_COPY  zero_ckpt_wgrad: the first CTA leaves out the copy of
- *                       its step `at` */
+ *                       its step `at`; zero_policy_loss: the first part of
+ *                       row `at` is not copied
+ *   ZERO_PLANT_NO_SEND  zero_token_logp, zero_policy_loss: the second CTA of
+ *                       a cluster does not send its sums of row `at` */
 typedef enum zero_plant {
   ZERO_PLANT_NOTHING = 0,
-  ZERO_PLANT_NO_COPY = 1
+  ZERO_PLANT_NO_COPY = 1,
+  ZERO_PLANT_NO_SEND = 2
 } zero_plant;
 ZERO_API int zero_selftest_plant(int32_t what, int64_t at, int64_t limit_ns);
 

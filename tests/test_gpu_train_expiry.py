@@ -33,3 +33,22 @@ def test_weight_gradient_gives_no_partial_sums(cases):
     # the step was one of a pair's first tile, or of a later one
     assert [c["first_lost"] for c in got] == [
         True, False, False, False, True, True, False, True, True]
+
+
+def test_policy_rows_left_are_nan(cases):
+    got = [c for c in cases if c["case"] == "policy"]
+    assert len(got) == 8
+    for c in got:
+        assert c["finite"] and c["after_right"], c
+        # from the row on, the rows of its CTAs and no others; left-out rows stay 0
+        assert c["at_lost"] and c["first_lost"] == c["at"] and c["off"] == 0, c
+        assert 1 <= c["lost"] <= 16 and c["others_right"], c
+        assert c["whole"] and c["loss_too"] and c["stats_nan"], c
+
+
+def test_log_probabilities_left_are_nan(cases):
+    got = [c for c in cases if c["case"] == "logp"]
+    assert len(got) == 2
+    for c in got:
+        assert c["finite"] and c["after_right"] and c["others_right"], c
+        assert c["at_lost"] and c["lost"] == 1, c
