@@ -39,7 +39,8 @@ __all__ = [
     "zero_embedding", "zero_embedding_workspace_bytes", "zero_embedding_grad",
     "zero_ckpt_bytes", "zero_ckpt_save", "zero_ckpt_load", "zero_ckpt_act",
     "zero_ckpt_act_grad", "zero_ckpt_wgrad", "zero_token_logp", "zero_policy_loss",
-    "ZERO_PLANT_NOTHING", "ZERO_PLANT_NO_COPY", "ZERO_PLANT_NO_SEND", "zero_selftest_plant",
+    "ZERO_PLANT_NOTHING", "ZERO_PLANT_NO_COPY", "ZERO_PLANT_NO_SEND", "ZERO_PLANT_SHORT",
+    "zero_selftest_plant",
 ]
 
 ZERO_BF16 = 0
@@ -53,7 +54,7 @@ ZERO_MAX_LOGIT_ROW_BYTES = 8 * 192 * 1024
 ZERO_CKPT_BLOCK = 32
 ZERO_CKPT_PAD = 128
 ZERO_ACT_GELU, ZERO_ACT_SWIGLU = range(2)
-ZERO_PLANT_NOTHING, ZERO_PLANT_NO_COPY, ZERO_PLANT_NO_SEND = range(3)
+ZERO_PLANT_NOTHING, ZERO_PLANT_NO_COPY, ZERO_PLANT_NO_SEND, ZERO_PLANT_SHORT = range(4)
 (ZERO_FULL_SHARD, ZERO_SHARD_GRAD_OP, ZERO_NO_SHARD, ZERO_HYBRID_SHARD,
  ZERO_NO_RESHARD_AFTER_FORWARD) = range(5)
 

@@ -1,8 +1,13 @@
 // checked.cuh -- range tests of the checked build (-DZERO_CHECKED).
 //
-// In libzero_checked.so every kernel tests the global and shared-memory
-// ranges it is about to touch against the extents the plan gives (window,
-// shard, records, stage slot, unit slices). A failing test skips the access,
+// In libzero_checked.so every kernel of the step tests the global and
+// shared-memory ranges it is about to touch against the extents the plan gives
+// (window, shard, records, stage slot, unit slices). The kernels behind
+// zero_train.h test the addresses of the elements they load and store in the
+// call's arrays, checkpoints and partial sums (train.cuh, Bounds); not tested
+// there are the per-token arrays and the sort's keys (indexed by the row at
+// hand), the weight gradient's loads of dy (TMA keeps to its map) and, but for
+// the loss's parts, shared memory. A failing test skips the access,
 // counts the violation and keeps the first one (site << 48 | low 48 bits of
 // the index); nothing traps. Each translation unit keeps its own counters
 // (device code is not linked across units); zero_checked_status collects

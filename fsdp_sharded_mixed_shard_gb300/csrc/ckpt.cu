@@ -27,10 +27,16 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kCols = 32 * kVec;
 
+// a call's buffers, for their bounds
+enum { kX, kU, kDy, kY, kDx, kDu, kCkptX, kCkptU, kBuffers };
+
 // Eight elements of a row of 16-bit elements starting at column c; those at
 // or past `cols` are 0. kGrid: rows lie on the 16-byte grid.
 template <bool kGrid>
-__device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t cols) {
+__device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t cols,
+                                       const Bounds& in) {
+  if (!in.holds(row + c, 2 * (cols - c < kVec ? cols - c : kVec), kSiteLoad))
+    return make_uint4(0, 0, 0, 0);
   if (c + kVec <= cols)
     return kGrid ? __ldcs(reinterpret_cast<const uint4*>(row + c)) : load8_any<true>(row + c);
   uint32_t h[8];
@@ -43,9 +49,10 @@ __device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t c
 // call it.
 template <bool kGrid>
 __device__ __forceinline__ void store_row(uint8_t* stage, uint16_t* row, int64_t c0, int lane,
-                                          int64_t cols, const uint4& v) {
+                                          int64_t cols, const uint4& v, const Bounds& in) {
   const int64_t c = c0 + lane * kVec;
   if constexpr (kGrid) {
+    if (!in.holds(row + c, 2 * (cols - c < kVec ? cols - c : kVec), kSiteStore)) return;
     if (c + kVec <= cols) {
       __stcs(reinterpret_cast<uint4*>(row + c), v);
       return;
@@ -57,7 +64,7 @@ __device__ __forceinline__ void store_row(uint8_t* stage, uint16_t* row, int64_t
   } else {
     const int64_t left = cols - c0;
     if (left > 0)
-      store_any(stage, row + c0, left < kCols ? static_cast<int>(left) : kCols, lane, v);
+      store_any(stage, row + c0, left < kCols ? static_cast<int>(left) : kCols, lane, v, in);
   }
 }
 
@@ -94,7 +101,7 @@ __device__ __forceinline__ uint32_t hold2(uint32_t x, uint32_t limit, uint32_t m
 // quotient is rounded to a whole number, ties to even, in the sum's last bits.
 template <bool kBf16>
 __device__ __forceinline__ void save8(const Ckpt& k, int64_t row, int64_t c, int64_t pitch,
-                                      bool in, const uint4& v) {
+                                      bool in, const uint4& v, const Bounds& bounds) {
   constexpr uint32_t kAbs = 0x7FFF7FFFu;
   uint32_t top = max_u16x2(max_u16x2(v.x & kAbs, v.y & kAbs), max_u16x2(v.z & kAbs, v.w & kAbs));
   top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -125,16 +132,17 @@ __device__ __forceinline__ void save8(const Ckpt& k, int64_t row, int64_t c, int
     q[2 * j] = __float_as_uint(a);
     q[2 * j + 1] = __float_as_uint(b);
   }
-  if (!in || !ZCHECK(c + kVec <= pitch, kSiteStore, c)) return;
+  if (!in) return;
   const auto low_bytes = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
   };
   uint2 out = make_uint2(low_bytes(q[0], q[1], q[2], q[3]), low_bytes(q[4], q[5], q[6], q[7]));
   if (!finite) out = make_uint2(0, 0);
-  __stcs(reinterpret_cast<uint2*>(k.q + row * pitch + c), out);
-  if ((threadIdx.x & 3) == 0)
-    k.scale[row * (pitch / ZERO_CKPT_BLOCK) + c / ZERO_CKPT_BLOCK] =
-        static_cast<uint8_t>(finite ? step : 255);
+  uint8_t* scale = k.scale + row * (pitch / ZERO_CKPT_BLOCK) + c / ZERO_CKPT_BLOCK;
+  if (bounds.holds(k.q + row * pitch + c, kVec, kSiteStore))
+    __stcs(reinterpret_cast<uint2*>(k.q + row * pitch + c), out);
+  if ((threadIdx.x & 3) == 0 && bounds.holds(scale, 1, kSiteStore))
+    *scale = static_cast<uint8_t>(finite ? step : 255);
 }
 
 // The lane's eight checkpointed values. A byte with its sign bit
@@ -180,7 +188,7 @@ __device__ __forceinline__ Gate gelu_gate(float x) {
   return sigmoid(kGeluC * __fmaf_rn(kGeluA * square(x), x, x));
 }
 
-struct Args {
+struct Args : Checked<kBuffers> {
   const uint16_t *x, *u, *dy;
   uint16_t *y, *dx, *du;
   Ckpt kx, ku;
@@ -204,11 +212,12 @@ __global__ void __launch_bounds__(kThreads) ckpt_kernel(const Args a) {
   if (r >= a.rows) return;
   const bool in = c < a.pitch;
   if constexpr (kOp == kSave || kOp == kGelu || kOp == kSwiglu) {
-    const uint4 vx = load8<kGrid>(a.x + r * a.ld, c, a.cols);
+    const uint4 vx = load8<kGrid>(a.x + r * a.ld, c, a.cols, a.bounds(kX));
     uint4 vu = make_uint4(0, 0, 0, 0);
-    if constexpr (kOp == kSwiglu) vu = load8<kGrid>(a.u + r * a.ld, c, a.cols);
-    save8<kBf16>(a.kx, r, c, a.pitch, in, vx);
-    if constexpr (kOp == kSwiglu) save8<kBf16>(a.ku, r, c, a.pitch, in, vu);
+    if constexpr (kOp == kSwiglu) vu = load8<kGrid>(a.u + r * a.ld, c, a.cols, a.bounds(kU));
+    save8<kBf16>(a.kx, r, c, a.pitch, in, vx, a.bounds(kCkptX));
+    if constexpr (kOp == kSwiglu)
+      save8<kBf16>(a.ku, r, c, a.pitch, in, vu, a.bounds(kCkptU));
     if constexpr (kOp != kSave) {
       float x[8], u[8], y[8];
       widen8<kBf16>(vx, x);
@@ -216,26 +225,30 @@ __global__ void __launch_bounds__(kThreads) ckpt_kernel(const Args a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         y[j] = kOp == kSwiglu ? x[j] * sigmoid(x[j]).p * u[j] : x[j] * gelu_gate(x[j]).p;
-      store_row<kGrid>(stage, a.y + r * a.ld_y, c0, lane, a.cols, narrow8<kBf16>(y));
+      store_row<kGrid>(stage, a.y + r * a.ld_y, c0, lane, a.cols, narrow8<kBf16>(y),
+                       a.bounds(kY));
     }
   } else {
     const int64_t blk = a.pitch / ZERO_CKPT_BLOCK;
     uint2 qx = make_uint2(0, 0), qu = qx;
     uint32_t sx = 1, su = 1;
     uint4 vd = make_uint4(0, 0, 0, 0);
-    if (in && ZCHECK(r < a.rows && c + kVec <= a.pitch, kSiteLoad, c)) {
-      qx = __ldcs(reinterpret_cast<const uint2*>(a.kx.q + r * a.pitch + c));
-      sx = a.kx.scale[r * blk + c / ZERO_CKPT_BLOCK];
-      if constexpr (kOp == kSwigluGrad) {
-        qu = __ldcs(reinterpret_cast<const uint2*>(a.ku.q + r * a.pitch + c));
-        su = a.ku.scale[r * blk + c / ZERO_CKPT_BLOCK];
-      }
-      if constexpr (kOp != kLoad) vd = load8<kGrid>(a.dy + r * a.ld_y, c, a.cols);
+    const auto read8 = [&](const Ckpt& k, const Bounds& bounds, uint2& q, uint32_t& s) {
+      if (bounds.holds(k.q + r * a.pitch + c, kVec, kSiteLoad))
+        q = __ldcs(reinterpret_cast<const uint2*>(k.q + r * a.pitch + c));
+      const uint8_t* scale = k.scale + r * blk + c / ZERO_CKPT_BLOCK;
+      if (bounds.holds(scale, 1, kSiteLoad)) s = *scale;
+    };
+    if (in) {
+      read8(a.kx, a.bounds(kCkptX), qx, sx);
+      if constexpr (kOp == kSwigluGrad) read8(a.ku, a.bounds(kCkptU), qu, su);
+      if constexpr (kOp != kLoad)
+        vd = load8<kGrid>(a.dy + r * a.ld_y, c, a.cols, a.bounds(kDy));
     }
     float x[8], u[8], d[8], y[8], gx[8], gu[8];
     unpack8(qx, sx, x);
     if constexpr (kOp == kLoad) {
-      store_row<kGrid>(stage, a.y + r * a.ld, c0, lane, a.cols, narrow8<kBf16>(x));
+      store_row<kGrid>(stage, a.y + r * a.ld, c0, lane, a.cols, narrow8<kBf16>(x), a.bounds(kY));
     } else {
       if constexpr (kOp == kSwigluGrad) unpack8(qu, su, u);
       widen8<kBf16>(vd, d);
@@ -256,10 +269,12 @@ __global__ void __launch_bounds__(kThreads) ckpt_kernel(const Args a) {
           gx[j] = d[j] * __fmaf_rn(y[j] * g.q, z1, g.p);
         }
       }
-      store_row<kGrid>(stage, a.dx + r * a.ld, c0, lane, a.cols, narrow8<kBf16>(gx));
-      if constexpr (kOp == kSwigluGrad)
-        store_row<kGrid>(stage, a.du + r * a.ld, c0, lane, a.cols, narrow8<kBf16>(gu));
-      if (a.y) store_row<kGrid>(stage, a.y + r * a.ld, c0, lane, a.cols, narrow8<kBf16>(y));
+      const auto put = [&](uint16_t* to, const float (&f)[8], const Bounds& bounds) {
+        store_row<kGrid>(stage, to + r * a.ld, c0, lane, a.cols, narrow8<kBf16>(f), bounds);
+      };
+      put(a.dx, gx, a.bounds(kDx));
+      if constexpr (kOp == kSwigluGrad) put(a.du, gu, a.bounds(kDu));
+      if (a.y) put(a.y, y, a.bounds(kY));
     }
   }
 }
@@ -280,8 +295,24 @@ Ckpt ckpt_of(const void* p, int64_t rows, int64_t pitch) {
   return Ckpt{q, reinterpret_cast<uint8_t*>(q) + rows * pitch};
 }
 
+// ld: of all 16-bit arrays but ld_y's, y's (forward) or dy's (backward)
+template <int kOp>
+void bound_buffers(Args& a) {
+  constexpr bool kBack = kOp == kGeluGrad || kOp == kSwigluGrad;
+  const auto array = [&](int k, const void* p, int64_t ld) {
+    a.set_bounds(k, p, a.rows, a.cols, ld, 2);
+  };
+  array(kX, a.x, a.ld), array(kU, a.u, a.ld), array(kDy, a.dy, a.ld_y);
+  array(kY, a.y, kBack || kOp == kLoad ? a.ld : a.ld_y), array(kDx, a.dx, a.ld);
+  array(kDu, a.du, a.ld);
+  const int64_t bytes = a.rows * (a.pitch + a.pitch / ZERO_CKPT_BLOCK);
+  a.set_bounds(kCkptX, a.kx.q, 1, bytes, 0, 1);
+  a.set_bounds(kCkptU, a.ku.q, 1, bytes, 0, 1);
+}
+
 template <int kOp>
 int launch(Args& a, int32_t dtype, bool on_grid, void* stream) {
+  bound_buffers<kOp>(a);
   const int64_t col_tiles = ceil_div(a.pitch, kCols);
   if (col_tiles > kMaxTiles || a.rows > kMaxTiles / col_tiles) return ZERO_ERANGE;
   a.col_tiles = static_cast<uint32_t>(col_tiles);
@@ -324,7 +355,7 @@ ZERO_API int zero_ckpt_save(const void* x, int64_t rows, int64_t cols, int64_t l
   if (rows == 0 || cols == 0) return ZERO_OK;
   if (!x || !ckpt) return ZERO_EINVAL;
   if (!aligned(x, 2) || !aligned(ckpt, 16)) return ZERO_EALIGN;
-  Args a = {};
+  Args a = new_args<Args>();
   a.x = static_cast<const uint16_t*>(x);
   a.rows = rows, a.cols = cols, a.pitch = pitch_of(cols), a.ld = ld;
   a.kx = ckpt_of(ckpt, rows, a.pitch);
@@ -338,7 +369,7 @@ ZERO_API int zero_ckpt_load(const void* ckpt, int64_t rows, int64_t cols, int32_
   if (rows == 0 || cols == 0) return ZERO_OK;
   if (!out || !ckpt) return ZERO_EINVAL;
   if (!aligned(out, 2) || !aligned(ckpt, 16)) return ZERO_EALIGN;
-  Args a = {};
+  Args a = new_args<Args>();
   a.y = static_cast<uint16_t*>(out);
   a.rows = rows, a.cols = cols, a.pitch = pitch_of(cols), a.ld = ld;
   a.kx = ckpt_of(ckpt, rows, a.pitch);
@@ -358,7 +389,7 @@ ZERO_API int zero_ckpt_act(int32_t act, const void* x, const void* u, int64_t ro
   if (!aligned(x, 2) || !aligned(u, 2) || !aligned(y, 2) || !aligned(ckpt_x, 16) ||
       !aligned(ckpt_u, 16))
     return ZERO_EALIGN;
-  Args a = {};
+  Args a = new_args<Args>();
   a.x = static_cast<const uint16_t*>(x);
   a.u = static_cast<const uint16_t*>(u);
   a.y = static_cast<uint16_t*>(y);
@@ -384,7 +415,7 @@ ZERO_API int zero_ckpt_act_grad(int32_t act, const void* ckpt_x, const void* ckp
   if (!aligned(dy, 2) || !aligned(dx, 2) || !aligned(du, 2) || !aligned(y, 2) ||
       !aligned(ckpt_x, 16) || !aligned(ckpt_u, 16))
     return ZERO_EALIGN;
-  Args a = {};
+  Args a = new_args<Args>();
   a.dy = static_cast<const uint16_t*>(dy);
   a.dx = static_cast<uint16_t*>(dx);
   a.du = static_cast<uint16_t*>(du);
@@ -399,11 +430,12 @@ ZERO_API int zero_ckpt_act_grad(int32_t act, const void* ckpt_x, const void* ckp
 }
 
 ZERO_API int zero_selftest_plant(int32_t what, int64_t at, int64_t limit_ns) {
-  if (what < ZERO_PLANT_NOTHING || what > ZERO_PLANT_NO_SEND || limit_ns < 1 ||
+  if (what < ZERO_PLANT_NOTHING || what > ZERO_PLANT_SHORT || limit_ns < 1 ||
       limit_ns > 1000000000)
     return ZERO_EINVAL;
 #ifdef ZERO_CHECKED
-  zt::g_plant = {what, at, what ? static_cast<uint64_t>(limit_ns) : zt::kWaitLimitNs};
+  const bool wait = what == ZERO_PLANT_NO_COPY || what == ZERO_PLANT_NO_SEND;
+  zt::g_plant = {what, at, wait ? static_cast<uint64_t>(limit_ns) : zt::kWaitLimitNs};
   return ZERO_OK;
 #else
   (void)at;

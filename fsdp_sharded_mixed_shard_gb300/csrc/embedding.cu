@@ -62,11 +62,18 @@ constexpr int kMaxPasses = 3;
 static_assert(kDigits == kSortThreads, "one thread per digit");
 static_assert(kTile % kSortThreads == 0, "whole rounds");
 
+// the buffers of a call, for their bounds
+enum { kTable, kOut, kLookupBuffers };
+enum { kDy, kGrad, kParts, kSpans, kGradBuffers };
+
 // A lane's eight neighbouring columns [c, c + 8) of a row; columns past dim
 // are 0 (loads) or left alone (stores). kVecRows: rows lie on the 16-byte grid
 // and dim is a multiple of 8.
 template <bool kVecRows>
-__device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t dim) {
+__device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t dim,
+                                       const Bounds& in) {
+  if (!in.holds(row + c, 2 * (dim - c < kVec ? dim - c : kVec), kSiteLoad))
+    return make_uint4(0, 0, 0, 0);
   if constexpr (kVecRows)
     return c < dim ? __ldcs(reinterpret_cast<const uint4*>(row + c)) : make_uint4(0, 0, 0, 0);
   if (c + kVec <= dim) return load8_any<false>(row + c);
@@ -79,13 +86,14 @@ __device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t d
 // The warp's slice of a row from column c0 on; all lanes call it.
 template <bool kVecRows>
 __device__ __forceinline__ void store_slice(uint8_t* stage, uint16_t* row, int64_t c0, int lane,
-                                            int64_t dim, const uint4& v) {
+                                            int64_t dim, const uint4& v, const Bounds& in) {
   if constexpr (kVecRows) {
     const int64_t c = c0 + lane * kVec;
-    if (c < dim) __stcs(reinterpret_cast<uint4*>(row + c), v);
+    if (c < dim && in.holds(row + c, 16, kSiteStore))
+      __stcs(reinterpret_cast<uint4*>(row + c), v);
   } else {
     const int64_t left = dim - c0;
-    store_any(stage, row + c0, left < kSlice ? static_cast<int>(left) : kSlice, lane, v);
+    store_any(stage, row + c0, left < kSlice ? static_cast<int>(left) : kSlice, lane, v, in);
   }
 }
 
@@ -97,7 +105,7 @@ struct Stages {
 
 // ------------------------------------------------------------------ lookup ----
 
-struct LookupArgs {
+struct LookupArgs : Checked<kLookupBuffers> {
   const void* tokens;
   const uint16_t* table;
   uint16_t* out;
@@ -122,9 +130,9 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const LookupArgs a) {
   for (int k = 0; k < kLookup; ++k) {
     const int64_t t = t0 + k;
     const int64_t id = t < a.n ? load_id(a.tokens, a.token_bytes, t, a.vocab) : -1;
-    v[k] = id >= 0 && ZCHECK(id < a.vocab, kSiteLoad, id)
-               ? load8<kVecRows>(a.table + id * a.dim, c0 + lane * kVec, a.dim)
-               : make_uint4(0, 0, 0, 0);
+    v[k] = id >= 0 ? load8<kVecRows>(a.table + id * a.dim, c0 + lane * kVec, a.dim,
+                                     a.bounds(kTable))
+                   : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int k = 0; k < kLookup; ++k) {
@@ -134,7 +142,8 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const LookupArgs a) {
     widen8<kBf16>(v[k], f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] *= a.scale;
-    store_slice<kVecRows>(stage, a.out + t * a.dim, c0, lane, a.dim, narrow8<kBf16>(f));
+    store_slice<kVecRows>(stage, a.out + t * a.dim, c0, lane, a.dim, narrow8<kBf16>(f),
+                          a.bounds(kOut));
   }
 }
 
@@ -401,7 +410,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads)
 
 // -------------------------------------------------------------------- rows ----
 
-struct RowsArgs {
+struct RowsArgs : Checked<kGradBuffers> {
   const uint32_t* key;   // sorted ids; padding ids are vocab
   const uint32_t* pos;
   const uint16_t* dy;
@@ -464,24 +473,25 @@ __device__ __forceinline__ int64_t first_of(const uint32_t* key, int64_t n, int6
 template <bool kBf16, bool kVecRows>
 __device__ __forceinline__ void store_row(const RowsArgs& a, uint8_t* stage, int64_t v,
                                           int64_t c0, int lane, const float (&sum)[8], bool hit) {
-  if ((a.accumulate && !hit) || !ZCHECK(v < a.vocab, kSiteStore, v)) return;
+  if (a.accumulate && !hit) return;
   uint16_t* row = a.grad + v * a.dim;
   float f[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) f[j] = sum[j] * a.scale;
   if (a.accumulate) {
     float old[8];
-    widen8<kBf16>(load8<kVecRows>(row, c0 + lane * kVec, a.dim), old);
+    widen8<kBf16>(load8<kVecRows>(row, c0 + lane * kVec, a.dim, a.bounds(kGrad)), old);
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] += old[j];
   }
-  store_slice<kVecRows>(stage, row, c0, lane, a.dim, narrow8<kBf16>(f));
+  store_slice<kVecRows>(stage, row, c0, lane, a.dim, narrow8<kBf16>(f), a.bounds(kGrad));
 }
 
 // fp32 partial sums sit lane by lane: lane l's eight columns at [l * 8, l * 8 + 8)
 __device__ __forceinline__ void store_part(float* part, int64_t c0, int lane,
-                                           const float (&s)[8]) {
+                                           const float (&s)[8], const Bounds& in) {
   float4* p = reinterpret_cast<float4*>(part + c0 + lane * kVec);
+  if (!in.holds(p, 32, kSiteStore)) return;
   p[0] = make_float4(s[0], s[1], s[2], s[3]);
   p[1] = make_float4(s[4], s[5], s[6], s[7]);
 }
@@ -490,14 +500,16 @@ __device__ __forceinline__ void store_part(float* part, int64_t c0, int lane,
 // piece of memory whatever their length: share `part` of `parts`, in 16-byte
 // blocks but for the ends.
 __device__ __forceinline__ void clear_share(uint16_t* p, int64_t n, uint32_t part, uint32_t parts,
-                                            int lane) {
+                                            int lane, const Bounds& in) {
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p), hi = lo + 2 * static_cast<uintptr_t>(n);
   const uintptr_t in_lo = (lo + 15) & ~static_cast<uintptr_t>(15);
   const uintptr_t in_hi = hi & ~static_cast<uintptr_t>(15);
   if (part == 0) {  // at most seven elements before the first block and after the last
     const uintptr_t head = in_lo < hi ? in_lo : hi;
-    if (lo + 2 * lane < head) p[lane] = 0;
-    if (in_hi >= in_lo && in_hi + 2 * lane < hi) reinterpret_cast<uint16_t*>(in_hi)[lane] = 0;
+    uint16_t* end = reinterpret_cast<uint16_t*>(in_hi);
+    if (lo + 2 * lane < head && in.holds(p + lane, 2, kSiteStore)) p[lane] = 0;
+    if (in_hi >= in_lo && in_hi + 2 * lane < hi && in.holds(end + lane, 2, kSiteStore))
+      end[lane] = 0;
   }
   if (in_hi <= in_lo) return;
   const uint32_t blocks = static_cast<uint32_t>((in_hi - in_lo) >> 4);
@@ -505,7 +517,8 @@ __device__ __forceinline__ void clear_share(uint16_t* p, int64_t n, uint32_t par
   const uint32_t b0 = part * per, b1 = b0 + per < blocks ? b0 + per : blocks;
   uint4* q = reinterpret_cast<uint4*>(in_lo);
 #pragma unroll 4
-  for (uint32_t b = b0 + lane; b < b1; b += 32) __stcs(q + b, make_uint4(0, 0, 0, 0));
+  for (uint32_t b = b0 + lane; b < b1; b += 32)
+    if (in.holds(q + b, 16, kSiteStore)) __stcs(q + b, make_uint4(0, 0, 0, 0));
 }
 
 template <bool kBf16, bool kVecRows>
@@ -544,23 +557,26 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a) {
     // and its last in this one: join_kernel will add them up, from the run
     // that has the row's first token as an item of the merged list
     const int64_t first = (first_of(a.key, i0, row, lane) + row) / kRun;
-    if (lane == 0)
-      a.span[atomicAdd(a.n_spans, 1u)] =
-          make_uint4(static_cast<uint32_t>(row), static_cast<uint32_t>(first), u.run, 0);
+    if (lane == 0) {
+      uint4* to = a.span + atomicAdd(a.n_spans, 1u);
+      if (a.bounds(kSpans).holds(to, 16, kSiteRecord))
+        *to = make_uint4(static_cast<uint32_t>(row), static_cast<uint32_t>(first), u.run, 0);
+    }
   }
   bool hit = false;
   float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   // rows up to `end` have all their tokens: the first the sum, the rest none
   const auto done_until = [&](int64_t end) {
     if (row >= end) return;
-    if (begun) store_part(a.in_part + run * a.width, c0, lane, sum);
+    if (begun) store_part(a.in_part + run * a.width, c0, lane, sum, a.bounds(kParts));
     else store_row<kBf16, kVecRows>(a, stage, row, c0, lane, sum, hit);
     begun = hit = false;
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] = 0.f;
     ++row;
-    if (!a.accumulate && row < end && ZCHECK(end <= a.vocab, kSiteStore, end))
-      clear_share(a.grad + row * a.dim, (end - row) * a.dim, u.slice, a.slices, lane);
+    if (!a.accumulate && row < end)
+      clear_share(a.grad + row * a.dim, (end - row) * a.dim, u.slice, a.slices, lane,
+                  a.bounds(kGrad));
     row = end;
   };
   for (int i = 0; i < count; i += kBatch) {
@@ -572,8 +588,9 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a) {
       const uint32_t p = __shfl_sync(0xffffffffu, at < 32 ? pos[0] : pos[kPer - 1], at & 31);
       id[k] = __shfl_sync(0xffffffffu, at < 32 ? key[0] : key[kPer - 1], at & 31);
       if (at >= count) id[k] = 0xFFFFFFFFu;
-      if (id[k] < a.vocab && ZCHECK(p < a.n, kSiteLoad, p))
-        v[k] = load8<kVecRows>(a.dy + static_cast<int64_t>(p) * a.dim, c0 + lane * kVec, a.dim);
+      if (id[k] < a.vocab)
+        v[k] = load8<kVecRows>(a.dy + static_cast<int64_t>(p) * a.dim, c0 + lane * kVec, a.dim,
+                               a.bounds(kDy));
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
@@ -587,7 +604,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a) {
     }
   }
   done_until(row_end);
-  if (hit || begun) store_part(a.out_part + run * a.width, c0, lane, sum);
+  if (hit || begun) store_part(a.out_part + run * a.width, c0, lane, sum, a.bounds(kParts));
 }
 
 // Rows whose tokens span runs: the partial sums of the runs before the one
@@ -602,6 +619,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const RowsArgs a) {
   for (uint32_t at = blockIdx.x * kWarps + (threadIdx.x >> 5); at < units;
        at += gridDim.x * kWarps) {
     const Unit u = unit_of(a, at);
+    if (!a.bounds(kSpans).holds(a.span + u.run, 16, kSiteRecord)) continue;
     const uint4 span = a.span[u.run];
     const float* part = a.out_part + u.c0 + lane * kVec;
     float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -609,6 +627,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const RowsArgs a) {
     for (uint32_t k = span.y; k <= span.z; ++k) {
       const float4* p = reinterpret_cast<const float4*>(
           (k < span.z ? part : a.in_part + u.c0 + lane * kVec) + static_cast<int64_t>(k) * a.width);
+      if (!a.bounds(kParts).holds(p, 32, kSiteLoad)) continue;
       const float4 x = p[0], y = p[1];
       const float s[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
@@ -686,7 +705,7 @@ ZERO_API int zero_embedding(const void* tokens, int32_t token_bytes, int64_t n_t
   if (n_tokens == 0 || dim == 0) return ZERO_OK;
   if (!tokens || !out || (!table && vocab)) return ZERO_EINVAL;
   if (!aligned(tokens, token_bytes) || !aligned(table, 2) || !aligned(out, 2)) return ZERO_EALIGN;
-  LookupArgs a = {};
+  LookupArgs a = new_args<LookupArgs>();
   a.tokens = tokens;
   a.table = static_cast<const uint16_t*>(table);
   a.out = static_cast<uint16_t*>(out);
@@ -697,6 +716,8 @@ ZERO_API int zero_embedding(const void* tokens, int32_t token_bytes, int64_t n_t
   a.units = ceil_div(n_tokens, kLookup) * a.slices;
   a.token_bytes = token_bytes;
   a.scale = scale;
+  a.set_bounds(kTable, table, vocab, dim, dim, 2);
+  a.set_bounds(kOut, out, n_tokens, dim, dim, 2);
   const int64_t grid = ceil_div(a.units, kWarps);
   if (grid > kMaxGrid) return ZERO_ERANGE;
   const bool vec = dim % kVec == 0 && aligned(table, 16) && aligned(out, 16);
@@ -778,7 +799,7 @@ ZERO_API int zero_embedding_grad(const void* tokens, int32_t token_bytes, int64_
     }
     if (e != cudaSuccess) return ZERO_ECUDA;
   }
-  RowsArgs a = {};
+  RowsArgs a = new_args<RowsArgs>();
   a.key = key[last];
   a.pos = pos[last];
   a.dy = static_cast<const uint16_t*>(dy);
@@ -795,6 +816,11 @@ ZERO_API int zero_embedding_grad(const void* tokens, int32_t token_bytes, int64_
   a.n_runs = static_cast<uint32_t>(l.n_runs);
   a.scale = scale;
   a.accumulate = accumulate;
+  a.set_bounds(kDy, dy, n_tokens, dim, dim, 2);
+  a.set_bounds(kGrad, grad, vocab, dim, dim, 2);
+  // in_part follows out_part
+  a.set_bounds(kParts, a.out_part, 1, 1, 0, static_cast<int64_t>(l.bytes - l.out_part));
+  a.set_bounds(kSpans, a.span, 1, 1, 0, l.n_runs * static_cast<int64_t>(sizeof(uint4)));
   const bool vec = dim % kVec == 0 && aligned(dy, 16) && aligned(grad, 16);
   if (dtype == ZERO_BF16)
     return vec ? launch_rows<true, true>(a, st) : launch_rows<true, false>(a, st);

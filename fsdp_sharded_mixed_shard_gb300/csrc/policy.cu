@@ -47,7 +47,9 @@ constexpr int kParts = 2;      // parts of a row per warp
 constexpr int kBatch = 4;      // blocks per lane and step
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-struct Args : Plant {
+enum { kLogits, kDlogits, kBuffers };  // of a call, for their bounds
+
+struct Args : Checked<kBuffers> {
   const uint8_t* logits;
   uint8_t* dlogits;
   const void* actions;
@@ -434,7 +436,9 @@ __global__ void __launch_bounds__(32 * kWarps) logp_kernel(const Args a) {
     const Row r = row_of<B::kBytes, false>(a, row);
     float lp = 0.f;
     if (r.on()) {
-      const float picked = B::one(r.base + r.head + r.action * B::kBytes);
+      const uint8_t* at_action = r.base + r.head + r.action * B::kBytes;
+      const float picked =
+          a.bounds(kLogits).holds(at_action, B::kBytes, kSiteLoad) ? B::one(at_action) : 0.f;
       const int32_t b0 = static_cast<int64_t>(r.n_blk) * rank / n_cta;
       const int32_t b1 = static_cast<int64_t>(r.n_blk) * (rank + 1) / n_cta;
       const uint4* blocks = reinterpret_cast<const uint4*>(r.base);
@@ -444,8 +448,9 @@ __global__ void __launch_bounds__(32 * kWarps) logp_kernel(const Args a) {
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
           const int32_t at = b + k * kThreads;
-          v[k] = at < b1 && ZCHECK(at < r.n_blk, kSiteLoad, at) ? __ldcs(blocks + at)
-                                                               : no_block<kType>();
+          v[k] = at < b1 && a.bounds(kLogits).holds_blocks(blocks + at, 16, kSiteLoad)
+                     ? __ldcs(blocks + at)
+                     : no_block<kType>();
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) v[k] = own_part<kType>(r, b + k * kThreads, v[k]);
@@ -512,8 +517,10 @@ __global__ void __launch_bounds__(32 * kWarps, 24 / kWarps)
   const auto fetch = [&](const Row& r, int64_t row, int p) {  // one lane
     if (part0 + p == 0 && a.holds(ZERO_PLANT_NO_COPY, row)) return;
     const int32_t b0 = block_of(r, p), n = block_of(r, p + 1) - b0;
-    if (ZCHECK(n <= part_cap && b0 + n <= r.n_blk, kSiteStageBytes, n))
-      copy_blocks(part_at(p), r.base + static_cast<int64_t>(b0) * 16, n * 16, &landed[warp][p]);
+    const uint8_t* from = r.base + static_cast<int64_t>(b0) * 16;
+    const bool in = ZCHECK(n <= part_cap, kSiteStageBytes, n) &&
+                    a.bounds(kLogits).holds_blocks(from, n * 16, kSiteLoad);
+    copy_blocks(part_at(p), from, in ? n * 16 : 0, &landed[warp][p]);
   };
   uint32_t use = 0, phase = 0;
   int64_t row = blockIdx.x / n_cta;
@@ -529,7 +536,8 @@ __global__ void __launch_bounds__(32 * kWarps, 24 / kWarps)
     next.action = -1;
     if (warp == 0) {
       if (on) {
-        picked = B::one(r.base + r.head + r.action * B::kBytes);
+        const uint8_t* at = r.base + r.head + r.action * B::kBytes;
+        if (a.bounds(kLogits).holds(at, B::kBytes, kSiteLoad)) picked = B::one(at);
         old = a.old_logp[row];
         adv = a.advantage[row];
         if (kl) ref = a.ref_logp[row];
@@ -610,6 +618,7 @@ __global__ void __launch_bounds__(32 * kWarps, 24 / kWarps)
     const Pair by = pair(turn.inv, turn.inv);
     const float slope = turn.slope;
     const int32_t action_at = r.head + r.action * B::kBytes;
+    const Bounds out = a.bounds(kDlogits);
 #pragma unroll 1
     for (int p = 0; p < kParts; ++p) {
       const int32_t b0 = block_of(r, p), n = dx ? block_of(r, p + 1) - b0 : 0;
@@ -619,7 +628,8 @@ __global__ void __launch_bounds__(32 * kWarps, 24 / kWarps)
       uint4* to = reinterpret_cast<uint4*>(dx + static_cast<int64_t>(b0) * 16);
       // loops of the warp, not of the lane: lanes past the end sit a turn out
       if (plain && !on) {
-        for (int32_t k = lane; k < n; k += 32) __stcs(to + k, make_uint4(0, 0, 0, 0));
+        for (int32_t k = lane; k < n; k += 32)
+          if (out.holds(to + k, 16, kSiteStore)) __stcs(to + k, make_uint4(0, 0, 0, 0));
       } else if (plain && (special < 0 || special >= n)) {
         for (int32_t k0 = 0; k0 < n; k0 += 32 * kBatch) {
           uint4 v[kBatch];
@@ -636,7 +646,7 @@ __global__ void __launch_bounds__(32 * kWarps, 24 / kWarps)
 #pragma unroll
             for (int i = 0; i < B::kElems / 2; ++i) unpair(e[i] * by, f[2 * i], f[2 * i + 1]);
             const int32_t k = k0 + 32 * j + lane;
-            if (k < n) __stcs(to + k, B::put(f));
+            if (k < n && out.holds(to + k, 16, kSiteStore)) __stcs(to + k, B::put(f));
           }
         }
       } else {
@@ -656,12 +666,13 @@ __global__ void __launch_bounds__(32 * kWarps, 24 / kWarps)
               if (b * 16 + j * B::kBytes == action_at) f[j] += slope;
           }
           if (same && b * 16 >= r.head && b * 16 + 16 <= r.end) {
-            __stcs(to + k, B::put(f));
+            if (out.holds(to + k, 16, kSiteStore)) __stcs(to + k, B::put(f));
           } else {
 #pragma unroll
             for (int j = 0; j < B::kElems; ++j) {
               const int32_t at = b * 16 + j * B::kBytes;
-              if (at >= r.head && at < r.end) B::set(dx + at, f[j]);
+              if (at >= r.head && at < r.end && out.holds(dx + at, B::kBytes, kSiteStore))
+                B::set(dx + at, f[j]);
             }
           }
         }
@@ -872,6 +883,7 @@ ZERO_API int zero_token_logp(const void* logits, int64_t rows, int64_t vocab, in
   if (rc != ZERO_OK || rows == 0) return rc;
   Args a = new_args<Args>();
   a.logits = static_cast<const uint8_t*>(logits);
+  a.set_bounds(kLogits, logits, rows, vocab, ld, dtype == ZERO_FP32 ? 4 : 2);
   a.actions = actions;
   a.action_bytes = action_bytes;
   a.rows = rows, a.vocab = vocab, a.ld = ld;
@@ -901,7 +913,9 @@ ZERO_API int zero_policy_loss(const void* logits, int64_t rows, int64_t vocab, i
     return ZERO_EALIGN;
   Args a = new_args<Args>();
   a.logits = static_cast<const uint8_t*>(logits);
+  a.set_bounds(kLogits, logits, rows, vocab, ld, dtype == ZERO_FP32 ? 4 : 2);
   a.dlogits = static_cast<uint8_t*>(dlogits);
+  a.set_bounds(kDlogits, dlogits, rows, vocab, ld, static_cast<int64_t>(size));
   a.actions = actions;
   a.action_bytes = action_bytes;
   a.old_logp = old_logp, a.ref_logp = ref_logp, a.advantage = advantage, a.weight = weight;

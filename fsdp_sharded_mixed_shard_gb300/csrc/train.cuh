@@ -171,39 +171,6 @@ __device__ __forceinline__ uint4 load8_any(const uint16_t* p) {
   return kAlike ? shifted_alike(x, block[1], d) : shifted(x, block[1], d);
 }
 
-// A warp's store of up to 256 neighbouring elements to any element address,
-// eight per lane (v), `count` of them in all: through shared memory, so that
-// whole 16-byte blocks of the destination leave as such and only the elements
-// before the first and after the last go one by one. All lanes call it; stage
-// is the warp's own kStageWarp bytes, 16-byte aligned.
-constexpr int kStageWarp = 16 + 512 + 16;
-
-__device__ __forceinline__ void store_any(uint8_t* stage, uint16_t* to, int count, int lane,
-                                          const uint4& v) {
-  const uintptr_t at = reinterpret_cast<uintptr_t>(to);
-  const int d = static_cast<int>(at & 15);
-  uint4* mine = reinterpret_cast<uint4*>(stage + 16);
-  __syncwarp();  // the stage's last use is read
-  mine[lane] = v;
-  __syncwarp();
-  // destination block k: bytes [16 k - d, 16 k - d + 16) of the run
-  uint8_t* blocks = reinterpret_cast<uint8_t*>(at - d);
-  const int bytes = 2 * count;
-  const auto block = [&](int k) {
-    if (16 * k - d < 0 || 16 * k - d + 16 > bytes) return;
-    const uint4 x = mine[k - 1];
-    const uint4 y = mine[k];
-    __stcs(reinterpret_cast<uint4*>(blocks + 16 * k), shifted_alike(x, y, 16 - d));
-  };
-  block(lane);  // block 32 is never whole unless d is 0, and then it is past the run
-  // at most seven elements before the first whole block and after the last
-  const uint16_t* elems = reinterpret_cast<const uint16_t*>(stage + 16);
-  const int head = d ? min((16 - d) >> 1, count) : 0;
-  const int tail = max(head, (((bytes + d) & ~15) - d) >> 1);
-  if (lane < head) to[lane] = elems[lane];
-  if (tail + lane < count) to[tail + lane] = elems[tail + lane];
-}
-
 __device__ __forceinline__ uint64_t global_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
@@ -239,6 +206,61 @@ struct Plant {
 #endif
 };
 
+// The bytes a call may touch of one of its buffers. The checked build tests
+// every element that a kernel is about to load or store against them, from the
+// address itself, and leaves out what lies outside; the release build has
+// neither the bytes nor the tests.
+struct Bounds {
+#ifdef ZERO_CHECKED
+  uintptr_t lo, hi;
+#endif
+  __device__ __forceinline__ bool holds(const void* p, int64_t bytes, int site) const {
+#ifdef ZERO_CHECKED
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    return bytes <= 0 || ZCHECK(at >= lo && at + bytes <= hi, site,
+                                static_cast<int64_t>(at - lo));
+#else
+    (void)p, (void)bytes, (void)site;
+    return true;
+#endif
+  }
+  // whole 16-byte blocks, the first and last of which may be the buffer's in part
+  __device__ __forceinline__ bool holds_blocks(const void* p, int64_t bytes, int site) const {
+#ifdef ZERO_CHECKED
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    return bytes <= 0 || ZCHECK(at + 16 > lo && at + bytes < hi + 16, site,
+                                static_cast<int64_t>(at - lo));
+#else
+    (void)p, (void)bytes, (void)site;
+    return true;
+#endif
+  }
+};
+
+// What the arguments of all kernels begin with: the plant and the bounds of the
+// call's kBuffers buffers.
+template <int kBuffers>
+struct Checked : Plant {
+#ifdef ZERO_CHECKED
+  Bounds buffers[kBuffers];
+  __device__ __forceinline__ Bounds bounds(int k) const { return buffers[k]; }
+#else
+  __device__ __forceinline__ Bounds bounds(int) const { return Bounds{}; }
+#endif
+  // host: buffer k is `rows` rows of `cols` elements of `size` bytes, ld apart
+  void set_bounds(int k, const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t size) {
+#ifdef ZERO_CHECKED
+    Bounds& b = buffers[k];
+    b.lo = b.hi = reinterpret_cast<uintptr_t>(p);
+    if (!p || rows <= 0 || cols <= 0) return;
+    b.hi += ((rows - 1) * ld + cols) * size;
+    if (what == ZERO_PLANT_SHORT && at == k) b.hi -= size;
+#else
+    (void)k, (void)p, (void)rows, (void)cols, (void)ld, (void)size;
+#endif
+  }
+};
+
 // arguments of a launch with the plant that holds for it, all else 0
 #ifdef ZERO_CHECKED
 Plant planted();
@@ -252,6 +274,41 @@ Args new_args() {
 template <class Args>
 Args new_args() { return Args{}; }
 #endif
+
+// A warp's store of up to 256 neighbouring elements to any element address,
+// eight per lane (v), `count` of them in all: through shared memory, so that
+// whole 16-byte blocks of the destination leave as such and only the elements
+// before the first and after the last go one by one. All lanes call it; stage
+// is the warp's own kStageWarp bytes, 16-byte aligned.
+constexpr int kStageWarp = 16 + 512 + 16;
+
+__device__ __forceinline__ void store_any(uint8_t* stage, uint16_t* to, int count, int lane,
+                                          const uint4& v, const Bounds& in) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(to);
+  const int d = static_cast<int>(at & 15);
+  uint4* mine = reinterpret_cast<uint4*>(stage + 16);
+  __syncwarp();  // the stage's last use is read
+  mine[lane] = v;
+  __syncwarp();
+  // destination block k: bytes [16 k - d, 16 k - d + 16) of the run
+  uint8_t* blocks = reinterpret_cast<uint8_t*>(at - d);
+  const int bytes = 2 * count;
+  const auto block = [&](int k) {
+    if (16 * k - d < 0 || 16 * k - d + 16 > bytes) return;
+    if (!in.holds(blocks + 16 * k, 16, kSiteStore)) return;
+    const uint4 x = mine[k - 1];
+    const uint4 y = mine[k];
+    __stcs(reinterpret_cast<uint4*>(blocks + 16 * k), shifted_alike(x, y, 16 - d));
+  };
+  block(lane);  // block 32 is never whole unless d is 0, and then it is past the run
+  // at most seven elements before the first whole block and after the last
+  const uint16_t* elems = reinterpret_cast<const uint16_t*>(stage + 16);
+  const int head = d ? min((16 - d) >> 1, count) : 0;
+  const int tail = max(head, (((bytes + d) & ~15) - d) >> 1);
+  if (lane < head && in.holds(to + lane, 2, kSiteStore)) to[lane] = elems[lane];
+  if (tail + lane < count && in.holds(to + tail + lane, 2, kSiteStore))
+    to[tail + lane] = elems[tail + lane];
+}
 
 // Token ids are int32 or int64; an id outside [0, limit) becomes -1.
 __device__ __forceinline__ int64_t load_id(const void* ids, int32_t bytes, int64_t i,

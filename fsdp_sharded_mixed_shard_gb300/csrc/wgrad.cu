@@ -90,7 +90,9 @@ constexpr int kPlaceCycles[2] = {1250, 2200};
 static_assert(kM * kJoinPitch * 4 <= kRing, "the tile fits the stages");
 static_assert(kM == ZERO_CKPT_PAD, "a checkpoint row is whole CTA tiles");
 
-struct Args : Plant {
+enum { kCkpt, kDw, kBuffers };  // of a call, for their bounds
+
+struct Args : Checked<kBuffers> {
   const int8_t* q;
   const uint8_t* scale;
   const uint16_t* dy;
@@ -311,8 +313,8 @@ __device__ __forceinline__ Piece load_piece(const Args& a, const Source& s, int6
   for (int k = 0; k < 2; ++k) {
     b.q[k] = make_uint4(0, 0, 0, 0);
     b.scale[k] = 127;
-    if (s.left > 4 * k &&
-        ZCHECK(s.q + k * q_step + 16 <= a.q + a.rows * a.pitch, kSiteLoad, s.left)) {
+    if (s.left > 4 * k && a.bounds(kCkpt).holds(s.q + k * q_step, 16, kSiteLoad) &&
+        a.bounds(kCkpt).holds(s.scale + k * scale_step, 1, kSiteLoad)) {
       b.q[k] = *reinterpret_cast<const uint4*>(s.q + k * q_step);
       b.scale[k] = s.scale[k * scale_step];
     }
@@ -439,7 +441,8 @@ constexpr int kOutCols = 64, kOutPitch = 16 + kOutCols * 2;
 // columns [c, c + width) of the tile's row that starts at `to`, which has
 // `count` columns
 __device__ __forceinline__ void store_staged(uint8_t* stage, uint16_t* to, int64_t n, int64_t rows,
-                                             int c, int width, int count, int lane) {
+                                             int c, int width, int count, int lane,
+                                             const Bounds& in) {
   const int k = lane & 7, row0 = lane >> 3;
   const int end = c + width < count ? c + width : count;  // columns there are so far
 #pragma unroll 1
@@ -450,16 +453,17 @@ __device__ __forceinline__ void store_staged(uint8_t* stage, uint16_t* to, int64
     const int d = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15);
     const uint4* block = reinterpret_cast<const uint4*>(stage + row * kOutPitch + 16) + k;
     const int begin = 2 * c + 16 * k - d;  // byte of the row the block starts at
-    if (begin >= 0 && begin + 16 <= 2 * end)
-      *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(at) + begin) =
-          shifted_back(block[-1], block[0], d);
+    uint8_t* whole = reinterpret_cast<uint8_t*>(at) + begin;
+    if (begin >= 0 && begin + 16 <= 2 * end && in.holds(whole, 16, kSiteStore))
+      *reinterpret_cast<uint4*>(whole) = shifted_back(block[-1], block[0], d);
     if (c == 0 || end == count) {
       const uint16_t* elems = reinterpret_cast<const uint16_t*>(stage + row * kOutPitch + 16);
       const int head = d ? min((16 - d) >> 1, end) : 0;
-      if (c == 0 && k < head) at[k] = elems[k];
+      if (c == 0 && k < head && in.holds(at + k, 2, kSiteStore)) at[k] = elems[k];
       // elements of the block that no later columns complete
       const int tail = max(c == 0 ? head : 0, (((2 * end + d) & ~15) - d) >> 1);
-      if (end == count && tail + k < end) at[tail + k] = elems[tail + k - c];
+      if (end == count && tail + k < end && in.holds(at + tail + k, 2, kSiteStore))
+        at[tail + k] = elems[tail + k - c];
     }
   }
 }
@@ -759,7 +763,7 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e)  // n is a multiple of 8
               if (i0 + lane < a.cols && j + c + 8 * e < a.n &&
-                  ZCHECK((i0 + lane) * a.n + j + c + 8 * e + 8 <= a.cols * a.n, kSiteStore, i0))
+                  a.bounds(kDw).holds(row + e, 16, kSiteStore))
                 row[e] = v[e];
           } else if (j + (c & ~(kOutCols - 1)) < a.n) {
             uint8_t* stage = out_stage[warp - kOutWarp0];
@@ -773,7 +777,8 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
             last = v[3];
             if (within || c + 32 == kWide * a.bn) {
               __syncwarp();
-              store_staged(stage, to, a.n, a.cols - i0, c - within, within + 32, count, lane);
+              store_staged(stage, to, a.n, a.cols - i0, c - within, within + 32, count, lane,
+                           a.bounds(kDw));
               __syncwarp();
             }
           }
@@ -844,9 +849,10 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
       const int count = left < a.bn ? static_cast<int>(left) : a.bn;
       uint16_t* to = a.dw + i * a.n + j;
       if (a.vec_out) {
-        if (lane * 8 < count) *reinterpret_cast<uint4*>(to + lane * 8) = narrow8<kBf16>(f);
+        if (lane * 8 < count && a.bounds(kDw).holds(to + lane * 8, 16, kSiteStore))
+          *reinterpret_cast<uint4*>(to + lane * 8) = narrow8<kBf16>(f);
       } else {
-        store_any(stage, to, count, lane, narrow8<kBf16>(f));
+        store_any(stage, to, count, lane, narrow8<kBf16>(f), a.bounds(kDw));
       }
     }
     cluster_sync();  // no CTA ends while another reads its sums
@@ -978,6 +984,8 @@ ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const
   a.scaler = d_scaler;
   a.rows = rows, a.cols = cols, a.n = n, a.ld = ld;
   a.vec_out = n % kVec == 0 && aligned(dw, 16);
+  a.set_bounds(kCkpt, ckpt, 1, rows * (a.pitch + a.pitch / ZERO_CKPT_BLOCK), 0, 1);
+  a.set_bounds(kDw, dw, cols, n, n, 2);
   int fit[kMaxSplit + 1];
   for (int split = 1; split <= kMaxSplit; split *= 2)
     fit[split] = resident_clusters(split);

@@ -204,11 +204,20 @@ ZERO_API int zero_policy_loss(const void* logits, int64_t rows, int64_t vocab, i
  *                       its step `at`; zero_policy_loss: the first part of
  *                       row `at` is not copied
  *   ZERO_PLANT_NO_SEND  zero_token_logp, zero_policy_loss: the second CTA of
- *                       a cluster does not send its sums of row `at` */
+ *                       a cluster does not send its sums of row `at`
+ *   ZERO_PLANT_SHORT    the range checks take buffer `at` of a call for one
+ *                       element shorter than it is, so that the access to its
+ *                       last element is a violation (zero_checked_status) and
+ *                       left out. Buffers by call: zero_embedding table, out;
+ *                       zero_embedding_grad dy, grad, partial sums, rows that
+ *                       span runs (the last two: taken for empty); zero_ckpt_* but wgrad x, u, dy, y (out of
+ *                       load), dx, du, ckpt_x, ckpt_u; zero_ckpt_wgrad ckpt,
+ *                       dw; loss logits, dlogits */
 typedef enum zero_plant {
   ZERO_PLANT_NOTHING = 0,
   ZERO_PLANT_NO_COPY = 1,
-  ZERO_PLANT_NO_SEND = 2
+  ZERO_PLANT_NO_SEND = 2,
+  ZERO_PLANT_SHORT = 3
 } zero_plant;
 ZERO_API int zero_selftest_plant(int32_t what, int64_t at, int64_t limit_ns);
 
