@@ -970,7 +970,9 @@ ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const
   using namespace zw;
   if (rows < 0 || cols < 0 || n < 0 || ld < n || !is_dtype16(dtype)) return ZERO_EINVAL;
   constexpr int64_t kMost = int64_t{1} << 31;
-  if (rows >= kMost || cols >= kMost || n >= kMost) return ZERO_ERANGE;
+  // TMA takes row distances below 2^40 bytes; off the grid eight rows are one
+  constexpr int64_t kMostLd = int64_t{1} << 36;
+  if (rows >= kMost || cols >= kMost || n >= kMost || ld >= kMostLd) return ZERO_ERANGE;
   if (cols == 0 || n == 0) return ZERO_OK;
   if (!dw || (rows && (!ckpt || !dy))) return ZERO_EINVAL;
   if (!aligned(ckpt, 16) || !aligned(dy, 2) || !aligned(dw, 2) || !aligned(d_scaler, 16))

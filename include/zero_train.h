@@ -142,7 +142,7 @@ ZERO_API int zero_ckpt_act_grad(int32_t act, const void* ckpt_x, const void* ckp
  * tensor's place in a gradient replica) and written whole (zeros when rows is
  * 0). A pipeline wait that expires fills the output tile with NaN and, when
  * d_scaler is not NULL, raises ZERO_DEVERR_TIMEOUT there.
- * rows, cols, n < 2^31 (ZERO_ERANGE). */
+ * rows, cols, n < 2^31, ld < 2^36 (ZERO_ERANGE). */
 ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const void* dy,
                              int64_t n, int64_t ld, int32_t dtype, void* dw,
                              zero_scaler* d_scaler, void* stream);

@@ -161,3 +161,10 @@ def test_plant_is_refused():
         refused(EINVAL, Z.zero_selftest_plant, *args)
     for what in range(Z.ZERO_PLANT_SHORT + 1):
         refused(-6, Z.zero_selftest_plant, what)
+
+
+def test_weight_gradient_row_distance():
+    """A row distance that no tensor map takes is out of range."""
+    ok = [P, 4, 100, P, 50, 56, BF, P, 0]
+    for ld in (1 << 36, (1 << 36) + 4, 1 << 62):
+        refused(ERANGE, Z.zero_ckpt_wgrad, *changed(ok, i5=ld))
