@@ -26,7 +26,9 @@
  * boundaries are moved as they are, others through 16-byte blocks that may
  * hold neighbouring elements, with the same results: a call may read the rest
  * of the block that holds a buffer's first or last element (any cudaMalloc'd
- * buffer covers it), and writes its own elements only.
+ * buffer covers it), and writes its own elements only. (The one exception:
+ * dlogits whose rows lie otherwise on the 16-byte grid than the logits' are
+ * written element by element.)
  * `ld` is the distance between the starts of two rows, in elements, at least
  * the row length (ZERO_EINVAL). Calls with no rows (or no elements) return
  * ZERO_OK and write only what the call still defines (the whole table's
@@ -56,7 +58,7 @@ extern "C" {
  *
  * tokens: n_tokens token ids, int32 or int64 (token_bytes 4 or 8). An id
  * outside [0, vocab) is padding: its output row is zeros and it takes no part
- * in the gradient.
+ * in the gradient. n_tokens <= 2^28, vocab <= 2^24, dim <= 2^28 (ZERO_ERANGE).
  * table: [vocab, dim] 16-bit elements, rows contiguous.
  *   out[t, :] = round16(scale * table[tokens[t], :])                          */
 ZERO_API int zero_embedding(const void* tokens, int32_t token_bytes, int64_t n_tokens,
@@ -77,7 +79,8 @@ ZERO_API size_t zero_embedding_workspace_bytes(int64_t n_tokens, int64_t vocab, 
  *   output layer, whose gradient is already there).
  * Tokens are sorted by id first, equal ids in the order of their positions;
  * the rows of dy are summed in that order, in runs whose bounds depend on the
- * ids alone. n_tokens <= 2^28, vocab <= 2^24 (ZERO_ERANGE). */
+ * ids alone. The workspace holds two fp32 rows for every 32 rows of the table
+ * and tokens together, whether or not tokens fall there. */
 ZERO_API int zero_embedding_grad(const void* tokens, int32_t token_bytes, int64_t n_tokens,
                                  const void* dy, int64_t vocab, int64_t dim, float scale,
                                  int32_t dtype, int32_t accumulate, void* grad,
@@ -96,7 +99,9 @@ ZERO_API int zero_embedding_grad(const void* tokens, int32_t token_bytes, int64_
  * as NaN throughout, so an overflowed activation still ends in a skipped step.
  * The value it stands for, q * 2^k, is exact in the 16-bit type: reading it
  * back never rounds. The error is at most half a step, a full one where
- * |x| > 127 steps: 2^-7 of the block's largest magnitude.                    */
+ * |x| > 127 steps: 2^-7 of the block's largest magnitude.
+ * rows times the row's blocks of 256 columns < 2^31 (ZERO_ERANGE), but for the
+ * weight gradient.                                                           */
 #define ZERO_CKPT_BLOCK 32
 #define ZERO_CKPT_PAD 128
 
@@ -140,8 +145,9 @@ ZERO_API int zero_ckpt_act_grad(int32_t act, const void* ckpt_x, const void* ckp
  *   dw[i, j] = round16(sum over t of x^[t, i] * dy[t, j])
  * on the tensor cores, accumulated in fp32; dw is [cols, n] contiguous (a
  * tensor's place in a gradient replica) and written whole (zeros when rows is
- * 0). A pipeline wait that expires fills the output tile with NaN and, when
- * d_scaler is not NULL, raises ZERO_DEVERR_TIMEOUT there.
+ * 0). A pipeline wait that expires (2 s) fills the tiles that its cluster of
+ * CTAs had left with NaN and, when d_scaler is not NULL, raises
+ * ZERO_DEVERR_TIMEOUT there.
  * rows, cols, n < 2^31, ld < 2^36 (ZERO_ERANGE). */
 ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const void* dy,
                              int64_t n, int64_t ld, int32_t dtype, void* dw,
@@ -149,11 +155,14 @@ ZERO_API int zero_ckpt_wgrad(const void* ckpt, int64_t rows, int64_t cols, const
 
 /* -------------------------------------------------------------------- loss --
  *
- * A pipeline wait that expires (2 s) makes the rows that its CTAs had left NaN.
+ * A pipeline wait that expires (2 s) makes the rows that its CTAs had left
+ * NaN; it raises no error word.
  *
  * logits: [rows, vocab], row distance ld, of type dtype (ZERO_BF16, ZERO_FP16
- * or ZERO_FP32). -inf entries are tokens ruled out (probability 0); a row of
- * nothing but -inf, or one with a NaN or +inf, has logp NaN.
+ * or ZERO_FP32), rows and ld <= 2^31 (ZERO_ERANGE). -inf entries are tokens
+ * ruled out (probability 0); a row of nothing but -inf, or one with a NaN or
+ * +inf, has logp NaN. Finite values of any size are logits like others (a mask
+ * of the type's lowest value among them).
  * actions: the tokens taken, int32 or int64 (action_bytes 4 or 8).
  *   logp[t] = logits[t, a_t] - log(sum over j of exp(logits[t, j]))
  * An action outside [0, vocab) leaves its row out: logp 0. A row may have at
@@ -178,8 +187,8 @@ typedef struct zero_policy_params {
  * gradient replicas hold S times the gradient as zero_step expects. A weight
  * of 0 (a prompt token, padding) or an action outside [0, vocab) leaves the
  * row out: its logits are not read, logp and loss are 0 and dlogits are 0.
- * ref_logp may be NULL: no KL term (with kl_coef 0 it is only reported in
- * stats). dlogits may be the logits buffer itself.
+ * ref_logp may be NULL: no KL term, its sum in stats is 0 (with kl_coef 0 it
+ * is only reported there). dlogits may be the logits buffer itself.
  * logp, loss (fp32 [rows]) are always written; dlogits [rows, vocab] with the
  * logits' type and row distance; stats, when not NULL, receives
  *   { sum w loss, sum w (exp(d) - d - 1), sum w [clipped], sum w }
