@@ -138,11 +138,12 @@ __device__ __forceinline__ void save8(const Ckpt& k, int64_t row, int64_t c, int
   };
   uint2 out = make_uint2(low_bytes(q[0], q[1], q[2], q[3]), low_bytes(q[4], q[5], q[6], q[7]));
   if (!finite) out = make_uint2(0, 0);
-  uint8_t* scale = k.scale + row * (pitch / ZERO_CKPT_BLOCK) + c / ZERO_CKPT_BLOCK;
   if (bounds.holds(k.q + row * pitch + c, kVec, kSiteStore))
     __stcs(reinterpret_cast<uint2*>(k.q + row * pitch + c), out);
-  if ((threadIdx.x & 3) == 0 && bounds.holds(scale, 1, kSiteStore))
-    *scale = static_cast<uint8_t>(finite ? step : 255);
+  if ((threadIdx.x & 3) == 0) {
+    uint8_t* scale = k.scale + row * (pitch / ZERO_CKPT_BLOCK) + c / ZERO_CKPT_BLOCK;
+    if (bounds.holds(scale, 1, kSiteStore)) *scale = static_cast<uint8_t>(finite ? step : 255);
+  }
 }
 
 // The lane's eight checkpointed values. A byte with its sign bit
@@ -233,15 +234,21 @@ __global__ void __launch_bounds__(kThreads) ckpt_kernel(const Args a) {
     uint2 qx = make_uint2(0, 0), qu = qx;
     uint32_t sx = 1, su = 1;
     uint4 vd = make_uint4(0, 0, 0, 0);
-    const auto read8 = [&](const Ckpt& k, const Bounds& bounds, uint2& q, uint32_t& s) {
-      if (bounds.holds(k.q + r * a.pitch + c, kVec, kSiteLoad))
-        q = __ldcs(reinterpret_cast<const uint2*>(k.q + r * a.pitch + c));
-      const uint8_t* scale = k.scale + r * blk + c / ZERO_CKPT_BLOCK;
-      if (bounds.holds(scale, 1, kSiteLoad)) s = *scale;
-    };
     if (in) {
-      read8(a.kx, a.bounds(kCkptX), qx, sx);
-      if constexpr (kOp == kSwigluGrad) read8(a.ku, a.bounds(kCkptU), qu, su);
+      const uint8_t* scale = a.kx.scale + r * blk + c / ZERO_CKPT_BLOCK;
+      if (a.bounds(kCkptX).holds(a.kx.q + r * a.pitch + c, kVec, kSiteLoad) &&
+          a.bounds(kCkptX).holds(scale, 1, kSiteLoad)) {
+        qx = __ldcs(reinterpret_cast<const uint2*>(a.kx.q + r * a.pitch + c));
+        sx = a.kx.scale[r * blk + c / ZERO_CKPT_BLOCK];
+      }
+      if constexpr (kOp == kSwigluGrad) {
+        scale = a.ku.scale + r * blk + c / ZERO_CKPT_BLOCK;
+        if (a.bounds(kCkptU).holds(a.ku.q + r * a.pitch + c, kVec, kSiteLoad) &&
+            a.bounds(kCkptU).holds(scale, 1, kSiteLoad)) {
+          qu = __ldcs(reinterpret_cast<const uint2*>(a.ku.q + r * a.pitch + c));
+          su = a.ku.scale[r * blk + c / ZERO_CKPT_BLOCK];
+        }
+      }
       if constexpr (kOp != kLoad)
         vd = load8<kGrid>(a.dy + r * a.ld_y, c, a.cols, a.bounds(kDy));
     }
@@ -269,12 +276,14 @@ __global__ void __launch_bounds__(kThreads) ckpt_kernel(const Args a) {
           gx[j] = d[j] * __fmaf_rn(y[j] * g.q, z1, g.p);
         }
       }
-      const auto put = [&](uint16_t* to, const float (&f)[8], const Bounds& bounds) {
-        store_row<kGrid>(stage, to + r * a.ld, c0, lane, a.cols, narrow8<kBf16>(f), bounds);
-      };
-      put(a.dx, gx, a.bounds(kDx));
-      if constexpr (kOp == kSwigluGrad) put(a.du, gu, a.bounds(kDu));
-      if (a.y) put(a.y, y, a.bounds(kY));
+      store_row<kGrid>(stage, a.dx + r * a.ld, c0, lane, a.cols, narrow8<kBf16>(gx),
+                       a.bounds(kDx));
+      if constexpr (kOp == kSwigluGrad)
+        store_row<kGrid>(stage, a.du + r * a.ld, c0, lane, a.cols, narrow8<kBf16>(gu),
+                         a.bounds(kDu));
+      if (a.y)
+        store_row<kGrid>(stage, a.y + r * a.ld, c0, lane, a.cols, narrow8<kBf16>(y),
+                         a.bounds(kY));
     }
   }
 }
