@@ -26,8 +26,13 @@
  * fp32 arithmetic, four blocks per lane and step, and the row's scalars by one
  * warp. Measured: 4096 x 128256 bf16, a quarter of the rows left out, 297 us
  * (91 % of copy bandwidth; ncu on 1024 rows: 400 MB moved for 394), 2048 x 50257
- * 73 us (73 %: 6 or 7 rows per cluster), 16 x 50257 8.0 us. Log-probabilities
- * alone stream the row through registers: 2048 x 128256 fp32 165 us (94 %).
+ * 73 us (73 %: 6 or 7 rows per cluster), 16 x 50257 8.2 us. Log-probabilities
+ * alone stream the row through registers: 2048 x 128256 fp32 150 us (7.0 TB/s
+ * read; the copy that is measured against also writes).
+ *
+ * Every wait is bounded (2 s). One that expires ends the work of its CTA and,
+ * as the others' waits for it expire, of its cluster: the rows left are NaN, and
+ * no CTA ends before what is on its way to it has landed.
  */
 #include "train.cuh"
 
@@ -272,6 +277,8 @@ __device__ __forceinline__ void copy_blocks(void* dst, const uint8_t* src, uint3
         : "memory");
 }
 
+// Acquires at cluster scope: what it waits for may be another CTA's sums. The
+// first tries come one after another, as a copy or the sums are mostly there.
 __device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(

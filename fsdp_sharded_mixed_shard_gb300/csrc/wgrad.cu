@@ -25,10 +25,14 @@
  *                   the other half of tensor memory meanwhile; two groups fill
  *                   it, and halve the value warps' work per product.
  * A step's values take about 850 cycles, 256 columns' products 512, so two
- * groups are what feeds the tensor cores: 8192 x 2048 x 8192 bf16 takes 157 us
- * (1750 TFLOP/s, the rate cuBLAS sustains under the power cap, 1734) against
- * 240 us with one group. 1024 x 768 x 2304 takes 13 us, of which 8 are set-up,
- * the first copies' latency and the output.
+ * groups are what feeds the tensor cores: 8192 x 2048 x 8192 bf16 takes 157 to
+ * 179 us by the card and its power cap (cuBLAS on bf16 operands 162 to 167 where
+ * this takes 176 to 179) against 240 us with one group. Its 152 tiles are two
+ * whole turns of the 76 pairs, which suits it best. Where tiles fill the turns
+ * less or only one column group fits them, the tensor cores wait: 8192 x 2048 x
+ * 5632 156 us (97 at their rate), x 2048 70 (35), 1024 x 4096 71 (35), 768 x 2304
+ * 41 (15). 1024 tokens x 768 x 2304 takes 13.5 us, of which 8 are set-up, the
+ * first copies' latency and the output.
  *
  * Few tiles and many tokens: a cluster of 2, 4 or 8 pairs shares a tile, each
  * pair a part of the tokens; the sums meet in shared memory and every CTA adds
@@ -38,7 +42,7 @@
  *
  * A dy whose rows do not start on 16-byte boundaries comes as the 16-byte
  * blocks that hold it, and three groups of warps move it to its places beside
- * the values (at Maps; 8000 x 2000 x 5555: 256 us against 152 at 5552. One
+ * the values (at Maps; 8000 x 2000 x 5555: 236 us against 150 at 5552. One
  * group for dy and two for the values took 416).
  *
  * Every wait is bounded (2 s). One that expires ends the work of its cluster:
@@ -130,14 +134,16 @@ __device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
 
 // CTA-scope release: what it publishes is this CTA's own shared or tensor
 // memory, read by this SM's tensor core after the proxy fence that precedes it
-// (a cluster-scope release would wait for this thread's loads ahead as well).
+// (a cluster-scope release would wait for this thread's loads ahead as well:
+// 224 us against 179 at 8192 x 2048 x 8192). The waits need no wider scope for
+// the same reason; no thread reads through them what another CTA wrote.
 __device__ __forceinline__ void bar_arrive_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
 
 // One try; the thread sleeps in it until the phase completes, at most about a
-// millisecond.
+// millisecond (22 warps that asked in turn would slow what they wait for).
 __device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
