@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(32 * kWarps, 24 / kWarps)
       for (int p = 0; p < kParts; ++p) {
         const int32_t b0 = block_of(r, p), n = block_of(r, p + 1) - b0;
         const uint4* part = part_at(p);
-        bar_wait(&landed[warp][p], phase, a.limit(), &lost);
+        bar_wait(&landed[warp][p], phase, a.limit(), &lost);  // expired: join_all sees `lost`
         const bool edge = b0 == 0 || b0 + n == r.n_blk;
         for (int32_t k0 = 0; k0 < n; k0 += 32 * kBatch) {
           uint4 v[kBatch];

@@ -117,7 +117,8 @@ def cases():
               (2048, 128, 256, 0), (2048, 128, 255, 1), (2000, 200, 104, 0)):  # split
         yield "wgrad", wgrad(*c)
     for dtype in ("bf16", "fp32"):
-        for c in ((9, 257, 0, 0, 0.5), (9, 257, 0, 0, 0.0), (9, 257, 0, 3, 0.5), (3, 50257, 1, 1, 0.5),
+        for c in ((9, 257, 0, 0, 0.5), (9, 257, 0, 0, 0.0), (9, 257, 0, 3, 0.5),
+                  (3, 50257, 1, 1, 0.5),
                   (4, 264, 0, 0, 0.5), (4, 5000, 0, 0, 0.0), (700, 264, 0, 0, 0.5)):
             yield "policy", policy(*c, dtype)
     yield "logp", logp(9, 257)

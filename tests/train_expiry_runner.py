@@ -62,7 +62,7 @@ POLICY = [
     (700, 257, "bf16", Z.ZERO_PLANT_NO_COPY, 4),       # a CTA per row
     (6000, 257, "bf16", Z.ZERO_PLANT_NO_COPY, 10),     # several rows per CTA
     (2048, 50257, "bf16", Z.ZERO_PLANT_NO_COPY, 0),    # pairs of CTAs, several rows each
-    (2048, 50257, "bf16", Z.ZERO_PLANT_NO_COPY, 901),  # a row copied while another's gradient leaves
+    (2048, 50257, "bf16", Z.ZERO_PLANT_NO_COPY, 901),  # copied while another row's gradient leaves
     (16, 50257, "fp16", Z.ZERO_PLANT_NO_COPY, 7),      # few rows
     (2048, 50257, "bf16", Z.ZERO_PLANT_NO_SEND, 500),
     (16, 50257, "fp16", Z.ZERO_PLANT_NO_SEND, 3),
