@@ -22,7 +22,8 @@ def test_every_buffer_is_tested():
     got = [json.loads(x) for x in r.stdout.splitlines() if x.startswith("{")]
     seen = {(c["case"], c["buffer"]) for c in got}
     assert seen == {("lookup", 0), ("lookup", 1), ("save", 0), ("save", 6), ("load", 3),
-                    ("load", 6), ("wgrad", 0), ("wgrad", 1), ("policy", 0), ("policy", 1), ("logp", 0),
+                    ("load", 6), ("wgrad", 0), ("wgrad", 1), ("policy", 0), ("policy", 1),
+                    ("logp", 0),
                     *((n, k) for n in ("table_grad", "table_grad_clear") for k in range(4)),
                     *(("act", k) for k in (0, 1, 3, 6, 7)),
                     *(("grad", k) for k in (2, 3, 4, 5, 6, 7))}
