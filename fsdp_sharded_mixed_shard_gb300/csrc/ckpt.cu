@@ -15,7 +15,7 @@
  * Measured on SwiGLU both ways, 8192 x 8192: 201 us, 89 % of copy bandwidth; a
  * CTA of eight rows by 256 columns took 206, two rows per warp 204.
  */
-#include "train.cuh"
+#include "rows.cuh"
 
 #include <algorithm>
 
@@ -25,48 +25,9 @@ using namespace zt;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kCols = 32 * kVec;
 
 // a call's buffers, for their bounds
 enum { kX, kU, kDy, kY, kDx, kDu, kCkptX, kCkptU, kBuffers };
-
-// Eight elements of a row of 16-bit elements starting at column c; those at
-// or past `cols` are 0. kGrid: rows lie on the 16-byte grid.
-template <bool kGrid>
-__device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t cols,
-                                       const Bounds& in) {
-  if (!in.holds(row + c, 2 * (cols - c < kVec ? cols - c : kVec), kSiteLoad))
-    return make_uint4(0, 0, 0, 0);
-  if (c + kVec <= cols)
-    return kGrid ? __ldcs(reinterpret_cast<const uint4*>(row + c)) : load8_any<true>(row + c);
-  uint32_t h[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) h[j] = c + j < cols ? row[c + j] : 0;
-  return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-}
-
-// A warp's 256 columns of a row from c0 on, those before `cols`; all lanes
-// call it.
-template <bool kGrid>
-__device__ __forceinline__ void store_row(uint8_t* stage, uint16_t* row, int64_t c0, int lane,
-                                          int64_t cols, const uint4& v, const Bounds& in) {
-  const int64_t c = c0 + lane * kVec;
-  if constexpr (kGrid) {
-    if (!in.holds(row + c, 2 * (cols - c < kVec ? cols - c : kVec), kSiteStore)) return;
-    if (c + kVec <= cols) {
-      __stcs(reinterpret_cast<uint4*>(row + c), v);
-      return;
-    }
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c + j < cols) row[c + j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
-  } else {
-    const int64_t left = cols - c0;
-    if (left > 0)
-      store_any(stage, row + c0, left < kCols ? static_cast<int>(left) : kCols, lane, v, in);
-  }
-}
 
 struct Ckpt {
   int8_t* q;       // [rows][pitch]
@@ -331,10 +292,6 @@ int launch(Args& a, int32_t dtype, bool on_grid, void* stream) {
   return status_of(launch_pdl(fn, dim3(static_cast<unsigned>(ceil_div(a.rows * col_tiles, kWarps))),
                               dim3(kThreads), 0, static_cast<cudaStream_t>(stream), a));
 }
-
-// whether every row start of a [.., ld] array of 16-bit elements lies on the
-// 16-byte grid
-bool on_grid(const void* p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
 
 }  // namespace zc
 
