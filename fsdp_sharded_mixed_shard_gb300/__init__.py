@@ -1,9 +1,8 @@
 """libzero Python binding: the per-shard ZeRO step of mixed-precision AdamW on
 one GB300.
 
-A thin ctypes layer over the C ABI in include/zero.h, include/zero_units.h
-and include/zero_train.h: every function below
-has the C function's name and only marshals arguments (device pointers are
+A thin ctypes layer over the C ABI in include/zero.h, include/zero_units.h,
+include/zero_train.h and include/zero_block.h: every function below has the C function's name and only marshals arguments (device pointers are
 plain Python ints, host arrays become C arrays); all computation happens in
 the sm_103a kernels of _lib/libzero.so. Loading fails loudly when the library
 has not been built (run ``__graft_entry__.build()``); there is no fallback.
@@ -41,6 +40,11 @@ __all__ = [
     "zero_ckpt_act_grad", "zero_ckpt_wgrad", "zero_token_logp", "zero_policy_loss",
     "ZERO_PLANT_NOTHING", "ZERO_PLANT_NO_COPY", "ZERO_PLANT_NO_SEND", "ZERO_PLANT_SHORT",
     "zero_selftest_plant",
+    "ZERO_NORM_RMS", "ZERO_NORM_LAYER", "ZERO_MAX_JOIN_COLS", "ZERO_FP8_BLOCK", "ZERO_E4M3",
+    "ZERO_E5M2", "ZeroDropoutParams", "ZeroJoinParams", "ZeroJoinWeights",
+    "zero_dropout", "zero_block_join", "zero_block_join_workspace_bytes", "zero_block_join_grad",
+    "zero_fp8_bytes", "zero_fp8_quant", "zero_fp8_weight_bytes", "zero_fp8_quant_weight",
+    "zero_fp8_linear", "zero_fp8_linear_dgrad",
 ]
 
 ZERO_BF16 = 0
@@ -55,6 +59,10 @@ ZERO_CKPT_BLOCK = 32
 ZERO_CKPT_PAD = 128
 ZERO_ACT_GELU, ZERO_ACT_SWIGLU = range(2)
 ZERO_PLANT_NOTHING, ZERO_PLANT_NO_COPY, ZERO_PLANT_NO_SEND, ZERO_PLANT_SHORT = range(4)
+ZERO_NORM_RMS, ZERO_NORM_LAYER = range(2)
+ZERO_MAX_JOIN_COLS = 8192
+ZERO_FP8_BLOCK = 128
+ZERO_E4M3, ZERO_E5M2 = range(2)
 (ZERO_FULL_SHARD, ZERO_SHARD_GRAD_OP, ZERO_NO_SHARD, ZERO_HYBRID_SHARD,
  ZERO_NO_RESHARD_AFTER_FORWARD) = range(5)
 
@@ -142,6 +150,24 @@ class ZeroStrategyCost(C.Structure):
 class ZeroPolicyParams(C.Structure):
     """zero_train.h zero_policy_params: clip range and KL coefficient."""
     _fields_ = [("clip_lo", C.c_double), ("clip_hi", C.c_double), ("kl_coef", C.c_double)]
+
+
+class ZeroDropoutParams(C.Structure):
+    """zero_block.h zero_dropout_params; d_step is a device address or None."""
+    _fields_ = [("p", C.c_double), ("seed", C.c_uint64), ("call", C.c_uint32),
+                ("d_step", C.c_void_p)]
+
+
+class ZeroJoinParams(C.Structure):
+    """zero_block.h zero_join_params."""
+    _fields_ = [("norm", C.c_int32), ("eps", C.c_double), ("stream_scale", C.c_double),
+                ("branch_scale", C.c_double), ("drop", ZeroDropoutParams)]
+
+
+class ZeroJoinWeights(C.Structure):
+    """zero_block.h zero_join_weights: device addresses, 0 or None where unused."""
+    _fields_ = [("w_post", C.c_void_p), ("b_post", C.c_void_p), ("gate", C.c_void_p),
+                ("w_pre", C.c_void_p), ("b_pre", C.c_void_p)]
 
 
 _lib = None
@@ -242,6 +268,22 @@ def lib():
         L.zero_policy_loss.argtypes = [_VP, i64, i64, i64, i32, _VP, i32, _VP, _VP, _VP, _VP,
                                        _P(ZeroPolicyParams), _VP, _VP, _VP, _VP, _VP, _VP]
         L.zero_selftest_plant.argtypes = [i32, i64, i64]
+        L.zero_dropout.argtypes = [_P(ZeroDropoutParams), _VP, _VP, i64, i64, i64, i32, _VP, i64,
+                                   _VP]
+        L.zero_block_join.argtypes = [_P(ZeroJoinParams), _P(ZeroJoinWeights), _VP, _VP, i64, i64,
+                                      i64, i32, _VP, _VP, _VP, _VP]
+        L.zero_block_join_workspace_bytes.argtypes = [i64, i64]
+        L.zero_block_join_workspace_bytes.restype = C.c_size_t
+        L.zero_block_join_grad.argtypes = [_P(ZeroJoinParams), _P(ZeroJoinWeights), _VP, _VP, _VP,
+                                           _VP, _VP, i64, i64, i64, i32, _VP, _VP,
+                                           _P(ZeroJoinWeights), _VP, _VP]
+        for name in ("zero_fp8_bytes", "zero_fp8_weight_bytes"):
+            getattr(L, name).argtypes = [i64, i64]
+            getattr(L, name).restype = C.c_size_t
+        L.zero_fp8_quant.argtypes = [_VP, i64, i64, i64, i32, i32, _VP, _VP]
+        L.zero_fp8_quant_weight.argtypes = [_VP, i64, i64, i32, _VP, _VP]
+        L.zero_fp8_linear.argtypes = [_VP, i32, i64, _VP, i64, i64, i32, _VP, i64, _VP, _VP]
+        L.zero_fp8_linear_dgrad.argtypes = L.zero_fp8_linear.argtypes
         _lib = L
     return _lib
 
@@ -620,6 +662,64 @@ def zero_policy_loss(logits, rows, vocab, ld, dtype, actions, action_bytes, old_
         logits or None, rows, vocab, ld, dtype, actions or None, action_bytes, old_logp or None,
         ref_logp or None, advantage or None, weight or None, C.byref(params), d_scaler or None,
         logp or None, loss or None, stats or None, dlogits or None, stream or None))
+
+
+# ------------------------------------------------------ operators of a block ----
+# Argument layouts, types and errors are in include/zero_block.h.
+
+def zero_dropout(params, x, residual, rows, cols, ld, dtype, out, ld_out, stream=0):
+    _check("zero_dropout", lib().zero_dropout(
+        C.byref(params), x or None, residual or None, rows, cols, ld, dtype, out or None, ld_out,
+        stream or None))
+
+
+def zero_block_join(params, weights, h, y, rows, cols, ld, dtype, h_out, z, stats=0, stream=0):
+    _check("zero_block_join", lib().zero_block_join(
+        C.byref(params), C.byref(weights), h or None, y or None, rows, cols, ld, dtype,
+        h_out or None, z or None, stats or None, stream or None))
+
+
+def zero_block_join_workspace_bytes(rows, cols):
+    return int(lib().zero_block_join_workspace_bytes(rows, cols))
+
+
+def zero_block_join_grad(params, weights, h_out, y, stats, dz, dh_out, rows, cols, ld, dtype, dh,
+                         dy, grads, workspace, stream=0):
+    _check("zero_block_join_grad", lib().zero_block_join_grad(
+        C.byref(params), C.byref(weights), h_out or None, y or None, stats or None, dz or None,
+        dh_out or None, rows, cols, ld, dtype, dh or None, dy or None, C.byref(grads),
+        workspace or None, stream or None))
+
+
+def zero_fp8_bytes(rows, cols):
+    return int(lib().zero_fp8_bytes(rows, cols))
+
+
+def zero_fp8_quant(x, rows, cols, ld, dtype, format, copy, stream=0):
+    _check("zero_fp8_quant", lib().zero_fp8_quant(x or None, rows, cols, ld, dtype, format,
+                                                  copy or None, stream or None))
+
+
+def zero_fp8_weight_bytes(k, n):
+    return int(lib().zero_fp8_weight_bytes(k, n))
+
+
+def zero_fp8_quant_weight(w, k, n, dtype, copy, stream=0):
+    _check("zero_fp8_quant_weight", lib().zero_fp8_quant_weight(w or None, k, n, dtype,
+                                                                copy or None, stream or None))
+
+
+def zero_fp8_linear(x_copy, x_format, rows, w_copy, k, n, dtype, y, ld, d_scaler=0, stream=0):
+    _check("zero_fp8_linear", lib().zero_fp8_linear(
+        x_copy or None, x_format, rows, w_copy or None, k, n, dtype, y or None, ld,
+        d_scaler or None, stream or None))
+
+
+def zero_fp8_linear_dgrad(dy_copy, dy_format, rows, w_copy, k, n, dtype, dx, ld, d_scaler=0,
+                          stream=0):
+    _check("zero_fp8_linear_dgrad", lib().zero_fp8_linear_dgrad(
+        dy_copy or None, dy_format, rows, w_copy or None, k, n, dtype, dx or None, ld,
+        d_scaler or None, stream or None))
 
 
 # ------------------------------------------------------------ checked build --

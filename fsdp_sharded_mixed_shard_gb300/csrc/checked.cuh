@@ -3,11 +3,11 @@
 // In libzero_checked.so every kernel of the step tests the global and
 // shared-memory ranges it is about to touch against the extents the plan gives
 // (window, shard, records, stage slot, unit slices). The kernels behind
-// zero_train.h test the addresses of the elements they load and store in the
+// zero_train.h and zero_block.h test the addresses of the elements they load and store in the
 // call's arrays, checkpoints and partial sums (train.cuh, Bounds); not tested
-// there are the per-token arrays and the sort's keys (indexed by the row at
-// hand), the weight gradient's loads of dy (TMA keeps to its map) and, but for
-// the loss's parts, shared memory. A failing test skips the access,
+// there are the per-token arrays, the sort's keys and the norms' and gates'
+// parameters (indexed by the row or column at hand), what TMA loads (it keeps to
+// its map) and, but for the loss's parts, shared memory. A failing test skips the access,
 // counts the violation and keeps the first one (site << 48 | low 48 bits of
 // the index); nothing traps. Each translation unit keeps its own counters
 // (device code is not linked across units); zero_checked_status collects
@@ -47,13 +47,16 @@ static __device__ __noinline__ bool check_failed(int site, int64_t where) {
 }
 #define ZCHECK(cond, site, where) ((cond) ? true : check_failed((site), (where)))
 
-// The units behind zero_train.h define ZERO_CHECKED_LEAF and one collector
+// The units behind zero_train.h and zero_block.h define ZERO_CHECKED_LEAF and one collector
 // each; any other unit's collect_checks collects theirs too.
 extern "C" {
 int ze_collect_checks(unsigned long long* count, unsigned long long* first);
 int zc_collect_checks(unsigned long long* count, unsigned long long* first);
 int zp_collect_checks(unsigned long long* count, unsigned long long* first);
 int zw_collect_checks(unsigned long long* count, unsigned long long* first);
+int zd_collect_checks(unsigned long long* count, unsigned long long* first);
+int zj_collect_checks(unsigned long long* count, unsigned long long* first);
+int zf_collect_checks(unsigned long long* count, unsigned long long* first);
 }
 
 // this unit's counters: add them to *count, keep the first code if *first
@@ -72,7 +75,9 @@ static inline int collect_checks(unsigned long long* count, unsigned long long* 
   if (*first == 0) *first = f;
 #ifndef ZERO_CHECKED_LEAF
   if (ze_collect_checks(count, first) || zc_collect_checks(count, first) ||
-      zp_collect_checks(count, first) || zw_collect_checks(count, first))
+      zp_collect_checks(count, first) || zw_collect_checks(count, first) ||
+      zd_collect_checks(count, first) || zj_collect_checks(count, first) ||
+      zf_collect_checks(count, first))
     return -1;
 #endif
   return 0;

@@ -34,14 +34,6 @@ struct Ckpt {
   uint8_t* scale;  // [rows][pitch / 32]
 };
 
-// Two 16-bit magnitudes at once: as integers they are ordered like the values,
-// infinity and NaN above all numbers.
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 // x held in [-limit, limit], pairs of 16-bit values
 template <bool kBf16>
 __device__ __forceinline__ uint32_t hold2(uint32_t x, uint32_t limit, uint32_t minus_limit) {

@@ -1,0 +1,93 @@
+/*
+ * dropout.cu -- dropout whose mask is never stored (zero_block.h).
+ *
+ * A thread takes 8 neighbouring elements of a row, which share one draw of the
+ * generator (draws.cuh); a warp 256 columns, running on into the next row.
+ */
+#include "draws.cuh"
+#include "rows.cuh"
+
+#include <algorithm>
+
+namespace zd {
+
+using namespace zt;
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+
+enum { kX, kResidual, kOut, kBuffers };  // a call's buffers, for their bounds
+
+struct Args : Checked<kBuffers> {
+  const uint16_t *x, *residual;
+  uint16_t* out;
+  int64_t rows, cols, ld, ld_out;
+  uint32_t col_tiles;
+  Drop drop;
+};
+
+template <bool kBf16, bool kGrid>
+__global__ void __launch_bounds__(kThreads) dropout_kernel(const Args a) {
+  pdl_begin();
+  __shared__ __align__(16) uint8_t stages[kGrid ? 1 : kWarps][kGrid ? 16 : kStageWarp];
+  uint8_t* stage = stages[kGrid ? 0 : threadIdx.x >> 5];
+  const int lane = threadIdx.x & 31;
+  const uint32_t tile = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const uint32_t row = tile / a.col_tiles;
+  const int64_t r = row;
+  if (r >= a.rows) return;
+  const int64_t c0 = static_cast<int64_t>(tile - row * a.col_tiles) * kCols, c = c0 + lane * kVec;
+  const uint4 vx = load8<kGrid>(a.x + r * a.ld, c, a.cols, a.bounds(kX));
+  uint4 vr = make_uint4(0, 0, 0, 0);
+  if (a.residual)
+    vr = load8<kGrid>(a.residual + r * a.ld_out, c, a.cols, a.bounds(kResidual));
+  float x[8], s[8];
+  widen8<kBf16>(vx, x);
+  if (a.drop.threshold)
+    drop8(a.drop, draw8(a.drop, step_of(a.drop), row, static_cast<uint32_t>(c >> 3)), x);
+  if (a.residual) {
+    widen8<kBf16>(vr, s);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] += s[j];
+  }
+  store_row<kGrid>(stage, a.out + r * a.ld_out, c0, lane, a.cols, narrow8<kBf16>(x),
+                   a.bounds(kOut));
+}
+
+}  // namespace zd
+
+#ifdef ZERO_CHECKED
+extern "C" int zd_collect_checks(unsigned long long* count, unsigned long long* first) {
+  return collect_checks(count, first);
+}
+#endif
+
+extern "C" ZERO_API int zero_dropout(const zero_dropout_params* params, const void* x,
+                                     const void* residual, int64_t rows, int64_t cols, int64_t ld,
+                                     int32_t dtype, void* out, int64_t ld_out, void* stream) {
+  using namespace zd;
+  if (!params || rows < 0 || cols < 0 || ld < cols || ld_out < cols || !is_dtype16(dtype))
+    return ZERO_EINVAL;
+  if (const int bad = check_drop(*params)) return bad;
+  constexpr int64_t kMost = int64_t{1} << 31;
+  const int64_t col_tiles = ceil_div(std::min(cols, kMost), kCols);
+  if (rows >= kMost || cols >= kMost || rows * col_tiles >= kMost) return ZERO_ERANGE;
+  if (rows == 0 || cols == 0) return ZERO_OK;
+  if (!x || !out || (x == out && ld != ld_out)) return ZERO_EINVAL;
+  if (!aligned(x, 2) || !aligned(residual, 2) || !aligned(out, 2)) return ZERO_EALIGN;
+  Args a = new_args<Args>();
+  a.x = static_cast<const uint16_t*>(x);
+  a.residual = static_cast<const uint16_t*>(residual);
+  a.out = static_cast<uint16_t*>(out);
+  a.rows = rows, a.cols = cols, a.ld = ld, a.ld_out = ld_out;
+  a.col_tiles = static_cast<uint32_t>(col_tiles);
+  a.drop = drop_of(*params);
+  a.set_bounds(kX, x, rows, cols, ld, 2);
+  a.set_bounds(kResidual, residual, rows, cols, ld_out, 2);
+  a.set_bounds(kOut, out, rows, cols, ld_out, 2);
+  const bool grid = on_grid(x, ld) && on_grid(out, ld_out) && aligned(residual, 16);
+  const auto fn = dtype == ZERO_BF16 ? (grid ? dropout_kernel<true, true> : dropout_kernel<true, false>)
+                                     : (grid ? dropout_kernel<false, true> : dropout_kernel<false, false>);
+  return status_of(launch_pdl(fn, dim3(static_cast<unsigned>(ceil_div(rows * col_tiles, kWarps))),
+                              dim3(kThreads), 0, static_cast<cudaStream_t>(stream), a));
+}

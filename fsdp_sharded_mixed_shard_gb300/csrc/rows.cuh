@@ -47,6 +47,14 @@ __device__ __forceinline__ void store_row(uint8_t* stage, uint16_t* row, int64_t
   }
 }
 
+// Two 16-bit magnitudes at once: as integers they are ordered like the values,
+// infinity and NaN above all numbers.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // whether every row start of a [.., ld] array of 16-bit elements lies on the
 // 16-byte grid
 inline bool on_grid(const void* p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }

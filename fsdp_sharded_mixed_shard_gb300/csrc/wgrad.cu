@@ -306,54 +306,6 @@ __device__ __forceinline__ void place(uint8_t* stage_b, const Pieces& p, int r, 
     *reinterpret_cast<uint4*>(to + (k & 1) * (4 * 1024) + (k >> 1) * kChunk) = p.v[k];
 }
 
-// An output warp's 32 columns of its lanes' rows, in the 16-bit type.
-template <bool kBf16>
-__device__ __forceinline__ void narrow32(const float (&f)[32], uint4 (&v)[4]) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    v[k] = make_uint4(
-        narrow2<kBf16>(f[8 * k], f[8 * k + 1]), narrow2<kBf16>(f[8 * k + 2], f[8 * k + 3]),
-        narrow2<kBf16>(f[8 * k + 4], f[8 * k + 5]), narrow2<kBf16>(f[8 * k + 6], f[8 * k + 7]));
-}
-
-// Rows of dw off the 16-byte grid leave through shared memory, kOutCols columns
-// of 32 rows at a time and eight lanes per row, in the whole blocks of their
-// addresses (a lane storing its own row element by element wrote every 32-byte
-// sector 16 times). A block may begin in the columns before: each row's stage
-// starts with its last eight of those. Only the elements before a tile's first
-// block and after its last go one by one.
-constexpr int kOutCols = 64, kOutPitch = 16 + kOutCols * 2;
-
-// columns [c, c + width) of the tile's row that starts at `to`, which has
-// `count` columns
-__device__ __forceinline__ void store_staged(uint8_t* stage, uint16_t* to, int64_t n, int64_t rows,
-                                             int c, int width, int count, int lane,
-                                             const Bounds& in) {
-  const int k = lane & 7, row0 = lane >> 3;
-  const int end = c + width < count ? c + width : count;  // columns there are so far
-#pragma unroll 1
-  for (int pass = 0; pass < 8; ++pass) {
-    const int row = pass * 4 + row0;
-    if (row >= rows) continue;
-    uint16_t* at = to + row * n;
-    const int d = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15);
-    const uint4* block = reinterpret_cast<const uint4*>(stage + row * kOutPitch + 16) + k;
-    const int begin = 2 * c + 16 * k - d;  // byte of the row the block starts at
-    uint8_t* whole = reinterpret_cast<uint8_t*>(at) + begin;
-    if (begin >= 0 && begin + 16 <= 2 * end && in.holds(whole, 16, kSiteStore))
-      *reinterpret_cast<uint4*>(whole) = shifted_back(block[-1], block[0], d);
-    if (c == 0 || end == count) {
-      const uint16_t* elems = reinterpret_cast<const uint16_t*>(stage + row * kOutPitch + 16);
-      const int head = d ? min((16 - d) >> 1, end) : 0;
-      if (c == 0 && k < head && in.holds(at + k, 2, kSiteStore)) at[k] = elems[k];
-      // elements of the block that no later columns complete
-      const int tail = max(c == 0 ? head : 0, (((2 * end + d) & ~15) - d) >> 1);
-      if (end == count && tail + k < end && in.holds(at + tail + k, 2, kSiteStore))
-        at[tail + k] = elems[tail + k - c];
-    }
-  }
-}
-
 // ------------------------------------------------------------------ kernel ----
 
 // A step of this pair's work: token block `step` of tile `tile`.
@@ -364,19 +316,6 @@ struct Cursor {
     while (step >= steps) {
       step -= steps;
       tile += tile_stride;
-    }
-  }
-};
-
-template <int kStages>
-struct Ring {  // stage and the parity of its current use
-  int32_t stage = 0;
-  uint32_t parity = 0;
-  __device__ __forceinline__ void advance(int by) {
-    stage += by;
-    if (stage >= kStages) {
-      stage -= kStages;
-      parity ^= 1;
     }
   }
 };
