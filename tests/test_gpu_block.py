@@ -498,8 +498,8 @@ def test_fp8_products_of_nothing():
     assert bool((y[:, :33] == 0).all()) and bool((y[:, 33:] == 7).all())
     zero = torch.zeros(5, 300, device="cuda", dtype=torch.bfloat16)
     w = rand((300, 40), "bf16", 1)
-    Z.zero_fp8_linear(at(copy_of(zero, 5, 300, 300, "bf16", "e4m3")), 0, 5,
-                      at(weight_of(w, 300, 40, "bf16")), 300, 40, Z.ZERO_BF16, at(y), 40, 0, stream())
+    x8, w8 = copy_of(zero, 5, 300, 300, "bf16", "e4m3"), weight_of(w, 300, 40, "bf16")
+    Z.zero_fp8_linear(at(x8), 0, 5, at(w8), 300, 40, Z.ZERO_BF16, at(y), 40, 0, stream())
     assert bool((y == 0).all())
 
 
