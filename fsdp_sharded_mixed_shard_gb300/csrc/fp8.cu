@@ -17,11 +17,13 @@
  * its rows (the operand's slow axis), dy W^T over its columns.
  *
  * A pair of CTAs (one tcgen05.mma over two SMs) forms a tile of 256 rows by up
- * to 192 columns, 128 reduction steps at a time: each CTA brings 128 rows of
+ * to 256 columns, 128 reduction steps at a time: each CTA brings 128 rows of
  * the left operand, half of the right one and the scale tiles through a ring of
  * stages. Warps by role: copies, products, four for the output, which read a
- * finished tile while the next one's sums form in the other half of tensor
- * memory (two tiles of 192 columns leave room there for the scales).
+ * finished tile while the next one's sums form elsewhere in tensor memory. Two
+ * tiles of 256 columns and the scales do not fit there, so that two such tiles
+ * share 32 columns: those are read first, and the next tile's products wait for
+ * them alone.
  *
  * Few tiles and a long reduction: a cluster of 2, 4 or 8 pairs shares a tile,
  * each pair a part of the reduction; the sums meet in shared memory and every
@@ -173,20 +175,24 @@ __global__ void __launch_bounds__(256) quant_weight_kernel(const QuantArgs a) {
 
 // ---------------------------------------------------------------- products ----
 
-constexpr int kM = 128, kN = 192, kK = kBlock;  // rows per CTA, columns at most, steps per stage
+constexpr int kM = 128, kN = 256, kK = kBlock;  // rows per CTA, columns at most, steps per stage
 constexpr int kOutWarps = 4;
 constexpr int kCopyWarp = 0, kProductWarp = 1, kOutWarp0 = 2, kWarps = kOutWarp0 + kOutWarps;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBytesA = kM * kK, kBytesB = kK * 128, kScaleTiles = 2;  // of the right operand
 constexpr int kBytesScales = 2048;
 constexpr int kStageBytes = kBytesA + kBytesB + kBytesScales, kStages = 6;
-constexpr int kRing = kStages * kStageBytes, kSmem = kRing + 1024;
+constexpr int kRing = kStages * kStageBytes;
+constexpr int kOutBytes = 5 * 1024;  // an output warp's stage: 32 rows of 64 columns
+constexpr int kSmem = kRing + kOutWarps * kOutBytes + 1024;
 constexpr int kJoinPitch = kN + 4;  // fp32 row of a tile in shared memory
 constexpr int kMaxSplit = 8, kJoinAhead = 4;
-// tensor memory: two tiles' sums, then scales in kScaleSets sets of 16 columns
-// (4 of the left operand, up to 8 of the right one)
-constexpr int kTensorColumns = 512, kScaleColumn = 2 * kN, kScaleSets = 4;
+// tensor memory: two tiles' sums, the second from kSecond on, then scales in two
+// sets of 16 columns (4 of the left operand, up to 8 of the right one)
+constexpr int kTensorColumns = 512, kSecond = 224, kScaleColumn = 480, kScaleSets = 2;
+static_assert(kSecond + kN <= kScaleColumn && kN - kSecond == 32, "the tiles share 32 columns");
 static_assert(kScaleColumn + 16 * kScaleSets <= kTensorColumns, "tensor memory");
+static_assert(32 * kOutPitch <= kOutBytes && 32 * 128 <= kOutBytes, "output stage");
 static_assert((1 + kScaleTiles) * kTileBytes <= kBytesScales && kStageBytes % 1024 == 0, "stages");
 static_assert(kM * kJoinPitch * 4 <= kRing, "the tile fits the stages");
 // costs in cycles: a column put out, the join of a split, clusters of 16 CTAs
@@ -199,21 +205,71 @@ struct Args : Checked<kBuffers> {
   zero_scaler* scaler;
   int64_t rows, n, ld;
   int32_t blocks;  // of the reduction
-  int32_t split, vec_out, bn, m_tiles, tiles, scale_tiles, a_format;
+  int32_t split, tma_out, bn, m_tiles, tiles, scale_tiles, a_format;
 };
 
 struct Maps {
-  CUtensorMap a, b, scale_a, scale_b;
+  CUtensorMap a, b, scale_a, scale_b, out;
 };
 
-// A box of a 3-d map into this CTA, counted by the pair's barrier.
+// What one lane starts (copies, products, commits) is issued by the whole warp
+// with one lane elected in the instruction itself: the operands then are the
+// warp's, in uniform registers. Behind a branch on the lane each operand goes
+// there lane by lane, and the issuing thread, not the tensor core, is the bound
+// (four products of 256 x 192 x 32 and their commit took 413 cycles, 384 so).
+__device__ __forceinline__ void copy_box2(void* dst, const CUtensorMap* map, int32_t x, int32_t y,
+                                          uint32_t cluster_bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2 [%0], [%1, {%2, %3}], [%4];\n}" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(cluster_bar)
+      : "memory");
+}
+
 __device__ __forceinline__ void copy_box3(void* dst, const CUtensorMap* map, int32_t x, int32_t y,
                                           int32_t z, uint32_t cluster_bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];\n}" ::"r"(smem_u32(dst)),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(cluster_bar)
       : "memory");
+}
+
+__device__ __forceinline__ void expect_bytes(uint64_t* bar, uint32_t bytes) {
+  asm volatile(
+      "{\n .reg .pred e;\n .reg .b64 st;\n elect.sync _|e, 0xffffffff;\n"
+      " @e mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n}" ::"r"(smem_u32(bar)),
+      "r"(bytes)
+      : "memory");
+}
+
+// arrive at `bar` of both CTAs of the pair once the products issued so far are done
+__device__ __forceinline__ void commit_pair(uint64_t* bar, uint16_t pair_mask) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
+      ".b64 [%0], %1;\n}" ::"r"(smem_u32(bar)),
+      "h"(pair_mask)
+      : "memory");
+}
+
+// the stage's 32 rows of 64 columns to the output; rows and columns past its
+// ends stay away
+__device__ __forceinline__ void store_box(const CUtensorMap* map, const void* src, int32_t x,
+                                          int32_t y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];\n"
+      "cp.async.bulk.commit_group;" ::"l"(map),
+      "r"(smem_u32(src)), "r"(x), "r"(y)
+      : "memory");
+}
+
+// the warp waits together and has one verdict
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* failed,
+                                          uint64_t limit) {
+  return __all_sync(0xffffffffu, bar_wait(bar, parity, failed, limit));
 }
 
 // Shared-memory operands with 128-byte swizzle: rows of 128 bytes, eight rows
@@ -241,9 +297,10 @@ __device__ __forceinline__ uint32_t product_desc(int a_format, bool slow, int bn
 __device__ __forceinline__ void product(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t desc,
                                         uint32_t scale_a, uint32_t scale_b, uint32_t add) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n"
+      "{\n .reg .pred p, e;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n"
+      " elect.sync _|e, 0xffffffff;\n"
       " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
-      " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], da, db, %3, [%6], "
+      " @e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], da, db, %3, [%6], "
       "[%7], p;\n}" ::"r"(d),
       "r"(a_low), "r"(b_low), "r"(desc), "r"(add), "r"(kOperandHigh), "r"(scale_a), "r"(scale_b)
       : "memory");
@@ -252,8 +309,8 @@ __device__ __forceinline__ void product(uint32_t d, uint32_t a_low, uint32_t b_l
 // a scale tile of each CTA of the pair into its tensor memory, all four quarters
 __device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t low) {
   asm volatile(
-      "{\n .reg .b64 s;\n mov.b64 s, {%1, %2};\n"
-      " tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], s;\n}" ::"r"(tmem),
+      "{\n .reg .pred e;\n .reg .b64 s;\n elect.sync _|e, 0xffffffff;\n mov.b64 s, {%1, %2};\n"
+      " @e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], s;\n}" ::"r"(tmem),
       "r"(low), "r"(kScaleHigh)
       : "memory");
 }
@@ -265,11 +322,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t raw[];
   uint8_t* stages = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   // full: in the pair's first CTA, counted by both; empty and done: in each
-  __shared__ uint64_t full[kStages], empty[kStages], done[2], free_sums[2];
+  __shared__ uint64_t full[kStages], empty[kStages], done[2], freed[2];
   __shared__ uint32_t tmem_base;
   __shared__ int failed;
-  __shared__ __align__(16) uint8_t out_stage[kOutWarps][32 * kOutPitch];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the warp's, not the lane's
   const uint64_t limit = a.limit();
   const int n_cta = 2 * a.split;
   const int rank = static_cast<int>(blockIdx.x) % n_cta;
@@ -284,6 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return static_cast<int64_t>(tile % a.m_tiles) * (2 * kM) + half * kM;
   };
   const auto column_of = [&](int tile) { return static_cast<int64_t>(tile / a.m_tiles) * a.bn; };
+  const bool shared_columns = a.bn > kSecond;
 
   if (warp == kProductWarp) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -299,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int k = 0; k < 2; ++k) {
       bar_init(&done[k], 1);
-      bar_init(&free_sums[k], 2 * kOutWarps);
+      bar_init(&freed[k], 2 * kOutWarps);
     }
     failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -314,48 +372,46 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_begin();
 
   if (warp == kCopyWarp) {
-    if (lane == 0) {
-      const uint32_t full_at = in_cta(full, leader);
-      const int b_rows = kSlow ? kK : a.bn / 2;
-      const uint32_t bytes = 2 * (kBytesA + b_rows * 128);
-      const uint32_t scale_bytes = 2 * (1 + a.scale_tiles) * kTileBytes;
-      Ring<kStages> ring;
-      bool ok = true;
-      int left_fresh = kStages;
-      for (int k = 0; k < my_tiles && ok; ++k) {
-        const int tile = tile0 + k * tile_stride;
-        const int32_t i = static_cast<int32_t>(row_of(tile));
-        const int32_t j = static_cast<int32_t>(column_of(tile));
-        const int32_t jb = j + half * (a.bn / 2);
-        for (int b = s0; b < s1; ++b) {
-          const int s = ring.stage;
-          if (left_fresh > 0) --left_fresh;
-          else if (!bar_wait(&empty[s], ring.parity ^ 1, &failed, limit)) {
-            ok = false;
-            break;
-          }
-          if (blockIdx.x == 0 &&
-              a.holds(ZERO_PLANT_NO_COPY, static_cast<int64_t>(k) * (s1 - s0) + b - s0)) {
-            ring.advance(1);
-            continue;
-          }
-          uint8_t* to = stages + s * kStageBytes;
-          const bool scales = b == s0 || b % 4 == 0;
-          if (half == 0) bar_expect(&full[s], bytes + (scales ? scale_bytes : 0));
-          const uint32_t bar = full_at + s * 8;
-          copy_box(to, &maps.a, b * kK, i, bar);
-          if (kSlow) copy_box(to + kBytesA, &maps.b, jb, b * kK, bar);
-          else copy_box(to + kBytesA, &maps.b, b * kK, jb, bar);
-          if (scales) {
-            copy_box3(to + kBytesA + kBytesB, &maps.scale_a, 0, b / 4, i / 128, bar);
-            copy_box3(to + kBytesA + kBytesB + kTileBytes, &maps.scale_b, 0, b / 4, j / 128, bar);
-          }
-          ring.advance(1);
+    const uint32_t full_at = in_cta(full, leader);
+    const int b_rows = kSlow ? kK : a.bn / 2;
+    const uint32_t bytes = 2 * (kBytesA + b_rows * 128);
+    const uint32_t scale_bytes = 2 * (1 + a.scale_tiles) * kTileBytes;
+    Ring<kStages> ring;
+    bool ok = true;
+    int left_fresh = kStages;
+    for (int k = 0; k < my_tiles && ok; ++k) {
+      const int tile = tile0 + k * tile_stride;
+      const int32_t i = static_cast<int32_t>(row_of(tile));
+      const int32_t j = static_cast<int32_t>(column_of(tile));
+      const int32_t jb = j + half * (a.bn / 2);
+      for (int b = s0; b < s1; ++b) {
+        const int s = ring.stage;
+        if (left_fresh > 0) --left_fresh;
+        else if (!warp_wait(&empty[s], ring.parity ^ 1, &failed, limit)) {
+          ok = false;
+          break;
         }
+        if (blockIdx.x == 0 &&
+            a.holds(ZERO_PLANT_NO_COPY, static_cast<int64_t>(k) * (s1 - s0) + b - s0)) {
+          ring.advance(1);
+          continue;
+        }
+        uint8_t* to = stages + s * kStageBytes;
+        const bool scales = b == s0 || b % 4 == 0;
+        if (half == 0) expect_bytes(&full[s], bytes + (scales ? scale_bytes : 0));
+        const uint32_t bar = full_at + s * 8;
+        copy_box2(to, &maps.a, b * kK, i, bar);
+        if (kSlow) copy_box2(to + kBytesA, &maps.b, jb, b * kK, bar);
+        else copy_box2(to + kBytesA, &maps.b, b * kK, jb, bar);
+        if (scales) {
+          copy_box3(to + kBytesA + kBytesB, &maps.scale_a, 0, b / 4, i / 128, bar);
+          copy_box3(to + kBytesA + kBytesB + kTileBytes, &maps.scale_b, 0, b / 4, j / 128, bar);
+        }
+        ring.advance(1);
       }
     }
   } else if (warp == kProductWarp) {
-    if (half == 0 && lane == 0) {
+    if (half == 0) {
       const uint16_t pair_mask = static_cast<uint16_t>(3u << leader);
       const uint32_t desc = product_desc(a.a_format, kSlow, a.bn);
       const uint32_t at0 = smem_u32(stages);
@@ -364,17 +420,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       uint32_t set = 0;
       for (int k = 0; k < my_tiles && ok && s1 > s0; ++k) {
-        const int buf = k & 1, use = k >> 1;
-        const uint32_t sums = tmem + buf * kN;
+        const int buf = k & 1;
+        const uint32_t sums = tmem + buf * kSecond;
         // where in its scale tile the first column's scales are: a tensor memory
         // column per 32 of them
         const uint32_t shift =
             static_cast<uint32_t>(column_of(tile0 + k * tile_stride) % 128) / 32;
-        ok = use == 0 || bar_wait(&free_sums[buf], (use - 1) & 1, &failed, limit);
+        // the tile before the last one is read whole or, where it is not in the
+        // way, the last one's shared columns are (and with them all of that)
+        const int after = k - (shared_columns ? 1 : 2);
+        ok = after < 0 || warp_wait(&freed[after & 1], (after >> 1) & 1, &failed, limit);
         uint32_t scales = 0;
         for (int b = s0; b < s1 && ok; ++b) {
           const int s = ring.stage;
-          ok = bar_wait(&full[s], ring.parity, &failed, limit);
+          ok = warp_wait(&full[s], ring.parity, &failed, limit);
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           const uint32_t at = at0 + s * kStageBytes;
@@ -391,85 +450,83 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q = 0; q < kK / 32; ++q)
             product(sums, low_a + q * kNextA, low_b + q * kNextB, desc | id << 4 | id << 29, scales,
                     scales + 4 + shift, q > 0 || b > s0 ? 1u : 0u);
-          commit(&empty[s], pair_mask);
+          commit_pair(&empty[s], pair_mask);
           ring.advance(1);
         }
-        if (ok) commit(&done[buf], pair_mask);  // whole sums only
+        if (ok) commit_pair(&done[buf], pair_mask);  // whole sums only
       }
     }
   } else {
     // this warp's quarter of tensor memory's lanes
     const int row0 = (warp & 3) * 32;
+    uint8_t* stage = stages + kRing + (warp - kOutWarp0) * kOutBytes;
+    const int chunks = a.bn / kOutCols;
     bool ok = true;
     for (int k = 0; k < my_tiles; ++k) {
       const int tile = tile0 + k * tile_stride;
       const int buf = k & 1, use = k >> 1;
-      // the warp's verdict: its lanes read tensor memory together
-      if (s1 > s0 && ok)
-        ok = __all_sync(0xffffffffu, bar_wait(&done[buf], use & 1, &failed, limit));
+      if (s1 > s0 && ok) ok = warp_wait(&done[buf], use & 1, &failed, limit);
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint32_t sums = tmem + (static_cast<uint32_t>(row0) << 16) + buf * kN;
+      const uint32_t sums = tmem + (static_cast<uint32_t>(row0) << 16) + buf * kSecond;
       const int64_t i0 = row_of(tile) + row0, j = column_of(tile);
+      // given up: the sums stay taken, others may still read theirs
+      const auto free_sums = [&]() {
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (ok && lane == 0) bar_arrive_at(in_cta(&freed[buf], leader));
+      };
       uint4 last = make_uint4(0, 0, 0, 0);  // the eight columns before, of this lane's row
 #pragma unroll 1
-      for (int c = 0; c < a.bn; c += 32) {
-        float f[32];
+      for (int m = 0; m < chunks; ++m) {
+        // the first tile's shared columns are its last ones
+        const int c = (!shared_columns || buf ? m : (m ? m - 1 : chunks - 1)) * kOutCols;
+        float f[2][32];
         if (ok && s1 > s0) {
-          read_sums(sums + c, f);
+          read_sums(sums + c, f[0]);
+          read_sums(sums + c + 32, f[1]);
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) f[e] = ok ? 0.f : __uint_as_float(0x7FC00000u);
+          for (int e = 0; e < 32; ++e) f[0][e] = f[1][e] = ok ? 0.f : __uint_as_float(0x7FC00000u);
         }
-        if (a.split == 1) {
-          uint4 v[4];
-          narrow32<kBf16>(f, v);
-          uint16_t* to = a.out + i0 * a.ld + j;  // the tile's columns of this warp's first row
-          if (a.vec_out) {
-            uint16_t* row = to + lane * a.ld + c;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int64_t left = a.n - (j + c + 8 * e);
-              if (i0 + lane >= a.rows || left <= 0 ||
-                  !a.bounds(kOut).holds(row + 8 * e, left < 8 ? 2 * left : 16, kSiteStore))
-                continue;
-              if (left >= 8) {
-                *reinterpret_cast<uint4*>(row + 8 * e) = v[e];
-              } else {
-                const uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                  if (q < left) row[8 * e + q] = static_cast<uint16_t>(w[q >> 1] >> (16 * (q & 1)));
-              }
-            }
-          } else if (j + (c & ~(kOutCols - 1)) < a.n) {
-            uint8_t* stage = out_stage[warp - kOutWarp0];
-            uint4* row = reinterpret_cast<uint4*>(stage + lane * kOutPitch);
-            const int within = c & (kOutCols - 1);
-            const int count = static_cast<int>(min(a.n - j, static_cast<int64_t>(a.bn)));
-            if (within == 0) row[0] = last;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) row[1 + within / 8 + e] = v[e];
-            last = v[3];
-            if (within || c + 32 == a.bn) {
-              __syncwarp();
-              store_staged(stage, to, a.ld, a.rows - i0, c - within, within + 32, count, lane,
-                           a.bounds(kOut));
-              __syncwarp();
-            }
-          }
-        } else {
+        if (m == (shared_columns ? 0 : chunks - 1)) free_sums();
+        if (a.split > 1) {
           float4* p = reinterpret_cast<float4*>(
               reinterpret_cast<float*>(stages) + (row0 + lane) * kJoinPitch + c);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            p[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+          for (int e = 0; e < 16; ++e)
+            p[e] = make_float4(f[e / 8][4 * e % 32], f[e / 8][4 * e % 32 + 1],
+                               f[e / 8][4 * e % 32 + 2], f[e / 8][4 * e % 32 + 3]);
+          continue;
+        }
+        uint4 v[2][4];
+        narrow32<kBf16>(f[0], v[0]);
+        narrow32<kBf16>(f[1], v[1]);
+        if (a.tma_out) {
+          // the store before has read the stage
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
+          uint4* row = reinterpret_cast<uint4*>(stage + lane * 128);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) row[e ^ (lane & 7)] = v[e / 4][e % 4];
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0 && i0 < a.rows && j + c < a.n)
+            store_box(&maps.out, stage, static_cast<int32_t>(j + c), static_cast<int32_t>(i0));
+        } else if (j + c < a.n) {
+          uint16_t* to = a.out + i0 * a.ld + j;  // the tile's columns of this warp's first row
+          uint4* row = reinterpret_cast<uint4*>(stage + lane * kOutPitch);
+          const int count = static_cast<int>(min(a.n - j, static_cast<int64_t>(a.bn)));
+          row[0] = last;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) row[1 + e] = v[e / 4][e % 4];
+          last = v[1][3];
+          __syncwarp();
+          store_staged(stage, to, a.ld, a.rows - i0, c, kOutCols, count, lane, a.bounds(kOut));
+          __syncwarp();
         }
       }
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      __syncwarp();
-      // given up: the sums stay taken, others may still read theirs
-      if (ok && lane == 0) bar_arrive_at(in_cta(&free_sums[buf], leader));
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   __syncthreads();
   cluster_sync();
@@ -487,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int share = kM / a.split;
     const int64_t j = column_of(tile0);
     // the output warps' stages as one, a row's worth for each warp
-    uint8_t* stage = &out_stage[0][0] + warp * ((kStageWarp + 15) & ~15);
+    uint8_t* stage = stages + kRing + warp * ((kStageWarp + 15) & ~15);
     for (int m = warp; m < share; m += kWarps) {
       // rows dealt out in turn, so that a short tile's are shared too
       const int row = m * a.split + part;
@@ -560,6 +617,18 @@ bool encode_scales(CUtensorMap* map, const uint8_t* base, int64_t row_tiles, int
   return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t*>(base), dims,
                           strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A map of the output, a warp's 32 rows of 64 columns to a box.
+bool encode_out(CUtensorMap* map, void* base, int64_t n, int64_t rows, int64_t ld) {
+  const EncodeTiled encode = encode_tiled();
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[2] = {kOutCols, 32}, unit[2] = {1, 1};
+  return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, base, dims, strides, box, unit,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_NONE,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -640,7 +709,8 @@ int multiply(const void* copy, int32_t format, int64_t rows, const void* w_copy,
   a.rows = rows, a.n = n, a.ld = ld;
   a.blocks = static_cast<int32_t>(blocks_of(k));
   a.a_format = format;
-  a.vec_out = ld % kVec == 0 && aligned(out, 16);
+  // TMA stores whole 16-byte blocks on their grid, row distances below 2^40 bytes
+  a.tma_out = n % kVec == 0 && ld % kVec == 0 && aligned(out, 16) && ld < int64_t{1} << 39;
   a.set_bounds(kOut, out, rows, n, ld, 2);
   int fit[kMaxSplit + 1];
   for (int split = 1; split <= kMaxSplit; split *= 2) fit[split] = resident_clusters(split);
@@ -650,7 +720,9 @@ int multiply(const void* copy, int32_t format, int64_t rows, const void* w_copy,
   // pairs times blocks of 2 cycles per column, a tile put out alone at the end,
   // and the join of a split, which needs room for all its clusters at once.
   int64_t best = 0;
-  for (int bn = kN; bn >= 128; bn -= 64)
+  // Off the grid the columns leave in order, which two tiles that share some
+  // do not.
+  for (int bn = a.tma_out ? kN : kN - 64; bn >= 128; bn -= 64)
     for (int split = 1; split <= kMaxSplit; split *= 2) {
       const int64_t all = m_tiles * ceil_div(n, bn), turns = ceil_div(all, pairs);
       if (split > 1 && (all > fit[split] || a.blocks < 2 * split)) break;
@@ -668,7 +740,7 @@ int multiply(const void* copy, int32_t format, int64_t rows, const void* w_copy,
   a.m_tiles = static_cast<int32_t>(m_tiles);
   a.tiles = static_cast<int32_t>(tiles);
   // row tiles of scales that a tile's columns may touch
-  a.scale_tiles = a.bn == 128 ? 1 : 2;
+  a.scale_tiles = ceil_div(a.bn, 128);
   const int clusters = static_cast<int>(std::min(tiles, a.split > 1 ? tiles : pairs));
   const int64_t pitch = blocks_of(k) * kBlock, w_pitch = blocks_of(w_cols) * kBlock;
   const uint8_t *left = static_cast<const uint8_t*>(copy),
@@ -679,7 +751,8 @@ int multiply(const void* copy, int32_t format, int64_t rows, const void* w_copy,
   if (!encode_bytes(&maps.a, left, pitch, rows, kM) ||
       !encode_bytes(&maps.b, right, w_pitch, w_rows, kSlow ? kK : a.bn / 2) ||
       !encode_scales(&maps.scale_a, left + rows * pitch, blocks_of(rows), groups_of(k), 1) ||
-      !encode_scales(&maps.scale_b, scales, blocks_of(n), groups_of(k), a.scale_tiles))
+      !encode_scales(&maps.scale_b, scales, blocks_of(n), groups_of(k), a.scale_tiles) ||
+      (a.tma_out && !encode_out(&maps.out, out, n, rows, ld)))
     return ZERO_ECUDA;
   return dtype == ZERO_BF16 ? launch<true, kSlow>(maps, a, clusters, st)
                             : launch<false, kSlow>(maps, a, clusters, st);
