@@ -195,7 +195,11 @@ static_assert(kScaleColumn + 16 * kScaleSets <= kTensorColumns, "tensor memory")
 static_assert(32 * kOutPitch <= kOutBytes && 32 * 128 <= kOutBytes, "output stage");
 static_assert((1 + kScaleTiles) * kTileBytes <= kBytesScales && kStageBytes % 1024 == 0, "stages");
 static_assert(kM * kJoinPitch * 4 <= kRing, "the tile fits the stages");
-// costs in cycles: a column put out, the join of a split, clusters of 16 CTAs
+// costs in cycles: a block, and its thirds per column (128, 192 and 256 columns
+// took 484, 595 to 625 and 661 to 717 at 8192 x 2048 x 8192 and 8192^3, most of
+// it waiting for the copies); a column put out, the join of a split, clusters of
+// 16 CTAs
+constexpr int kBlockCycles = 340, kColumnThirds = 4;
 constexpr int kOutCycles = 28, kJoinCycles = 3500, kBigClusterCycles = 4000;
 
 enum { kOut, kBuffers };
@@ -475,7 +479,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (ok && lane == 0) bar_arrive_at(in_cta(&freed[buf], leader));
       };
-      uint4 last = make_uint4(0, 0, 0, 0);  // the eight columns before, of this lane's row
 #pragma unroll 1
       for (int m = 0; m < chunks; ++m) {
         // the first tile's shared columns are its last ones
@@ -488,6 +491,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) f[0][e] = f[1][e] = ok ? 0.f : __uint_as_float(0x7FC00000u);
         }
+        // the eight columns before, for stores off the grid
+        float before[8] = {f[0][0], f[0][0], f[0][0], f[0][0], f[0][0], f[0][0], f[0][0], f[0][0]};
+        if (!a.tma_out && a.split == 1 && c && ok) read_eight(sums + c - 8, before);
         if (m == (shared_columns ? 0 : chunks - 1)) free_sums();
         if (a.split > 1) {
           float4* p = reinterpret_cast<float4*>(
@@ -516,10 +522,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint16_t* to = a.out + i0 * a.ld + j;  // the tile's columns of this warp's first row
           uint4* row = reinterpret_cast<uint4*>(stage + lane * kOutPitch);
           const int count = static_cast<int>(min(a.n - j, static_cast<int64_t>(a.bn)));
-          row[0] = last;
+          row[0] = narrow8<kBf16>(before);
 #pragma unroll
           for (int e = 0; e < 8; ++e) row[1 + e] = v[e / 4][e % 4];
-          last = v[1][3];
           __syncwarp();
           store_staged(stage, to, a.ld, a.rows - i0, c, kOutCols, count, lane, a.bounds(kOut));
           __syncwarp();
@@ -717,16 +722,15 @@ int multiply(const void* copy, int32_t format, int64_t rows, const void* w_copy,
   if (fit[1] <= 0) return ZERO_ECUDA;
   const int64_t pairs = fit[1], m_tiles = ceil_div(rows, 2 * kM);
   // Tile width and split of the reduction by the cycles they take: turns of all
-  // pairs times blocks of 2 cycles per column, a tile put out alone at the end,
-  // and the join of a split, which needs room for all its clusters at once.
+  // pairs times their blocks, a tile put out alone at the end, and the join of a
+  // split, which needs room for all its clusters at once.
   int64_t best = 0;
-  // Off the grid the columns leave in order, which two tiles that share some
-  // do not.
-  for (int bn = a.tma_out ? kN : kN - 64; bn >= 128; bn -= 64)
+  for (int bn = kN; bn >= 128; bn -= 64)
     for (int split = 1; split <= kMaxSplit; split *= 2) {
       const int64_t all = m_tiles * ceil_div(n, bn), turns = ceil_div(all, pairs);
       if (split > 1 && (all > fit[split] || a.blocks < 2 * split)) break;
-      const int64_t cost = turns * ceil_div(a.blocks, split) * (2 * bn) + kOutCycles * bn +
+      const int64_t cost = turns * ceil_div(a.blocks, split) *
+                               (kBlockCycles + kColumnThirds * bn / 3) + kOutCycles * bn +
                            (split > 1 ? kJoinCycles : 0) +
                            (split == kMaxSplit ? kBigClusterCycles : 0);
       if (best == 0 || cost < best) {

@@ -120,6 +120,20 @@ __device__ __forceinline__ void read_sums(uint32_t addr, float (&f)[32]) {
   for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(r[j]);
 }
 
+// 32 lanes x 8 columns of tensor memory
+__device__ __forceinline__ void read_eight(uint32_t addr, float (&f)[8]) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(addr)
+      : "memory");
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(r[j]);
+}
+
 __device__ __forceinline__ void cluster_sync() {
   __syncwarp();
   asm volatile(
