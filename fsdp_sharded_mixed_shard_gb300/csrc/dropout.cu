@@ -1,8 +1,9 @@
 /*
  * dropout.cu -- dropout whose mask is never stored (zero_block.h).
  *
- * A thread takes 8 neighbouring elements of a row, which share one draw of the
- * generator (draws.cuh); a warp 256 columns, running on into the next row.
+ * A thread takes two times 8 neighbouring elements of a row, 8 of which share
+ * one draw of the generator (draws.cuh); a warp 512 columns, the warps of a CTA
+ * running on into the next row.
  */
 #include "draws.cuh"
 #include "rows.cuh"
@@ -15,6 +16,7 @@ using namespace zt;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kPieces = 2;
 
 enum { kX, kResidual, kOut, kBuffers };  // a call's buffers, for their bounds
 
@@ -36,22 +38,33 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const Args a) {
   const uint32_t row = tile / a.col_tiles;
   const int64_t r = row;
   if (r >= a.rows) return;
-  const int64_t c0 = static_cast<int64_t>(tile - row * a.col_tiles) * kCols, c = c0 + lane * kVec;
-  const uint4 vx = load8<kGrid>(a.x + r * a.ld, c, a.cols, a.bounds(kX));
-  uint4 vr = make_uint4(0, 0, 0, 0);
-  if (a.residual)
-    vr = load8<kGrid>(a.residual + r * a.ld_out, c, a.cols, a.bounds(kResidual));
-  float x[8], s[8];
-  widen8<kBf16>(vx, x);
-  if (a.drop.threshold)
-    drop8(a.drop, draw8(a.drop, step_of(a.drop), row, static_cast<uint32_t>(c >> 3)), x);
-  if (a.residual) {
-    widen8<kBf16>(vr, s);
+  const int64_t c0 = static_cast<int64_t>(tile - row * a.col_tiles) * (kPieces * kCols);
+  const uint32_t step = step_of(a.drop);
+  uint4 vx[kPieces], vr[kPieces];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] += s[j];
+  for (int k = 0; k < kPieces; ++k) {
+    const int64_t c = c0 + k * kCols + lane * kVec;
+    vx[k] = load8<kGrid>(a.x + r * a.ld, c, a.cols, a.bounds(kX));
+    vr[k] = make_uint4(0, 0, 0, 0);
+    if (a.residual)
+      vr[k] = load8<kGrid>(a.residual + r * a.ld_out, c, a.cols, a.bounds(kResidual));
   }
-  store_row<kGrid>(stage, a.out + r * a.ld_out, c0, lane, a.cols, narrow8<kBf16>(x),
-                   a.bounds(kOut));
+#pragma unroll
+  for (int k = 0; k < kPieces; ++k) {
+    const int64_t c = c0 + k * kCols;
+    if (c >= a.cols) break;
+    float x[8], s[8];
+    widen8<kBf16>(vx[k], x);
+    if (a.drop.threshold)
+      drop8(a.drop, draw8(a.drop, step, row, static_cast<uint32_t>(c >> 3) + lane), x);
+    if (a.residual) {
+      widen8<kBf16>(vr[k], s);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] += s[j];
+    }
+    store_row<kGrid>(stage, a.out + r * a.ld_out, c, lane, a.cols, narrow8<kBf16>(x),
+                     a.bounds(kOut));
+  }
 }
 
 }  // namespace zd
@@ -70,8 +83,8 @@ extern "C" ZERO_API int zero_dropout(const zero_dropout_params* params, const vo
     return ZERO_EINVAL;
   if (const int bad = check_drop(*params)) return bad;
   constexpr int64_t kMost = int64_t{1} << 31;
-  const int64_t col_tiles = ceil_div(std::min(cols, kMost), kCols);
-  if (rows >= kMost || cols >= kMost || rows * col_tiles >= kMost) return ZERO_ERANGE;
+  if (rows >= kMost || cols >= kMost || rows * ceil_div(cols, kCols) >= kMost) return ZERO_ERANGE;
+  const int64_t col_tiles = ceil_div(cols, kPieces * kCols);
   if (rows == 0 || cols == 0) return ZERO_OK;
   if (!x || !out || (x == out && ld != ld_out)) return ZERO_EINVAL;
   if (!aligned(x, 2) || !aligned(residual, 2) || !aligned(out, 2)) return ZERO_EALIGN;

@@ -138,7 +138,13 @@ class Join64:
         e = self.s * self.keep * d
         ee = (self.s * self.keep).abs() * ed + 2.0 ** -21 * e.abs()
         if w["gate"] is not None:
-            out["gate"] = self.sums(e * n, ee * n.abs() + e.abs() * en)
+            # summed as w_post sum e xhat + b_post sum e, whose terms may cancel
+            # in n: the sums' error is that of both
+            parts = n.abs()
+            if post is not None:
+                parts = (post[0] * w["w_post"]).abs()
+                parts = parts + (w["b_post"].abs() if w["b_post"] is not None else 0.0)
+            out["gate"] = self.sums(e * n, ee * parts + e.abs() * (en + ROWS * parts))
             e, ee = e * w["gate"], ee * w["gate"].abs() + 2.0 ** -23 * (e * w["gate"]).abs()
         if post is not None:
             xhat, _, r, ex = post

@@ -100,7 +100,7 @@ def test_join_grad():
     w = Z.zero_block_join_workspace_bytes
     assert w(0, 100) == 0 and w(-1, 100) == 0 and w(5, -1) == 0
     assert w(5, Z.ZERO_MAX_JOIN_COLS + 1) == 0 and w(1 << 31, 8) == 0
-    assert w(1, 1) == 5 * 8 * 4 and w(1 << 30, 768) == 152 * 5 * 768 * 4
+    assert w(1, 1) == 4 * 8 * 4 and w(1 << 30, 768) == 152 * 4 * 768 * 4
 
 
 def test_fp8_sizes():
