@@ -55,6 +55,18 @@ __device__ __forceinline__ void drop8(const Drop& d, const uint4& draw, float (&
   }
 }
 
+// Which of the eight stay, a bit each.
+__device__ __forceinline__ uint32_t keep8(const Drop& d, const uint4& draw) {
+  const uint32_t w[4] = {draw.x, draw.y, draw.z, draw.w};
+  uint32_t keep = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    keep |= (w[j] << 16) >= d.threshold ? 1u << (2 * j) : 0;
+    keep |= w[j] >= d.threshold ? 2u << (2 * j) : 0;
+  }
+  return keep;
+}
+
 // 0 <= p < 1, aligned pointers
 inline int check_drop(const zero_dropout_params& p) {
   if (!(p.p >= 0.0 && p.p < 1.0)) return ZERO_EINVAL;

@@ -2,25 +2,32 @@
  * join.cu -- where a block's output joins the residual stream: norms after the
  * block and before the next, gate, dropout and residual scale (zero_block.h).
  *
- * A team of warps holds a row in registers, eight neighbouring columns per
- * thread (two times eight past 4096 columns), from the load to the last store:
+ * A team of warps holds a row in registers from the load to the last store:
  * forward 8 bytes per element, backward 12, and nothing is read twice. What a
- * norm needs of the whole row (a sum of squares; with ZERO_NORM_LAYER the mean
- * before it, from which the squares are then taken) goes through shuffles and,
- * past 256 columns, one exchange between the team's warps. Each team works
- * through rows of its own with the next row's loads under way.
+ * norm needs of the whole row goes through shuffles and, where the team has
+ * several warps, one exchange between them. These and a row's addresses cost
+ * about as many instructions as a vector of eight elements does, so a thread
+ * takes as many vectors as its registers hold beside the next row's loads: four
+ * forward, two backward. (With one vector per thread the forward pass
+ * was bound by instructions: 8192 x 2048 bf16 31 us, 360 instructions per 256
+ * elements.)
  *
  * With m the dropout's factor (0 or its scale), c = branch_scale gate w_post and
  * d = branch_scale gate b_post, the forward pass is
  *   h_out = stream_scale h + m (c y^ + d)
- * and the backward pass needs, of each column, only
- *   P = sum dz h^,  Q = sum dz,  A = sum m D y^,  B = sum m D   over the rows:
+ * and the backward pass, with g = dz w_pre, E = dh_out + r g and k = c m,
+ *   D = E - r (c1 h^ + c2),  c1 = mean(g h^),  c2 = mean(g)
+ *   dy = r' (k D - y^ mean(k D y^) - mean(k D)),
+ * (the means without a square belong to ZERO_NORM_LAYER alone), where
+ *   mean(k D y^) = mean(k y^ E) - r (c1 mean(k y^ h^) + c2 mean(k y^)),
+ * and mean(k D) likewise: all of a row's sums are taken in one go, before D is
+ * known. Of each column it needs, over the rows,
+ *   P = sum dz h^,  Q = sum dz,  A = sum m D y^,  B = sum m D:
  *   dw_pre = P, db_pre = Q, dw_post = branch_scale gate A,
  *   db_post = branch_scale gate B, dgate = branch_scale (w_post A + b_post B).
- * c, d and these sums are kept per thread, in fp32 registers (in shared memory
- * past 4096 columns). A CTA joins its teams' sums in order and leaves one vector
- * each in the workspace; a second kernel adds the (at most kMaxParts) vectors in
- * order.
+ * A thread adds those of its own columns up in shared memory. A CTA joins its
+ * teams' in order and leaves one vector each in the workspace; a second kernel
+ * adds the (at most kMaxParts) vectors in order.
  */
 #include "draws.cuh"
 #include "rows.cuh"
@@ -32,19 +39,16 @@ namespace zj {
 
 using namespace zt;
 
-constexpr int kMaxThreads = 512;
+constexpr int kMaxThreads = 512;  // of a CTA, one per SM, 128 registers each
 constexpr int kMaxWarps = kMaxThreads / 32;
-constexpr int kMaxParts = 152;  // CTAs of the backward pass: one per SM
-static_assert(ZERO_MAX_JOIN_COLS == 2 * kMaxThreads * kVec, "two vectors per thread");
-
-// threads per SM of the forward pass: 64 registers each, 96 with the means and
-// biases of ZERO_NORM_LAYER
-template <bool kLayer>
-__device__ __host__ constexpr int resident_threads() { return kLayer ? 640 : 1024; }
+constexpr int kMaxParts = 152;    // CTAs
+// vectors per thread at most
+constexpr int kForwardVectors = 4, kBackVectors = 2;
+static_assert(ZERO_MAX_JOIN_COLS <= kBackVectors * kMaxThreads * kVec, "a row fits a CTA");
 
 enum { kH, kY, kHOut, kZ, kStats, kDz, kDhOut, kDh, kDy, kParts, kBuffers };  // of a call
 enum { kWPost, kBPost, kGate, kWPre, kBPre, kParams };
-enum { kSumP, kSumQ, kSumA, kSumB, kSums };
+enum { kSumP, kSumA, kSumQ, kSumB, kSums };
 
 struct Args : Checked<kBuffers> {
   const uint16_t *h, *y, *h_out, *dz, *dh_out;
@@ -56,7 +60,7 @@ struct Args : Checked<kBuffers> {
   int32_t slots;
   int64_t rows, ld;
   int32_t cols, pitch;   // pitch: cols rounded up to whole vectors
-  int32_t team_warps, teams;
+  int32_t team_warps, teams, slots_of_row;  // vectors that a team has room for
   float eps, inv_cols, stream_scale, branch_scale;
   Drop drop;
 };
@@ -105,58 +109,74 @@ __device__ __forceinline__ uint4 narrow_pairs(const Eight& e) {
   return narrow8<kBf16>(f);
 }
 
-__device__ __forceinline__ void drop_pairs(const Drop& d, const uint4& draw, Eight& e) {
+// Which of a row's eight columns from `col` on stay, a bit each.
+__device__ __forceinline__ uint32_t kept(const Drop& d, uint32_t step, int64_t row, int col) {
+  const uint4 w = draw8(d, step, static_cast<uint32_t>(row), static_cast<uint32_t>(col) / kVec);
+  return keep8(d, w);
+}
+
+__device__ __forceinline__ void drop_pairs(const Drop& d, uint32_t keep, Eight& e) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float a, b;
+    unpair(e.p[j] * both(d.scale), a, b);
+    e.p[j] = pair(keep >> (2 * j) & 1 ? a : 0.f, keep >> (2 * j + 1) & 1 ? b : 0.f);
+  }
+}
+
+// Eight floats in shared memory as two words of 16 bytes, `apart` words apart:
+// neighbouring lanes' words lie side by side.
+__device__ __forceinline__ Eight read_eight_at(const float4* at, int apart) {
+  const float4 x = at[0], y = at[apart];
+  return Eight{{pair(x.x, x.y), pair(x.z, x.w), pair(y.x, y.y), pair(y.z, y.w)}};
+}
+
+__device__ __forceinline__ void write_eight_at(float4* at, int apart, const Eight& e) {
   float f[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) unpair(e.p[j], f[2 * j], f[2 * j + 1]);
-  drop8(d, draw, f);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) e.p[j] = pair(f[2 * j], f[2 * j + 1]);
+  at[0] = make_float4(f[0], f[1], f[2], f[3]);
+  at[apart] = make_float4(f[4], f[5], f[6], f[7]);
 }
 
-// kCount numbers for each of a thread's columns: in registers, or, where it has
-// two vectors, in shared memory (its own words, 16 bytes a lane).
-template <int kV, int kCount>
-struct Columns {
-  Eight r[kCount];
-  __device__ __forceinline__ explicit Columns(float4*) {}
-  __device__ __forceinline__ Eight get(int k, int) const { return r[k]; }
-  __device__ __forceinline__ void set(int k, int, const Eight& e) { r[k] = e; }
-};
+// Where an array's vectors of this row are. kGrid: rows lie on the 16-byte grid
+// and consist of whole vectors.
+template <bool kGrid>
+__device__ __forceinline__ uint4 load_at(const uint16_t* x, int64_t row_start, int col, int cols,
+                                         const Bounds& in) {
+  if constexpr (kGrid) {
+    const uint16_t* at = x + row_start + col;
+    if (col >= cols || !in.holds(at, 16, kSiteLoad)) return make_uint4(0, 0, 0, 0);
+    return __ldcs(reinterpret_cast<const uint4*>(at));
+  } else {
+    return load8<false>(x + row_start, col, cols, in);
+  }
+}
 
-template <int kCount>
-struct Columns<2, kCount> {
-  float4* own;
-  __device__ __forceinline__ explicit Columns(float4* smem) : own(smem + threadIdx.x) {}
-  __device__ __forceinline__ float4* at(int k, int v) const {
-    return own + (k * 2 + v) * 2 * kMaxThreads;
+template <bool kGrid>
+__device__ __forceinline__ void store_at(uint8_t* stage, uint16_t* x, int64_t row_start, int first,
+                                         int lane, int cols, const uint4& v, const Bounds& in) {
+  if constexpr (kGrid) {
+    uint16_t* at = x + row_start + (first + lane * kVec);
+    if (first + lane * kVec < cols && in.holds(at, 16, kSiteStore))
+      __stcs(reinterpret_cast<uint4*>(at), v);
+  } else {
+    store_row<false>(stage, x + row_start, first, lane, cols, v, in);
   }
-  __device__ __forceinline__ Eight get(int k, int v) const {
-    const float4 x = at(k, v)[0], y = at(k, v)[kMaxThreads];
-    return Eight{{pair(x.x, x.y), pair(x.z, x.w), pair(y.x, y.y), pair(y.z, y.w)}};
-  }
-  __device__ __forceinline__ void set(int k, int v, const Eight& e) {
-    float f[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) unpair(e.p[j], f[2 * j], f[2 * j + 1]);
-    at(k, v)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    at(k, v)[kMaxThreads] = make_float4(f[4], f[5], f[6], f[7]);
-  }
-};
-
-template <int kV>
-constexpr int columns_bytes(int count) { return kV == 1 ? 0 : count * 2 * kMaxThreads * kVec * 4; }
+}
 
 // A team's warps' sums, each team's padded with zeros to whole float4. Two sets
 // in turn, so that one barrier each is enough: a warp that writes to one again
 // has passed the other's barrier, before which all have read this one's.
+constexpr int kMaxValues = 8;
 struct Exchange {
-  float4 sums[2][2][8];  // [set][value]
+  float4 sums[2][kMaxValues][8];  // [set][value]
 };
 
-// of every thread of the CTA, before the first sum
+// by every thread of the CTA, which waits for all others, before the first sum
 __device__ __forceinline__ void clear(Exchange& ex) {
-  if (threadIdx.x < 32) (&ex.sums[0][0][0])[threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = threadIdx.x; k < 2 * kMaxValues * 8; k += blockDim.x)
+    (&ex.sums[0][0][0])[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   __syncthreads();
 }
 
@@ -165,9 +185,9 @@ template <int kValues>
 __device__ __forceinline__ void team_sum(const Args& a, const Place& p, Exchange& ex, int& turn,
                                          float (&x)[kValues]) {
 #pragma unroll
-  for (int k = 0; k < kValues; ++k)
+  for (int d = 16; d > 0; d >>= 1)
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x[k] += __shfl_xor_sync(0xffffffffu, x[k], d);
+    for (int k = 0; k < kValues; ++k) x[k] += __shfl_xor_sync(0xffffffffu, x[k], d);
   if (a.team_warps == 1) return;
   const int fours = (a.team_warps + 3) >> 2;
   if (p.lane == 0)
@@ -192,47 +212,46 @@ __device__ __forceinline__ float inverse_root(float mean_square, float eps) {
                                                     : __uint_as_float(0x7FC00000u);
 }
 
-// A row held by the team -> (x - mean) r in place; returns (mean or 0, r).
-// `there`: how many of the thread's columns of each vector are columns.
-template <bool kLayer, int kV>
-__device__ __forceinline__ float2 normalise(const Args& a, const Place& p, Exchange& ex, int& turn,
-                                            Eight (&x)[kV], const int (&there)[kV]) {
+// Statistics (mean or 0, 1 / sqrt(mean square + eps)) of a row held by the team;
+// past the last column it holds zeros. `there`: the thread's columns of each
+// vector that are columns.
+template <bool kBf16, bool kLayer, int kV>
+__device__ __forceinline__ float2 row_stats(const Args& a, const Place& p, Exchange& ex, int& turn,
+                                            const uint4 (&x)[kV], const int (&there)[kV]) {
   float mean = 0.f;
   if constexpr (kLayer) {
     Pair s = both(0.f);
 #pragma unroll
-    for (int v = 0; v < kV; ++v)
-      s = s + ((x[v].p[0] + x[v].p[1]) + (x[v].p[2] + x[v].p[3]));
-    float sum[1] = {sum_of(s)};
-    team_sum<1>(a, p, ex, turn, sum);
-    mean = sum[0] * a.inv_cols;
-#pragma unroll
     for (int v = 0; v < kV; ++v) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[v].p[j] = x[v].p[j] + both(-mean);
-      if (there[v] < kVec) {  // past the last column 0 is not a value
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float lo, hi;
-          unpair(x[v].p[j], lo, hi);
-          x[v].p[j] = pair(2 * j < there[v] ? lo : 0.f, 2 * j + 1 < there[v] ? hi : 0.f);
-        }
-      }
+      const Eight e = widen_pairs<kBf16>(x[v]);
+      s = s + ((e.p[0] + e.p[1]) + (e.p[2] + e.p[3]));
     }
+    float sum[1] = {sum_of(s)};
+    team_sum(a, p, ex, turn, sum);
+    mean = sum[0] * a.inv_cols;
   }
   Pair s = both(0.f);
+  float edge = 0.f;
 #pragma unroll
-  for (int v = 0; v < kV; ++v)
+  for (int v = 0; v < kV; ++v) {
+    const Eight e = widen_pairs<kBf16>(x[v]);
+    if (!kLayer || there[v] == kVec) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s = fma2(x[v].p[j], x[v].p[j], s);
-  float sum[1] = {sum_of(s)};
-  team_sum<1>(a, p, ex, turn, sum);
-  const float r = inverse_root(sum[0] * a.inv_cols, a.eps);
+      for (int j = 0; j < 4; ++j) {
+        const Pair d = kLayer ? e.p[j] + both(-mean) : e.p[j];
+        s = fma2(d, d, s);
+      }
+    } else {  // past the last column 0 is not a value
+      float f[8];
+      widen8<kBf16>(x[v], f);
 #pragma unroll
-  for (int v = 0; v < kV; ++v)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[v].p[j] = x[v].p[j] * both(r);
-  return make_float2(mean, r);
+      for (int j = 0; j < 8; ++j)
+        if (j < there[v]) edge = __fmaf_rn(f[j] - mean, f[j] - mean, edge);
+    }
+  }
+  float sum[1] = {sum_of(s) + edge};
+  team_sum(a, p, ex, turn, sum);
+  return make_float2(mean, inverse_root(sum[0] * a.inv_cols, a.eps));
 }
 
 // (x - mean) r
@@ -255,295 +274,291 @@ __device__ __forceinline__ Eight scaled(const Eight& x, const Eight& y, float s)
   return e;
 }
 
+// The numbers that the kernels need per column, in shared memory for all teams:
+// kCount times as many vectors of eight floats as a row has.
+enum { kC, kPre, kD, kBias };
+
+template <bool kBf16, int kCount>
+__device__ __forceinline__ void stage_columns(const Args& a, float4* w) {
+  const int n = a.slots_of_row;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int c = i * kVec;  // past the last column parameters count as 0
+    const Eight gate = load_param<kBf16>(a.param[kGate], c, a.cols, 1.f);
+    const auto put = [&](int k, const Eight& e) { write_eight_at(w + 2 * k * n + i, n, e); };
+    put(kC, scaled(gate, load_param<kBf16>(a.param[kWPost], c, a.cols, 1.f), a.branch_scale));
+    put(kPre, load_param<kBf16>(a.param[kWPre], c, a.cols, 0.f));
+    if constexpr (kCount > 2) {
+      put(kD, scaled(gate, load_param<kBf16>(a.param[kBPost], c, a.cols, 0.f), a.branch_scale));
+      put(kBias, load_param<kBf16>(a.param[kBPre], c, a.cols, 0.f));
+    }
+  }
+}
+
+__device__ __forceinline__ Eight column(const Args& a, const float4* w, int k, int col) {
+  return read_eight_at(w + 2 * k * a.slots_of_row + col / kVec, a.slots_of_row);
+}
+
 constexpr int kStagePitch = (kStageWarp + 15) & ~15;
 
-enum { kC, kPre, kD, kBias };  // the forward pass's numbers per column
-
 template <bool kBf16, bool kGrid, bool kLayer, int kV>
-__global__ void __launch_bounds__(kV == 1 ? resident_threads<kLayer>() : kMaxThreads, 1)
-    join_kernel(const Args a) {
+__global__ void __launch_bounds__(kMaxThreads, 1) join_kernel(const Args a) {
   pdl_begin();
-  extern __shared__ float4 smem_columns[];
+  extern __shared__ float4 smem[];
   __shared__ Exchange exchange;
   __shared__ __align__(16) uint8_t stages[kGrid ? 16 : kMaxWarps * kStagePitch];
   const Place p(a);
   uint8_t* stage = stages + (kGrid ? 0 : (threadIdx.x >> 5) * kStagePitch);
   int turn = 0;
   const bool post = a.param[kWPost] != nullptr, pre = a.param[kWPre] != nullptr;
-  Columns<kV, kLayer ? 4 : 2> w(smem_columns);
+  const uint32_t step = step_of(a.drop);
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * a.teams;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.teams + p.team;
   int col[kV], there[kV];
+  uint4 y[kV], next[kV];
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
     col[v] = p.first(a, v) + p.lane * kVec;
     there[v] = max(0, min(kVec, a.cols - col[v]));
-    const Eight gate = load_param<kBf16>(a.param[kGate], col[v], a.cols, 1.f);
-    w.set(kC, v, scaled(gate, load_param<kBf16>(a.param[kWPost], col[v], a.cols, 1.f),
-                        a.branch_scale));
-    w.set(kPre, v, load_param<kBf16>(a.param[kWPre], col[v], a.cols, 0.f));
-    if constexpr (kLayer) {
-      w.set(kD, v, scaled(gate, load_param<kBf16>(a.param[kBPost], col[v], a.cols, 0.f),
-                          a.branch_scale));
-      w.set(kBias, v, load_param<kBf16>(a.param[kBPre], col[v], a.cols, 0.f));
-    }
   }
-  clear(exchange);
-  const uint32_t step = step_of(a.drop);
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * a.teams;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * a.teams + p.team;
-  uint4 y[kV], h[kV];
-  const auto load = [&](int64_t r) {
+  const auto load = [&](int64_t row) {
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
-      y[v] = load8<kGrid>(a.y + r * a.ld, col[v], a.cols, a.bounds(kY));
-      h[v] = load8<kGrid>(a.h + r * a.ld, col[v], a.cols, a.bounds(kH));
+      y[v] = load_at<kGrid>(a.y, row * a.ld, col[v], a.cols, a.bounds(kY));
+      next[v] = load_at<kGrid>(a.h, row * a.ld, col[v], a.cols, a.bounds(kH));
     }
   };
-  if (row < a.rows) load(row);
-  for (; row < a.rows; row += stride) {
-    float2 sy = make_float2(0.f, 0.f), sh = sy;
-    Eight x[kV];
+  if (row0 < a.rows) load(row0);  // under way while the columns' numbers are set up
+  stage_columns<kBf16, kLayer ? 4 : 2>(a, smem);
+  clear(exchange);
+  for (int64_t row = row0; row < a.rows; row += stride) {
+    uint4 h[kV];
 #pragma unroll
-    for (int v = 0; v < kV; ++v) x[v] = widen_pairs<kBf16>(y[v]);
-    if (post) sy = normalise<kLayer, kV>(a, p, exchange, turn, x, there);
+    for (int v = 0; v < kV; ++v) h[v] = next[v];
+    float2 sy = make_float2(0.f, 1.f), sh = make_float2(0.f, 0.f);
+    if (post) sy = row_stats<kBf16, kLayer, kV>(a, p, exchange, turn, y, there);
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
-      const Eight c = w.get(kC, v);
+      Eight x = widen_pairs<kBf16>(y[v]);
+      const Eight c = column(a, smem, kC, col[v]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[v].p[j] = x[v].p[j] * c.p[j];
+      for (int j = 0; j < 4; ++j) x.p[j] = normed<kLayer>(x.p[j], sy) * c.p[j];
       if constexpr (kLayer) {
-        const Eight d = w.get(kD, v);
+        const Eight d = column(a, smem, kD, col[v]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[v].p[j] = x[v].p[j] + d.p[j];
+        for (int j = 0; j < 4; ++j) x.p[j] = x.p[j] + d.p[j];
       }
-      if (a.drop.threshold)
-        drop_pairs(a.drop,
-                   draw8(a.drop, step, static_cast<uint32_t>(row),
-                         static_cast<uint32_t>(col[v]) / kVec), x[v]);
+      if (a.drop.threshold) drop_pairs(a.drop, kept(a.drop, step, row, col[v]), x);
       const Eight s = widen_pairs<kBf16>(h[v]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[v].p[j] = fma2(s.p[j], both(a.stream_scale), x[v].p[j]);
-      const uint4 out = narrow_pairs<kBf16>(x[v]);
-      store_row<kGrid>(stage, a.h_new + row * a.ld, p.first(a, v), p.lane, a.cols, out,
-                       a.bounds(kHOut));
-      x[v] = widen_pairs<kBf16>(out);
+      for (int j = 0; j < 4; ++j) x.p[j] = fma2(s.p[j], both(a.stream_scale), x.p[j]);
+      h[v] = narrow_pairs<kBf16>(x);
+      store_at<kGrid>(stage, a.h_new, row * a.ld, p.first(a, v), p.lane, a.cols, h[v],
+                      a.bounds(kHOut));
     }
     if (row + stride < a.rows) load(row + stride);
     if (pre) {
-      sh = normalise<kLayer, kV>(a, p, exchange, turn, x, there);
+      sh = row_stats<kBf16, kLayer, kV>(a, p, exchange, turn, h, there);
 #pragma unroll
       for (int v = 0; v < kV; ++v) {
-        const Eight c = w.get(kPre, v);
+        Eight x = widen_pairs<kBf16>(h[v]);
+        const Eight c = column(a, smem, kPre, col[v]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[v].p[j] = x[v].p[j] * c.p[j];
+        for (int j = 0; j < 4; ++j) x.p[j] = normed<kLayer>(x.p[j], sh) * c.p[j];
         if constexpr (kLayer) {
-          const Eight d = w.get(kBias, v);
+          const Eight d = column(a, smem, kBias, col[v]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[v].p[j] = x[v].p[j] + d.p[j];
+          for (int j = 0; j < 4; ++j) x.p[j] = x.p[j] + d.p[j];
         }
-        store_row<kGrid>(stage, a.z + row * a.ld, p.first(a, v), p.lane, a.cols,
-                         narrow_pairs<kBf16>(x[v]), a.bounds(kZ));
+        store_at<kGrid>(stage, a.z, row * a.ld, p.first(a, v), p.lane, a.cols,
+                        narrow_pairs<kBf16>(x), a.bounds(kZ));
       }
     }
     if (a.stats && p.warp == 0 && p.lane == 0 &&
         a.bounds(kStats).holds(a.stats + row, 16, kSiteStore))
-      a.stats[row] = make_float4(sy.x, sy.y, sh.x, sh.y);
+      a.stats[row] = make_float4(post ? sy.x : 0.f, post ? sy.y : 0.f, sh.x, sh.y);
   }
 }
 
-// the backward pass's numbers per column: w_pre and c, then the sums
-enum { kBackPre, kBackC, kBackSums };
+// Sums over the rows of a thread's own columns, in shared memory: eight floats
+// for each sum and vector, the thread's own words.
+template <int kV>
+struct ColumnSums {
+  float4* own;
+  __device__ __forceinline__ float4* at(int k, int v) const {
+    return own + (k * kV + v) * 2 * kMaxThreads;
+  }
+  __device__ __forceinline__ ColumnSums(float4* sums, int count) : own(sums + threadIdx.x) {
+    for (int k = 0; k < count; ++k)
+#pragma unroll
+      for (int v = 0; v < kV; ++v)
+        write_eight_at(at(k, v), kMaxThreads, Eight{{both(0.f), both(0.f), both(0.f), both(0.f)}});
+  }
+  // += x y
+  __device__ __forceinline__ void add(int k, int v, const Eight& x, const Eight& y) const {
+    Eight s = read_eight_at(at(k, v), kMaxThreads);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s.p[j] = fma2(x.p[j], y.p[j], s.p[j]);
+    write_eight_at(at(k, v), kMaxThreads, s);
+  }
+  // += x
+  __device__ __forceinline__ void add(int k, int v, const Eight& x) const {
+    Eight s = read_eight_at(at(k, v), kMaxThreads);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s.p[j] = s.p[j] + x.p[j];
+    write_eight_at(at(k, v), kMaxThreads, s);
+  }
+};
 
-template <bool kLayer>
-__device__ __host__ constexpr int back_columns() { return kBackSums + (kLayer ? kSums : 2); }
-// where a sum is among them (without ZERO_NORM_LAYER there are P and A)
-template <bool kLayer>
-__device__ __host__ constexpr int back_sum(int k) { return kBackSums + (kLayer ? k : k / 2); }
+// P, A and, with ZERO_NORM_LAYER, Q and B after them
+__host__ __device__ constexpr int sums_of(bool layer) { return layer ? kSums : 2; }
+
+// a row's sums, by their place among the values that a team adds up
+enum { kGH, kYE, kYH, kY1, kE1, kH1, kG1, kK1, kRowSums };
+static_assert(kRowSums <= kMaxValues, "exchange");
 
 template <bool kBf16, bool kGrid, bool kLayer, int kV>
 __global__ void __launch_bounds__(kMaxThreads, 1) join_grad_kernel(const Args a) {
+  constexpr int kValues = kLayer ? kRowSums : 3;
   pdl_begin();
-  extern __shared__ float4 smem_columns[];
+  extern __shared__ float4 smem[];
   __shared__ Exchange exchange;
   __shared__ __align__(16) uint8_t stages[kGrid ? 16 : kMaxWarps * kStagePitch];
+  float4* sums_smem = smem + 2 * 2 * a.slots_of_row;  // behind the columns' numbers
   const Place p(a);
   uint8_t* stage = stages + (kGrid ? 0 : (threadIdx.x >> 5) * kStagePitch);
   int turn = 0;
   const bool post = a.param[kWPost] != nullptr, pre = a.param[kWPre] != nullptr;
-  const bool branch_sums = post || a.param[kGate] != nullptr;
-  Columns<kV, back_columns<kLayer>()> w(smem_columns);
-  int col[kV];
-#pragma unroll
-  for (int v = 0; v < kV; ++v) {
-    col[v] = p.first(a, v) + p.lane * kVec;
-    w.set(kBackPre, v, load_param<kBf16>(a.param[kWPre], col[v], a.cols, 0.f));
-    w.set(kBackC, v, scaled(load_param<kBf16>(a.param[kGate], col[v], a.cols, 1.f),
-                            load_param<kBf16>(a.param[kWPost], col[v], a.cols, 1.f),
-                            a.branch_scale));
-#pragma unroll
-    for (int k = kBackSums; k < back_columns<kLayer>(); ++k)
-      w.set(k, v, Eight{{both(0.f), both(0.f), both(0.f), both(0.f)}});
-  }
-  // a sum += x y (or x)
-  const auto add = [&](int sum, int v, const Eight& x, const Eight& y) {
-    Eight s = w.get(back_sum<kLayer>(sum), v);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) s.p[j] = fma2(x.p[j], y.p[j], s.p[j]);
-    w.set(back_sum<kLayer>(sum), v, s);
-  };
-  const auto add_one = [&](int sum, int v, const Eight& x) {
-    Eight s = w.get(back_sum<kLayer>(sum), v);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) s.p[j] = s.p[j] + x.p[j];
-    w.set(back_sum<kLayer>(sum), v, s);
-  };
-  clear(exchange);
+  const bool need_y = post || a.param[kGate] != nullptr;
   const uint32_t step = step_of(a.drop);
   const int64_t stride = static_cast<int64_t>(gridDim.x) * a.teams;
   int64_t row = static_cast<int64_t>(blockIdx.x) * a.teams + p.team;
   const uint4 none = make_uint4(0, 0, 0, 0);
-  uint4 y[kV], h[kV], dz[kV], dh[kV];
+  int col[kV];
+#pragma unroll
+  for (int v = 0; v < kV; ++v) col[v] = p.first(a, v) + p.lane * kVec;
+  uint4 y[kV], h[kV], dz[kV], up[kV];
   float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
   const auto load = [&](int64_t r) {
+    const int64_t at = r * a.ld;
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
-      dz[v] = pre ? load8<kGrid>(a.dz + r * a.ld, col[v], a.cols, a.bounds(kDz)) : none;
-      h[v] = pre ? load8<kGrid>(a.h_out + r * a.ld, col[v], a.cols, a.bounds(kHOut)) : none;
-      dh[v] = a.dh_out ? load8<kGrid>(a.dh_out + r * a.ld, col[v], a.cols, a.bounds(kDhOut)) : none;
-      y[v] = branch_sums ? load8<kGrid>(a.y + r * a.ld, col[v], a.cols, a.bounds(kY)) : none;
+      dz[v] = pre ? load_at<kGrid>(a.dz, at, col[v], a.cols, a.bounds(kDz)) : none;
+      h[v] = pre ? load_at<kGrid>(a.h_out, at, col[v], a.cols, a.bounds(kHOut)) : none;
+      up[v] = a.dh_out ? load_at<kGrid>(a.dh_out, at, col[v], a.cols, a.bounds(kDhOut)) : none;
+      y[v] = need_y ? load_at<kGrid>(a.y, at, col[v], a.cols, a.bounds(kY)) : none;
     }
     if (a.bounds(kStats).holds(a.stats + r, 16, kSiteLoad)) st = a.stats[r];
   };
-  if (row < a.rows) load(row);
+  if (row < a.rows) load(row);  // under way while the columns' numbers are set up
+  stage_columns<kBf16, 2>(a, smem);
+  const ColumnSums<kV> sums(sums_smem, sums_of(kLayer));
+  clear(exchange);
   for (; row < a.rows; row += stride) {
-    const float2 sy = make_float2(st.x, st.y), sh = make_float2(st.z, st.w);
-    // through the norm before the next block: D, the whole gradient of h_out
-    Eight d[kV];
-    if (pre) {
-      Pair along = both(0.f), flat = both(0.f);
-      Eight x[kV], g[kV];
+    const float2 sy = make_float2(st.x, st.y);
+    const float2 sh = pre ? make_float2(st.z, st.w) : make_float2(0.f, 0.f);
+    Eight d[kV], xh[kV], xy[kV];  // E, then D; h^; y^ (or y)
+    uint32_t keep[kV];
+    Pair part[kValues];
 #pragma unroll
-      for (int v = 0; v < kV; ++v) {
-        const Eight c = w.get(kBackPre, v);
-        const Eight up = widen_pairs<kBf16>(dz[v]);
-        x[v] = widen_pairs<kBf16>(h[v]);
+    for (int q = 0; q < kValues; ++q) part[q] = both(0.f);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[v].p[j] = normed<kLayer>(x[v].p[j], sh);
-          g[v].p[j] = up.p[j] * c.p[j];
-          along = fma2(g[v].p[j], x[v].p[j], along);
-          if constexpr (kLayer) flat = flat + g[v].p[j];
-        }
-        add(kSumP, v, up, x[v]);
-        if constexpr (kLayer) add_one(kSumQ, v, up);
+    for (int v = 0; v < kV; ++v) {
+      const Eight w = column(a, smem, kPre, col[v]), g0 = widen_pairs<kBf16>(dz[v]);
+      Eight k = column(a, smem, kC, col[v]), g;
+      xh[v] = widen_pairs<kBf16>(h[v]);
+      xy[v] = widen_pairs<kBf16>(y[v]);
+      d[v] = widen_pairs<kBf16>(up[v]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        xh[v].p[j] = normed<kLayer>(xh[v].p[j], sh);
+        g.p[j] = g0.p[j] * w.p[j];
+        part[kGH] = fma2(g.p[j], xh[v].p[j], part[kGH]);
+        d[v].p[j] = fma2(g.p[j], both(sh.y), d[v].p[j]);
       }
-      float s[kLayer ? 2 : 1];
-      s[0] = sum_of(along);
-      if constexpr (kLayer) s[1] = sum_of(flat);
-      team_sum(a, p, exchange, turn, s);
-      const Pair c1 = both(-s[0] * a.inv_cols), r = both(sh.y);
+      sums.add(0, v, g0, xh[v]);
+      if constexpr (kLayer) sums.add(2, v, g0);
+      if (post)
 #pragma unroll
-      for (int v = 0; v < kV; ++v) {
-        const Eight up = widen_pairs<kBf16>(dh[v]);
+        for (int j = 0; j < 4; ++j) xy[v].p[j] = normed<kLayer>(xy[v].p[j], sy);
+      if (a.drop.threshold) {
+        keep[v] = kept(a.drop, step, row, col[v]);
+        drop_pairs(a.drop, keep[v], k);
+      }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          Pair t = fma2(x[v].p[j], c1, g[v].p[j]);
-          if constexpr (kLayer) t = t + both(-s[1] * a.inv_cols);
-          d[v].p[j] = fma2(t, r, up.p[j]);
+      for (int j = 0; j < 4; ++j) {
+        const Pair ky = k.p[j] * xy[v].p[j];
+        part[kYE] = fma2(ky, d[v].p[j], part[kYE]);
+        part[kYH] = fma2(ky, xh[v].p[j], part[kYH]);
+        if constexpr (kLayer) {
+          part[kY1] = part[kY1] + ky;
+          part[kE1] = fma2(k.p[j], d[v].p[j], part[kE1]);
+          part[kH1] = fma2(k.p[j], xh[v].p[j], part[kH1]);
+          part[kG1] = part[kG1] + g.p[j];
+          part[kK1] = part[kK1] + k.p[j];
         }
       }
-    } else {
-#pragma unroll
-      for (int v = 0; v < kV; ++v) d[v] = widen_pairs<kBf16>(dh[v]);
     }
-    // through gate, dropout and the norm after the block
-    Pair along = both(0.f), flat = both(0.f);
-    Eight x[kV];
+    if (row + stride < a.rows) load(row + stride);
+    float s[kValues];
+#pragma unroll
+    for (int q = 0; q < kValues; ++q) s[q] = sum_of(part[q]);
+    team_sum(a, p, exchange, turn, s);
+    const float c1 = sh.y * (s[kGH] * a.inv_cols);  // r c1, r c2
+    float c2 = 0.f, along = s[kYE] - c1 * s[kYH], flat = 0.f;
+    if constexpr (kLayer) {
+      c2 = sh.y * (s[kG1] * a.inv_cols);
+      along = s[kYE] - (c1 * s[kYH] + c2 * s[kY1]);
+      flat = (s[kE1] - (c1 * s[kH1] + c2 * s[kK1])) * a.inv_cols;
+    }
+    along *= a.inv_cols;
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
       Eight e;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) e.p[j] = d[v].p[j] * both(a.stream_scale);
-      store_row<kGrid>(stage, a.dh + row * a.ld, p.first(a, v), p.lane, a.cols,
-                       narrow_pairs<kBf16>(e), a.bounds(kDh));
-      if (a.drop.threshold)
-        drop_pairs(a.drop,
-                   draw8(a.drop, step, static_cast<uint32_t>(row),
-                         static_cast<uint32_t>(col[v]) / kVec), d[v]);
-      x[v] = widen_pairs<kBf16>(y[v]);
-      if (post) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[v].p[j] = normed<kLayer>(x[v].p[j], sy);
-      }
-      add(kSumA, v, d[v], x[v]);
-      if constexpr (kLayer) add_one(kSumB, v, d[v]);
-      const Eight c = w.get(kBackC, v);
-#pragma unroll
       for (int j = 0; j < 4; ++j) {
-        d[v].p[j] = d[v].p[j] * c.p[j];
-        along = fma2(d[v].p[j], x[v].p[j], along);
-        if constexpr (kLayer) flat = flat + d[v].p[j];
+        d[v].p[j] = fma2(xh[v].p[j], both(-c1), d[v].p[j]);
+        if constexpr (kLayer) d[v].p[j] = d[v].p[j] + both(-c2);
+        e.p[j] = d[v].p[j] * both(a.stream_scale);
       }
-    }
-    if (row + stride < a.rows) load(row + stride);
-    if (post) {
-      float s[kLayer ? 2 : 1];
-      s[0] = sum_of(along);
-      if constexpr (kLayer) s[1] = sum_of(flat);
-      team_sum(a, p, exchange, turn, s);
-      const Pair c1 = both(-s[0] * a.inv_cols), r = both(sy.y);
+      store_at<kGrid>(stage, a.dh, row * a.ld, p.first(a, v), p.lane, a.cols,
+                      narrow_pairs<kBf16>(e), a.bounds(kDh));
+      if (a.drop.threshold) drop_pairs(a.drop, keep[v], d[v]);
+      sums.add(1, v, d[v], xy[v]);
+      if constexpr (kLayer) sums.add(3, v, d[v]);
+      const Eight c = column(a, smem, kC, col[v]);
 #pragma unroll
-      for (int v = 0; v < kV; ++v)
+      for (int j = 0; j < 4; ++j) e.p[j] = d[v].p[j] * c.p[j];
+      if (post)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          Pair t = fma2(x[v].p[j], c1, d[v].p[j]);
-          if constexpr (kLayer) t = t + both(-s[1] * a.inv_cols);
-          d[v].p[j] = t * r;
+          Pair t = fma2(xy[v].p[j], both(-along), e.p[j]);
+          if constexpr (kLayer) t = t + both(-flat);
+          e.p[j] = t * both(sy.y);
         }
+      store_at<kGrid>(stage, a.dy, row * a.ld, p.first(a, v), p.lane, a.cols,
+                      narrow_pairs<kBf16>(e), a.bounds(kDy));
     }
-#pragma unroll
-    for (int v = 0; v < kV; ++v)
-      store_row<kGrid>(stage, a.dy + row * a.ld, p.first(a, v), p.lane, a.cols,
-                       narrow_pairs<kBf16>(d[v]), a.bounds(kDy));
   }
   // this CTA's vectors: the teams' sums joined in order
   if (a.slots == 0) return;
+  __syncthreads();
+  const int team_threads = 32 * a.team_warps;
   float* part = a.parts + static_cast<int64_t>(blockIdx.x) * a.slots * a.pitch;
-  const auto leave = [&](int slot, int c, const float4& lo, const float4& hi) {
-    float* to = part + static_cast<int64_t>(slot) * a.pitch + c;
-    if (c >= a.pitch || !a.bounds(kParts).holds(to, 32, kSiteStore)) return;
-    reinterpret_cast<float4*>(to)[0] = lo;
-    reinterpret_cast<float4*>(to)[1] = hi;
-  };
-  if constexpr (kV == 1) {
-    const int team_threads = 32 * a.team_warps, t = p.warp * 32 + p.lane;
-    for (int k = 0; k < a.teams; ++k) {
-      if (p.team == k) {
+  for (int i = threadIdx.x; i < sums_of(kLayer) * a.slots_of_row; i += blockDim.x) {
+    const int q = i / a.slots_of_row, vector = i - q * a.slots_of_row;
+    const int v = vector / team_threads, t = vector - v * team_threads;
+    const int slot = a.slot[q], c = vector * kVec;
+    if (slot < 0 || c >= a.pitch) continue;
+    const float4* from = sums_smem + (q * kV + v) * 2 * kMaxThreads + t;
+    Eight s = read_eight_at(from, kMaxThreads);
+    for (int k = 1; k < a.teams; ++k) {
+      const Eight x = read_eight_at(from + k * team_threads, kMaxThreads);
 #pragma unroll
-        for (int q = 0; q < kSums; q += kLayer ? 1 : 2) {
-          float f[8];
-          const Eight e = w.get(back_sum<kLayer>(q), 0);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) unpair(e.p[j], f[2 * j], f[2 * j + 1]);
-          float4 *lo = smem_columns + (2 * q) * team_threads + t, *hi = lo + team_threads;
-          const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-          const float4 x = k ? *lo : z, y4 = k ? *hi : z;
-          *lo = make_float4(x.x + f[0], x.y + f[1], x.z + f[2], x.w + f[3]);
-          *hi = make_float4(y4.x + f[4], y4.y + f[5], y4.z + f[6], y4.w + f[7]);
-        }
-      }
-      __syncthreads();
+      for (int j = 0; j < 4; ++j) s.p[j] = s.p[j] + x.p[j];
     }
-    for (int q = p.team; q < kSums; q += a.teams)
-      if (a.slot[q] >= 0)
-        leave(a.slot[q], col[0], smem_columns[2 * q * team_threads + t],
-              smem_columns[(2 * q + 1) * team_threads + t]);
-  } else {
-    for (int q = 0; q < kSums; ++q)
-      if (a.slot[q] >= 0)
-        for (int v = 0; v < kV; ++v) {
-          const float4* at = w.at(back_sum<kLayer>(q), v);
-          leave(a.slot[q], col[v], at[0], at[kMaxThreads]);
-        }
+    float* to = part + static_cast<int64_t>(slot) * a.pitch + c;
+    if (a.bounds(kParts).holds(to, 32, kSiteStore))
+      write_eight_at(reinterpret_cast<float4*>(to), 1, s);
   }
 }
 
@@ -616,14 +631,22 @@ __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const JoinArgs
 
 int64_t pitch_of(int64_t cols) { return ceil_div(cols, kVec) * kVec; }
 
-// A row's team, and how many of at most `threads` together a CTA has: rows are
-// spread over `sms` SMs first.
-void set_teams(Args& a, int64_t rows, int64_t cols, int threads) {
-  const int64_t vectors = ceil_div(cols, kVec), per = vectors > kMaxThreads ? 2 : 1;
-  a.team_warps = static_cast<int32_t>(ceil_div(ceil_div(vectors, per), 32));
-  const int64_t most = std::max(1, threads / 32 / a.team_warps);
-  a.teams = static_cast<int32_t>(std::min(most, std::max<int64_t>(1, ceil_div(rows, kMaxParts))));
+// A row's team of warps and a CTA's teams; returns the vectors per thread, which
+// is the most that both the row and `most` allow. Where that leaves too few warps
+// for the device (few rows: a call's latency counts), a thread takes fewer.
+int set_teams(Args& a, int64_t rows, int64_t cols, int most) {
+  const int64_t vectors = ceil_div(cols, kVec);
+  int per = 1;
+  while (per < most && 32 * per < vectors) per *= 2;
+  while (per > 1 && ceil_div(vectors, 32 * per / 2) <= kMaxWarps &&
+         rows * ceil_div(vectors, 32 * per) < kMaxParts * kMaxWarps / 2)
+    per /= 2;
+  a.team_warps = static_cast<int32_t>(ceil_div(vectors, 32 * per));
+  a.teams = static_cast<int32_t>(std::min<int64_t>(
+      kMaxWarps / a.team_warps, std::max<int64_t>(1, ceil_div(rows, kMaxParts))));
+  a.slots_of_row = 32 * per * a.team_warps;
   a.pitch = static_cast<int32_t>(pitch_of(cols));
+  return per;
 }
 
 int check(const zero_join_params* p, const zero_join_weights* w, int64_t rows, int64_t cols,
@@ -657,36 +680,31 @@ void set_common(Args& a, const zero_join_params& p, const zero_join_weights& w, 
 }
 
 template <class Kernel>
-cudaError_t launch_with(Kernel fn, const Args& a, int64_t ctas, int bytes, cudaStream_t st) {
-  if (bytes > 48 * 1024) {
+cudaError_t launch_with(Kernel fn, const Args& a, int columns, int sums, cudaStream_t st) {
+  const int bytes = 32 * (columns * a.slots_of_row + sums * kMaxThreads);
+  if (bytes > 40 * 1024) {  // 48 KB with the kernels' own
     const cudaError_t e =
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
   }
+  const int64_t ctas = std::min<int64_t>(kMaxParts, ceil_div(a.rows, a.teams));
   return launch_pdl(fn, dim3(static_cast<unsigned>(ctas)), dim3(32 * a.team_warps * a.teams),
                     bytes, st, a);
 }
 
 template <bool kBf16, bool kGrid, bool kLayer>
-cudaError_t launch_join(Args& a, cudaStream_t st) {
-  constexpr int kThreads = resident_threads<kLayer>();
-  set_teams(a, a.rows, a.cols, 256);
-  const int per_sm = std::max(1, kThreads / (32 * a.team_warps * a.teams));
-  const int64_t ctas = std::min<int64_t>(per_sm * kMaxParts, ceil_div(a.rows, a.teams));
-  if (a.pitch <= kMaxThreads * kVec)
-    return launch_with(join_kernel<kBf16, kGrid, kLayer, 1>, a, ctas, 0, st);
-  return launch_with(join_kernel<kBf16, kGrid, kLayer, 2>, a,
-                     std::min<int64_t>(kMaxParts, ctas), columns_bytes<2>(kLayer ? 4 : 2), st);
+cudaError_t launch_join(const Args& a, int per, cudaStream_t st) {
+  constexpr int kColumns = kLayer ? 4 : 2;
+  if (per == 1) return launch_with(join_kernel<kBf16, kGrid, kLayer, 1>, a, kColumns, 0, st);
+  if (per == 2) return launch_with(join_kernel<kBf16, kGrid, kLayer, 2>, a, kColumns, 0, st);
+  return launch_with(join_kernel<kBf16, kGrid, kLayer, 4>, a, kColumns, 0, st);
 }
 
 template <bool kBf16, bool kGrid, bool kLayer>
-cudaError_t launch_grad(const Args& a, int64_t ctas, cudaStream_t st) {
-  // one vector: room to join the teams' sums
-  return a.pitch <= kMaxThreads * kVec
-             ? launch_with(join_grad_kernel<kBf16, kGrid, kLayer, 1>, a, ctas,
-                           kSums * 32 * a.team_warps * kVec * 4, st)
-             : launch_with(join_grad_kernel<kBf16, kGrid, kLayer, 2>, a, ctas,
-                           columns_bytes<2>(back_columns<kLayer>()), st);
+cudaError_t launch_grad(const Args& a, int per, cudaStream_t st) {
+  constexpr int kAll = sums_of(kLayer);
+  if (per == 1) return launch_with(join_grad_kernel<kBf16, kGrid, kLayer, 1>, a, 2, kAll, st);
+  return launch_with(join_grad_kernel<kBf16, kGrid, kLayer, 2>, a, 2, 2 * kAll, st);
 }
 
 // fn<bf16, grid, layer>(...) for run-time values
@@ -733,9 +751,10 @@ ZERO_API int zero_block_join(const zero_join_params* params, const zero_join_wei
   a.set_bounds(kHOut, h_out, rows, cols, ld, 2);
   a.set_bounds(kZ, z, rows, cols, ld, 2);
   a.set_bounds(kStats, stats, 1, rows, rows, 16);
-  const bool grid = on_grid(h, ld) && aligned(y, 16) && aligned(h_out, 16) && aligned(z, 16);
+  const int per = set_teams(a, rows, cols, kForwardVectors);
+  const bool grid = cols % kVec == 0 && on_grid(h, ld) && aligned(y, 16) && aligned(h_out, 16) && aligned(z, 16);
   return status_of(ZJ_PICK(launch_join, dtype == ZERO_BF16, grid, params->norm == ZERO_NORM_LAYER,
-                           a, static_cast<cudaStream_t>(stream)));
+                           a, per, static_cast<cudaStream_t>(stream)));
 }
 
 ZERO_API size_t zero_block_join_workspace_bytes(int64_t rows, int64_t cols) {
@@ -762,8 +781,8 @@ ZERO_API int zero_block_join_grad(const zero_join_params* params, const zero_joi
   if (cols == 0) return ZERO_OK;
   JoinArgs j = new_args<JoinArgs>();
   Args a = new_args<Args>();
-  const bool needed[kSums] = {g[kWPre] != nullptr, g[kBPre] != nullptr,
-                              g[kWPost] || g[kGate], g[kBPost] != nullptr};
+  const bool needed[kSums] = {g[kWPre] != nullptr, g[kWPost] || g[kGate], g[kBPre] != nullptr,
+                              g[kBPost] != nullptr};
   for (int k = 0; k < kSums; ++k) a.slot[k] = j.slot[k] = needed[k] ? j.slots++ : -1;
   for (int k = 0; k < kParams; ++k) {
     j.param[k] = static_cast<const uint16_t*>(w[k]);
@@ -791,7 +810,7 @@ ZERO_API int zero_block_join_grad(const zero_join_params* params, const zero_joi
     a.stats = reinterpret_cast<float4*>(const_cast<float*>(stats));
     a.parts = static_cast<float*>(workspace);
     a.slots = j.slots;
-    set_teams(a, rows, cols, kMaxThreads);
+    const int per = set_teams(a, rows, cols, kBackVectors);
     const int64_t ctas = std::min<int64_t>(kMaxParts, ceil_div(rows, a.teams));
     j.n_parts = static_cast<int32_t>(ctas);
     a.set_bounds(kHOut, h_out, rows, cols, ld, 2);
@@ -802,10 +821,10 @@ ZERO_API int zero_block_join_grad(const zero_join_params* params, const zero_joi
     a.set_bounds(kDh, dh, rows, cols, ld, 2);
     a.set_bounds(kDy, dy, rows, cols, ld, 2);
     a.set_bounds(kParts, workspace, 1, ctas * j.slots * j.pitch, 0, 4);
-    const bool grid = on_grid(dh, ld) && aligned(dy, 16) && aligned(h_out, 16) && aligned(y, 16) &&
+    const bool grid = cols % kVec == 0 && on_grid(dh, ld) && aligned(dy, 16) && aligned(h_out, 16) && aligned(y, 16) &&
                       aligned(dz, 16) && aligned(dh_out, 16);
     const int bad = status_of(ZJ_PICK(launch_grad, bf16, grid, params->norm == ZERO_NORM_LAYER, a,
-                                      ctas, st));
+                                      per, st));
     if (bad) return bad;
   }
   if (j.slots == 0) return ZERO_OK;

@@ -70,14 +70,16 @@ def norm64(x, layer, eps):
     return xhat, mean, r, err
 
 
-def norm_back64(g, eg, xhat, ex, r, layer):
+def norm_back64(g, eg, xhat, ex, r, layer, parts=None):
     """Gradient through a norm and its fp32 error: r (g - xhat mean(g xhat) -
-    mean(g)), eg and ex the errors of g and xhat."""
+    mean(g)), eg and ex the errors of g and xhat; parts: the magnitudes that g is
+    summed from, where its sums over the row are taken part by part."""
+    parts = g.abs() if parts is None else parts
     m = lambda t: t.mean(1, keepdim=True)  # noqa: E731
     c1, c2 = m(g * xhat), m(g) if layer else torch.zeros_like(g[:, :1])
     out = r * (g - xhat * c1 - c2)
-    e1 = m(eg * xhat.abs()) + m(g.abs() * ex) + SUM * m((g * xhat).abs())
-    e2 = (m(eg) + SUM * m(g.abs())) if layer else 0.0
+    e1 = m(eg * xhat.abs()) + m(parts * ex) + SUM * m(parts * xhat.abs())
+    e2 = (m(eg) + SUM * m(parts)) if layer else 0.0
     mag = g.abs() + (xhat * c1).abs() + c2.abs()
     err = r * (eg + xhat.abs() * e1 + ex * c1.abs() + e2 + 2.0 ** -21 * mag) + ROOT * r * mag
     return out, err
@@ -124,10 +126,13 @@ class Join64:
         w, out = self.w, {}
         d = dh_out if dh_out is not None else torch.zeros_like(h_out)
         ed = torch.zeros_like(d)
+        parts = d.abs()  # D's sums over a row are those of its terms
         if w["w_pre"] is not None:
             xhat, _, r, ex = norm64(h_out, self.layer, self.eps)
             g = dz * w["w_pre"]
             through, ed = norm_back64(g, 2.0 ** -23 * g.abs(), xhat, ex, r, self.layer)
+            c1, c2 = (g * xhat).mean(1, keepdim=True), g.mean(1, keepdim=True)
+            parts = parts + r * (g.abs() + (xhat * c1).abs() + (c2.abs() if self.layer else 0.0))
             d = d + through
             ed = ed + 2.0 ** -23 * (d.abs() + through.abs())
             out["w_pre"] = self.sums(dz * xhat, dz.abs() * ex)
@@ -151,8 +156,11 @@ class Join64:
             out["w_post"] = self.sums(e * xhat, ee * xhat.abs() + e.abs() * ex)
             out["b_post"] = self.sums(e, ee)
             q = e * w["w_post"]
+            parts = parts * (self.s * self.keep * w["w_post"]).abs()
+            if w["gate"] is not None:
+                parts = parts * w["gate"].abs()
             e, ee = norm_back64(q, ee * w["w_post"].abs() + 2.0 ** -23 * q.abs(), xhat, ex, r,
-                                self.layer)
+                                self.layer, parts)
         out["dy"] = e, rounded(e, ee, self.dtype)
         return out
 
