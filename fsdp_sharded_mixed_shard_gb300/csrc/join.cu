@@ -42,6 +42,7 @@ using namespace zt;
 constexpr int kMaxThreads = 512;  // of a CTA, one per SM, 128 registers each
 constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxParts = 152;    // CTAs
+constexpr int kMostBytes = 224 * 1024;  // of shared memory, beside the kernels' own
 // vectors per thread at most
 constexpr int kForwardVectors = 4, kBackVectors = 2;
 static_assert(ZERO_MAX_JOIN_COLS <= kBackVectors * kMaxThreads * kVec, "a row fits a CTA");
@@ -416,7 +417,37 @@ __host__ __device__ constexpr int sums_of(bool layer) { return layer ? kSums : 2
 enum { kGH, kYE, kYH, kY1, kE1, kH1, kG1, kK1, kRowSums };
 static_assert(kRowSums <= kMaxValues, "exchange");
 
-template <bool kBf16, bool kGrid, bool kLayer, int kV>
+// A row's vectors on their way into shared memory, each thread's into words of
+// its own, while the row before is worked on: kArrays arrays of kV vectors.
+enum { kInDz, kInH, kInUp, kInY, kArrays };
+
+template <int kV>
+struct Ahead {
+  uint4* own;
+  __device__ __forceinline__ uint4* at(int array, int v) const {
+    return own + (array * kV + v) * kMaxThreads;
+  }
+  __device__ __forceinline__ void clear() const {  // past the last column there are zeros
+#pragma unroll
+    for (int k = 0; k < kArrays; ++k)
+#pragma unroll
+      for (int v = 0; v < kV; ++v) *at(k, v) = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void start(int array, int v, const uint16_t* x, int64_t row_start,
+                                        int col, int cols, const Bounds& in) const {
+    const uint16_t* from = x + row_start + col;
+    if (col >= cols || !in.holds(from, 16, kSiteLoad)) return;
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(at(array, v)));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  }
+  __device__ __forceinline__ void wait() const {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+};
+
+// kAhead: rows come by Ahead (kGrid only), else by loads into registers half a
+// row's work before.
+template <bool kBf16, bool kGrid, bool kLayer, int kV, bool kAhead>
 __global__ void __launch_bounds__(kMaxThreads, 1) join_grad_kernel(const Args a) {
   constexpr int kValues = kLayer ? kRowSums : 3;
   pdl_begin();
@@ -438,10 +469,20 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_grad_kernel(const Args a)
   for (int v = 0; v < kV; ++v) col[v] = p.first(a, v) + p.lane * kVec;
   uint4 y[kV], h[kV], dz[kV], up[kV];
   float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
+  const Ahead<kV> ahead = {
+      reinterpret_cast<uint4*>(sums_smem + sums_of(kLayer) * kV * 2 * kMaxThreads) + threadIdx.x};
+  if constexpr (kAhead) ahead.clear();
   const auto load = [&](int64_t r) {
     const int64_t at = r * a.ld;
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
+      if constexpr (kAhead) {
+        if (pre) ahead.start(kInDz, v, a.dz, at, col[v], a.cols, a.bounds(kDz));
+        if (pre) ahead.start(kInH, v, a.h_out, at, col[v], a.cols, a.bounds(kHOut));
+        if (a.dh_out) ahead.start(kInUp, v, a.dh_out, at, col[v], a.cols, a.bounds(kDhOut));
+        if (need_y) ahead.start(kInY, v, a.y, at, col[v], a.cols, a.bounds(kY));
+        continue;
+      }
       dz[v] = pre ? load_at<kGrid>(a.dz, at, col[v], a.cols, a.bounds(kDz)) : none;
       h[v] = pre ? load_at<kGrid>(a.h_out, at, col[v], a.cols, a.bounds(kHOut)) : none;
       up[v] = a.dh_out ? load_at<kGrid>(a.dh_out, at, col[v], a.cols, a.bounds(kDhOut)) : none;
@@ -456,6 +497,17 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_grad_kernel(const Args a)
   for (; row < a.rows; row += stride) {
     const float2 sy = make_float2(st.x, st.y);
     const float2 sh = pre ? make_float2(st.z, st.w) : make_float2(0.f, 0.f);
+    if constexpr (kAhead) {
+      ahead.wait();
+#pragma unroll
+      for (int v = 0; v < kV; ++v) {
+        dz[v] = *ahead.at(kInDz, v);
+        h[v] = *ahead.at(kInH, v);
+        up[v] = *ahead.at(kInUp, v);
+        y[v] = *ahead.at(kInY, v);
+      }
+      if (row + stride < a.rows) load(row + stride);
+    }
     Eight d[kV], xh[kV], xy[kV];  // E, then D; h^; y^ (or y)
     uint32_t keep[kV];
     Pair part[kValues];
@@ -498,7 +550,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_grad_kernel(const Args a)
         }
       }
     }
-    if (row + stride < a.rows) load(row + stride);
+    if (!kAhead && row + stride < a.rows) load(row + stride);
     float s[kValues];
 #pragma unroll
     for (int q = 0; q < kValues; ++q) s[q] = sum_of(part[q]);
@@ -679,9 +731,14 @@ void set_common(Args& a, const zero_join_params& p, const zero_join_weights& w, 
   a.drop = drop_of(p.drop);
 }
 
+// `columns` numbers per column and `words` of 16 bytes per thread
+int smem_bytes(const Args& a, int columns, int words) {
+  return 32 * columns * a.slots_of_row + 16 * words * kMaxThreads;
+}
+
 template <class Kernel>
-cudaError_t launch_with(Kernel fn, const Args& a, int columns, int sums, cudaStream_t st) {
-  const int bytes = 32 * (columns * a.slots_of_row + sums * kMaxThreads);
+cudaError_t launch_with(Kernel fn, const Args& a, int columns, int words, cudaStream_t st) {
+  const int bytes = smem_bytes(a, columns, words);
   if (bytes > 40 * 1024) {  // 48 KB with the kernels' own
     const cudaError_t e =
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -702,9 +759,14 @@ cudaError_t launch_join(const Args& a, int per, cudaStream_t st) {
 
 template <bool kBf16, bool kGrid, bool kLayer>
 cudaError_t launch_grad(const Args& a, int per, cudaStream_t st) {
-  constexpr int kAll = sums_of(kLayer);
-  if (per == 1) return launch_with(join_grad_kernel<kBf16, kGrid, kLayer, 1>, a, 2, kAll, st);
-  return launch_with(join_grad_kernel<kBf16, kGrid, kLayer, 2>, a, 2, 2 * kAll, st);
+  constexpr int kSumWords = 2 * sums_of(kLayer), kWords = kSumWords + kArrays;
+  if (per == 1)
+    return launch_with(join_grad_kernel<kBf16, kGrid, kLayer, 1, kGrid>, a, 2,
+                       kGrid ? kWords : kSumWords, st);
+  // the widest rows with all four sums leave no room for the next row
+  if (kGrid && smem_bytes(a, 2, 2 * kWords) <= kMostBytes)
+    return launch_with(join_grad_kernel<kBf16, kGrid, kLayer, 2, kGrid>, a, 2, 2 * kWords, st);
+  return launch_with(join_grad_kernel<kBf16, kGrid, kLayer, 2, false>, a, 2, 2 * kSumWords, st);
 }
 
 // fn<bf16, grid, layer>(...) for run-time values
