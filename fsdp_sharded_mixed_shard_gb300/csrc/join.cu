@@ -413,8 +413,16 @@ struct ColumnSums {
 // P, A and, with ZERO_NORM_LAYER, Q and B after them
 __host__ __device__ constexpr int sums_of(bool layer) { return layer ? kSums : 2; }
 
-// a row's sums, by their place among the values that a team adds up
-enum { kGH, kYE, kYH, kY1, kE1, kH1, kG1, kK1, kRowSums };
+// a row's sums, by their place among the values that a team adds up: those for
+// the norm before the next block (one, or two with ZERO_NORM_LAYER), then those
+// for the norm after this one
+enum { kGH, kG1, kRowSums = 8 };
+template <bool kLayer>
+struct Branch {
+  static constexpr int kFirst = kLayer ? 2 : 1;
+  static constexpr int kYE = kFirst, kYH = kYE + 1, kY1 = kYE + 2, kE1 = kYE + 3, kH1 = kYE + 4,
+                       kK1 = kYE + 5;
+};
 static_assert(kRowSums <= kMaxValues, "exchange");
 
 // A row's vectors on their way into shared memory, each thread's into words of
@@ -445,11 +453,12 @@ struct Ahead {
   }
 };
 
-// kAhead: rows come by Ahead (kGrid only), else by loads into registers half a
-// row's work before.
-template <bool kBf16, bool kGrid, bool kLayer, int kV, bool kAhead>
+// kPost: there is a norm after the block. kAhead: rows come by Ahead (kGrid only),
+// else by loads into registers half a row's work before.
+template <bool kBf16, bool kGrid, bool kLayer, bool kPost, int kV, bool kAhead>
 __global__ void __launch_bounds__(kMaxThreads, 1) join_grad_kernel(const Args a) {
-  constexpr int kValues = kLayer ? kRowSums : 3;
+  using B = Branch<kLayer>;
+  constexpr int kValues = !kPost ? B::kFirst : kLayer ? kRowSums : 3;
   pdl_begin();
   extern __shared__ float4 smem[];
   __shared__ Exchange exchange;
@@ -458,8 +467,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_grad_kernel(const Args a)
   const Place p(a);
   uint8_t* stage = stages + (kGrid ? 0 : (threadIdx.x >> 5) * kStagePitch);
   int turn = 0;
-  const bool post = a.param[kWPost] != nullptr, pre = a.param[kWPre] != nullptr;
-  const bool need_y = post || a.param[kGate] != nullptr;
+  const bool pre = a.param[kWPre] != nullptr;
+  const bool need_y = kPost || a.param[kGate] != nullptr;
   const uint32_t step = step_of(a.drop);
   const int64_t stride = static_cast<int64_t>(gridDim.x) * a.teams;
   int64_t row = static_cast<int64_t>(blockIdx.x) * a.teams + p.team;
@@ -516,7 +525,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_grad_kernel(const Args a)
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
       const Eight w = column(a, smem, kPre, col[v]), g0 = widen_pairs<kBf16>(dz[v]);
-      Eight k = column(a, smem, kC, col[v]), g;
+      Eight g;
       xh[v] = widen_pairs<kBf16>(h[v]);
       xy[v] = widen_pairs<kBf16>(y[v]);
       d[v] = widen_pairs<kBf16>(up[v]);
@@ -528,41 +537,47 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_grad_kernel(const Args a)
         d[v].p[j] = fma2(g.p[j], both(sh.y), d[v].p[j]);
       }
       sums.add(0, v, g0, xh[v]);
-      if constexpr (kLayer) sums.add(2, v, g0);
-      if (post)
+      if constexpr (kLayer) {
+        sums.add(2, v, g0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) xy[v].p[j] = normed<kLayer>(xy[v].p[j], sy);
-      if (a.drop.threshold) {
-        keep[v] = kept(a.drop, step, row, col[v]);
-        drop_pairs(a.drop, keep[v], k);
+        for (int j = 0; j < 4; ++j) part[kG1] = part[kG1] + g.p[j];
       }
+      if (a.drop.threshold) keep[v] = kept(a.drop, step, row, col[v]);
+      if constexpr (kPost) {
+        Eight k = column(a, smem, kC, col[v]);
+        if (a.drop.threshold) drop_pairs(a.drop, keep[v], k);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const Pair ky = k.p[j] * xy[v].p[j];
-        part[kYE] = fma2(ky, d[v].p[j], part[kYE]);
-        part[kYH] = fma2(ky, xh[v].p[j], part[kYH]);
-        if constexpr (kLayer) {
-          part[kY1] = part[kY1] + ky;
-          part[kE1] = fma2(k.p[j], d[v].p[j], part[kE1]);
-          part[kH1] = fma2(k.p[j], xh[v].p[j], part[kH1]);
-          part[kG1] = part[kG1] + g.p[j];
-          part[kK1] = part[kK1] + k.p[j];
+        for (int j = 0; j < 4; ++j) {
+          xy[v].p[j] = normed<kLayer>(xy[v].p[j], sy);
+          const Pair ky = k.p[j] * xy[v].p[j];
+          part[B::kYE] = fma2(ky, d[v].p[j], part[B::kYE]);
+          part[B::kYH] = fma2(ky, xh[v].p[j], part[B::kYH]);
+          if constexpr (kLayer) {
+            part[B::kY1] = part[B::kY1] + ky;
+            part[B::kE1] = fma2(k.p[j], d[v].p[j], part[B::kE1]);
+            part[B::kH1] = fma2(k.p[j], xh[v].p[j], part[B::kH1]);
+            part[B::kK1] = part[B::kK1] + k.p[j];
+          }
         }
       }
     }
     if (!kAhead && row + stride < a.rows) load(row + stride);
+    // r c1, r c2, mean(k D y^), mean(k D)
     float s[kValues];
 #pragma unroll
     for (int q = 0; q < kValues; ++q) s[q] = sum_of(part[q]);
     team_sum(a, p, exchange, turn, s);
-    const float c1 = sh.y * (s[kGH] * a.inv_cols);  // r c1, r c2
-    float c2 = 0.f, along = s[kYE] - c1 * s[kYH], flat = 0.f;
-    if constexpr (kLayer) {
-      c2 = sh.y * (s[kG1] * a.inv_cols);
-      along = s[kYE] - (c1 * s[kYH] + c2 * s[kY1]);
-      flat = (s[kE1] - (c1 * s[kH1] + c2 * s[kK1])) * a.inv_cols;
+    const float c1 = sh.y * (s[kGH] * a.inv_cols);
+    float c2 = 0.f, along = 0.f, flat = 0.f;
+    if constexpr (kLayer) c2 = sh.y * (s[kG1] * a.inv_cols);
+    if constexpr (kPost) {
+      along = s[B::kYE] - c1 * s[B::kYH];
+      if constexpr (kLayer) {
+        along -= c2 * s[B::kY1];
+        flat = (s[B::kE1] - (c1 * s[B::kH1] + c2 * s[B::kK1])) * a.inv_cols;
+      }
+      along *= a.inv_cols;
     }
-    along *= a.inv_cols;
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
       Eight e;
@@ -575,12 +590,14 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_grad_kernel(const Args a)
       store_at<kGrid>(stage, a.dh, row * a.ld, p.first(a, v), p.lane, a.cols,
                       narrow_pairs<kBf16>(e), a.bounds(kDh));
       if (a.drop.threshold) drop_pairs(a.drop, keep[v], d[v]);
-      sums.add(1, v, d[v], xy[v]);
-      if constexpr (kLayer) sums.add(3, v, d[v]);
+      if (need_y) {
+        sums.add(1, v, d[v], xy[v]);
+        if constexpr (kLayer) sums.add(3, v, d[v]);
+      }
       const Eight c = column(a, smem, kC, col[v]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) e.p[j] = d[v].p[j] * c.p[j];
-      if (post)
+      if constexpr (kPost)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           Pair t = fma2(xy[v].p[j], both(-along), e.p[j]);
@@ -627,30 +644,44 @@ struct JoinArgs : Checked<1> {
 };
 
 constexpr int kJoinThreads = 256, kJoinGroups = kJoinThreads / 8;
+constexpr int kJoinEach = (kMaxParts + kJoinGroups - 1) / kJoinGroups;  // vectors of a group
 
 template <bool kBf16>
 __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const JoinArgs a) {
   pdl_begin();
-  __shared__ float4 sums[2][kJoinGroups][8];
+  __shared__ float4 sums[2][kJoinThreads / 32][8];
   const int lane = threadIdx.x & 7, group = threadIdx.x >> 3;
   const bool branch = blockIdx.y != 0;
   const int c = (blockIdx.x * 8 + lane) * 4;
   const int64_t step = static_cast<int64_t>(a.slots) * a.pitch;
-  const int lo = a.n_parts * group / kJoinGroups, hi = a.n_parts * (group + 1) / kJoinGroups;
+  // all loads before the first sum: a group's vectors are kJoinGroups apart
+  float4 x[2][kJoinEach];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int slot = branch ? a.slot[k ? kSumB : kSumA] : a.slot[k ? kSumQ : kSumP];
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (slot >= 0 && c < a.pitch) {
-      const float* from = a.parts + static_cast<int64_t>(slot) * a.pitch + c;
-#pragma unroll 5
-      for (int q = lo; q < hi; ++q) {
-        if (!a.bounds(0).holds(from + q * step, 16, kSiteLoad)) continue;
-        const float4 x = *reinterpret_cast<const float4*>(from + q * step);
-        s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
-      }
+#pragma unroll
+    for (int q = 0; q < kJoinEach; ++q) {
+      const int part = q * kJoinGroups + group;
+      const float* from = a.parts + part * step + static_cast<int64_t>(slot) * a.pitch + c;
+      x[k][q] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (slot >= 0 && c < a.pitch && part < a.n_parts && a.bounds(0).holds(from, 16, kSiteLoad))
+        x[k][q] = *reinterpret_cast<const float4*>(from);
     }
-    sums[k][group][lane] = s;
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float4 s = x[k][0];
+#pragma unroll
+    for (int q = 1; q < kJoinEach; ++q)
+      s.x += x[k][q].x, s.y += x[k][q].y, s.z += x[k][q].z, s.w += x[k][q].w;
+#pragma unroll
+    for (int d = 8; d < 32; d *= 2) {
+      s.x += __shfl_xor_sync(0xffffffffu, s.x, d);
+      s.y += __shfl_xor_sync(0xffffffffu, s.y, d);
+      s.z += __shfl_xor_sync(0xffffffffu, s.z, d);
+      s.w += __shfl_xor_sync(0xffffffffu, s.w, d);
+    }
+    if ((threadIdx.x & 31) < 8) sums[k][threadIdx.x >> 5][lane] = s;
   }
   __syncthreads();
   // a warp: one column per thread
@@ -660,8 +691,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const JoinArgs
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     s[k] = 0.f;
-    for (int g = 0; g < kJoinGroups; ++g)
-      s[k] += reinterpret_cast<const float*>(&sums[k][g][0])[t];
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w)
+      s[k] += reinterpret_cast<const float*>(&sums[k][w][0])[t];
   }
   const auto param = [&](int w, float none) {
     return a.param[w] ? widen<kBf16>(a.param[w][at]) : none;
@@ -693,6 +725,11 @@ int set_teams(Args& a, int64_t rows, int64_t cols, int most) {
   while (per > 1 && ceil_div(vectors, 32 * per / 2) <= kMaxWarps &&
          rows * ceil_div(vectors, 32 * per) < kMaxParts * kMaxWarps / 2)
     per /= 2;
+  // two vectors per thread leave up to half of a row's last warp idle: one, where
+  // that fits a quarter tighter (8192 x 768 backward 25 us against 27)
+  const auto room = [&](int n) { return n * ceil_div(vectors, 32 * n); };
+  if (most == kBackVectors && per == 2 && vectors <= kMaxThreads && 4 * room(2) > 5 * room(1))
+    per = 1;
   a.team_warps = static_cast<int32_t>(ceil_div(vectors, 32 * per));
   a.teams = static_cast<int32_t>(std::min<int64_t>(
       kMaxWarps / a.team_warps, std::max<int64_t>(1, ceil_div(rows, kMaxParts))));
@@ -757,16 +794,22 @@ cudaError_t launch_join(const Args& a, int per, cudaStream_t st) {
   return launch_with(join_kernel<kBf16, kGrid, kLayer, 4>, a, kColumns, 0, st);
 }
 
-template <bool kBf16, bool kGrid, bool kLayer>
-cudaError_t launch_grad(const Args& a, int per, cudaStream_t st) {
+template <bool kBf16, bool kGrid, bool kLayer, bool kPost>
+cudaError_t launch_grad_of(const Args& a, int per, cudaStream_t st) {
   constexpr int kSumWords = 2 * sums_of(kLayer), kWords = kSumWords + kArrays;
   if (per == 1)
-    return launch_with(join_grad_kernel<kBf16, kGrid, kLayer, 1, kGrid>, a, 2,
+    return launch_with(join_grad_kernel<kBf16, kGrid, kLayer, kPost, 1, kGrid>, a, 2,
                        kGrid ? kWords : kSumWords, st);
   // the widest rows with all four sums leave no room for the next row
   if (kGrid && smem_bytes(a, 2, 2 * kWords) <= kMostBytes)
-    return launch_with(join_grad_kernel<kBf16, kGrid, kLayer, 2, kGrid>, a, 2, 2 * kWords, st);
-  return launch_with(join_grad_kernel<kBf16, kGrid, kLayer, 2, false>, a, 2, 2 * kSumWords, st);
+    return launch_with(join_grad_kernel<kBf16, kGrid, kLayer, kPost, 2, kGrid>, a, 2, 2 * kWords, st);
+  return launch_with(join_grad_kernel<kBf16, kGrid, kLayer, kPost, 2, false>, a, 2, 2 * kSumWords, st);
+}
+
+template <bool kBf16, bool kGrid, bool kLayer>
+cudaError_t launch_grad(const Args& a, int per, cudaStream_t st) {
+  return a.param[kWPost] ? launch_grad_of<kBf16, kGrid, kLayer, true>(a, per, st)
+                         : launch_grad_of<kBf16, kGrid, kLayer, false>(a, per, st);
 }
 
 // fn<bf16, grid, layer>(...) for run-time values
