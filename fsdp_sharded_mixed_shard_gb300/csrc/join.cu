@@ -25,8 +25,7 @@
  *   P = sum dz h^,  Q = sum dz,  A = sum m D y^,  B = sum m D:
  *   dw_pre = P, db_pre = Q, dw_post = branch_scale gate A,
  *   db_post = branch_scale gate B, dgate = branch_scale (w_post A + b_post B).
- * A thread adds those of its own columns up in shared memory. A CTA joins its
- * teams' in order and leaves one vector each in the workspace; a second kernel
+ * A thread adds those of its own columns up. A CTA joins its teams' in order and leaves one vector each in the workspace; a second kernel
  * adds the (at most kMaxParts) vectors in order.
  */
 #include "draws.cuh"
@@ -42,7 +41,6 @@ using namespace zt;
 constexpr int kMaxThreads = 512;  // of a CTA, one per SM, 128 registers each
 constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxParts = 152;    // CTAs
-constexpr int kMostBytes = 224 * 1024;  // of shared memory, beside the kernels' own
 // vectors per thread at most
 constexpr int kForwardVectors = 4, kBackVectors = 2;
 static_assert(ZERO_MAX_JOIN_COLS <= kBackVectors * kMaxThreads * kVec, "a row fits a CTA");
@@ -140,19 +138,78 @@ __device__ __forceinline__ void write_eight_at(float4* at, int apart, const Eigh
   at[apart] = make_float4(f[4], f[5], f[6], f[7]);
 }
 
-// Where an array's vectors of this row are. kGrid: rows lie on the 16-byte grid
-// and consist of whole vectors.
-template <bool kGrid>
-__device__ __forceinline__ uint4 load_at(const uint16_t* x, int64_t row_start, int col, int cols,
-                                         const Bounds& in) {
-  if constexpr (kGrid) {
-    const uint16_t* at = x + row_start + col;
-    if (col >= cols || !in.holds(at, 16, kSiteLoad)) return make_uint4(0, 0, 0, 0);
-    return __ldcs(reinterpret_cast<const uint4*>(at));
-  } else {
-    return load8<false>(x + row_start, col, cols, in);
+// kGrid: rows lie on the 16-byte grid and consist of whole vectors.
+
+// A row of kArrays arrays on its way into shared memory, the row after the one
+// that is worked on: each warp its own kV times 256 columns, as the 16-byte blocks
+// that hold them.
+template <int kArrays, int kV, bool kGrid>
+struct Ahead {
+  static constexpr int kSpan = kGrid ? 32 : 34;  // blocks of 256 columns
+  static constexpr int kBytes = kArrays * kV * kMaxWarps * kSpan * 16;
+  uint4* own;  // the warp's
+  int lane;
+  __device__ __forceinline__ Ahead(void* smem)
+      : own(static_cast<uint4*>(smem) + (threadIdx.x >> 5) * kSpan), lane(threadIdx.x & 31) {
+    if constexpr (kGrid)  // past the last column nothing comes
+#pragma unroll
+      for (int k = 0; k < kArrays; ++k)
+#pragma unroll
+        for (int v = 0; v < kV; ++v) at(k, v)[lane] = make_uint4(0, 0, 0, 0);
   }
-}
+  __device__ __forceinline__ uint4* at(int array, int v) const {
+    return own + (array * kV + v) * (kMaxWarps * kSpan);
+  }
+  __device__ __forceinline__ static void copy(uint4* to, const uint4* from) {
+    const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+  }
+  // columns [first, first + 256) of the row of x that starts at row_start
+  __device__ __forceinline__ void start(int array, int v, const uint16_t* x, int64_t row_start,
+                                        int first, int cols, const Bounds& in) const {
+    const uint16_t* from = x + row_start + first;
+    if constexpr (kGrid) {
+      from += lane * kVec;
+      if (first + lane * kVec < cols && in.holds(from, 16, kSiteLoad))
+        copy(at(array, v) + lane, reinterpret_cast<const uint4*>(from));
+    } else {
+      const uintptr_t begin = reinterpret_cast<uintptr_t>(from);
+      const int d = static_cast<int>(begin & 15), n = min(kCols, cols - first);
+      const uint4* block = reinterpret_cast<const uint4*>(begin - d);
+      const int blocks = n > 0 ? (d + 2 * n + 15) >> 4 : 0;
+      if (lane < blocks && in.holds_blocks(block + lane, 16, kSiteLoad))
+        copy(at(array, v) + lane, block + lane);
+      if (blocks > 32 && lane == 0 && in.holds_blocks(block + 32, 16, kSiteLoad))
+        copy(at(array, v) + 32, block + 32);
+    }
+  }
+  // all that the warp has started is there
+  __device__ __forceinline__ void wait() const {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if constexpr (!kGrid) __syncwarp();
+  }
+  // the lane's eight columns, of which `there` are columns and the others 0
+  __device__ __forceinline__ uint4 read(int array, int v, const uint16_t* x, int64_t row_start,
+                                        int there) const {
+    uint4 b = at(array, v)[lane];
+    if constexpr (!kGrid) {
+      const int d = static_cast<int>(reinterpret_cast<uintptr_t>(x + row_start) & 15);
+      b = shifted_alike(b, at(array, v)[lane + 1], d);
+    }
+    if (!kGrid && there < kVec) {
+      const uint32_t low = 0xFFFFu;
+      b.x = there > 1 ? b.x : there == 1 ? b.x & low : 0;
+      b.y = there > 3 ? b.y : there == 3 ? b.y & low : 0;
+      b.z = there > 5 ? b.z : there == 5 ? b.z & low : 0;
+      b.w = there == 7 ? b.w & low : 0;
+    }
+    return b;
+  }
+  // the warp has read all: the next row may come
+  __device__ __forceinline__ void done() const {
+    if constexpr (!kGrid) __syncwarp();
+  }
+};
 
 template <bool kGrid>
 __device__ __forceinline__ void store_at(uint8_t* stage, uint16_t* x, int64_t row_start, int first,
@@ -315,26 +372,33 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_kernel(const Args a) {
   const int64_t stride = static_cast<int64_t>(gridDim.x) * a.teams;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.teams + p.team;
   int col[kV], there[kV];
-  uint4 y[kV], next[kV];
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
     col[v] = p.first(a, v) + p.lane * kVec;
     there[v] = max(0, min(kVec, a.cols - col[v]));
   }
-  const auto load = [&](int64_t row) {
+  // behind the columns' numbers
+  const Ahead<2, kV, kGrid> ahead(smem + 2 * (kLayer ? 4 : 2) * a.slots_of_row);
+  const auto start = [&](int64_t row) {
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
-      y[v] = load_at<kGrid>(a.y, row * a.ld, col[v], a.cols, a.bounds(kY));
-      next[v] = load_at<kGrid>(a.h, row * a.ld, col[v], a.cols, a.bounds(kH));
+      ahead.start(0, v, a.y, row * a.ld, p.first(a, v), a.cols, a.bounds(kY));
+      ahead.start(1, v, a.h, row * a.ld, p.first(a, v), a.cols, a.bounds(kH));
     }
   };
-  if (row0 < a.rows) load(row0);  // under way while the columns' numbers are set up
+  if (row0 < a.rows) start(row0);  // under way while the columns' numbers are set up
   stage_columns<kBf16, kLayer ? 4 : 2>(a, smem);
   clear(exchange);
   for (int64_t row = row0; row < a.rows; row += stride) {
-    uint4 h[kV];
+    uint4 y[kV], h[kV];
+    ahead.wait();
 #pragma unroll
-    for (int v = 0; v < kV; ++v) h[v] = next[v];
+    for (int v = 0; v < kV; ++v) {
+      y[v] = ahead.read(0, v, a.y, row * a.ld, there[v]);
+      h[v] = ahead.read(1, v, a.h, row * a.ld, there[v]);
+    }
+    ahead.done();
+    if (row + stride < a.rows) start(row + stride);
     float2 sy = make_float2(0.f, 1.f), sh = make_float2(0.f, 0.f);
     if (post) sy = row_stats<kBf16, kLayer, kV>(a, p, exchange, turn, y, there);
 #pragma unroll
@@ -356,7 +420,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_kernel(const Args a) {
       store_at<kGrid>(stage, a.h_new, row * a.ld, p.first(a, v), p.lane, a.cols, h[v],
                       a.bounds(kHOut));
     }
-    if (row + stride < a.rows) load(row + stride);
     if (pre) {
       sh = row_stats<kBf16, kLayer, kV>(a, p, exchange, turn, h, there);
 #pragma unroll
@@ -380,38 +443,32 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_kernel(const Args a) {
   }
 }
 
-// Sums over the rows of a thread's own columns, in shared memory: eight floats
-// for each sum and vector, the thread's own words.
+// Sums over the rows of a thread's own columns: P and A in shared memory, eight
+// floats for each sum and vector in the thread's own words; Q and B, which belong
+// to ZERO_NORM_LAYER, in registers until the rows are done.
 template <int kV>
 struct ColumnSums {
   float4* own;
   __device__ __forceinline__ float4* at(int k, int v) const {
     return own + (k * kV + v) * 2 * kMaxThreads;
   }
-  __device__ __forceinline__ ColumnSums(float4* sums, int count) : own(sums + threadIdx.x) {
-    for (int k = 0; k < count; ++k)
+  __device__ __forceinline__ explicit ColumnSums(float4* sums) : own(sums + threadIdx.x) {
 #pragma unroll
-      for (int v = 0; v < kV; ++v)
-        write_eight_at(at(k, v), kMaxThreads, Eight{{both(0.f), both(0.f), both(0.f), both(0.f)}});
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int v = 0; v < kV; ++v) put(k, v, Eight{{both(0.f), both(0.f), both(0.f), both(0.f)}});
+  }
+  __device__ __forceinline__ void put(int k, int v, const Eight& e) const {
+    write_eight_at(at(k, v), kMaxThreads, e);
   }
   // += x y
   __device__ __forceinline__ void add(int k, int v, const Eight& x, const Eight& y) const {
     Eight s = read_eight_at(at(k, v), kMaxThreads);
 #pragma unroll
     for (int j = 0; j < 4; ++j) s.p[j] = fma2(x.p[j], y.p[j], s.p[j]);
-    write_eight_at(at(k, v), kMaxThreads, s);
-  }
-  // += x
-  __device__ __forceinline__ void add(int k, int v, const Eight& x) const {
-    Eight s = read_eight_at(at(k, v), kMaxThreads);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) s.p[j] = s.p[j] + x.p[j];
-    write_eight_at(at(k, v), kMaxThreads, s);
+    put(k, v, s);
   }
 };
-
-// P, A and, with ZERO_NORM_LAYER, Q and B after them
-__host__ __device__ constexpr int sums_of(bool layer) { return layer ? kSums : 2; }
 
 // a row's sums, by their place among the values that a team adds up: those for
 // the norm before the next block (one, or two with ZERO_NORM_LAYER), then those
@@ -425,37 +482,8 @@ struct Branch {
 };
 static_assert(kRowSums <= kMaxValues, "exchange");
 
-// A row's vectors on their way into shared memory, each thread's into words of
-// its own, while the row before is worked on: kArrays arrays of kV vectors.
-enum { kInDz, kInH, kInUp, kInY, kArrays };
-
-template <int kV>
-struct Ahead {
-  uint4* own;
-  __device__ __forceinline__ uint4* at(int array, int v) const {
-    return own + (array * kV + v) * kMaxThreads;
-  }
-  __device__ __forceinline__ void clear() const {  // past the last column there are zeros
-#pragma unroll
-    for (int k = 0; k < kArrays; ++k)
-#pragma unroll
-      for (int v = 0; v < kV; ++v) *at(k, v) = make_uint4(0, 0, 0, 0);
-  }
-  __device__ __forceinline__ void start(int array, int v, const uint16_t* x, int64_t row_start,
-                                        int col, int cols, const Bounds& in) const {
-    const uint16_t* from = x + row_start + col;
-    if (col >= cols || !in.holds(from, 16, kSiteLoad)) return;
-    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(at(array, v)));
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-  }
-  __device__ __forceinline__ void wait() const {
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  }
-};
-
-// kPost: there is a norm after the block. kAhead: rows come by Ahead (kGrid only),
-// else by loads into registers half a row's work before.
-template <bool kBf16, bool kGrid, bool kLayer, bool kPost, int kV, bool kAhead>
+// kPost: there is a norm after the block.
+template <bool kBf16, bool kGrid, bool kLayer, bool kPost, int kV>
 __global__ void __launch_bounds__(kMaxThreads, 1) join_grad_kernel(const Args a) {
   using B = Branch<kLayer>;
   constexpr int kValues = !kPost ? B::kFirst : kLayer ? kRowSums : 3;
@@ -472,51 +500,50 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_grad_kernel(const Args a)
   const uint32_t step = step_of(a.drop);
   const int64_t stride = static_cast<int64_t>(gridDim.x) * a.teams;
   int64_t row = static_cast<int64_t>(blockIdx.x) * a.teams + p.team;
-  const uint4 none = make_uint4(0, 0, 0, 0);
-  int col[kV];
+  int col[kV], there[kV];
 #pragma unroll
-  for (int v = 0; v < kV; ++v) col[v] = p.first(a, v) + p.lane * kVec;
-  uint4 y[kV], h[kV], dz[kV], up[kV];
+  for (int v = 0; v < kV; ++v) {
+    col[v] = p.first(a, v) + p.lane * kVec;
+    there[v] = max(0, min(kVec, a.cols - col[v]));
+  }
   float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
-  const Ahead<kV> ahead = {
-      reinterpret_cast<uint4*>(sums_smem + sums_of(kLayer) * kV * 2 * kMaxThreads) + threadIdx.x};
-  if constexpr (kAhead) ahead.clear();
-  const auto load = [&](int64_t r) {
+  const Ahead<4, kV, kGrid> ahead(sums_smem + 2 * kV * 2 * kMaxThreads);
+  const auto start = [&](int64_t r) {
     const int64_t at = r * a.ld;
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
-      if constexpr (kAhead) {
-        if (pre) ahead.start(kInDz, v, a.dz, at, col[v], a.cols, a.bounds(kDz));
-        if (pre) ahead.start(kInH, v, a.h_out, at, col[v], a.cols, a.bounds(kHOut));
-        if (a.dh_out) ahead.start(kInUp, v, a.dh_out, at, col[v], a.cols, a.bounds(kDhOut));
-        if (need_y) ahead.start(kInY, v, a.y, at, col[v], a.cols, a.bounds(kY));
-        continue;
-      }
-      dz[v] = pre ? load_at<kGrid>(a.dz, at, col[v], a.cols, a.bounds(kDz)) : none;
-      h[v] = pre ? load_at<kGrid>(a.h_out, at, col[v], a.cols, a.bounds(kHOut)) : none;
-      up[v] = a.dh_out ? load_at<kGrid>(a.dh_out, at, col[v], a.cols, a.bounds(kDhOut)) : none;
-      y[v] = need_y ? load_at<kGrid>(a.y, at, col[v], a.cols, a.bounds(kY)) : none;
+      const int first = p.first(a, v);
+      if (pre) ahead.start(0, v, a.dz, at, first, a.cols, a.bounds(kDz));
+      if (pre) ahead.start(1, v, a.h_out, at, first, a.cols, a.bounds(kHOut));
+      if (a.dh_out) ahead.start(2, v, a.dh_out, at, first, a.cols, a.bounds(kDhOut));
+      if (need_y) ahead.start(3, v, a.y, at, first, a.cols, a.bounds(kY));
     }
     if (a.bounds(kStats).holds(a.stats + r, 16, kSiteLoad)) st = a.stats[r];
   };
-  if (row < a.rows) load(row);  // under way while the columns' numbers are set up
+  if (row < a.rows) start(row);  // under way while the columns' numbers are set up
   stage_columns<kBf16, 2>(a, smem);
-  const ColumnSums<kV> sums(sums_smem, sums_of(kLayer));
+  const ColumnSums<kV> sums(sums_smem);
+  Eight sum_q[kV], sum_b[kV];
+#pragma unroll
+  for (int v = 0; v < kV; ++v)
+    sum_q[v] = sum_b[v] = Eight{{both(0.f), both(0.f), both(0.f), both(0.f)}};
   clear(exchange);
   for (; row < a.rows; row += stride) {
     const float2 sy = make_float2(st.x, st.y);
     const float2 sh = pre ? make_float2(st.z, st.w) : make_float2(0.f, 0.f);
-    if constexpr (kAhead) {
-      ahead.wait();
+    const int64_t at = row * a.ld;
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    uint4 y[kV], h[kV], dz[kV], up[kV];
+    ahead.wait();
 #pragma unroll
-      for (int v = 0; v < kV; ++v) {
-        dz[v] = *ahead.at(kInDz, v);
-        h[v] = *ahead.at(kInH, v);
-        up[v] = *ahead.at(kInUp, v);
-        y[v] = *ahead.at(kInY, v);
-      }
-      if (row + stride < a.rows) load(row + stride);
+    for (int v = 0; v < kV; ++v) {
+      dz[v] = pre ? ahead.read(0, v, a.dz, at, there[v]) : none;
+      h[v] = pre ? ahead.read(1, v, a.h_out, at, there[v]) : none;
+      up[v] = a.dh_out ? ahead.read(2, v, a.dh_out, at, there[v]) : none;
+      y[v] = need_y ? ahead.read(3, v, a.y, at, there[v]) : none;
     }
+    ahead.done();
+    if (row + stride < a.rows) start(row + stride);
     Eight d[kV], xh[kV], xy[kV];  // E, then D; h^; y^ (or y)
     uint32_t keep[kV];
     Pair part[kValues];
@@ -538,9 +565,11 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_grad_kernel(const Args a)
       }
       sums.add(0, v, g0, xh[v]);
       if constexpr (kLayer) {
-        sums.add(2, v, g0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) part[kG1] = part[kG1] + g.p[j];
+        for (int j = 0; j < 4; ++j) {
+          sum_q[v].p[j] = sum_q[v].p[j] + g0.p[j];
+          part[kG1] = part[kG1] + g.p[j];
+        }
       }
       if (a.drop.threshold) keep[v] = kept(a.drop, step, row, col[v]);
       if constexpr (kPost) {
@@ -561,7 +590,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_grad_kernel(const Args a)
         }
       }
     }
-    if (!kAhead && row + stride < a.rows) load(row + stride);
     // r c1, r c2, mean(k D y^), mean(k D)
     float s[kValues];
 #pragma unroll
@@ -592,7 +620,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_grad_kernel(const Args a)
       if (a.drop.threshold) drop_pairs(a.drop, keep[v], d[v]);
       if (need_y) {
         sums.add(1, v, d[v], xy[v]);
-        if constexpr (kLayer) sums.add(3, v, d[v]);
+        if constexpr (kLayer)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sum_b[v].p[j] = sum_b[v].p[j] + d[v].p[j];
       }
       const Eight c = column(a, smem, kC, col[v]);
 #pragma unroll
@@ -608,26 +638,36 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_grad_kernel(const Args a)
                       narrow_pairs<kBf16>(e), a.bounds(kDy));
     }
   }
-  // this CTA's vectors: the teams' sums joined in order
+  // this CTA's vectors: the teams' sums joined in order, P and A, then Q and B by
+  // the same words
   if (a.slots == 0) return;
-  __syncthreads();
   const int team_threads = 32 * a.team_warps;
   float* part = a.parts + static_cast<int64_t>(blockIdx.x) * a.slots * a.pitch;
-  for (int i = threadIdx.x; i < sums_of(kLayer) * a.slots_of_row; i += blockDim.x) {
-    const int q = i / a.slots_of_row, vector = i - q * a.slots_of_row;
-    const int v = vector / team_threads, t = vector - v * team_threads;
-    const int slot = a.slot[q], c = vector * kVec;
-    if (slot < 0 || c >= a.pitch) continue;
-    const float4* from = sums_smem + (q * kV + v) * 2 * kMaxThreads + t;
-    Eight s = read_eight_at(from, kMaxThreads);
-    for (int k = 1; k < a.teams; ++k) {
-      const Eight x = read_eight_at(from + k * team_threads, kMaxThreads);
+  for (int round = 0; round < (kLayer ? 2 : 1); ++round) {
+    if (kLayer && round)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s.p[j] = s.p[j] + x.p[j];
+      for (int v = 0; v < kV; ++v) {
+        sums.put(0, v, sum_q[v]);
+        sums.put(1, v, sum_b[v]);
+      }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * a.slots_of_row; i += blockDim.x) {
+      const int q = i / a.slots_of_row, vector = i - q * a.slots_of_row;
+      const int v = vector / team_threads, t = vector - v * team_threads;
+      const int slot = a.slot[2 * round + q], c = vector * kVec;
+      if (slot < 0 || c >= a.pitch) continue;
+      const float4* from = sums_smem + (q * kV + v) * 2 * kMaxThreads + t;
+      Eight s = read_eight_at(from, kMaxThreads);
+      for (int k = 1; k < a.teams; ++k) {
+        const Eight x = read_eight_at(from + k * team_threads, kMaxThreads);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s.p[j] = s.p[j] + x.p[j];
+      }
+      float* to = part + static_cast<int64_t>(slot) * a.pitch + c;
+      if (a.bounds(kParts).holds(to, 32, kSiteStore))
+        write_eight_at(reinterpret_cast<float4*>(to), 1, s);
     }
-    float* to = part + static_cast<int64_t>(slot) * a.pitch + c;
-    if (a.bounds(kParts).holds(to, 32, kSiteStore))
-      write_eight_at(reinterpret_cast<float4*>(to), 1, s);
+    __syncthreads();
   }
 }
 
@@ -768,15 +808,11 @@ void set_common(Args& a, const zero_join_params& p, const zero_join_weights& w, 
   a.drop = drop_of(p.drop);
 }
 
-// `columns` numbers per column and `words` of 16 bytes per thread
-int smem_bytes(const Args& a, int columns, int words) {
-  return 32 * columns * a.slots_of_row + 16 * words * kMaxThreads;
-}
-
+// `columns` numbers per column and `more` bytes of shared memory
 template <class Kernel>
-cudaError_t launch_with(Kernel fn, const Args& a, int columns, int words, cudaStream_t st) {
-  const int bytes = smem_bytes(a, columns, words);
-  if (bytes > 40 * 1024) {  // 48 KB with the kernels' own
+cudaError_t launch_with(Kernel fn, const Args& a, int columns, int more, cudaStream_t st) {
+  const int bytes = 32 * columns * a.slots_of_row + more;
+  if (bytes > 32 * 1024) {  // 48 KB with the kernels' own
     const cudaError_t e =
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
@@ -786,30 +822,32 @@ cudaError_t launch_with(Kernel fn, const Args& a, int columns, int words, cudaSt
                     bytes, st, a);
 }
 
-template <bool kBf16, bool kGrid, bool kLayer>
-cudaError_t launch_join(const Args& a, int per, cudaStream_t st) {
-  constexpr int kColumns = kLayer ? 4 : 2;
-  if (per == 1) return launch_with(join_kernel<kBf16, kGrid, kLayer, 1>, a, kColumns, 0, st);
-  if (per == 2) return launch_with(join_kernel<kBf16, kGrid, kLayer, 2>, a, kColumns, 0, st);
-  return launch_with(join_kernel<kBf16, kGrid, kLayer, 4>, a, kColumns, 0, st);
+template <bool kBf16, bool kGrid, bool kLayer, int kV>
+cudaError_t launch_join_of(const Args& a, cudaStream_t st) {
+  return launch_with(join_kernel<kBf16, kGrid, kLayer, kV>, a, kLayer ? 4 : 2,
+                     Ahead<2, kV, kGrid>::kBytes, st);
 }
 
-template <bool kBf16, bool kGrid, bool kLayer, bool kPost>
-cudaError_t launch_grad_of(const Args& a, int per, cudaStream_t st) {
-  constexpr int kSumWords = 2 * sums_of(kLayer), kWords = kSumWords + kArrays;
-  if (per == 1)
-    return launch_with(join_grad_kernel<kBf16, kGrid, kLayer, kPost, 1, kGrid>, a, 2,
-                       kGrid ? kWords : kSumWords, st);
-  // the widest rows with all four sums leave no room for the next row
-  if (kGrid && smem_bytes(a, 2, 2 * kWords) <= kMostBytes)
-    return launch_with(join_grad_kernel<kBf16, kGrid, kLayer, kPost, 2, kGrid>, a, 2, 2 * kWords, st);
-  return launch_with(join_grad_kernel<kBf16, kGrid, kLayer, kPost, 2, false>, a, 2, 2 * kSumWords, st);
+template <bool kBf16, bool kGrid, bool kLayer>
+cudaError_t launch_join(const Args& a, int per, cudaStream_t st) {
+  return per == 1   ? launch_join_of<kBf16, kGrid, kLayer, 1>(a, st)
+         : per == 2 ? launch_join_of<kBf16, kGrid, kLayer, 2>(a, st)
+                    : launch_join_of<kBf16, kGrid, kLayer, 4>(a, st);
+}
+
+template <bool kBf16, bool kGrid, bool kLayer, bool kPost, int kV>
+cudaError_t launch_grad_of(const Args& a, cudaStream_t st) {
+  return launch_with(join_grad_kernel<kBf16, kGrid, kLayer, kPost, kV>, a, 2,
+                     2 * kV * 32 * kMaxThreads + Ahead<4, kV, kGrid>::kBytes, st);
 }
 
 template <bool kBf16, bool kGrid, bool kLayer>
 cudaError_t launch_grad(const Args& a, int per, cudaStream_t st) {
-  return a.param[kWPost] ? launch_grad_of<kBf16, kGrid, kLayer, true>(a, per, st)
-                         : launch_grad_of<kBf16, kGrid, kLayer, false>(a, per, st);
+  if (a.param[kWPost])
+    return per == 1 ? launch_grad_of<kBf16, kGrid, kLayer, true, 1>(a, st)
+                    : launch_grad_of<kBf16, kGrid, kLayer, true, 2>(a, st);
+  return per == 1 ? launch_grad_of<kBf16, kGrid, kLayer, false, 1>(a, st)
+                  : launch_grad_of<kBf16, kGrid, kLayer, false, 2>(a, st);
 }
 
 // fn<bf16, grid, layer>(...) for run-time values
