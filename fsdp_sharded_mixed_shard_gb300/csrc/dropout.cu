@@ -16,7 +16,7 @@ using namespace zt;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kPieces = 2;
+constexpr int kPieces = 2;  // of 256 columns per warp
 
 enum { kX, kResidual, kOut, kBuffers };  // a call's buffers, for their bounds
 
@@ -29,7 +29,7 @@ struct Args : Checked<kBuffers> {
 };
 
 template <bool kBf16, bool kGrid>
-__global__ void __launch_bounds__(kThreads) dropout_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, kGrid ? 6 : 5) dropout_kernel(const Args a) {
   pdl_begin();
   __shared__ __align__(16) uint8_t stages[kGrid ? 1 : kWarps][kGrid ? 16 : kStageWarp];
   uint8_t* stage = stages[kGrid ? 0 : threadIdx.x >> 5];
@@ -41,13 +41,20 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const Args a) {
   const int64_t c0 = static_cast<int64_t>(tile - row * a.col_tiles) * (kPieces * kCols);
   const uint32_t step = step_of(a.drop);
   uint4 vx[kPieces], vr[kPieces];
+  const auto column = [&](int k) { return c0 + k * kCols + lane * kVec; };
+  if constexpr (kGrid) {
 #pragma unroll
-  for (int k = 0; k < kPieces; ++k) {
-    const int64_t c = c0 + k * kCols + lane * kVec;
-    vx[k] = load8<kGrid>(a.x + r * a.ld, c, a.cols, a.bounds(kX));
-    vr[k] = make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < kPieces; ++k) {
+      vx[k] = load8<true>(a.x + r * a.ld, column(k), a.cols, a.bounds(kX));
+      vr[k] = make_uint4(0, 0, 0, 0);
+      if (a.residual)
+        vr[k] = load8<true>(a.residual + r * a.ld_out, column(k), a.cols, a.bounds(kResidual));
+    }
+  } else {
     if (a.residual)
-      vr[k] = load8<kGrid>(a.residual + r * a.ld_out, c, a.cols, a.bounds(kResidual));
+      load_all<false>(vr, [&](int) { return a.residual + r * a.ld_out; }, column, a.cols,
+                      a.bounds(kResidual));
+    load_all<false>(vx, [&](int) { return a.x + r * a.ld; }, column, a.cols, a.bounds(kX));
   }
 #pragma unroll
   for (int k = 0; k < kPieces; ++k) {
@@ -84,6 +91,7 @@ extern "C" ZERO_API int zero_dropout(const zero_dropout_params* params, const vo
   if (const int bad = check_drop(*params)) return bad;
   constexpr int64_t kMost = int64_t{1} << 31;
   if (rows >= kMost || cols >= kMost || rows * ceil_div(cols, kCols) >= kMost) return ZERO_ERANGE;
+  const bool grid = on_grid(x, ld) && on_grid(out, ld_out) && aligned(residual, 16);
   const int64_t col_tiles = ceil_div(cols, kPieces * kCols);
   if (rows == 0 || cols == 0) return ZERO_OK;
   if (!x || !out || (x == out && ld != ld_out)) return ZERO_EINVAL;
@@ -98,7 +106,6 @@ extern "C" ZERO_API int zero_dropout(const zero_dropout_params* params, const vo
   a.set_bounds(kX, x, rows, cols, ld, 2);
   a.set_bounds(kResidual, residual, rows, cols, ld_out, 2);
   a.set_bounds(kOut, out, rows, cols, ld_out, 2);
-  const bool grid = on_grid(x, ld) && on_grid(out, ld_out) && aligned(residual, 16);
   const auto fn = dtype == ZERO_BF16 ? (grid ? dropout_kernel<true, true> : dropout_kernel<true, false>)
                                      : (grid ? dropout_kernel<false, true> : dropout_kernel<false, false>);
   return status_of(launch_pdl(fn, dim3(static_cast<unsigned>(ceil_div(rows * col_tiles, kWarps))),

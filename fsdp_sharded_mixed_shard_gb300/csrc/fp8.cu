@@ -120,9 +120,10 @@ __global__ void __launch_bounds__(32 * kQuantWarps) quant_kernel(const QuantArgs
   const int64_t r = row;
   if (r >= a.rows) return;
   const int64_t c = static_cast<int64_t>(tile - row * a.col_tiles) * kQuantCols + lane * 16;
-  const uint4 v0 = load8<kGrid>(a.x + r * a.ld, c, a.cols, a.bounds(kX));
-  const uint4 v1 = load8<kGrid>(a.x + r * a.ld, c + 8, a.cols, a.bounds(kX));
-  uint32_t top = max_u16x2(top_of(v0), top_of(v1));
+  uint4 v[2];
+  load_all<kGrid>(v, [&](int) { return a.x + r * a.ld; }, [&](int k) { return c + 8 * k; }, a.cols,
+                  a.bounds(kX));
+  uint32_t top = max_u16x2(top_of(v[0]), top_of(v[1]));
 #pragma unroll
   for (int d = 1; d < 8; d *= 2) top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, d));
   top = max(top & 0xFFFFu, top >> 16);
@@ -130,8 +131,8 @@ __global__ void __launch_bounds__(32 * kQuantWarps) quant_kernel(const QuantArgs
   const uint32_t scale = scale_of<kBf16>(top, a.format);
   uint8_t* q = a.q + r * a.pitch + c;
   if (a.bounds(kCopy).holds(q, 16, kSiteStore)) {
-    const uint2 lo = narrow_fp8<kBf16>(v0, scale, a.format);
-    const uint2 hi = narrow_fp8<kBf16>(v1, scale, a.format);
+    const uint2 lo = narrow_fp8<kBf16>(v[0], scale, a.format);
+    const uint2 hi = narrow_fp8<kBf16>(v[1], scale, a.format);
     *reinterpret_cast<uint4*>(q) = make_uint4(lo.x, lo.y, hi.x, hi.y);
   }
   if ((lane & 7) == 0) {
@@ -141,44 +142,52 @@ __global__ void __launch_bounds__(32 * kQuantWarps) quant_kernel(const QuantArgs
   }
 }
 
-// A CTA takes one 128 x 128 block of a weight, a thread eight pieces of eight
-// columns in registers, so that it is read once.
+// A CTA takes two neighbouring 128 x 128 blocks of a weight, a warp 16 rows of
+// 256 columns in registers, so that it is read once and in runs of 512 bytes.
+// (Single blocks, runs of 256 bytes: 2048 x 8192 15 us.)
+constexpr int kWeightRows = 16;
+
 template <bool kBf16, bool kGrid>
 __global__ void __launch_bounds__(256) quant_weight_kernel(const QuantArgs a) {
   pdl_begin();
-  __shared__ uint32_t tops[8];
-  const int64_t kb = blockIdx.x / a.col_tiles, nb = blockIdx.x - kb * a.col_tiles;
-  const int tid = threadIdx.x, r0 = tid >> 4;
-  const int64_t c = nb * kBlock + (tid & 15) * kVec;
-  uint4 v[8];
+  __shared__ uint32_t tops[2][8];
+  const int64_t kb = blockIdx.x / a.col_tiles, nt = blockIdx.x - kb * a.col_tiles;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, side = lane >> 4;
+  const int64_t c = nt * kCols + lane * kVec, r0 = kb * kBlock + warp * kWeightRows;
+  uint4 v[kWeightRows];
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = kb * kBlock + r0 + 16 * i;
-    v[i] = r < a.rows ? load8<kGrid>(a.x + r * a.cols, c, a.cols, a.bounds(kX))
-                      : make_uint4(0, 0, 0, 0);
-    top = max_u16x2(top, top_of(v[i]));
+  for (int h = 0; h < 2; ++h) {  // two halves: off the grid a row takes twice the registers
+    uint4 w[kWeightRows / 2];
+    const auto row = [&](int i) { return r0 + h * (kWeightRows / 2) + i; };
+    load_all<kGrid>(w, [&](int i) { return a.x + row(i) * a.cols; },
+                    [&](int i) { return row(i) < a.rows ? c : a.cols; }, a.cols, a.bounds(kX));
+#pragma unroll
+    for (int i = 0; i < kWeightRows / 2; ++i) v[h * (kWeightRows / 2) + i] = w[i];
   }
 #pragma unroll
-  for (int d = 1; d < 32; d *= 2) top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, d));
-  if ((tid & 31) == 0) tops[tid >> 5] = top;
+  for (int i = 0; i < kWeightRows; ++i) top = max_u16x2(top, top_of(v[i]));
+#pragma unroll
+  for (int d = 1; d < 16; d *= 2) top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, d));
+  if ((lane & 15) == 0) tops[side][warp] = top;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < 8; ++w) top = max_u16x2(top, tops[w]);
+  for (int w = 0; w < 8; ++w) top = max_u16x2(top, tops[side][w]);
   const uint32_t scale = scale_of<kBf16>(max(top & 0xFFFFu, top >> 16), ZERO_E4M3);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = kb * kBlock + r0 + 16 * i;
-    uint8_t* q = a.q + r * a.pitch + c;
-    if (r < a.rows && a.bounds(kCopy).holds(q, kVec, kSiteStore))
+  for (int i = 0; i < kWeightRows; ++i) {
+    uint8_t* q = a.q + (r0 + i) * a.pitch + c;
+    if (r0 + i < a.rows && c < a.pitch && a.bounds(kCopy).holds(q, kVec, kSiteStore))
       *reinterpret_cast<uint2*>(q) = narrow_fp8<kBf16>(v[i], scale, ZERO_E4M3);
   }
-  // the scale of each of the block's 128 columns, then of its rows
-  const int m = tid & 127;
-  uint8_t* s = tid < 128
-                   ? a.scale + scale_at(nb * 128 + m, kb, (a.rows + 511) / 512)
-                   : a.scale_t + scale_at(kb * 128 + m, nb, (a.cols + 511) / 512);
-  if (a.bounds(kCopy).holds(s, 1, kSiteStore)) *s = static_cast<uint8_t>(scale);
+  // the scale of each of a block's 128 columns and rows
+  const int64_t nb = 2 * nt + side;
+  if (nb * kBlock >= a.cols) return;
+  const int m = warp * 16 + (lane & 15);
+  uint8_t* by_column = a.scale + scale_at(nb * 128 + m, kb, (a.rows + 511) / 512);
+  uint8_t* by_row = a.scale_t + scale_at(kb * 128 + m, nb, (a.cols + 511) / 512);
+  if (a.bounds(kCopy).holds(by_column, 1, kSiteStore)) *by_column = static_cast<uint8_t>(scale);
+  if (a.bounds(kCopy).holds(by_row, 1, kSiteStore)) *by_row = static_cast<uint8_t>(scale);
 }
 
 // ---------------------------------------------------------------- products ----
@@ -205,10 +214,11 @@ static_assert((1 + kScaleTiles) * kTileBytes <= kBytesScales && kStageBytes % 10
 static_assert(kM * kJoinPitch * 4 <= kRing, "the tile fits the stages");
 // costs in cycles: a block, and its thirds per column (128, 192 and 256 columns
 // took 484, 595 to 625 and 661 to 717 at 8192 x 2048 x 8192 and 8192^3, most of
-// it waiting for the copies); a column put out, the join of a split, clusters of
-// 16 CTAs
+// it waiting for the copies); a column put out; the join of a split, by rows per
+// warp (600 x 512 x 512 4.8 us, split in two 10.1; 16 x 8192 x 256 16 us, split in
+// two, four and eight 11.4, 8.0 and 7.2); clusters of 16 CTAs
 constexpr int kBlockCycles = 340, kColumnThirds = 4;
-constexpr int kOutCycles = 28, kJoinCycles = 3500, kBigClusterCycles = 4000;
+constexpr int kOutCycles = 14, kJoinCycles = 1500, kJoinRowCycles = 900, kBigClusterCycles = 4000;
 
 enum { kOut, kBuffers };
 
@@ -732,6 +742,9 @@ int multiply(const void* copy, int32_t format, int64_t rows, const void* w_copy,
   // Tile width and split of the reduction by the cycles they take: turns of all
   // pairs times their blocks, a tile put out alone at the end, and the join of a
   // split, which needs room for all its clusters at once.
+  const auto join_rows = [&](int split) {  // of a warp
+    return ceil_div(ceil_div(std::min<int64_t>(rows, kM), split), kWarps);
+  };
   int64_t best = 0;
   for (int bn = kN; bn >= 128; bn -= 64)
     for (int split = 1; split <= kMaxSplit; split *= 2) {
@@ -739,7 +752,7 @@ int multiply(const void* copy, int32_t format, int64_t rows, const void* w_copy,
       if (split > 1 && (all > fit[split] || a.blocks < 2 * split)) break;
       const int64_t cost = turns * ceil_div(a.blocks, split) *
                                (kBlockCycles + kColumnThirds * bn / 3) + kOutCycles * bn +
-                           (split > 1 ? kJoinCycles : 0) +
+                           (split > 1 ? kJoinCycles + join_rows(split) * kJoinRowCycles : 0) +
                            (split == kMaxSplit ? kBigClusterCycles : 0);
       if (best == 0 || cost < best) {
         best = cost;
@@ -835,7 +848,7 @@ ZERO_API int zero_fp8_quant_weight(const void* w, int64_t k, int64_t n, int32_t 
   a.q = static_cast<uint8_t*>(copy);
   a.scale = a.q + k * a.pitch;
   a.scale_t = a.scale + blocks_of(n) * groups_of(k) * kTileBytes;
-  a.col_tiles = static_cast<uint32_t>(blocks_of(n));
+  a.col_tiles = static_cast<uint32_t>(ceil_div(n, kCols));
   a.format = ZERO_E4M3;
   a.set_bounds(kX, w, k, n, n, 2);
   a.set_bounds(kCopy, copy, 1, static_cast<int64_t>(zero_fp8_weight_bytes(k, n)), 0, 1);
@@ -843,7 +856,7 @@ ZERO_API int zero_fp8_quant_weight(const void* w, int64_t k, int64_t n, int32_t 
   const auto fn = dtype == ZERO_BF16
                       ? (grid ? quant_weight_kernel<true, true> : quant_weight_kernel<true, false>)
                       : (grid ? quant_weight_kernel<false, true> : quant_weight_kernel<false, false>);
-  return status_of(launch_pdl(fn, dim3(static_cast<unsigned>(blocks_of(k) * blocks_of(n))),
+  return status_of(launch_pdl(fn, dim3(static_cast<unsigned>(blocks_of(k) * ceil_div(n, kCols))),
                               dim3(256), 0, static_cast<cudaStream_t>(stream), a));
 }
 

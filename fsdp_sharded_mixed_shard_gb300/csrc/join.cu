@@ -196,13 +196,7 @@ struct Ahead {
       const int d = static_cast<int>(reinterpret_cast<uintptr_t>(x + row_start) & 15);
       b = shifted_alike(b, at(array, v)[lane + 1], d);
     }
-    if (!kGrid && there < kVec) {
-      const uint32_t low = 0xFFFFu;
-      b.x = there > 1 ? b.x : there == 1 ? b.x & low : 0;
-      b.y = there > 3 ? b.y : there == 3 ? b.y & low : 0;
-      b.z = there > 5 ? b.z : there == 5 ? b.z & low : 0;
-      b.w = there == 7 ? b.w & low : 0;
-    }
+    if constexpr (!kGrid) b = first_of(b, there);
     return b;
   }
   // the warp has read all: the next row may come

@@ -24,6 +24,58 @@ __device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t c
   return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
 }
 
+// The same in two steps, so that several loads off the grid are under way
+// together: the one or two 16-byte blocks that hold the elements, then the
+// elements. All lanes of the warp take vectors of one row.
+struct Blocks {
+  uint4 x, y;
+  int distance, count;
+};
+
+__device__ __forceinline__ Blocks load_blocks(const uint16_t* row, int64_t c, int64_t cols,
+                                              const Bounds& in) {
+  Blocks b;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
+  const uint4* block = reinterpret_cast<const uint4*>(at & ~static_cast<uintptr_t>(15));
+  b.distance = static_cast<int>(at & 15);
+  b.count = c < cols ? static_cast<int>(cols - c < kVec ? cols - c : kVec) : 0;
+  b.x = b.y = make_uint4(0, 0, 0, 0);
+  if (b.count > 0 && in.holds_blocks(block, 16, kSiteLoad)) b.x = block[0];
+  if (b.distance + 2 * b.count > 16 && in.holds_blocks(block + 1, 16, kSiteLoad)) b.y = block[1];
+  return b;
+}
+
+// the first `there` of eight elements, the others 0
+__device__ __forceinline__ uint4 first_of(uint4 v, int there) {
+  if (there >= kVec) return v;
+  const uint32_t low = 0xFFFFu;
+  v.x = there > 1 ? v.x : there == 1 ? v.x & low : 0;
+  v.y = there > 3 ? v.y : there == 3 ? v.y & low : 0;
+  v.z = there > 5 ? v.z : there == 5 ? v.z & low : 0;
+  v.w = there == 7 ? v.w & low : 0;
+  return v;
+}
+
+__device__ __forceinline__ uint4 eight_of(const Blocks& b) {
+  return first_of(shifted_alike(b.x, b.y, b.distance), b.count);
+}
+
+// kCount vectors of eight, by a grid's rows or off it; row(k), column(k)
+template <bool kGrid, int kCount, class Row, class Column>
+__device__ __forceinline__ void load_all(uint4 (&v)[kCount], Row row, Column column, int64_t cols,
+                                         const Bounds& in) {
+  if constexpr (kGrid) {
+#pragma unroll
+    for (int k = 0; k < kCount; ++k) v[k] = load8<true>(row(k), column(k), cols, in);
+  } else {
+    Blocks b[kCount];
+#pragma unroll
+    for (int k = 0; k < kCount; ++k) b[k] = load_blocks(row(k), column(k), cols, in);
+#pragma unroll
+    for (int k = 0; k < kCount; ++k) v[k] = eight_of(b[k]);
+  }
+}
+
 // A warp's 256 columns of a row from c0 on, those before `cols`; all lanes
 // call it.
 template <bool kGrid>
