@@ -5,9 +5,9 @@
 // (window, shard, records, stage slot, unit slices). The kernels behind
 // zero_train.h and zero_block.h test the addresses of the elements they load and store in the
 // call's arrays, checkpoints and partial sums (train.cuh, Bounds); not tested
-// there are the per-token arrays, the sort's keys and the norms' and gates'
-// parameters (indexed by the row or column at hand), what TMA loads (it keeps to
-// its map) and, but for the loss's parts, shared memory. A failing test skips the access,
+// there are the per-token arrays, the sort's keys and the gradients of the norms'
+// and gates' parameters (indexed by the row or column at hand), what TMA loads and
+// stores (it keeps to its map) and, but for the loss's parts, shared memory. A failing test skips the access,
 // counts the violation and keeps the first one (site << 48 | low 48 bits of
 // the index); nothing traps. Each translation unit keeps its own counters
 // (device code is not linked across units); zero_checked_status collects

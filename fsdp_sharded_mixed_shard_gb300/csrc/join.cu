@@ -45,8 +45,10 @@ constexpr int kMaxParts = 152;    // CTAs
 constexpr int kForwardVectors = 4, kBackVectors = 2;
 static_assert(ZERO_MAX_JOIN_COLS <= kBackVectors * kMaxThreads * kVec, "a row fits a CTA");
 
-enum { kH, kY, kHOut, kZ, kStats, kDz, kDhOut, kDh, kDy, kParts, kBuffers };  // of a call
 enum { kWPost, kBPost, kGate, kWPre, kBPre, kParams };
+// of a call, the parameters last
+enum { kH, kY, kHOut, kZ, kStats, kDz, kDhOut, kDh, kDy, kParts, kParam0,
+       kBuffers = kParam0 + kParams };
 enum { kSumP, kSumA, kSumQ, kSumB, kSums };
 
 struct Args : Checked<kBuffers> {
@@ -314,8 +316,9 @@ __device__ __forceinline__ Pair normed(const Pair& x, const float2& st) {
 
 // Eight of a parameter's elements, `none` where there is no parameter.
 template <bool kBf16>
-__device__ __forceinline__ Eight load_param(const uint16_t* w, int c, int cols, float none) {
-  if (w) return widen_pairs<kBf16>(load8<false>(w, c, cols, Bounds{}));
+__device__ __forceinline__ Eight load_param(const Args& a, int param, int c, float none) {
+  if (a.param[param])
+    return widen_pairs<kBf16>(load8<false>(a.param[param], c, a.cols, a.bounds(kParam0 + param)));
   return Eight{{both(none), both(none), both(none), both(none)}};
 }
 
@@ -335,13 +338,13 @@ __device__ __forceinline__ void stage_columns(const Args& a, float4* w) {
   const int n = a.slots_of_row;
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
     const int c = i * kVec;  // past the last column parameters count as 0
-    const Eight gate = load_param<kBf16>(a.param[kGate], c, a.cols, 1.f);
+    const Eight gate = load_param<kBf16>(a, kGate, c, 1.f);
     const auto put = [&](int k, const Eight& e) { write_eight_at(w + 2 * k * n + i, n, e); };
-    put(kC, scaled(gate, load_param<kBf16>(a.param[kWPost], c, a.cols, 1.f), a.branch_scale));
-    put(kPre, load_param<kBf16>(a.param[kWPre], c, a.cols, 0.f));
+    put(kC, scaled(gate, load_param<kBf16>(a, kWPost, c, 1.f), a.branch_scale));
+    put(kPre, load_param<kBf16>(a, kWPre, c, 0.f));
     if constexpr (kCount > 2) {
-      put(kD, scaled(gate, load_param<kBf16>(a.param[kBPost], c, a.cols, 0.f), a.branch_scale));
-      put(kBias, load_param<kBf16>(a.param[kBPre], c, a.cols, 0.f));
+      put(kD, scaled(gate, load_param<kBf16>(a, kBPost, c, 0.f), a.branch_scale));
+      put(kBias, load_param<kBf16>(a, kBPre, c, 0.f));
     }
   }
 }
@@ -793,7 +796,10 @@ int check(const zero_join_params* p, const zero_join_weights* w, int64_t rows, i
 void set_common(Args& a, const zero_join_params& p, const zero_join_weights& w, int64_t rows,
                 int64_t cols, int64_t ld) {
   const void* params[kParams] = {w.w_post, w.b_post, w.gate, w.w_pre, w.b_pre};
-  for (int k = 0; k < kParams; ++k) a.param[k] = static_cast<const uint16_t*>(params[k]);
+  for (int k = 0; k < kParams; ++k) {
+    a.param[k] = static_cast<const uint16_t*>(params[k]);
+    a.set_bounds(kParam0 + k, params[k], 1, cols, 0, 2);
+  }
   a.rows = rows, a.cols = static_cast<int32_t>(cols), a.ld = ld;
   a.eps = static_cast<float>(p.eps);
   a.inv_cols = static_cast<float>(1.0 / static_cast<double>(cols));
