@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 8; ++e) row[1 + e] = v[e / 4][e % 4];
           __syncwarp();
-          store_staged(stage, to, a.ld, a.rows - i0, c, kOutCols, count, lane, a.bounds(kOut));
+          store_staged<4>(stage, to, a.ld, a.rows - i0, c, kOutCols, count, lane, a.bounds(kOut));
           __syncwarp();
         }
       }
@@ -709,6 +709,7 @@ int resident_clusters(int split) {
 bool known_format(int32_t f) { return f == ZERO_E4M3 || f == ZERO_E5M2; }
 
 constexpr int64_t kMost = int64_t{1} << 31;
+constexpr int64_t kMostProduct = int64_t{1} << 30;  // tiles' ends stay below 2^31
 
 // out[rows, n] from the left copy [rows, k] and the weight's copy [w_rows, w_cols]
 template <bool kSlow>
@@ -719,7 +720,7 @@ int multiply(const void* copy, int32_t format, int64_t rows, const void* w_copy,
     return ZERO_EINVAL;
   const int64_t n = kSlow ? w_cols : w_rows, k = kSlow ? w_rows : w_cols;
   if (ld < n) return ZERO_EINVAL;
-  if (rows >= kMost || w_rows >= kMost || w_cols >= kMost) return ZERO_ERANGE;
+  if (rows >= kMostProduct || w_rows >= kMostProduct || w_cols >= kMostProduct) return ZERO_ERANGE;
   if (rows == 0 || n == 0) return ZERO_OK;
   if (!out || (k && (!copy || !w_copy))) return ZERO_EINVAL;
   if (!aligned(copy, 16) || !aligned(w_copy, 16) || !aligned(out, 2) || !aligned(d_scaler, 16))

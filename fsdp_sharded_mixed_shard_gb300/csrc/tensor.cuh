@@ -160,13 +160,14 @@ __device__ __forceinline__ void narrow32(const float (&f)[32], uint4 (&v)[4]) {
 constexpr int kOutCols = 64, kOutPitch = 16 + kOutCols * 2;
 
 // columns [c, c + width) of the tile's row that starts at `to`, which has
-// `count` columns
+// `count` columns; kTogether passes of four rows at a time
+template <int kTogether>
 __device__ __forceinline__ void store_staged(uint8_t* stage, uint16_t* to, int64_t n, int64_t rows,
                                              int c, int width, int count, int lane,
                                              const Bounds& in) {
   const int k = lane & 7, row0 = lane >> 3;
   const int end = c + width < count ? c + width : count;  // columns there are so far
-#pragma unroll 1
+#pragma unroll kTogether
   for (int pass = 0; pass < 8; ++pass) {
     const int row = pass * 4 + row0;
     if (row >= rows) continue;

@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
             last = v[3];
             if (within || c + 32 == kWide * a.bn) {
               __syncwarp();
-              store_staged(stage, to, a.n, a.cols - i0, c - within, within + 32, count, lane,
+              store_staged<1>(stage, to, a.n, a.cols - i0, c - within, within + 32, count, lane,
                            a.bounds(kDw));
               __syncwarp();
             }

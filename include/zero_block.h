@@ -90,7 +90,7 @@ typedef enum zero_norm { ZERO_NORM_RMS = 0, ZERO_NORM_LAYER = 1 } zero_norm;
 
 typedef struct zero_join_params {
   int32_t norm;
-  double eps;           /* >= 0 */
+  double eps;           /* >= 0; with 0 a row of zeros comes out NaN */
   double stream_scale;  /* finite */
   double branch_scale;  /* finite */
   zero_dropout_params drop; /* p = 0: none */
@@ -179,7 +179,8 @@ ZERO_API int zero_fp8_quant_weight(const void* w, int64_t k, int64_t n, int32_t 
  * where the reduction is empty. A pipeline wait that expires (2 s) fills the
  * tiles that its cluster of CTAs had left with NaN and, when d_scaler is not
  * NULL, raises ZERO_DEVERR_TIMEOUT there.
- * rows, k, n < 2^31 (ZERO_ERANGE). */
+ * Sums past the smallest normal fp32 number (2^-126) may come out 0.
+ * rows, k, n < 2^30 (ZERO_ERANGE). */
 ZERO_API int zero_fp8_linear(const void* x_copy, int32_t x_format, int64_t rows,
                              const void* w_copy, int64_t k, int64_t n, int32_t dtype, void* y,
                              int64_t ld, zero_scaler* d_scaler, void* stream);

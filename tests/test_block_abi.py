@@ -140,6 +140,6 @@ def test_fp8_products(f, n):
         refused(EINVAL, f, *changed(ok, **bad))
     for bad in (dict(i0=P + 8), dict(i3=P + 8), dict(i7=P + 1), dict(i9=P + 8)):
         refused(EALIGN, f, *changed(ok, **bad))
-    for bad in (dict(i2=1 << 31), dict(i4=1 << 31, i8=1 << 32), dict(i5=1 << 31, i8=1 << 32)):
+    for bad in (dict(i2=1 << 30), dict(i4=1 << 30, i8=1 << 32), dict(i5=1 << 30, i8=1 << 32)):
         refused(ERANGE, f, *changed(ok, **bad))
     f(*changed(ok, i2=0, i0=0, i3=0, i7=0))

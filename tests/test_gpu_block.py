@@ -86,6 +86,21 @@ def test_dropout_leaves_out_what_is_not_finite():
     assert 0.4 < (f > 0).double().mean().item() < 0.6
 
 
+def test_dropout_in_place_off_the_grid():
+    rows, cols = 61, 1001
+    p = Z.ZeroDropoutParams(0.3, 11, 12, 0)
+    x, r = (place(rand((rows, cols), "fp16", k), cols, 3, "fp16") for k in (1, 2))
+    run = lambda x, r, o: Z.zero_dropout(p, at(x), at(r), rows, cols, cols, Z.ZERO_FP16,  # noqa: E731
+                                         at(o), cols, stream())
+    out = target(rows, cols, cols, 3, "fp16")[1]
+    run(x, r, out)
+    for mine in (x, r):
+        before = mine.clone()
+        run(x, r, mine)
+        assert torch.equal(mine, out)
+        mine.copy_(before)
+
+
 def test_dropout_in_place_and_again():
     """In place over x or the residual, the same bits; another call, step, seed
     or row: other masks."""
@@ -462,6 +477,20 @@ def test_fp8_products(dtype, fmt, rows, k, n, past, shift):
     assert bool((scaler == 0).all())
     untouched(wy, y)
     untouched(wd, dx)
+
+
+@pytest.mark.parametrize("up,down", [(-100, 90), (100, -110), (-60, -40), (30, 40)])
+def test_fp8_products_of_far_scales(up, down):
+    """Scales far from 1, whose product is not: they add up as exponents do."""
+    rows, k, n = 40, 384, 264
+    x = (rand((rows, k), "bf16", 1).double() * 2.0 ** up).to(torch.bfloat16)
+    w = (rand((k, n), "bf16", 2).double() * 2.0 ** down).to(torch.bfloat16)
+    x8, w8 = copy_of(x, rows, k, k, "bf16", "e4m3"), weight_of(w, k, n, "bf16")
+    y = torch.empty(rows, n, device="cuda", dtype=torch.bfloat16)
+    Z.zero_fp8_linear(at(x8), 0, rows, at(w8), k, n, Z.ZERO_BF16, at(y), n, 0, stream())
+    xv, wv = fp8_64(x, "e4m3", 1)[1], fp8_64(w, "e4m3", 128)[1]
+    want = xv @ wv
+    within(y, want, product_bound(want, xv, wv, k, "bf16"), "y")
 
 
 def test_fp8_products_of_what_is_not_finite():
