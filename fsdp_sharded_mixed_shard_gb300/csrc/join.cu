@@ -314,14 +314,6 @@ __device__ __forceinline__ Pair normed(const Pair& x, const float2& st) {
   return kLayer ? (x + both(-st.x)) * both(st.y) : x * both(st.y);
 }
 
-// Eight of a parameter's elements, `none` where there is no parameter.
-template <bool kBf16>
-__device__ __forceinline__ Eight load_param(const Args& a, int param, int c, float none) {
-  if (a.param[param])
-    return widen_pairs<kBf16>(load8<false>(a.param[param], c, a.cols, a.bounds(kParam0 + param)));
-  return Eight{{both(none), both(none), both(none), both(none)}};
-}
-
 __device__ __forceinline__ Eight scaled(const Eight& x, const Eight& y, float s) {
   Eight e;
 #pragma unroll
@@ -338,13 +330,21 @@ __device__ __forceinline__ void stage_columns(const Args& a, float4* w) {
   const int n = a.slots_of_row;
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
     const int c = i * kVec;  // past the last column parameters count as 0
-    const Eight gate = load_param<kBf16>(a, kGate, c, 1.f);
+    Blocks b[kParams];  // all loads before the first use
+#pragma unroll
+    for (int k = 0; k < kParams; ++k)
+      if (a.param[k]) b[k] = load_blocks(a.param[k], c, a.cols, a.bounds(kParam0 + k));
+    const auto param = [&](int k, float none) {
+      return a.param[k] ? widen_pairs<kBf16>(eight_of(b[k]))
+                        : Eight{{both(none), both(none), both(none), both(none)}};
+    };
     const auto put = [&](int k, const Eight& e) { write_eight_at(w + 2 * k * n + i, n, e); };
-    put(kC, scaled(gate, load_param<kBf16>(a, kWPost, c, 1.f), a.branch_scale));
-    put(kPre, load_param<kBf16>(a, kWPre, c, 0.f));
+    const Eight gate = param(kGate, 1.f);
+    put(kC, scaled(gate, param(kWPost, 1.f), a.branch_scale));
+    put(kPre, param(kWPre, 0.f));
     if constexpr (kCount > 2) {
-      put(kD, scaled(gate, load_param<kBf16>(a, kBPost, c, 0.f), a.branch_scale));
-      put(kBias, load_param<kBf16>(a, kBPre, c, 0.f));
+      put(kD, scaled(gate, param(kBPost, 0.f), a.branch_scale));
+      put(kBias, param(kBPre, 0.f));
     }
   }
 }
