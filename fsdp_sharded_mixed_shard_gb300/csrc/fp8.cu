@@ -25,6 +25,12 @@
  * share 32 columns: those are read first, and the next tile's products wait for
  * them alone.
  *
+ * One lane issues, but the whole warp with it (at copy_box2). 8192 x 2048 x 8192
+ * takes 82 us for x W and 84 for dy W^T (3.3 PFLOP/s; 8192^3 306 us, 3.6), where
+ * the same kernel without any copies takes 80 to 86 (299): the tensor cores, whose
+ * clock the power cap holds down, are what bounds it. The right operand brought
+ * for two pairs at once by multicast was no faster (84 to 86; 322).
+ *
  * Few tiles and a long reduction: a cluster of 2, 4 or 8 pairs shares a tile,
  * each pair a part of the reduction; the sums meet in shared memory and every
  * CTA adds its share of the rows over the cluster in rank order. Split and tile
@@ -205,7 +211,9 @@ constexpr int kSmem = kRing + kOutWarps * kOutBytes + 1024;
 constexpr int kJoinPitch = kN + 4;  // fp32 row of a tile in shared memory
 constexpr int kMaxSplit = 8, kJoinAhead = 4;
 // tensor memory: two tiles' sums, the second from kSecond on, then scales in two
-// sets of 16 columns (4 of the left operand, up to 8 of the right one)
+// sets of 16 columns (4 of the left operand, up to 8 of the right one). Copies of
+// scales and products run in the order in which one thread issues them, so that a
+// set is not written before the products that were to read it.
 constexpr int kTensorColumns = 512, kSecond = 224, kScaleColumn = 480, kScaleSets = 2;
 static_assert(kSecond + kN <= kScaleColumn && kN - kSecond == 32, "the tiles share 32 columns");
 static_assert(kScaleColumn + 16 * kScaleSets <= kTensorColumns, "tensor memory");

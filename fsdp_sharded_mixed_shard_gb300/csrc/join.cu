@@ -25,8 +25,19 @@
  *   P = sum dz h^,  Q = sum dz,  A = sum m D y^,  B = sum m D:
  *   dw_pre = P, db_pre = Q, dw_post = branch_scale gate A,
  *   db_post = branch_scale gate B, dgate = branch_scale (w_post A + b_post B).
- * A thread adds those of its own columns up. A CTA joins its teams' in order and leaves one vector each in the workspace; a second kernel
- * adds the (at most kMaxParts) vectors in order.
+ * A thread adds those of its own columns up. A CTA joins its teams' in order and
+ * leaves one vector each in the workspace; a second kernel adds the (at most
+ * kMaxParts) vectors in order.
+ *
+ * The row after the one at hand is on its way into shared memory meanwhile, as
+ * the 16-byte blocks that hold it, so that memory is busy all the time and rows
+ * off the 16-byte grid need no more registers (at Ahead). Measured, bf16,
+ * ZERO_NORM_RMS with all parameters: 8192 x 2048 forward 21 to 22 us (91 % of copy
+ * bandwidth), backward 39 (77 %), 4096 x 8192 49 and 74 (80 %); 8192 x 2047 41 and
+ * 67, where putting vectors together takes the time. With loads half a row's work
+ * ahead into registers the backward pass took 46 and 102, rows off the grid 67 and
+ * 121. What bounds them now: instructions and the latency of a row's sums
+ * (the issue slots are 40 to 60 % busy), beside memory.
  */
 #include "draws.cuh"
 #include "rows.cuh"
@@ -440,12 +451,14 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_kernel(const Args a) {
   }
 }
 
-// Sums over the rows of a thread's own columns: P and A in shared memory, eight
-// floats for each sum and vector in the thread's own words; Q and B, which belong
-// to ZERO_NORM_LAYER, in registers until the rows are done.
-template <int kV>
+// Sums over the rows of a thread's own columns. Two of them have room in registers
+// until the rows are done: P and A or, with ZERO_NORM_LAYER, Q and B, while P and A
+// then are in shared memory, eight floats for each sum and vector in the thread's
+// own words.
+template <bool kLayer, int kV>
 struct ColumnSums {
   float4* own;
+  Eight r[2][kV];
   __device__ __forceinline__ float4* at(int k, int v) const {
     return own + (k * kV + v) * 2 * kMaxThreads;
   }
@@ -453,17 +466,33 @@ struct ColumnSums {
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int v = 0; v < kV; ++v) put(k, v, Eight{{both(0.f), both(0.f), both(0.f), both(0.f)}});
+      for (int v = 0; v < kV; ++v) {
+        r[k][v] = Eight{{both(0.f), both(0.f), both(0.f), both(0.f)}};
+        if constexpr (kLayer) put(k, v, r[k][v]);
+      }
   }
   __device__ __forceinline__ void put(int k, int v, const Eight& e) const {
     write_eight_at(at(k, v), kMaxThreads, e);
   }
-  // += x y
-  __device__ __forceinline__ void add(int k, int v, const Eight& x, const Eight& y) const {
-    Eight s = read_eight_at(at(k, v), kMaxThreads);
+  // P (0) or A (1) += x y
+  __device__ __forceinline__ void add(int k, int v, const Eight& x, const Eight& y) {
+    Eight s = kLayer ? read_eight_at(at(k, v), kMaxThreads) : r[k][v];
 #pragma unroll
     for (int j = 0; j < 4; ++j) s.p[j] = fma2(x.p[j], y.p[j], s.p[j]);
-    put(k, v, s);
+    if constexpr (kLayer) put(k, v, s);
+    else r[k][v] = s;
+  }
+  // Q (0) or B (1) += x
+  __device__ __forceinline__ void add(int k, int v, const Eight& x) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[k][v].p[j] = r[k][v].p[j] + x.p[j];
+  }
+  // those in registers into shared memory
+  __device__ __forceinline__ void leave() const {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int v = 0; v < kV; ++v) put(k, v, r[k][v]);
   }
 };
 
@@ -519,11 +548,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_grad_kernel(const Args a)
   };
   if (row < a.rows) start(row);  // under way while the columns' numbers are set up
   stage_columns<kBf16, 2>(a, smem);
-  const ColumnSums<kV> sums(sums_smem);
-  Eight sum_q[kV], sum_b[kV];
-#pragma unroll
-  for (int v = 0; v < kV; ++v)
-    sum_q[v] = sum_b[v] = Eight{{both(0.f), both(0.f), both(0.f), both(0.f)}};
+  ColumnSums<kLayer, kV> sums(sums_smem);
   clear(exchange);
   for (; row < a.rows; row += stride) {
     const float2 sy = make_float2(st.x, st.y);
@@ -562,11 +587,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_grad_kernel(const Args a)
       }
       sums.add(0, v, g0, xh[v]);
       if constexpr (kLayer) {
+        sums.add(0, v, g0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          sum_q[v].p[j] = sum_q[v].p[j] + g0.p[j];
-          part[kG1] = part[kG1] + g.p[j];
-        }
+        for (int j = 0; j < 4; ++j) part[kG1] = part[kG1] + g.p[j];
       }
       if (a.drop.threshold) keep[v] = kept(a.drop, step, row, col[v]);
       if constexpr (kPost) {
@@ -617,9 +640,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_grad_kernel(const Args a)
       if (a.drop.threshold) drop_pairs(a.drop, keep[v], d[v]);
       if (need_y) {
         sums.add(1, v, d[v], xy[v]);
-        if constexpr (kLayer)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sum_b[v].p[j] = sum_b[v].p[j] + d[v].p[j];
+        if constexpr (kLayer) sums.add(1, v, d[v]);
       }
       const Eight c = column(a, smem, kC, col[v]);
 #pragma unroll
@@ -641,12 +662,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_grad_kernel(const Args a)
   const int team_threads = 32 * a.team_warps;
   float* part = a.parts + static_cast<int64_t>(blockIdx.x) * a.slots * a.pitch;
   for (int round = 0; round < (kLayer ? 2 : 1); ++round) {
-    if (kLayer && round)
-#pragma unroll
-      for (int v = 0; v < kV; ++v) {
-        sums.put(0, v, sum_q[v]);
-        sums.put(1, v, sum_b[v]);
-      }
+    if (!kLayer || round) sums.leave();
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * a.slots_of_row; i += blockDim.x) {
       const int q = i / a.slots_of_row, vector = i - q * a.slots_of_row;

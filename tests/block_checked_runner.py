@@ -70,7 +70,8 @@ def join(cols, shift, layer, back):
     fwd = lambda: Z.zero_block_join(p, T.weights_of(w), at(h), at(y), rows, cols, cols, BF,  # noqa: E731
                                     at(h_out), at(z), at(stats), stream())
     if not back:
-        last = {k: None for k in range(10, 15) if w[NAMES[k - 10]] is not None}
+        # the parameters come in whole blocks: seen where the last element is alone in one
+        last = {10 + k: None for k, name in enumerate(NAMES) if w[name] is not None and cols % 8 == 1}
         return fwd, {0: None, 1: None, 2: h_out, 3: z, 4: stats, **last}
     fwd()
     run = lambda: Z.zero_block_join_grad(  # noqa: E731
