@@ -174,8 +174,8 @@ ZERO_API int zero_fp8_quant_weight(const void* w, int64_t k, int64_t n, int32_t 
                                    void* stream);
 
 /* y = round16(x W) [rows, n] from x's copy [rows, k] and W's [k, n];
- * dx = round16(dy W^T) [rows, k] from dy's copy [rows, n] and W's. x_format and
- * dy_format are those of the copies. ld is the row distance of y, dx. Zeros
+ * dx = round16(dy W^T) [rows, k] from dy's copy [rows, n] and W's. Sizes and
+ * formats are those that the copies were made with. ld is the row distance of y, dx. Zeros
  * where the reduction is empty. A pipeline wait that expires (2 s) fills the
  * tiles that its cluster of CTAs had left with NaN and, when d_scaler is not
  * NULL, raises ZERO_DEVERR_TIMEOUT there.

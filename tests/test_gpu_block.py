@@ -600,3 +600,92 @@ def test_block_captured_and_replayed():
             assert torch.equal(a, b)
     assert not torch.equal(want[0][1], want[1][1])
     assert math.isfinite(dx.double().norm().item())
+
+
+def test_offsets_past_32_bits():
+    """Rows 2^31 elements apart: every operator's result is that of the same rows
+    side by side."""
+    rows, cols, ld = 3, 264, 1 << 31
+    far = lambda: torch.empty((rows - 1) * ld + cols, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    view = lambda t: t.as_strided((rows, cols), (ld, 1))  # noqa: E731
+    bf, st = Z.ZERO_BF16, stream()
+    a, b, c, d = (far() for _ in range(4))
+    x, y = rand((rows, cols), "bf16", 1), rand((rows, cols), "bf16", 2)
+    near = [torch.empty(rows, cols, device="cuda", dtype=torch.bfloat16) for _ in range(4)]
+    p = Z.ZeroDropoutParams(0.25, 5, 6, 0)
+    view(a).copy_(x)
+    view(b).copy_(y)
+    Z.zero_dropout(p, at(a), at(b), rows, cols, ld, bf, at(c), ld, st)
+    Z.zero_dropout(p, at(x), at(y), rows, cols, cols, bf, at(near[0]), cols, st)
+    assert torch.equal(view(c), near[0])
+    n = Z.zero_fp8_bytes(rows, cols)
+    q = [torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    Z.zero_fp8_quant(at(a), rows, cols, ld, bf, 0, at(q[0]), st)
+    Z.zero_fp8_quant(at(x), rows, cols, cols, bf, 0, at(q[1]), st)
+    assert torch.equal(*q)
+    w8 = weight_of(rand((cols, cols), "bf16", 3), cols, cols, "bf16")
+    Z.zero_fp8_linear(at(q[0]), 0, rows, at(w8), cols, cols, bf, at(c), ld, 0, st)
+    Z.zero_fp8_linear(at(q[0]), 0, rows, at(w8), cols, cols, bf, at(near[0]), cols, 0, st)
+    assert torch.equal(view(c), near[0])
+    # the join in place over h and y, its gradient over dh_out and dz
+    w = {k: rand((1, cols), "bf16", 10 + i)[0] for i, k in enumerate(NAMES)}
+    g = [{k: torch.empty_like(v) for k, v in w.items()} for _ in range(2)]
+    hp = Z.ZeroJoinParams(Z.ZERO_NORM_LAYER, 1e-5, 1.0, 0.5, p)
+    work = torch.empty(Z.zero_block_join_workspace_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+    stats = [torch.empty(rows, 4, device="cuda") for _ in range(2)]
+    view(c).copy_(x)
+    view(d).copy_(y)
+    Z.zero_block_join(hp, weights_of(w), at(a), at(b), rows, cols, ld, bf, at(a), at(b), at(stats[0]), st)
+    Z.zero_block_join(hp, weights_of(w), at(x), at(y), rows, cols, cols, bf, at(near[0]), at(near[1]),
+                      at(stats[1]), st)
+    assert torch.equal(view(a), near[0]) and torch.equal(view(b), near[1])
+    Z.zero_block_join_grad(hp, weights_of(w), at(a), at(b), at(stats[0]), at(c), at(d), rows, cols, ld,
+                           bf, at(d), at(c), weights_of(g[0]), at(work), st)
+    Z.zero_block_join_grad(hp, weights_of(w), at(near[0]), at(near[1]), at(stats[1]), at(x), at(y), rows,
+                           cols, cols, bf, at(near[2]), at(near[3]), weights_of(g[1]), at(work), st)
+    assert torch.equal(view(d), near[2]) and torch.equal(view(c), near[3])
+    for k in NAMES:
+        assert torch.equal(g[0][k], g[1][k])
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own workspace, that run beside one
+    another give what they give alone."""
+    rows, dim, hidden = 3000, 512, 1024
+    side = [torch.cuda.Stream() for _ in range(2)]
+    cases = []
+    for k in range(2):
+        c = join_case("bf16", rows, dim, dim, 0, bool(k), NAMES if k else ("w_post", "gate", "w_pre"),
+                      0.1, 1.0, 0.5, seed=20 + k)
+        x, w = rand((rows, hidden), "bf16", 30 + k), rand((hidden, dim), "bf16", 32 + k, 0.05)
+        t = dict(c=c, x8=copy_of(x, rows, hidden, hidden, "bf16", "e4m3"),
+                 w8=weight_of(w, hidden, dim, "bf16"), stats=torch.empty(rows, 4, device="cuda"),
+                 work=torch.empty(Z.zero_block_join_workspace_bytes(rows, dim), dtype=torch.uint8,
+                                  device="cuda"),
+                 out=[torch.empty(rows, dim, device="cuda", dtype=torch.bfloat16) for _ in range(5)],
+                 g={n: None if v is None else torch.empty_like(v) for n, v in c["w"].items()})
+        cases.append(t)
+    torch.cuda.synchronize()
+
+    def run(t, st):
+        c, (y, h_out, z, dh, dy), bf = t["c"], t["out"], Z.ZERO_BF16
+        Z.zero_fp8_linear(at(t["x8"]), 0, rows, at(t["w8"]), hidden, dim, bf, at(y), dim, 0, st)
+        Z.zero_block_join(params_of(c), weights_of(c["w"]), at(c["h"]), at(y), rows, dim, dim, bf,
+                          at(h_out), at(z), at(t["stats"]), st)
+        Z.zero_block_join_grad(params_of(c), weights_of(c["w"]), at(h_out), at(y), at(t["stats"]),
+                               at(c["dz"]), at(c["dh_out"]), rows, dim, dim, bf, at(dh), at(dy),
+                               weights_of(t["g"]), at(t["work"]), st)
+
+    results = lambda t: [o.clone() for o in t["out"] + [v for v in t["g"].values() if v is not None]]  # noqa: E731
+    alone = []
+    for t, s in zip(cases, side):
+        run(t, s.cuda_stream)
+        torch.cuda.synchronize()
+        alone.append(results(t))
+    for _ in range(20):
+        for t, s in zip(cases, side):
+            run(t, s.cuda_stream)
+    torch.cuda.synchronize()
+    for t, want in zip(cases, alone):
+        for a, b in zip(results(t), want):
+            assert torch.equal(a, b)
