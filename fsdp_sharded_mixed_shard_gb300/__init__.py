@@ -2,9 +2,10 @@
 one GB300.
 
 A thin ctypes layer over the C ABI in include/zero.h, include/zero_units.h,
-include/zero_train.h and include/zero_block.h: every function below has the C function's name and only marshals arguments (device pointers are
-plain Python ints, host arrays become C arrays); all computation happens in
-the sm_103a kernels of _lib/libzero.so. Loading fails loudly when the library
+include/zero_train.h and include/zero_block.h: every function below has the C
+function's name and only marshals arguments (device pointers are plain Python
+ints, host arrays become C arrays); all computation happens in the sm_103a
+kernels of _lib/libzero.so. Loading fails loudly when the library
 has not been built (run ``__graft_entry__.build()``); there is no fallback.
 """
 import ctypes as C

@@ -110,8 +110,9 @@ extern "C" ZERO_API int zero_dropout(const zero_dropout_params* params, const vo
   a.set_bounds(kX, x, rows, cols, ld, 2);
   a.set_bounds(kResidual, residual, rows, cols, ld_out, 2);
   a.set_bounds(kOut, out, rows, cols, ld_out, 2);
-  const auto fn = dtype == ZERO_BF16 ? (grid ? dropout_kernel<true, true> : dropout_kernel<true, false>)
-                                     : (grid ? dropout_kernel<false, true> : dropout_kernel<false, false>);
+  const auto fn = dtype == ZERO_BF16
+                      ? (grid ? dropout_kernel<true, true> : dropout_kernel<true, false>)
+                      : (grid ? dropout_kernel<false, true> : dropout_kernel<false, false>);
   return status_of(launch_pdl(fn, dim3(static_cast<unsigned>(ceil_div(rows * col_tiles, kWarps))),
                               dim3(kThreads), 0, static_cast<cudaStream_t>(stream), a));
 }

@@ -330,8 +330,8 @@ __device__ __forceinline__ void product(uint32_t d, uint32_t a_low, uint32_t b_l
       "{\n .reg .pred p, e;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n"
       " elect.sync _|e, 0xffffffff;\n"
       " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
-      " @e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], da, db, %3, [%6], "
-      "[%7], p;\n}" ::"r"(d),
+      " @e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], da, db, %3, "
+      "[%6], [%7], p;\n}" ::"r"(d),
       "r"(a_low), "r"(b_low), "r"(desc), "r"(add), "r"(kOperandHigh), "r"(scale_a), "r"(scale_b)
       : "memory");
 }
@@ -690,20 +690,31 @@ bool prepare(Kernel fn) {
              cudaSuccess;
 }
 
+// Devices whose answers are kept (a call's checks cost about as much host time
+// as its launch otherwise).
+constexpr int kDevices = 64;
+
+// the current device, -1 on error or past those
+int current_device() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kDevices ? dev : -1;
+}
+
 template <bool kBf16, bool kSlow>
-int launch(const Maps& maps, const Args& a, int clusters, cudaStream_t st) {
+int launch(const Maps& maps, const Args& a, int clusters, int dev, cudaStream_t st) {
   const auto fn = product_kernel<kBf16, kSlow>;
-  if (!prepare(fn)) return ZERO_ECUDA;
+  static std::atomic<bool> prepared[kDevices];
+  if (!prepared[dev].load(std::memory_order_relaxed)) {
+    if (!prepare(fn)) return ZERO_ECUDA;
+    prepared[dev].store(true, std::memory_order_relaxed);
+  }
   Launch l(clusters, a.split, st);
   return status_of(cudaLaunchKernelEx(&l.cfg, fn, maps, a));
 }
 
 // Clusters of `split` pairs that the device holds at once (0 on error).
-int resident_clusters(int split) {
-  constexpr int kDevices = 64;
+int resident_clusters(int dev, int split) {
   static std::atomic<int> known[kDevices][kMaxSplit + 1];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
   int n = known[dev][split].load(std::memory_order_relaxed);
   if (n == 0) {
     const auto fn = product_kernel<true, true>;
@@ -744,8 +755,10 @@ int multiply(const void* copy, int32_t format, int64_t rows, const void* w_copy,
   // TMA stores whole 16-byte blocks on their grid, row distances below 2^40 bytes
   a.tma_out = n % kVec == 0 && ld % kVec == 0 && aligned(out, 16) && ld < int64_t{1} << 39;
   a.set_bounds(kOut, out, rows, n, ld, 2);
+  const int dev = current_device();
+  if (dev < 0) return ZERO_ECUDA;
   int fit[kMaxSplit + 1];
-  for (int split = 1; split <= kMaxSplit; split *= 2) fit[split] = resident_clusters(split);
+  for (int split = 1; split <= kMaxSplit; split *= 2) fit[split] = resident_clusters(dev, split);
   if (fit[1] <= 0) return ZERO_ECUDA;
   const int64_t pairs = fit[1], m_tiles = ceil_div(rows, 2 * kM);
   // Tile width and split of the reduction by the cycles they take: turns of all
@@ -788,8 +801,8 @@ int multiply(const void* copy, int32_t format, int64_t rows, const void* w_copy,
       !encode_scales(&maps.scale_b, scales, blocks_of(n), groups_of(k), a.scale_tiles) ||
       (a.tma_out && !encode_out(&maps.out, out, n, rows, ld)))
     return ZERO_ECUDA;
-  return dtype == ZERO_BF16 ? launch<true, kSlow>(maps, a, clusters, st)
-                            : launch<false, kSlow>(maps, a, clusters, st);
+  return dtype == ZERO_BF16 ? launch<true, kSlow>(maps, a, clusters, dev, st)
+                            : launch<false, kSlow>(maps, a, clusters, dev, st);
 }
 
 }  // namespace zf
@@ -829,10 +842,12 @@ ZERO_API int zero_fp8_quant(const void* x, int64_t rows, int64_t cols, int64_t l
   a.set_bounds(kX, x, rows, cols, ld, 2);
   a.set_bounds(kCopy, copy, 1, static_cast<int64_t>(zero_fp8_bytes(rows, cols)), 0, 1);
   const bool grid = on_grid(x, ld);
-  const auto fn = dtype == ZERO_BF16 ? (grid ? quant_kernel<true, true> : quant_kernel<true, false>)
-                                     : (grid ? quant_kernel<false, true> : quant_kernel<false, false>);
-  return status_of(launch_pdl(fn, dim3(static_cast<unsigned>(ceil_div(rows * col_tiles, kQuantWarps))),
-                              dim3(32 * kQuantWarps), 0, static_cast<cudaStream_t>(stream), a));
+  const auto fn = dtype == ZERO_BF16
+                      ? (grid ? quant_kernel<true, true> : quant_kernel<true, false>)
+                      : (grid ? quant_kernel<false, true> : quant_kernel<false, false>);
+  const dim3 ctas(static_cast<unsigned>(ceil_div(rows * col_tiles, kQuantWarps)));
+  return status_of(launch_pdl(fn, ctas, dim3(32 * kQuantWarps), 0,
+                              static_cast<cudaStream_t>(stream), a));
 }
 
 ZERO_API size_t zero_fp8_weight_bytes(int64_t k, int64_t n) {
@@ -862,9 +877,10 @@ ZERO_API int zero_fp8_quant_weight(const void* w, int64_t k, int64_t n, int32_t 
   a.set_bounds(kX, w, k, n, n, 2);
   a.set_bounds(kCopy, copy, 1, static_cast<int64_t>(zero_fp8_weight_bytes(k, n)), 0, 1);
   const bool grid = on_grid(w, n);
-  const auto fn = dtype == ZERO_BF16
-                      ? (grid ? quant_weight_kernel<true, true> : quant_weight_kernel<true, false>)
-                      : (grid ? quant_weight_kernel<false, true> : quant_weight_kernel<false, false>);
+  const bool bf16 = dtype == ZERO_BF16;
+  const auto fn =
+      grid ? (bf16 ? quant_weight_kernel<true, true> : quant_weight_kernel<false, true>)
+           : (bf16 ? quant_weight_kernel<true, false> : quant_weight_kernel<false, false>);
   return status_of(launch_pdl(fn, dim3(static_cast<unsigned>(blocks_of(k) * ceil_div(n, kCols))),
                               dim3(256), 0, static_cast<cudaStream_t>(stream), a));
 }

@@ -911,7 +911,8 @@ ZERO_API int zero_block_join(const zero_join_params* params, const zero_join_wei
   a.set_bounds(kZ, z, rows, cols, ld, 2);
   a.set_bounds(kStats, stats, 1, rows, rows, 16);
   const int per = set_teams(a, rows, cols, kForwardVectors);
-  const bool grid = cols % kVec == 0 && on_grid(h, ld) && aligned(y, 16) && aligned(h_out, 16) && aligned(z, 16);
+  const bool grid = cols % kVec == 0 && on_grid(h, ld) && aligned(y, 16) && aligned(h_out, 16) &&
+                    aligned(z, 16);
   return status_of(ZJ_PICK(launch_join, dtype == ZERO_BF16, grid, params->norm == ZERO_NORM_LAYER,
                            a, per, static_cast<cudaStream_t>(stream)));
 }
@@ -980,8 +981,8 @@ ZERO_API int zero_block_join_grad(const zero_join_params* params, const zero_joi
     a.set_bounds(kDh, dh, rows, cols, ld, 2);
     a.set_bounds(kDy, dy, rows, cols, ld, 2);
     a.set_bounds(kParts, workspace, 1, ctas * j.slots * j.pitch, 0, 4);
-    const bool grid = cols % kVec == 0 && on_grid(dh, ld) && aligned(dy, 16) && aligned(h_out, 16) && aligned(y, 16) &&
-                      aligned(dz, 16) && aligned(dh_out, 16);
+    const bool grid = cols % kVec == 0 && on_grid(dh, ld) && aligned(dy, 16) &&
+                      aligned(h_out, 16) && aligned(y, 16) && aligned(dz, 16) && aligned(dh_out, 16);
     const int bad = status_of(ZJ_PICK(launch_grad, bf16, grid, params->norm == ZERO_NORM_LAYER, a,
                                       per, st));
     if (bad) return bad;
