@@ -127,13 +127,21 @@ __device__ __forceinline__ uint32_t kept(const Drop& d, uint32_t step, int64_t r
   return keep8(d, w);
 }
 
-__device__ __forceinline__ void drop_pairs(const Drop& d, uint32_t keep, Eight& e) {
+// what is left out becomes 0, whatever it was
+__device__ __forceinline__ Eight kept_only(uint32_t keep, Eight e) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     float a, b;
-    unpair(e.p[j] * both(d.scale), a, b);
+    unpair(e.p[j], a, b);
     e.p[j] = pair(keep >> (2 * j) & 1 ? a : 0.f, keep >> (2 * j + 1) & 1 ? b : 0.f);
   }
+  return e;
+}
+
+__device__ __forceinline__ void drop_pairs(const Drop& d, uint32_t keep, Eight& e) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) e.p[j] = e.p[j] * both(d.scale);
+  e = kept_only(keep, e);
 }
 
 // Eight floats in shared memory as two words of 16 bytes, `apart` words apart:
@@ -163,12 +171,11 @@ struct Ahead {
   uint4* own;  // the warp's
   int lane;
   __device__ __forceinline__ Ahead(void* smem)
-      : own(static_cast<uint4*>(smem) + (threadIdx.x >> 5) * kSpan), lane(threadIdx.x & 31) {
-    if constexpr (kGrid)  // past the last column nothing comes
+      : own(static_cast<uint4*>(smem) + (threadIdx.x >> 5) * kSpan), lane(threadIdx.x & 31) {}
+  // the lane's v-th vector lies past the last column, where nothing comes
+  __device__ __forceinline__ void clear(int v) const {
 #pragma unroll
-      for (int k = 0; k < kArrays; ++k)
-#pragma unroll
-        for (int v = 0; v < kV; ++v) at(k, v)[lane] = make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < kArrays; ++k) at(k, v)[lane] = make_uint4(0, 0, 0, 0);
   }
   __device__ __forceinline__ uint4* at(int array, int v) const {
     return own + (array * kV + v) * (kMaxWarps * kSpan);
@@ -213,9 +220,7 @@ struct Ahead {
     return b;
   }
   // the warp has read all: the next row may come
-  __device__ __forceinline__ void done() const {
-    if constexpr (!kGrid) __syncwarp();
-  }
+  __device__ __forceinline__ void done() const { __syncwarp(); }
 };
 
 template <bool kGrid>
@@ -387,6 +392,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_kernel(const Args a) {
   }
   // behind the columns' numbers
   const Ahead<2, kV, kGrid> ahead(smem + 2 * (kLayer ? 4 : 2) * a.slots_of_row);
+#pragma unroll
+  for (int v = 0; v < kV; ++v)
+    if (kGrid && there[v] == 0) ahead.clear(v);
   const auto start = [&](int64_t row) {
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
@@ -534,6 +542,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_grad_kernel(const Args a)
   }
   float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
   const Ahead<4, kV, kGrid> ahead(sums_smem + 2 * kV * 2 * kMaxThreads);
+#pragma unroll
+  for (int v = 0; v < kV; ++v)
+    if (kGrid && there[v] == 0) ahead.clear(v);
   const auto start = [&](int64_t r) {
     const int64_t at = r * a.ld;
 #pragma unroll
@@ -639,6 +650,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_grad_kernel(const Args a)
                       narrow_pairs<kBf16>(e), a.bounds(kDh));
       if (a.drop.threshold) drop_pairs(a.drop, keep[v], d[v]);
       if (need_y) {
+        // what was left out of y counts for nothing in the gate's gradient either
+        if (!kPost && a.drop.threshold) xy[v] = kept_only(keep[v], xy[v]);
         sums.add(1, v, d[v], xy[v]);
         if constexpr (kLayer) sums.add(1, v, d[v]);
       }

@@ -335,6 +335,25 @@ def test_join_rows_that_are_not_finite():
         within(z[good], want[good], bound[good], "z")
 
 
+@pytest.mark.parametrize("cols", [264, 263])
+def test_join_leaves_out_what_is_not_finite(cols):
+    """Without a norm after the block, an infinity that dropout leaves out counts for
+    nothing: not in h_out, z or any gradient."""
+    rows = 40
+    c = join_case("bf16", rows, cols, cols, 0, False, ("gate", "w_pre"), 0.5, 1.0, 1.0, seed=8)
+    clean = c["y"].clone()
+    c["y"][c["keep"] == 0] = float("inf")
+    new = lambda: torch.empty(rows, cols, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    h_out, z, dh, dy, stats = new(), new(), new(), new(), torch.empty(rows, 4, device="cuda")
+    forward(c, h_out, z, stats)
+    grads = {k: torch.empty_like(c["w"][k]) if k in ("gate", "w_pre") else None for k in NAMES}
+    backward(c, h_out, stats, dh, dy, grads)
+    within(h_out, *c["ref"].h_out(c["h"].double(), clean.double()), "h_out")
+    want = c["ref"].grads(h_out.double(), clean.double(), c["dz"].double(), c["dh_out"].double())
+    for name, got in (("dh", dh), ("dy", dy), ("gate", grads["gate"]), ("w_pre", grads["w_pre"])):
+        within(got, *want[name], name)
+
+
 def test_join_with_no_rows():
     grads = {k: torch.full((100,), 7.0, device="cuda", dtype=torch.bfloat16) for k in NAMES}
     w = weights_of(grads)
