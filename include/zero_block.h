@@ -82,7 +82,8 @@ ZERO_API int zero_dropout(const zero_dropout_params* params, const void* x, cons
  * (z must be NULL). Statistics are those of the stored h_out, so that the
  * gradient is that of what was computed. Sums are fp32: a row that is normalised
  * and holds an infinity or a NaN, or whose squares pass fp32's range (values
- * past about 1e18), comes out NaN throughout, so that its step is skipped.
+ * past about 1e18), comes out NaN throughout (but for what dropout leaves out
+ * of n), so that its step is skipped.
  * rows < 2^31, cols <= ZERO_MAX_JOIN_COLS (ZERO_ERANGE). */
 #define ZERO_MAX_JOIN_COLS 8192
 
