@@ -53,3 +53,14 @@ def test_random_products(seed):
         rows = max(1, rows // 2)
     T.test_fp8_products(r.choice(["bf16", "fp16"]), r.choice(["e4m3", "e5m2"]), rows, k, n,
                         r.choice([0, 0, 1, 8]), r.choice([0, 0, 8, 3]))
+
+
+@pytest.mark.parametrize("rows,k,n", [(8192, 128, 4096), (8192, 64, 4096), (6000, 250, 5000),
+                                      (4096, 700, 4096)])
+def test_short_reductions_of_many_tiles(rows, k, n):
+    """One to six blocks per tile and several tiles per pair of SMs, scales that
+    differ from block to block: each tile's scales and sums follow close on
+    another's."""
+    for fmt in ("e4m3", "e5m2"):
+        T.test_fp8_products("bf16", fmt, rows, k, n, 0, 0)
+        T.test_fp8_products("fp16", fmt, n, rows, k, 0, 0)  # the other way: dy W^T over k
