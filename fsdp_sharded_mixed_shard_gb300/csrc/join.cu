@@ -837,13 +837,20 @@ void set_common(Args& a, const zero_join_params& p, const zero_join_weights& w, 
   a.drop = drop_of(p.drop);
 }
 
-// `columns` numbers per column and `more` bytes of shared memory
-template <class Kernel>
+// The widest row's vectors in a team of kV per thread.
+template <int kV>
+constexpr int kMostSlots = std::min(32 * kV * kMaxWarps, ZERO_MAX_JOIN_COLS / kVec);
+static_assert(ZERO_MAX_JOIN_COLS / kVec % (32 * kForwardVectors) == 0, "whole warps");
+
+// `columns` numbers per column and `more` bytes of shared memory. A kernel's limit
+// is the same for every call, that of its widest row: all host threads share it, and
+// one that set it for a row of its own would take it from another's launch.
+template <int kV, class Kernel>
 cudaError_t launch_with(Kernel fn, const Args& a, int columns, int more, cudaStream_t st) {
   const int bytes = 32 * columns * a.slots_of_row + more;
   if (bytes > 32 * 1024) {  // 48 KB with the kernels' own
-    const cudaError_t e =
-        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               32 * columns * kMostSlots<kV> + more);
     if (e != cudaSuccess) return e;
   }
   const int64_t ctas = std::min<int64_t>(kMaxParts, ceil_div(a.rows, a.teams));
@@ -853,8 +860,8 @@ cudaError_t launch_with(Kernel fn, const Args& a, int columns, int more, cudaStr
 
 template <bool kBf16, bool kGrid, bool kLayer, int kV>
 cudaError_t launch_join_of(const Args& a, cudaStream_t st) {
-  return launch_with(join_kernel<kBf16, kGrid, kLayer, kV>, a, kLayer ? 4 : 2,
-                     Ahead<2, kV, kGrid>::kBytes, st);
+  return launch_with<kV>(join_kernel<kBf16, kGrid, kLayer, kV>, a, kLayer ? 4 : 2,
+                         Ahead<2, kV, kGrid>::kBytes, st);
 }
 
 template <bool kBf16, bool kGrid, bool kLayer>
@@ -866,8 +873,8 @@ cudaError_t launch_join(const Args& a, int per, cudaStream_t st) {
 
 template <bool kBf16, bool kGrid, bool kLayer, bool kPost, int kV>
 cudaError_t launch_grad_of(const Args& a, cudaStream_t st) {
-  return launch_with(join_grad_kernel<kBf16, kGrid, kLayer, kPost, kV>, a, 2,
-                     2 * kV * 32 * kMaxThreads + Ahead<4, kV, kGrid>::kBytes, st);
+  return launch_with<kV>(join_grad_kernel<kBf16, kGrid, kLayer, kPost, kV>, a, 2,
+                         2 * kV * 32 * kMaxThreads + Ahead<4, kV, kGrid>::kBytes, st);
 }
 
 template <bool kBf16, bool kGrid, bool kLayer>
