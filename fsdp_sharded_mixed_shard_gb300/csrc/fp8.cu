@@ -140,6 +140,10 @@ __global__ void __launch_bounds__(32 * kQuantWarps) quant_kernel(const QuantArgs
     const uint2 lo = narrow_fp8<kBf16>(v[0], scale, a.format);
     const uint2 hi = narrow_fp8<kBf16>(v[1], scale, a.format);
     *reinterpret_cast<uint4*>(q) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    if (scale == 255) {  // NaN, but past the last column zeros as everywhere
+#pragma unroll 1
+      for (int64_t j = max(c, a.cols); j < c + 16; ++j) a.q[r * a.pitch + j] = 0;
+    }
   }
   if ((lane & 7) == 0) {
     uint8_t* s = a.scale + scale_at(row, static_cast<uint32_t>(c) / kBlock,
@@ -180,11 +184,16 @@ __global__ void __launch_bounds__(256) quant_weight_kernel(const QuantArgs a) {
 #pragma unroll
   for (int w = 0; w < 8; ++w) top = max_u16x2(top, tops[side][w]);
   const uint32_t scale = scale_of<kBf16>(max(top & 0xFFFFu, top >> 16), ZERO_E4M3);
+  // zeros past the last column, also where the block is not finite
+  const int64_t left = a.cols - c;
+  const uint64_t all = ~0ull, bits = left >= kVec ? all : left > 0 ? all >> (8 * (kVec - left)) : 0;
+  const uint2 columns = make_uint2(static_cast<uint32_t>(bits), static_cast<uint32_t>(bits >> 32));
 #pragma unroll
   for (int i = 0; i < kWeightRows; ++i) {
     uint8_t* q = a.q + (r0 + i) * a.pitch + c;
+    const uint2 n = narrow_fp8<kBf16>(v[i], scale, ZERO_E4M3);
     if (r0 + i < a.rows && c < a.pitch && a.bounds(kCopy).holds(q, kVec, kSiteStore))
-      *reinterpret_cast<uint2*>(q) = narrow_fp8<kBf16>(v[i], scale, ZERO_E4M3);
+      *reinterpret_cast<uint2*>(q) = make_uint2(n.x & columns.x, n.y & columns.y);
   }
   // the scale of each of a block's 128 columns and rows
   const int64_t nb = 2 * nt + side;
