@@ -43,6 +43,7 @@
 #include "rows.cuh"
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 namespace zj {
@@ -808,8 +809,9 @@ int check(const zero_join_params* p, const zero_join_weights* w, int64_t rows, i
           int64_t ld, int32_t dtype) {
   if (!p || !w || rows < 0 || cols < 0 || ld < cols || !is_dtype16(dtype)) return ZERO_EINVAL;
   if (p->norm != ZERO_NORM_RMS && p->norm != ZERO_NORM_LAYER) return ZERO_EINVAL;
-  if (!(p->eps >= 0.0) || !std::isfinite(p->eps) || !std::isfinite(p->stream_scale) ||
-      !std::isfinite(p->branch_scale))
+  // as the kernels have them, in fp32 (comparisons that a NaN fails)
+  if (!(p->eps == 0.0 || (p->eps >= FLT_MIN && p->eps <= FLT_MAX)) ||
+      !(std::fabs(p->stream_scale) <= FLT_MAX) || !(std::fabs(p->branch_scale) <= FLT_MAX))
     return ZERO_EINVAL;
   if (const int bad = check_drop(p->drop)) return bad;
   const bool layer = p->norm == ZERO_NORM_LAYER;

@@ -91,9 +91,10 @@ typedef enum zero_norm { ZERO_NORM_RMS = 0, ZERO_NORM_LAYER = 1 } zero_norm;
 
 typedef struct zero_join_params {
   int32_t norm;
-  double eps;           /* >= 0; with 0 a row of zeros comes out NaN */
-  double stream_scale;  /* finite */
-  double branch_scale;  /* finite */
+  double eps;           /* 0, or a normal number of fp32 (2^-126 and more); with 0 a
+                         * row of zeros comes out NaN */
+  double stream_scale;  /* in fp32's range, as branch_scale */
+  double branch_scale;
   zero_dropout_params drop; /* p = 0: none */
 } zero_join_params;
 
