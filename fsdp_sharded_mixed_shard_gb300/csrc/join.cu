@@ -278,9 +278,13 @@ __device__ __forceinline__ void team_sum(const Args& a, const Place& p, Exchange
 }
 
 __device__ __forceinline__ float inverse_root(float mean_square, float eps) {
-  // squares past fp32's range: NaN, not 0
-  return mean_square < __uint_as_float(0x7F800000u) ? rsqrtf(mean_square + eps)
-                                                    : __uint_as_float(0x7FC00000u);
+  // NaN, not 0 or infinity, past fp32's range and below its normal numbers, where
+  // squares (with eps 0) are lost; from 2^-126 on what single squares lose of a mean
+  // is 2^-150 each, 2^-24 of it
+  const float x = mean_square + eps;
+  return x >= __uint_as_float(0x00800000u) && x < __uint_as_float(0x7F800000u)
+             ? rsqrtf(x)
+             : __uint_as_float(0x7FC00000u);
 }
 
 // Statistics (mean or 0, 1 / sqrt(mean square + eps)) of a row held by the team;

@@ -81,9 +81,10 @@ ZERO_API int zero_dropout(const zero_dropout_params* params, const void* x, cons
  * to ZERO_NORM_LAYER and need their w (ZERO_EINVAL otherwise). w_pre NULL: no z
  * (z must be NULL). Statistics are those of the stored h_out, so that the
  * gradient is that of what was computed. Sums are fp32: a row that is normalised
- * and holds an infinity or a NaN, or whose squares pass fp32's range (values
- * past about 1e18), comes out NaN throughout (but for what dropout leaves out
- * of n), so that its step is skipped.
+ * and holds an infinity or a NaN, or whose mean square plus eps passes fp32's range
+ * (values past about 1e18; with eps 0 also a mean square below 2^-126, values
+ * below about 1e-19, zeros among them), comes out NaN throughout (but for what
+ * dropout leaves out of n), so that its step is skipped.
  * rows < 2^31, cols <= ZERO_MAX_JOIN_COLS (ZERO_ERANGE). */
 #define ZERO_MAX_JOIN_COLS 8192
 
@@ -91,8 +92,7 @@ typedef enum zero_norm { ZERO_NORM_RMS = 0, ZERO_NORM_LAYER = 1 } zero_norm;
 
 typedef struct zero_join_params {
   int32_t norm;
-  double eps;           /* 0, or a normal number of fp32 (2^-126 and more); with 0 a
-                         * row of zeros comes out NaN */
+  double eps;           /* 0, or a normal number of fp32 (2^-126 and more) */
   double stream_scale;  /* in fp32's range, as branch_scale */
   double branch_scale;
   zero_dropout_params drop; /* p = 0: none */
