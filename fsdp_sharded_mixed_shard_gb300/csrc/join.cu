@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) join_grad_kernel(const Args a)
       if (a.dh_out) ahead.start(2, v, a.dh_out, at, first, a.cols, a.bounds(kDhOut));
       if (need_y) ahead.start(3, v, a.y, at, first, a.cols, a.bounds(kY));
     }
-    if (a.bounds(kStats).holds(a.stats + r, 16, kSiteLoad)) st = a.stats[r];
+    if ((kPost || pre) && a.bounds(kStats).holds(a.stats + r, 16, kSiteLoad)) st = a.stats[r];
   };
   if (row < a.rows) start(row);  // under way while the columns' numbers are set up
   stage_columns<kBf16, 2>(a, smem);
@@ -980,8 +980,9 @@ ZERO_API int zero_block_join_grad(const zero_join_params* params, const zero_joi
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf16 = dtype == ZERO_BF16;
   if (rows) {
-    if (!dh || !dy || !stats || dh == dy || (w[kWPre] && (!h_out || !dz)) || (!w[kWPre] && dz) ||
-        ((w[kWPost] || w[kGate]) && !y) || (j.slots && !workspace))
+    if (!dh || !dy || dh == dy || ((w[kWPost] || w[kWPre]) && !stats) ||
+        (w[kWPre] && (!h_out || !dz)) || (!w[kWPre] && dz) || ((w[kWPost] || w[kGate]) && !y) ||
+        (j.slots && !workspace))
       return ZERO_EINVAL;
     if (!aligned(h_out, 2) || !aligned(y, 2) || !aligned(dz, 2) || !aligned(dh_out, 2) ||
         !aligned(dh, 2) || !aligned(dy, 2) || !aligned(stats, 16) || !aligned(workspace, 16))

@@ -128,7 +128,8 @@ ZERO_API size_t zero_block_join_workspace_bytes(int64_t rows, int64_t cols);
  * and, summed over the rows in fp32 and rounded once, the gradient of each
  * parameter given in weights, written to its place in grads (which is NULL
  * exactly where weights is; ZERO_EINVAL otherwise). dz is NULL exactly where
- * w_pre is. y may be NULL where neither w_post nor gate is given.
+ * w_pre is. h_out may be NULL where w_pre is not given, y where neither w_post nor
+ * gate is, stats where neither w_post nor w_pre is, workspace where no parameter is.
  * All [rows, cols] arrays have row distance ld. dh may be dh_out itself, dy dz
  * itself, or the other way round. */
 ZERO_API int zero_block_join_grad(const zero_join_params* params, const zero_join_weights* weights,

@@ -32,3 +32,15 @@ def test_what_fp32_holds_is_taken(f, ok):
     for j in (join(a=MOST), join(s=-MOST), join(a=1e-60), join(s=0.0), join(eps=0.0),
               join(eps=LEAST), join(eps=MOST)):
         refused(ERANGE, f, *changed(ok, i0=j, **wide))
+
+
+def test_no_norm_needs_no_statistics():
+    """Without w_post and w_pre the gradient goes past its check of stats, with
+    either of them not: seen by the refusal that comes after it (a misaligned dh)."""
+    f = Z.zero_block_join_grad
+    gate = Z.ZeroJoinWeights(0, 0, P, 0, 0)
+    rest = dict(i4=0, i11=6 * P + 1)
+    refused(-2, f, *changed(BACK, i1=gate, i13=gate, i5=0, **rest))
+    for w in (Z.ZeroJoinWeights(P, 0, 0, 0, 0), Z.ZeroJoinWeights(0, 0, 0, P, 0)):
+        dz = 0 if w.w_post else 4 * P
+        refused(EINVAL, f, *changed(BACK, i1=w, i13=w, i5=dz, **rest))
