@@ -364,7 +364,9 @@ __device__ __forceinline__ void stage_columns(const Args& a, float4* w) {
     put(kC, scaled(gate, param(kWPost, 1.f), a.branch_scale));
     put(kPre, param(kWPre, 0.f));
     if constexpr (kCount > 2) {
-      put(kD, scaled(gate, param(kBPost, 0.f), a.branch_scale));
+      // a bias that is not there adds nothing, also where the gate is infinite
+      const Eight bias = param(kBPost, 0.f);
+      put(kD, a.param[kBPost] ? scaled(gate, bias, a.branch_scale) : bias);
       put(kBias, param(kBPre, 0.f));
     }
   }

@@ -84,7 +84,8 @@ ZERO_API int zero_dropout(const zero_dropout_params* params, const void* x, cons
  * and holds an infinity or a NaN, or whose mean square plus eps passes fp32's range
  * (values past about 1e18; with eps 0 also a mean square below 2^-126, values
  * below about 1e-19, zeros among them), comes out NaN throughout (but for what
- * dropout leaves out of n), so that its step is skipped.
+ * dropout leaves out of n), so that its step is skipped. A gate that is not finite
+ * makes h_out infinite or NaN where dropout keeps n, and stream_scale * h where not.
  * rows < 2^31, cols <= ZERO_MAX_JOIN_COLS (ZERO_ERANGE). */
 #define ZERO_MAX_JOIN_COLS 8192
 
