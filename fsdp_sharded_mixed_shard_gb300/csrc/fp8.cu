@@ -26,10 +26,15 @@
  * them alone.
  *
  * One lane issues, but the whole warp with it (at copy_box2). 8192 x 2048 x 8192
- * takes 82 us for x W and 84 for dy W^T (3.3 PFLOP/s; 8192^3 306 us, 3.6), where
- * the same kernel without any copies takes 80 to 86 (299): the tensor cores, whose
- * clock the power cap holds down, are what bounds it. The right operand brought
- * for two pairs at once by multicast was no faster (84 to 86; 322).
+ * takes 83 us for x W and 84 for dy W^T (3.3 PFLOP/s; 8192^3 305 to 312 us, 3.6).
+ * Time is cycles over a clock that power holds down: 159,000 cycles each way
+ * on random numbers as on zeros, 97 us at 1.63 GHz after seconds on end and 77 at
+ * the full 2.07 (8192^3: 506,000 at 1.39 GHz, 537,000 at 2.07). The tensor cores
+ * are busy for 110,000 of them (72 and 70 %; 8192^3 87 %). At 2.07 GHz a block costs
+ * 562 cycles, 512 of them products, and each of the 14 turns of tiles 2,400 more, for
+ * its start and end, the pairs without a tile in the last turn and the launch; dy W^T
+ * has 3.4 turns' tiles in four. The right operand brought for two pairs at once by
+ * multicast was no faster (84 to 86; 322).
  *
  * Few tiles and a long reduction: a cluster of 2, 4 or 8 pairs shares a tile,
  * each pair a part of the reduction; the sums meet in shared memory and every
@@ -230,8 +235,9 @@ static_assert(32 * kOutPitch <= kOutBytes && 32 * 128 <= kOutBytes, "output stag
 static_assert((1 + kScaleTiles) * kTileBytes <= kBytesScales && kStageBytes % 1024 == 0, "stages");
 static_assert(kM * kJoinPitch * 4 <= kRing, "the tile fits the stages");
 // costs in cycles: a block, and its thirds per column (128, 192 and 256 columns
-// took 484, 595 to 625 and 661 to 717 at 8192 x 2048 x 8192 and 8192^3, most of
-// it waiting for the copies); a column put out; the join of a split, by rows per
+// took 484, 595 to 625 and 661 to 717 at 8192 x 2048 x 8192 and 8192^3, what a tile
+// costs beside its blocks shared out among them; the products alone are 256, 384
+// and 512); a column put out; the join of a split, by rows per
 // warp (600 x 512 x 512 4.8 us, split in two 10.1; 16 x 8192 x 256 16 us, split in
 // two, four and eight 11.4, 8.0 and 7.2); clusters of 16 CTAs
 constexpr int kBlockCycles = 340, kColumnThirds = 4;
@@ -700,7 +706,8 @@ bool prepare(Kernel fn) {
 }
 
 // Devices whose answers are kept (a call's checks cost about as much host time
-// as its launch otherwise).
+// as its launch otherwise). A kernel's attributes hold in every context of its
+// device, also after a reset: the runtime sets them again where it loads the kernel.
 constexpr int kDevices = 64;
 
 // the current device, -1 on error or past those

@@ -32,12 +32,14 @@
  * The row after the one at hand is on its way into shared memory meanwhile, as
  * the 16-byte blocks that hold it, so that memory is busy all the time and rows
  * off the 16-byte grid need no more registers (at Ahead). Measured, bf16,
- * ZERO_NORM_RMS with all parameters: 8192 x 2048 forward 21 to 22 us (91 % of copy
- * bandwidth), backward 39 (77 %), 4096 x 8192 49 and 74 (80 %); 8192 x 2047 41 and
- * 67, where putting vectors together takes the time. With loads half a row's work
- * ahead into registers the backward pass took 46 and 102, rows off the grid 67 and
- * 121. What bounds them now: instructions and the latency of a row's sums
- * (the issue slots are 40 to 60 % busy), beside memory.
+ * ZERO_NORM_RMS with all parameters: 8192 x 2048 forward 20.5 to 22 us (91 % of copy
+ * bandwidth), backward 39 (77 %), 4096 x 8192 47 to 49 and 71 (84 %); 8192 x 2047 41
+ * and 67, where putting vectors together takes the time; 8192 x 2048 ZERO_NORM_LAYER
+ * with dropout 34 and 57. With loads half a row's work ahead into registers the
+ * backward pass took 46 and 102, rows off the grid 67 and 121. What bounds them now:
+ * instructions and the latency of a row's sums (the issue slots are 40 to 60 % busy),
+ * beside memory. The backward kernels with ZERO_NORM_LAYER on both sides and two
+ * vectors per thread spill 44 to 72 bytes of their 128 registers.
  */
 #include "draws.cuh"
 #include "rows.cuh"
@@ -799,7 +801,8 @@ int set_teams(Args& a, int64_t rows, int64_t cols, int most) {
          rows * ceil_div(vectors, 32 * per) < kMaxParts * kMaxWarps / 2)
     per /= 2;
   // two vectors per thread leave up to half of a row's last warp idle: one, where
-  // that fits a quarter tighter (8192 x 768 backward 25 us against 27)
+  // that fits a quarter tighter (8192 x 768 backward 25 us against 27). Forward a
+  // team is as it comes, with up to 46 % of its places empty (1111 columns).
   const auto room = [&](int n) { return n * ceil_div(vectors, 32 * n); };
   if (most == kBackVectors && per == 2 && vectors <= kMaxThreads && 4 * room(2) > 5 * room(1))
     per = 1;
