@@ -145,7 +145,9 @@ __global__ void __launch_bounds__(32 * kQuantWarps) quant_kernel(const QuantArgs
     const uint2 lo = narrow_fp8<kBf16>(v[0], scale, a.format);
     const uint2 hi = narrow_fp8<kBf16>(v[1], scale, a.format);
     *reinterpret_cast<uint4*>(q) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-    if (scale == 255) {  // NaN, but past the last column zeros as everywhere
+    // NaN, but past the last column zeros as everywhere. A loop that stays one, for 32
+    // registers: with 34 a CTA less fits (8192 x 8191 41 us, 38 so)
+    if (scale == 255) {
 #pragma unroll 1
       for (int64_t j = max(c, a.cols); j < c + 16; ++j) a.q[r * a.pitch + j] = 0;
     }
